@@ -492,6 +492,108 @@ int kvp_decode_step_plan(kvp_pool *pool, const int32_t *seq_ids, int32_t num_seq
 int kvp_decode_step_run(kvp_step_plan *plan, const kvp_step_io *io, void *workspace, size_t ws_bytes,
                         void *stream);
 
+/* ------------------------------------------- bounded caches and drafts */
+
+/*
+ * Accumulated attention weight of every cached token, from the log-sum-exp
+ * that an attention call left: for each layer, sequence s, kv head h and
+ * cached token t < seq_lens[s],
+ *   mass_out[l][s][h][t] = decay * mass_in[l][s][h][t]
+ *       + sum over the sequence's query tokens i at positions >= t, and over
+ *         the query heads of kv head h, of exp(scale * q_i . k_t - lse_i).
+ * Sequence s has q_lens[s] query tokens (host; NULL: one each; 0 allowed),
+ * the last of its seq_lens[s] cached tokens, as in a decode step (1) or after
+ * a prompt chunk; q [L][T][Hq][d] bf16 and lse [L][T][Hq] fp32 (natural log,
+ * of attention over every cached token up to the query's own) hold them
+ * sequence after sequence, T = sum of q_lens.  A row whose lse is -inf adds
+ * nothing.  mass_in and mass_out are device fp32, [L][num_seqs][Hkv]
+ * [mass_stride], mass_stride >= the longest sequence; they may be one buffer.
+ * mass_in holds the first prev_lens[s] tokens (host; NULL: seq_lens - q_lens,
+ * the tokens before this step's); later ones count as 0, and with mass_in
+ * NULL all do.  Entries of mass_out from seq_lens[s] on are left as they are.
+ * K is read once, V not at all.  Pages must be bf16; block_tables, seq_lens,
+ * desc (use_sharing is not used) and workspace as for
+ * paged_decode_attention, ws_bytes >= kvp_mass_workspace_size().  Cached keys
+ * must be finite.  KVP_ERR_STATE while `stream` is being captured.
+ */
+size_t kvp_mass_workspace_size(const kvp_attn_desc *desc, const int32_t *block_tables,
+                               const int32_t *seq_lens, const int32_t *q_lens, int32_t num_seqs,
+                               int32_t max_blocks);
+int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, const void *k_pool,
+                       const int32_t *block_tables, const int32_t *seq_lens, int32_t num_seqs,
+                       int32_t max_blocks, const kvp_attn_desc *desc, float decay,
+                       const float *mass_in, const int32_t *prev_lens, float *mass_out,
+                       int64_t mass_stride, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Evicts all but `budget` tokens of each of n distinct sequences, chosen per
+ * layer and kv head by accumulated attention weight: the first n_sink and the
+ * last n_recent tokens stay, and of the others the heaviest, among equal
+ * weights the lowest position (a NaN weighs less than anything).  mass is
+ * device fp32 [L][n][Hkv][mass_stride].  The kept tokens' K and V move, in
+ * order, to the sequence's first slots (which token a slot holds then differs
+ * by layer and head, while the table and the length, `budget`, are the
+ * sequence's), and the blocks past them are released.  kept (device int32
+ * [L][n][Hkv][budget]) receives the positions that the kept tokens had,
+ * mass_out (device, laid out like mass; NULL: not wanted; mass itself or
+ * apart from it) their weights in the first `budget` entries.  A sequence of
+ * at most `budget` tokens stays as it is: kept = 0, 1, ... then -1, its
+ * weights copied.
+ * Pages that another sequence or the prefix cache also holds are not written:
+ * the sequence gets fresh blocks for them, except for pages that hold sink
+ * tokens alone, which stay shared.  Sharing is judged at the start of the
+ * call, so sequences of one call that share a page with each other both get
+ * fresh blocks.
+ * seqs is a host array; ws_bytes >= seq_evict_workspace_size(), workspace
+ * 256-byte aligned, kept until the stream has passed the call.  All or
+ * nothing: KVP_ERR_OOM (no free blocks), KVP_ERR_INVALID and KVP_ERR_STATE (a
+ * pool without K/V storage or of 4-bit pages, or a stream being captured)
+ * change nothing; after KVP_ERR_CUDA from a launch the bookkeeping stands.
+ */
+size_t seq_evict_workspace_size(const kvp_pool *pool, const int32_t *seqs, int32_t n, int32_t budget);
+int seq_evict(kvp_pool *pool, const int32_t *seqs, int32_t n, const float *mass, int64_t mass_stride,
+              int32_t budget, int32_t n_sink, int32_t n_recent, int32_t *kept, float *mass_out,
+              void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Which drafted tokens the target accepts, and the token after them: the step
+ * between tree_verify_attention and seq_accept_draft ("CAST", section on
+ * speculative decoding: the target model accepts one path of the draft tree).
+ * Sequence b has n_draft <= 64 draft nodes with tree_parent [B][n_draft] as
+ * for tree_verify_attention (a chain: -1, 0, 1, ...) and draft_tokens
+ * [B][n_draft].  Row 0 of target is the target's next-token distribution
+ * after the context, row 1 + i that after draft node i; row r of draft is the
+ * distribution from which the children of that point were drawn, one after
+ * the other in node order (rows of nodes without children are not read).
+ * From the root on, the children of the current node are tried in node
+ * order: child i with token x is accepted when
+ *     u_accept[b][i] * q(x) * Z < p(x) - c * q(x),
+ * with c = 0, Z = 1 at the first child and, after each rejection, c += Z,
+ * then Z = sum over the vocabulary of max(p - c q, 0); an accepted child
+ * becomes the current node.  When none is (left), next_token is the first
+ * token at which the running sum of max(p - c q, 0) exceeds u_next[b] times
+ * its whole (p itself if nothing is left).  The tokens are then distributed
+ * as the target's own samples.  draft NULL stands for drafts that were chosen
+ * outright (greedy, or the best few): a child is accepted when
+ * u_accept * Z < p(x), and a rejection sets p(x) to 0 and takes it off Z.
+ * accepted [B]: the last accepted node or -1 (seq_accept_draft's argument);
+ * n_accepted [B]: how many; next_token [B] (-1 if a row of p is all zero).
+ *
+ * target / draft: device fp32 probabilities (each row sums to about 1; NaN
+ * and negative entries count as 0), element (b, r, x) at b * batch_stride +
+ * r * row_stride + x, strides >= 0 (0: one distribution for all).
+ * tree_parent, draft_tokens, u_* in [0, 1), and the outputs: device, int32
+ * and fp32.  A parent outside [-1, i) makes a root; a node whose token is
+ * outside [0, vocab) is left out.  Sums over the vocabulary are exact to
+ * 2^-60 an entry, so the result does not depend on the row's split over the
+ * GPU.  One kernel, no workspace; may be captured into a graph.
+ */
+int kvp_draft_verify(const float *target, int64_t target_batch_stride, int64_t target_row_stride,
+                     const float *draft, int64_t draft_batch_stride, int64_t draft_row_stride,
+                     const int32_t *tree_parent, const int32_t *draft_tokens, const float *u_accept,
+                     const float *u_next, int32_t batch, int32_t n_draft, int32_t vocab,
+                     int32_t *accepted, int32_t *n_accepted, int32_t *next_token, void *stream);
+
 /* Reads (and clears) the device error word that the last attention call on
  * this workspace left; synchronises `stream`.  *err_out = 0 when clean. */
 int kvp_device_error(void *workspace, void *stream, int32_t *err_out);

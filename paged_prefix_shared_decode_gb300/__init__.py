@@ -28,6 +28,7 @@ __all__ = [
     "DecodeStep", "KVP_STEP_HOST_MAPPED", "kvp_step_plan_create", "kvp_step_plan_destroy",
     "kvp_decode_step_plan", "kvp_decode_step_run", "StepPlan",
     "KVP_STATIC_WORKSPACE_BYTES",
+    "kvp_mass_workspace_size", "kvp_attention_mass", "seq_evict_workspace_size", "seq_evict", "kvp_draft_verify",
     "KVP_OK", "KVP_ERR_INVALID", "KVP_ERR_OOM", "KVP_ERR_STATE", "KVP_ERR_CUDA", "KVP_ERR_DEVICE",
     "KVP_ERR_WORKSPACE",
 ]
@@ -132,6 +133,14 @@ _SIGS = {
     "kvp_decode_step_run": ([_P, ctypes.POINTER(StepIO), _P, ctypes.c_size_t, _P], ctypes.c_int),
     "seq_alloc_prefix": ([_P, _P, _I32, _I32P], ctypes.c_int),
     "seq_accept_draft": ([_P, _I32, _I32, _P, _I32, _I32, _P, _I32P, _P], ctypes.c_int),
+    "kvp_mass_workspace_size": ([ctypes.POINTER(AttnDesc), _P, _P, _P, _I32, _I32], ctypes.c_size_t),
+    "kvp_attention_mass": ([_P, _P, _P, _P, _P, _P, _I32, _I32, ctypes.POINTER(AttnDesc), ctypes.c_float, _P, _P,
+                            _P, ctypes.c_int64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "seq_evict_workspace_size": ([_P, _P, _I32, _I32], ctypes.c_size_t),
+    "seq_evict": ([_P, _P, _I32, _P, ctypes.c_int64, _I32, _I32, _I32, _P, _P, _P, ctypes.c_size_t, _P],
+                  ctypes.c_int),
+    "kvp_draft_verify": ([_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P,
+                          _I32, _I32, _I32, _P, _P, _P, _P], ctypes.c_int),
     "kvp_radix_create": ([_P, ctypes.POINTER(_P)], ctypes.c_int),
     "kvp_radix_destroy": ([_P], ctypes.c_int),
     "kvp_radix_match": ([_P, _P, _I32, _P, _I32, _I32P, _I32P], ctypes.c_int),
@@ -542,6 +551,130 @@ def tree_verify_attention(q, tree_parent, n_draft: int, k_pool, v_pool, block_ta
                                         tp, cp, len(c), t.shape[1], ctypes.byref(desc), _dev(out),
                                         _dev(lse), _dev(workspace), _ws_bytes(workspace, ws_bytes),
                                         _stream(stream)), "tree_verify_attention")
+
+
+# ------------------------------------------------- bounded caches and drafts
+
+def _typed(name, x, dtype, shape=None):
+    """Checks a tensor argument's type, shape and device (None and integer
+    addresses pass) and returns it."""
+    if x is None or isinstance(x, int):
+        return x
+    import torch
+    if x.dtype != getattr(torch, dtype):
+        raise ValueError(f"{name}: expected {dtype}, got {x.dtype}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
+    if x.is_cuda and x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {x.device}, not the current device")
+    return x
+
+
+def _batch_i32(name, a, n):
+    """A host int32 array of one entry per sequence, or None."""
+    if a is None:
+        return None, None
+    a, p = _host_i32(a)
+    if a.shape != (n,):
+        raise ValueError(f"{name}: expected {n} entries, got shape {a.shape}")
+    return a, p
+
+
+def kvp_mass_workspace_size(desc: AttnDesc, block_tables, seq_lens, q_lens=None) -> int:
+    t, tp = _host_i32(block_tables)
+    ln, lp = _batch_i32("seq_lens", seq_lens, t.shape[0])
+    ql, qp = _batch_i32("q_lens", q_lens, t.shape[0])
+    n = load().kvp_mass_workspace_size(ctypes.byref(desc), tp, lp, qp, t.shape[0], t.shape[1])
+    if n == 0:
+        raise KvpError(KVP_ERR_INVALID, "kvp_mass_workspace_size")
+    return n
+
+
+def kvp_attention_mass(q, q_lens, lse, k_pool, block_tables, seq_lens, desc: AttnDesc, decay: float, mass_in,
+                       prev_lens, mass_out, workspace, ws_bytes=None, stream=None):
+    """mass_out = decay * mass_in + this call's attention weight per cached
+    token, [L][S][Hkv][stride] fp32; mass_in may be mass_out or None.  q
+    [L][T][Hq][d] and lse [L][T][Hq] hold q_lens[s] (None: 1) query tokens per
+    sequence; mass_in holds the first prev_lens[s] (None: seq_lens - q_lens)
+    tokens.  block_tables [S][MB], lengths: host int32 arrays."""
+    t, tp = _host_i32(block_tables)
+    S = t.shape[0]
+    ln, lp = _batch_i32("seq_lens", seq_lens, S)
+    ql, qp = _batch_i32("q_lens", q_lens, S)
+    pl, pp = _batch_i32("prev_lens", prev_lens, S)
+    T = S if ql is None else int(ql.sum())
+    d = desc
+    rows = (d.num_layers, T, d.num_q_heads)
+    stride = mass_out.shape[-1]
+    shape = (d.num_layers, S, d.num_kv_heads, stride)
+    _typed("q", q, "bfloat16", rows + (d.head_dim,))
+    _typed("lse", lse, "float32", rows)
+    _typed("k_pool", k_pool, "bfloat16", (d.num_layers, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim))
+    _typed("mass_in", mass_in, "float32", shape)
+    _typed("mass_out", mass_out, "float32", shape)
+    _check(load().kvp_attention_mass(_dev(q), qp, _dev(lse), _dev(k_pool), tp, lp, S, t.shape[1], ctypes.byref(desc),
+                                     decay, _dev(mass_in), pp, _dev(mass_out), stride, _dev(workspace),
+                                     _ws_bytes(workspace, ws_bytes), _stream(stream)), "kvp_attention_mass")
+
+
+def seq_evict_workspace_size(pool, seqs, budget: int) -> int:
+    s, sp = _host_i32(seqs)
+    n = load().seq_evict_workspace_size(pool, sp, len(s), budget)
+    if n == 0:
+        raise KvpError(KVP_ERR_INVALID, "seq_evict_workspace_size")
+    return n
+
+
+def seq_evict(pool, seqs, mass, budget: int, n_sink: int, n_recent: int, kept, mass_out, workspace, ws_bytes=None,
+              stream=None):
+    """Keeps `budget` tokens of each sequence by accumulated weight mass
+    [L][n][Hkv][stride] fp32; kept [L][n][Hkv][budget] int32 receives their
+    positions, mass_out (like mass, mass itself or None) their weights."""
+    s, sp = _host_i32(seqs)
+    stride = mass.shape[-1]
+    if mass.dim() != 4 or mass.shape[1] != len(s):
+        raise ValueError(f"mass: expected [L][{len(s)}][Hkv][stride], got shape {tuple(mass.shape)}")
+    _typed("mass", mass, "float32")
+    _typed("mass_out", mass_out, "float32", mass.shape)
+    _typed("kept", kept, "int32", (*mass.shape[:3], budget))
+    _check(load().seq_evict(pool, sp, len(s), _dev(mass), stride, budget, n_sink, n_recent, _dev(kept),
+                            _dev(mass_out), _dev(workspace), _ws_bytes(workspace, ws_bytes), _stream(stream)),
+           "seq_evict")
+
+
+def kvp_draft_verify(target, draft, tree_parent, draft_tokens, u_accept, u_next, accepted, n_accepted, next_token,
+                     stream=None):
+    """Which draft node the target accepts, how many nodes lead to it and the
+    token that follows.  target [B][>= n + 1][V] and draft [B][>= n][V] (None:
+    drafts chosen outright) fp32 probabilities, their last dimension
+    contiguous; tree_parent, draft_tokens int32 and u_accept fp32 [B][n];
+    u_next [B]; the outputs int32 [B]."""
+    B, n = draft_tokens.shape
+    V = target.shape[-1]
+
+    def rows(name, x, least):
+        if x is None:
+            return None, 0, 0
+        _typed(name, x, "float32")
+        if not x.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        if x.dim() != 3 or x.shape[0] != B or x.shape[1] < least or x.shape[2] != V or (V > 1 and x.stride(2) != 1):
+            raise ValueError(f"{name}: expected [{B}][>= {least}][{V}] with contiguous rows, got shape "
+                             f"{tuple(x.shape)}, strides {x.stride()}")
+        # a dimension of one entry is never stepped over
+        return x.data_ptr(), x.stride(0) if B > 1 else 0, x.stride(1) if x.shape[1] > 1 else V
+
+    tp, tb, tr = rows("target", target, n + 1)
+    dp, db, dr = rows("draft", draft, n)
+    for name, x, dtype, shape in (("tree_parent", tree_parent, "int32", (B, n)),
+                                  ("draft_tokens", draft_tokens, "int32", (B, n)),
+                                  ("u_accept", u_accept, "float32", (B, n)), ("u_next", u_next, "float32", (B,)),
+                                  ("accepted", accepted, "int32", (B,)), ("n_accepted", n_accepted, "int32", (B,)),
+                                  ("next_token", next_token, "int32", (B,))):
+        _typed(name, x, dtype, shape)
+    _check(load().kvp_draft_verify(tp, tb, tr, dp, db, dr, _dev(tree_parent), _dev(draft_tokens), _dev(u_accept),
+                                   _dev(u_next), B, n, V, _dev(accepted), _dev(n_accepted), _dev(next_token),
+                                   _stream(stream)), "kvp_draft_verify")
 
 
 def kvp_device_error(workspace, stream=None) -> int:

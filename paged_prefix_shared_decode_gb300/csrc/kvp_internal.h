@@ -8,6 +8,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/kvp.h"
+
 struct kvp_pool;
 
 namespace kvp {
@@ -241,5 +243,52 @@ struct Kv4Move {
     const int32_t *dst;
 };
 cudaError_t launch_kv4_move(const Kv4Move &m, cudaStream_t stream);
+
+// Accumulated attention weight per cached token (mass_kernels.cu).
+struct MassSeq {
+    int32_t len, nq, q0;   // cached tokens, query tokens, first query row of q
+    int32_t prev;          // tokens whose weight mass_in holds
+    int64_t table;         // offset of its block table in tables
+};
+struct MassLaunch {
+    const void *q, *k_pool;
+    const float *lse, *mass_in;
+    float *mass_out;
+    const MassSeq *seqs;
+    const int32_t *tables;
+    int64_t stride;
+    int32_t L, S, T, Hq, Hkv, G, D, NB, bs_log2;
+    int32_t tiles, chunks;   // set by launch_mass: 128-token steps per CTA, CTAs per sequence
+    float scale_log2, decay;
+};
+// max_len, max_rows: the longest sequence, and the most query rows (queries
+// x GQA group) of one.
+cudaError_t launch_mass(const MassLaunch &a, int max_len, int max_rows, cudaStream_t stream);
+
+// Eviction by accumulated weight (evict_kernels.cu).
+enum { kEvictKeep = 0, kEvictCopy = 1, kEvictPack = 2 };   // pages stay; fresh pages; some filled in place
+struct EvictSeq {
+    int32_t len, how;
+    int32_t src, dst;      // offsets of its old and new block table in tables
+};
+struct EvictLaunch {
+    void *k_pool, *v_pool;
+    const float *mass;
+    float *mass_out;       // may be mass, or null
+    int32_t *kept;
+    const EvictSeq *seqs;
+    const int32_t *tables;
+    int64_t stride;
+    int32_t L, S, Hkv, NB, bs, CH;   // CH: 16-byte chunks per row
+    int32_t budget, sink, recent;
+};
+cudaError_t launch_evict(const EvictLaunch &a, bool copies, bool packs, cudaStream_t stream);
+
+// A descriptor that the attention entry points accept.
+bool attn_desc_ok(const kvp_attn_desc *d);
+// Whether `stream` is being captured into a graph: calls that upload a plan
+// from host memory refuse it, since a replay would upload whatever that
+// memory then holds.
+bool stream_capturing(cudaStream_t stream);
 
 }  // namespace kvp

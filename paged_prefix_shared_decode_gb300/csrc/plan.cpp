@@ -758,6 +758,15 @@ int device_sm_count() {
     return v;
 }
 
+bool attn_desc_ok(const kvp_attn_desc *d) { return desc_ok(d); }
+
+bool stream_capturing(cudaStream_t stream) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    // (the legacy default stream cannot be captured; asked about it while
+    // another stream captures, the runtime returns an error)
+    return cudaStreamIsCapturing(stream, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone;
+}
+
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 long long launch_count() { return g_launches.load(std::memory_order_relaxed); }
 

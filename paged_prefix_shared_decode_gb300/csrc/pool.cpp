@@ -16,6 +16,7 @@
 // the front, a freed block goes to the front, a freed sequence releases its
 // table from the last entry to the first.  Sequence ids: lowest unused id.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -355,6 +356,126 @@ int seq_accept_draft(kvp_pool *p, int32_t seq, int32_t ctx_len, const int32_t *p
     if (path_out) std::copy(path, path + np, path_out);
     if (n_path_out) *n_path_out = np;
     return rc;
+}
+
+// Eviction: which pages stay, which are filled in place and which get fresh
+// blocks is decided from the refcounts at the start of the call, so that two
+// sequences of one call that share a page both leave it as it is.
+static size_t evict_bytes(const kvp_pool *p, const int32_t *seqs, int32_t n, int32_t budget, size_t *tables_at) {
+    const int32_t bs = p->desc.block_size;
+    size_t words = 0;
+    for (int32_t i = 0; i < n; ++i)
+        words += p->tables[seqs[i]].size() + (size_t)((std::min(p->lens[seqs[i]], budget) + bs - 1) / bs);
+    *tables_at = 256 + ((sizeof(kvp::EvictSeq) * (size_t)n + 255) & ~(size_t)255);
+    return (*tables_at + sizeof(int32_t) * words + 255) & ~(size_t)255;
+}
+
+size_t seq_evict_workspace_size(const kvp_pool *p, const int32_t *seqs, int32_t n, int32_t budget) {
+    if (!p || n <= 0 || !seqs || budget <= 0) return 0;
+    for (int32_t i = 0; i < n; ++i)
+        if (!is_live(p, seqs[i])) return 0;
+    size_t at = 0;
+    return evict_bytes(p, seqs, n, budget, &at);
+}
+
+int seq_evict(kvp_pool *p, const int32_t *seqs, int32_t n, const float *mass, int64_t mass_stride, int32_t budget,
+              int32_t n_sink, int32_t n_recent, int32_t *kept, float *mass_out, void *workspace, size_t ws_bytes,
+              void *stream) try {
+    if (!p || n <= 0 || !seqs || !mass || !kept || !workspace || ((uintptr_t)workspace & 255)) return KVP_ERR_INVALID;
+    if (((uintptr_t)mass | (uintptr_t)kept | (uintptr_t)mass_out) & 3) return KVP_ERR_INVALID;
+    if (budget <= 0 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget) return KVP_ERR_INVALID;
+    const kvp_pool_desc &d = p->desc;
+    const int64_t lh = (int64_t)d.num_layers * d.num_kv_heads;
+    if (lh > 65535 || lh * n > INT32_MAX) return KVP_ERR_INVALID;
+    std::set<int32_t> seen;
+    for (int32_t i = 0; i < n; ++i)
+        if (!is_live(p, seqs[i]) || !seen.insert(seqs[i]).second || p->lens[seqs[i]] > mass_stride)
+            return KVP_ERR_INVALID;
+    if (mass_out && mass_out != mass) {   // in place, or apart
+        const uintptr_t a = (uintptr_t)mass, b = (uintptr_t)mass_out, len = (uintptr_t)(lh * n * mass_stride) * 4;
+        if (a < b + len && b < a + len) return KVP_ERR_INVALID;
+    }
+    if (!p->k || p->kv4) return KVP_ERR_STATE;
+    if (kvp::stream_capturing((cudaStream_t)stream)) return KVP_ERR_STATE;
+    size_t tables_at = 0;
+    const size_t bytes = evict_bytes(p, seqs, n, budget, &tables_at);
+    if (ws_bytes < bytes) return KVP_ERR_INVALID;
+    const int32_t bs = d.block_size;
+    // pages of kept tokens that need a fresh block: those also held elsewhere,
+    // but for pages of sink tokens alone, which do not change
+    auto fresh = [&](int32_t s, int32_t j) { return (int64_t)(j + 1) * bs > n_sink && p->ref[p->tables[s][j]] > 1; };
+    int64_t need = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        if (p->lens[seqs[i]] <= budget) continue;
+        for (int32_t j = 0; j < (budget + bs - 1) / bs; ++j) need += fresh(seqs[i], j) ? 1 : 0;
+    }
+    if (need > (int64_t)p->free_.size()) return KVP_ERR_OOM;
+
+    std::vector<unsigned char> image(bytes, 0);
+    kvp::EvictSeq *es = reinterpret_cast<kvp::EvictSeq *>(image.data() + 256);
+    int32_t *tabs = reinterpret_cast<int32_t *>(image.data() + tables_at);
+    std::vector<std::vector<int32_t>> pages((size_t)n);   // the new tables
+    std::vector<int32_t> taken;
+    taken.reserve((size_t)need);
+    int32_t at = 0;
+    bool copies = false, packs = false;
+    for (int32_t i = 0; i < n; ++i) {
+        const auto &t = p->tables[seqs[i]];
+        const int32_t len = p->lens[seqs[i]], keep = (std::min(len, budget) + bs - 1) / bs;
+        pages[i].assign(t.begin(), t.begin() + keep);
+        int32_t how = kvp::kEvictKeep;
+        if (len > budget) {
+            how = kvp::kEvictCopy;
+            for (int32_t j = 0; j < keep; ++j) {
+                if (fresh(seqs[i], j)) {
+                    // the blocks are taken from the free list's front, but
+                    // leave it only when nothing can fail any more
+                    pages[i][j] = p->free_[p->free_.size() - 1 - taken.size()];
+                    taken.push_back(pages[i][j]);
+                } else if ((int64_t)(j + 1) * bs > n_sink) {
+                    how = kvp::kEvictPack;
+                }
+            }
+            copies |= how == kvp::kEvictCopy;
+            packs |= how == kvp::kEvictPack;
+        }
+        es[i] = kvp::EvictSeq{len, how, at, at + (int32_t)t.size()};
+        std::copy(t.begin(), t.end(), tabs + at);
+        std::copy(pages[i].begin(), pages[i].end(), tabs + at + t.size());
+        at += (int32_t)(t.size() + pages[i].size());
+    }
+    // (room for every block that goes back, so that nothing below throws)
+    p->free_.reserve((size_t)d.num_blocks);
+    cudaStream_t st = (cudaStream_t)stream;
+    // pageable source: the copy is staged before the call returns
+    if (cudaMemcpyAsync(workspace, image.data(), bytes, cudaMemcpyHostToDevice, st) != cudaSuccess)
+        return KVP_ERR_CUDA;
+
+    for (int32_t b : taken) p->ref[b] = 1;
+    p->free_.resize(p->free_.size() - taken.size());
+    for (int32_t i = 0; i < n; ++i) {
+        if (p->lens[seqs[i]] <= budget) continue;
+        auto &t = p->tables[seqs[i]];
+        // blocks that left the table, last first
+        for (size_t j = t.size(); j-- > 0;)
+            if ((j >= pages[i].size() || t[j] != pages[i][j]) && --p->ref[t[j]] == 0) p->free_.push_back(t[j]);
+        t.swap(pages[i]);
+        p->lens[seqs[i]] = budget;
+    }
+    kvp::EvictLaunch a{};
+    a.k_pool = p->k;
+    a.v_pool = p->v;
+    a.mass = mass;
+    a.mass_out = mass_out;
+    a.kept = kept;
+    a.seqs = reinterpret_cast<const kvp::EvictSeq *>(static_cast<const unsigned char *>(workspace) + 256);
+    a.tables = reinterpret_cast<const int32_t *>(static_cast<const unsigned char *>(workspace) + tables_at);
+    a.stride = mass_stride;
+    a.L = d.num_layers; a.S = n; a.Hkv = d.num_kv_heads; a.NB = d.num_blocks; a.bs = bs; a.CH = d.head_dim / 8;
+    a.budget = budget; a.sink = n_sink; a.recent = n_recent;
+    return kvp::launch_evict(a, copies, packs, st) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+} catch (const std::bad_alloc &) {
+    return KVP_ERR_OOM;
 }
 
 int seq_alloc_prefix(kvp_pool *p, const int32_t *blocks, int32_t n_blocks, int32_t *seq_out) {
