@@ -495,6 +495,34 @@ int kvp_decode_step_run(kvp_step_plan *plan, const kvp_step_io *io, void *worksp
 /* ------------------------------------------- bounded caches and drafts */
 
 /*
+ * Attention over a sliding window and the first few tokens (attention sinks)
+ * of each paged sequence, for decode steps and prompt chunks: sequence s has
+ * q_lens[s] query tokens (host; NULL: one each; 0 allowed), the last of its
+ * seq_lens[s] cached tokens (append first, then attend).  The query at
+ * position p sees the keys j <= p with j > p - window or j < sinks;
+ *   out = softmax(q k^T * scale) v over them, lse the natural log-sum-exp.
+ * window >= 1 (one at least as long as the sequence gives causal attention),
+ * sinks >= 0.  q, out: [L][T][Hq][d] bf16 and lse: [L][T][Hq] fp32 (or NULL),
+ * sequence after sequence, T = sum of q_lens.  block_tables, seq_lens, desc,
+ * workspace and errors as for paged_decode_attention, ws_bytes >=
+ * kvp_window_workspace_size() for the same arguments; pages must be bf16.
+ * With desc->use_sharing, batches of one query token per sequence read a
+ * block that several of them share and see once.  Only tokens that some query of the
+ * call sees are read; those must hold finite K and V (a query's masked
+ * neighbours enter its products with weight 0).  A sequence may have no
+ * cached token (q_lens[s] = 0 then).  KVP_ERR_STATE while `stream` is being
+ * captured: the plan is uploaded from host memory.
+ */
+size_t kvp_window_workspace_size(const kvp_attn_desc *desc, const int32_t *block_tables,
+                                 const int32_t *seq_lens, const int32_t *q_lens, int32_t num_seqs,
+                                 int32_t max_blocks, int32_t window, int32_t sinks);
+int paged_window_attention(const void *q, const int32_t *q_lens, const void *k_pool,
+                           const void *v_pool, const int32_t *block_tables,
+                           const int32_t *seq_lens, int32_t num_seqs, int32_t max_blocks,
+                           int32_t window, int32_t sinks, const kvp_attn_desc *desc, void *out,
+                           float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Accumulated attention weight of every cached token, from the log-sum-exp
  * that an attention call left: for each layer, sequence s, kv head h and
  * cached token t < seq_lens[s],

@@ -28,7 +28,7 @@ __all__ = [
     "DecodeStep", "KVP_STEP_HOST_MAPPED", "kvp_step_plan_create", "kvp_step_plan_destroy",
     "kvp_decode_step_plan", "kvp_decode_step_run", "StepPlan",
     "KVP_STATIC_WORKSPACE_BYTES",
-    "kvp_mass_workspace_size", "kvp_attention_mass", "seq_evict_workspace_size", "seq_evict", "kvp_draft_verify",
+    "kvp_window_workspace_size", "paged_window_attention", "kvp_mass_workspace_size", "kvp_attention_mass", "seq_evict_workspace_size", "seq_evict", "kvp_draft_verify",
     "KVP_OK", "KVP_ERR_INVALID", "KVP_ERR_OOM", "KVP_ERR_STATE", "KVP_ERR_CUDA", "KVP_ERR_DEVICE",
     "KVP_ERR_WORKSPACE",
 ]
@@ -133,6 +133,9 @@ _SIGS = {
     "kvp_decode_step_run": ([_P, ctypes.POINTER(StepIO), _P, ctypes.c_size_t, _P], ctypes.c_int),
     "seq_alloc_prefix": ([_P, _P, _I32, _I32P], ctypes.c_int),
     "seq_accept_draft": ([_P, _I32, _I32, _P, _I32, _I32, _P, _I32P, _P], ctypes.c_int),
+    "kvp_window_workspace_size": ([ctypes.POINTER(AttnDesc), _P, _P, _P, _I32, _I32, _I32, _I32], ctypes.c_size_t),
+    "paged_window_attention": ([_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, ctypes.POINTER(AttnDesc), _P, _P, _P,
+                                ctypes.c_size_t, _P], ctypes.c_int),
     "kvp_mass_workspace_size": ([ctypes.POINTER(AttnDesc), _P, _P, _P, _I32, _I32], ctypes.c_size_t),
     "kvp_attention_mass": ([_P, _P, _P, _P, _P, _P, _I32, _I32, ctypes.POINTER(AttnDesc), ctypes.c_float, _P, _P,
                             _P, ctypes.c_int64, _P, ctypes.c_size_t, _P], ctypes.c_int),
@@ -580,6 +583,42 @@ def _batch_i32(name, a, n):
     return a, p
 
 
+def _pool_shape(d: AttnDesc):
+    return d.num_layers, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim
+
+
+def kvp_window_workspace_size(desc: AttnDesc, block_tables, seq_lens, q_lens, window: int, sinks: int) -> int:
+    t, tp = _host_i32(block_tables)
+    ln, lp = _batch_i32("seq_lens", seq_lens, t.shape[0])
+    ql, qp = _batch_i32("q_lens", q_lens, t.shape[0])
+    n = load().kvp_window_workspace_size(ctypes.byref(desc), tp, lp, qp, t.shape[0], t.shape[1], window, sinks)
+    if n == 0:
+        raise KvpError(KVP_ERR_INVALID, "kvp_window_workspace_size")
+    return n
+
+
+def paged_window_attention(q, q_lens, k_pool, v_pool, block_tables, seq_lens, window: int, sinks: int,
+                           desc: AttnDesc, out, lse, workspace, ws_bytes=None, stream=None):
+    """Attention over the last `window` keys up to each query and the first
+    `sinks` tokens.  q, out [L][T][Hq][d] and lse [L][T][Hq] (or None) hold
+    q_lens[s] (None: 1) query tokens per sequence, the last of its seq_lens[s]
+    cached ones.  block_tables [S][MB], lengths: host int32 arrays."""
+    t, tp = _host_i32(block_tables)
+    S = t.shape[0]
+    ln, lp = _batch_i32("seq_lens", seq_lens, S)
+    ql, qp = _batch_i32("q_lens", q_lens, S)
+    T = S if ql is None else int(ql.sum())
+    rows = (desc.num_layers, T, desc.num_q_heads)
+    _typed("q", q, "bfloat16", rows + (desc.head_dim,))
+    _typed("out", out, "bfloat16", rows + (desc.head_dim,))
+    _typed("lse", lse, "float32", rows)
+    _typed("k_pool", k_pool, "bfloat16", _pool_shape(desc))
+    _typed("v_pool", v_pool, "bfloat16", _pool_shape(desc))
+    _check(load().paged_window_attention(_dev(q), qp, _dev(k_pool), _dev(v_pool), tp, lp, S, t.shape[1], window,
+                                         sinks, ctypes.byref(desc), _dev(out), _dev(lse), _dev(workspace),
+                                         _ws_bytes(workspace, ws_bytes), _stream(stream)), "paged_window_attention")
+
+
 def kvp_mass_workspace_size(desc: AttnDesc, block_tables, seq_lens, q_lens=None) -> int:
     t, tp = _host_i32(block_tables)
     ln, lp = _batch_i32("seq_lens", seq_lens, t.shape[0])
@@ -609,7 +648,7 @@ def kvp_attention_mass(q, q_lens, lse, k_pool, block_tables, seq_lens, desc: Att
     shape = (d.num_layers, S, d.num_kv_heads, stride)
     _typed("q", q, "bfloat16", rows + (d.head_dim,))
     _typed("lse", lse, "float32", rows)
-    _typed("k_pool", k_pool, "bfloat16", (d.num_layers, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim))
+    _typed("k_pool", k_pool, "bfloat16", _pool_shape(d))
     _typed("mass_in", mass_in, "float32", shape)
     _typed("mass_out", mass_out, "float32", shape)
     _check(load().kvp_attention_mass(_dev(q), qp, _dev(lse), _dev(k_pool), tp, lp, S, t.shape[1], ctypes.byref(desc),

@@ -181,7 +181,8 @@ struct KCfg4 {
 
 // One work unit with TS warps splitting each tile's tokens.  KV4: the pool
 // holds 4-bit codes and row exponents (a.k_pool / a.v_pool are the codes).
-template <int D, int TS, bool KV4, bool TREE>
+// WIN: rows see a sliding window of keys and the sink tokens.
+template <int D, int TS, bool KV4, bool TREE, bool WIN>
 __device__ __forceinline__ void run_unit(const AttnLaunch &a, const WorkItem &it, int l, int kvh,
                                          int ntile, unsigned char *smem, const KvTile *s_tiles, int *s_next) {
     using C = KCfg<D>;
@@ -416,6 +417,13 @@ __device__ __forceinline__ void run_unit(const AttnLaunch &a, const WorkItem &it
         if (has0) tm0 = a.tree_mask[qt0];
         if (has1) tm1 = a.tree_mask[qt1];
     }
+    // keys [w0, p0] and those below the sink count
+    int p0 = -1, p1 = -1;
+    if (WIN) {
+        if (has0) p0 = __ldg(a.q_pos + qt0);
+        if (has1) p1 = __ldg(a.q_pos + qt1);
+    }
+    const int w0 = WIN ? p0 - a.win + 1 : 0, w1 = WIN ? p1 - a.win + 1 : 0;
 
     float o[C::NO][4];
 #pragma unroll
@@ -441,9 +449,17 @@ __device__ __forceinline__ void run_unit(const AttnLaunch &a, const WorkItem &it
         const int ntok = kt.ntok_flags & 0xFFFF;
         const bool tree = TREE && ((kt.ntok_flags >> 16) & kTileTree);
         const int mlo = kt.members & 0xFFFF, mhi = kt.members >> 16;
-        const bool in0 = has0 && mem0 >= mlo && mem0 < mhi;
-        const bool in1 = has1 && mem1 >= mlo && mem1 < mhi;
         const int tb = sp * TOKW;
+        bool in0 = has0 && mem0 >= mlo && mem0 < mhi;
+        bool in1 = has1 && mem1 >= mlo && mem1 < mhi;
+        bool all0 = true, all1 = true;   // the row sees the warp's whole share of the tile
+        if (WIN) {
+            const int b = kt.tok0 + tb, e = b + TOKW;
+            in0 = in0 && b <= p0 && (e > w0 || b < a.sinks);
+            in1 = in1 && b <= p1 && (e > w1 || b < a.sinks);
+            all0 = e <= p0 + 1 && (b >= w0 || e <= a.sinks);
+            all1 = e <= p1 + 1 && (b >= w1 || e <= a.sinks);
+        }
         if (!__any_sync(0xffffffffu, in0 || in1) || tb >= ntok) continue;
 
         const uint32_t aK = KV4 ? smem_addr(smem + C4::BF_OFF) : smem_addr(smem + (t % C::NSTAGE) * C::STAGE_BYTES);
@@ -511,7 +527,7 @@ __device__ __forceinline__ void run_unit(const AttnLaunch &a, const WorkItem &it
         }
         // raw scores; masked ones -inf.  Padding rows (past the item's rows)
         // are never written, so whole tiles seen by every real row skip masking.
-        const bool fast = tb + TOKW <= ntok && !tree && (in0 || !has0) && (in1 || !has1);
+        const bool fast = tb + TOKW <= ntok && !tree && ((in0 && all0) || !has0) && ((in1 && all1) || !has1);
         if (!__all_sync(0xffffffffu, fast)) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -521,6 +537,10 @@ __device__ __forceinline__ void run_unit(const AttnLaunch &a, const WorkItem &it
                     const bool hi = e >= 2;
                     bool ok = tok < ntok && (hi ? in1 : in0);
                     if (tree) ok = ok && (((hi ? tm1 : tm0) >> (tok & 63)) & 1ull);
+                    if (WIN) {
+                        const int kp = kt.tok0 + tok;
+                        ok = ok && kp <= (hi ? p1 : p0) && (kp >= (hi ? w1 : w0) || kp < a.sinks);
+                    }
                     if (!ok) s[j][e] = -INFINITY;
                 }
             }
@@ -753,7 +773,7 @@ __device__ __forceinline__ void run_unit(const AttnLaunch &a, const WorkItem &it
     }
 }
 
-template <int D, bool KV4, bool TREE>
+template <int D, bool KV4, bool TREE, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, KCfg<D>::MIN_BLOCKS) attn_item_kernel(const AttnLaunch a) {
     using C = KCfg<D>;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -790,10 +810,16 @@ __global__ void __launch_bounds__(kThreads, KCfg<D>::MIN_BLOCKS) attn_item_kerne
         const int lk = unit % (a.L * a.Hkv);
         const int kvh = lk % a.Hkv, l = lk / a.Hkv;
         const WorkItem it = a.items[item_idx];
-        const int ntile = it.tile_end - it.tile_begin;
+        int ntile = it.tile_end - it.tile_begin;
         const int4 *src = reinterpret_cast<const int4 *>(a.tiles + it.tile_begin);
         int4 *dst = reinterpret_cast<int4 *>(s_tiles);
+        if (WIN) {
+            const int4 *pre = reinterpret_cast<const int4 *>(a.tiles + it.pre_begin);
+            for (int i = threadIdx.x; i < it.n_pre * 2; i += kThreads) dst[i] = pre[i];
+            dst += it.n_pre * 2;
+        }
         for (int i = threadIdx.x; i < ntile * 2; i += kThreads) dst[i] = src[i];
+        if (WIN) ntile += it.n_pre;
         __syncthreads();
         const int rows = it.n_members * a.G;
         if (!waited) {
@@ -803,9 +829,9 @@ __global__ void __launch_bounds__(kThreads, KCfg<D>::MIN_BLOCKS) attn_item_kerne
         // The two-way split pays at head dim 128 (two CTAs per SM leave few
         // warps to hide latency); at head dim 64 the extra copy of the tile
         // loop costs more in instruction fetch than the split gains.
-        if (rows <= 16) run_unit<D, 4, KV4, TREE>(a, it, l, kvh, ntile, smem, s_tiles, &s_unit);
-        else if (D == 128 && rows <= 32) run_unit<D, 2, KV4, TREE>(a, it, l, kvh, ntile, smem, s_tiles, &s_unit);
-        else run_unit<D, 1, KV4, TREE>(a, it, l, kvh, ntile, smem, s_tiles, &s_unit);
+        if (rows <= 16) run_unit<D, 4, KV4, TREE, WIN>(a, it, l, kvh, ntile, smem, s_tiles, &s_unit);
+        else if (D == 128 && rows <= 32) run_unit<D, 2, KV4, TREE, WIN>(a, it, l, kvh, ntile, smem, s_tiles, &s_unit);
+        else run_unit<D, 1, KV4, TREE, WIN>(a, it, l, kvh, ntile, smem, s_tiles, &s_unit);
         __syncthreads();
     }
 }
@@ -1040,7 +1066,7 @@ struct Occupancy {
 
 // Per device: the kernel's shared-memory attribute is set and its
 // occupancy queried once for each device that runs it.
-template <int D, bool KV4 = false, bool TREE = false>
+template <int D, bool KV4 = false, bool TREE = false, bool WIN = false>
 Occupancy &occupancy() {
     static Occupancy occ[kMaxDevices];
     static std::once_flag once[kMaxDevices];
@@ -1054,12 +1080,12 @@ Occupancy &occupancy() {
         o.per_sm = C::MIN_BLOCKS;
         o.sms = device_sm_count();
         const int smem_bytes = KV4 ? KCfg4<D>::SMEM : C::SMEM;
-        if (cudaFuncSetAttribute(attn_item_kernel<D, KV4, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(attn_item_kernel<D, KV4, TREE, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  smem_bytes) != cudaSuccess)
             return;
         int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_item_kernel<D, KV4, TREE>, kThreads, smem_bytes) ==
-                cudaSuccess && n > 0)
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_item_kernel<D, KV4, TREE, WIN>, kThreads,
+                                                          smem_bytes) == cudaSuccess && n > 0)
             o.per_sm = n;
         o.ok = true;
     });
@@ -1117,6 +1143,14 @@ cudaError_t launch_d(const AttnLaunch &a, cudaStream_t stream, cudaEvent_t befor
         if (!o4.ok) return cudaErrorInvalidDevice;
         const int grid = a.n_units < o4.sms * o4.per_sm ? a.n_units : o4.sms * o4.per_sm;
         e = launch_pdl(attn_item_kernel<D, true, false>, dim3(grid), dim3(kThreads), KCfg4<D>::SMEM, mma_stream, a);
+        count_launch();
+        if (e == cudaSuccess) e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    } else if (a.n_units > 0 && a.win > 0) {
+        Occupancy &ow = occupancy<D, false, false, true>();
+        if (!ow.ok) return cudaErrorInvalidDevice;
+        const int grid = a.n_units < ow.sms * ow.per_sm ? a.n_units : ow.sms * ow.per_sm;
+        e = launch_pdl(attn_item_kernel<D, false, false, true>, dim3(grid), dim3(kThreads), C::SMEM, mma_stream, a);
         count_launch();
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e != cudaSuccess) return e;

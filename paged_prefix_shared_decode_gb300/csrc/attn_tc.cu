@@ -234,6 +234,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+template <bool WIN>
+__device__ __forceinline__ int item_tiles(const WorkItem &it) {
+    return it.tile_end - it.tile_begin + (WIN ? it.n_pre : 0);
+}
+
 template <int D>
 struct TcCfg {
     static constexpr int NSLAB = D / 64;               // 64-column slabs (128-byte rows)
@@ -278,6 +283,13 @@ __device__ __forceinline__ uint32_t valid_bits(int nv, bool tree, uint64_t tmask
     uint32_t vm = nv >= j0 + 32 ? 0xffffffffu : (nv <= j0 ? 0u : (1u << (nv - j0)) - 1u);
     if (tree) vm &= (uint32_t)(tmask >> j0);
     return vm;
+}
+// Sliding window: bits of the keys tok0 .. tok0 + n - 1 that a query at
+// position pos sees (up to its own, less than win behind it, or a sink).
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+__device__ __forceinline__ uint64_t window_bits(int tok0, int n, int pos, int win, int sinks) {
+    const int upto = min(n, pos - tok0 + 1);
+    return (low_bits(upto) & ~low_bits(pos - win + 1 - tok0)) | low_bits(min(upto, sinks - tok0));
 }
 // Max of the valid scores among 32 (-inf if none).  Masking uses selects, not
 // per-element branches, and is skipped when the whole warp is unmasked.
@@ -337,16 +349,17 @@ __device__ __forceinline__ void exp_pack16(const uint32_t (&x)[32], int j0, floa
 
 // P = 2^(s * sc + nm) of one step, packed into pk (word i holds scores 2i,
 // 2i + 1); adds the sum of P to ls.  S is only read.
+// (m0, m1: masks of the step's two tiles, used where tr0 / tr1 are set.)
 __device__ __forceinline__ void p_pass(uint32_t s_tm, float nm, float sc, int nv0, bool tr0, int nv1, bool tr1,
-                                       uint64_t tmask, uint32_t (&pk)[64], float &ls) {
+                                       uint64_t m0, uint64_t m1, uint32_t (&pk)[64], float &ls) {
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
         uint32_t x[32], y[32];
         tmem_ld32(s_tm + 64 * hh, x);
         tmem_ld32(s_tm + 64 * hh + 32, y);
         tmem_wait_ld();
-        const uint32_t vx = valid_bits(hh ? nv1 : nv0, hh ? tr1 : tr0, tmask, 0);
-        const uint32_t vy = valid_bits(hh ? nv1 : nv0, hh ? tr1 : tr0, tmask, 32);
+        const uint32_t vx = valid_bits(hh ? nv1 : nv0, hh ? tr1 : tr0, hh ? m1 : m0, 0);
+        const uint32_t vy = valid_bits(hh ? nv1 : nv0, hh ? tr1 : tr0, hh ? m1 : m0, 32);
         uint32_t *q = pk + 32 * hh;
         if (__all_sync(0xffffffffu, (vx & vy) == 0xffffffffu)) {
             exp_pack16<false>(x, 0, sc, nm, vx, q, ls);
@@ -367,32 +380,33 @@ __device__ __forceinline__ void p_store(uint32_t s_tm, const uint32_t (&pk)[64])
     tmem_st32(s_tm + 32, *reinterpret_cast<const uint32_t(*)[32]>(pk + 32));
 }
 // Row max of one step's valid raw scores (-inf if none).
-__device__ __forceinline__ float step_max(uint32_t s_tm, int nv0, bool tr0, int nv1, bool tr1, uint64_t tmask) {
+__device__ __forceinline__ float step_max(uint32_t s_tm, int nv0, bool tr0, int nv1, bool tr1, uint64_t m0,
+                                          uint64_t m1) {
     uint32_t x[32], y[32];
     tmem_ld32(s_tm, x);
     tmem_ld32(s_tm + 32, y);
     tmem_wait_ld();
-    float mx = fmaxf(max32(x, valid_bits(nv0, tr0, tmask, 0)), max32(y, valid_bits(nv0, tr0, tmask, 32)));
+    float mx = fmaxf(max32(x, valid_bits(nv0, tr0, m0, 0)), max32(y, valid_bits(nv0, tr0, m0, 32)));
     tmem_ld32(s_tm + 64, x);
     tmem_ld32(s_tm + 96, y);
     tmem_wait_ld();
-    return fmaxf(mx, fmaxf(max32(x, valid_bits(nv1, tr1, tmask, 0)), max32(y, valid_bits(nv1, tr1, tmask, 32))));
+    return fmaxf(mx, fmaxf(max32(x, valid_bits(nv1, tr1, m1, 0)), max32(y, valid_bits(nv1, tr1, m1, 32))));
 }
 // The slow path, kept out of line so that its registers do not add to the
 // common path's: the step's max, the new running max (raised for the rows
 // marked bad), P again, stored.  Returns (new m, sum of P).
 __device__ __noinline__ float2 recompute_step(uint32_t s_tm, float m, float sc, int nv0, bool tr0, int nv1, bool tr1,
-                                              uint64_t tmask, bool bad) {
-    const float tmx = step_max(s_tm, nv0, tr0, nv1, tr1, tmask) * sc;
+                                              uint64_t m0, uint64_t m1, bool bad) {
+    const float tmx = step_max(s_tm, nv0, tr0, nv1, tr1, m0, m1) * sc;
     const float m_new = bad ? fmaxf(m, tmx) : m;
     float ls = 0.f;
     uint32_t pk[64];
-    p_pass(s_tm, m_new == -INFINITY ? 0.f : -m_new, sc, nv0, tr0, nv1, tr1, tmask, pk, ls);
+    p_pass(s_tm, m_new == -INFINITY ? 0.f : -m_new, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
     p_store(s_tm, pk);
     return make_float2(m_new, ls);
 }
 
-template <int D, bool KV4>
+template <int D, bool KV4, bool WIN>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap, const AttnLaunch a, const int box_rows,
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int lk = unit / n_items;
             const int kvh = lk % a.Hkv, l = lk / a.Hkv;
             const WorkItem it = a.tc_items[item_idx];
-            const int ntile = it.tile_end - it.tile_begin;
+            const int ntile = item_tiles<WIN>(it);
             const int nsteps = (ntile + 1) >> 1;
             const size_t layer_base = (size_t)l * a.NB * block_stride + (size_t)kvh * head_stride;
             const int row_base_lh = (l * a.NB) * a.Hkv + kvh;   // row of block b = (row_base_lh + b*Hkv) * bs
@@ -689,10 +703,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             WorkItem it{};
             if (!done) {
                 it = a.tc_items[unit % n_items];
-                const int ntile = it.tile_end - it.tile_begin;
+                const int ntile = item_tiles<WIN>(it);
                 const int4 *src = reinterpret_cast<const int4 *>(a.tiles + it.tile_begin);
                 int4 *dst = reinterpret_cast<int4 *>(s_desc + slot * kMaxItemTiles);
-                for (int i = lane; i < ntile * 2; i += 32) dst[i] = src[i];
+                if (WIN) {
+                    const int4 *pre = reinterpret_cast<const int4 *>(a.tiles + it.pre_begin);
+                    for (int i = lane; i < ntile * 2; i += 32) dst[i] = i < 2 * it.n_pre ? pre[i] : src[i - 2 * it.n_pre];
+                } else {
+                    for (int i = lane; i < ntile * 2; i += 32) dst[i] = src[i];
+                }
             }
             if (lane == 0) s_unit[slot] = done ? -1 : unit;
             __syncwarp();
@@ -782,7 +801,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int unit = s_unit[slot];
                 if (unit < 0) break;
                 const WorkItem it = a.tc_items[unit % n_items];
-                const int ntile = it.tile_end - it.tile_begin;
+                const int ntile = item_tiles<WIN>(it);
                 const int nsteps = (ntile + 1) >> 1;
                 const bool pair = it.n_members * G > 128;
                 bool ok = wait(bar(C::B_Q_FULL), uc & 1);
@@ -922,7 +941,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int lk = unit / n_items;
             const int kvh = lk % a.Hkv, l = lk / a.Hkv;
             const WorkItem it = a.tc_items[item_idx];
-            const int ntile = it.tile_end - it.tile_begin;
+            const int ntile = item_tiles<WIN>(it);
             const int nsteps = (ntile + 1) >> 1;
             const KvTile *tiles = s_desc + slot * kMaxItemTiles;
             const int rows = it.n_members * G;
@@ -934,7 +953,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int mem = rr / G;
             int qt = 0;
             if (has) qt = __ldg(a.members + it.member_off + mem);
-            const uint64_t tmask = has && a.tree_mask ? a.tree_mask[qt] : ~0ull;
+            const uint64_t tmask = !WIN && has && a.tree_mask ? a.tree_mask[qt] : ~0ull;
+            const int pos = WIN && has ? __ldg(a.q_pos + qt) : 0;
             // a warp none of whose 32 rows is in the unit (a half-filled
             // 128-row tile) only keeps the group's barriers: the rows of P it
             // would write are never read back into an output row, since every
@@ -959,17 +979,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 int nv0 = 0, nv1 = 0;
                 bool tr0 = false, tr1 = false;
+                uint64_t m0 = tmask, m1 = tmask;
                 {
                     const KvTile &k0 = tiles[2 * t];
                     const int mlo = k0.members & 0xFFFF, mhi = k0.members >> 16;
                     nv0 = has && mem >= mlo && mem < mhi ? (k0.ntok_flags & 0xFFFF) : 0;
                     tr0 = (k0.ntok_flags >> 16) & kTileTree;
+                    if (WIN) m0 = nv0 > 0 ? window_bits(k0.tok0, nv0, pos, a.win, a.sinks) : 0ull;
                 }
                 if (2 * t + 1 < ntile) {
                     const KvTile &k1 = tiles[2 * t + 1];
                     const int mlo = k1.members & 0xFFFF, mhi = k1.members >> 16;
                     nv1 = has && mem >= mlo && mem < mhi ? (k1.ntok_flags & 0xFFFF) : 0;
                     tr1 = (k1.ntok_flags >> 16) & kTileTree;
+                    if (WIN) m1 = nv1 > 0 ? window_bits(k1.tok0, nv1, pos, a.win, a.sinks) : 0ull;
+                } else if (WIN) {
+                    m1 = 0ull;
+                }
+                if (WIN) {   // the masks alone say what is valid
+                    nv0 = nv1 = kTileTokens;
+                    tr0 = tr1 = true;
                 }
                 // A row's running max m is raised only when the step's P would
                 // sum to more than 2^32, so every p <= 2^32, well inside bf16
@@ -981,16 +1010,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (__all_sync(0xffffffffu, m == -INFINITY)) {
                     // this group's first step of the unit: find m first
                     // (scale > 0: max of scaled scores = scale * max of raw scores)
-                    m = step_max(s_tm, nv0, tr0, nv1, tr1, tmask) * sc;
+                    m = step_max(s_tm, nv0, tr0, nv1, tr1, m0, m1) * sc;
                 }
                 float ls = 0.f;
                 uint32_t pk[64];
-                p_pass(s_tm, m == -INFINITY ? 0.f : -m, sc, nv0, tr0, nv1, tr1, tmask, pk, ls);
-                const bool bad = m == -INFINITY ? (nv0 > 0 || nv1 > 0) : !(ls <= kSlackSum);
+                p_pass(s_tm, m == -INFINITY ? 0.f : -m, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
+                const bool some = WIN ? (m0 | m1) != 0 : nv0 > 0 || nv1 > 0;
+                const bool bad = m == -INFINITY ? some : !(ls <= kSlackSum);
                 if (!__any_sync(0xffffffffu, bad)) {
                     p_store(s_tm, pk);
                 } else {
-                    const float2 r2 = recompute_step(s_tm, m, sc, nv0, tr0, nv1, tr1, tmask, bad);
+                    const float2 r2 = recompute_step(s_tm, m, sc, nv0, tr0, nv1, tr1, m0, m1, bad);
                     const bool resc = r2.x != m && m != -INFINITY;
                     if (__any_sync(0xffffffffu, resc)) {
                         // O_g holds P V up to step t-2, complete since S(t) is
@@ -1139,7 +1169,7 @@ struct TcOcc {
 };
 
 // Per device: the shared-memory attribute is set once for each device.
-template <int D, bool KV4>
+template <int D, bool KV4, bool WIN>
 TcOcc &tc_occ() {
     static TcOcc occ[kMaxDevices];
     static std::once_flag once[kMaxDevices];
@@ -1147,7 +1177,7 @@ TcOcc &tc_occ() {
     const int dev = current_device();
     if (dev < 0) return none;
     std::call_once(once[dev], [dev] {
-        if (cudaFuncSetAttribute(attn_tc_kernel<D, KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(attn_tc_kernel<D, KV4, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  TcCfg<D>::SMEM) != cudaSuccess)
             return;
         occ[dev].sms = device_sm_count();
@@ -1156,9 +1186,9 @@ TcOcc &tc_occ() {
     return occ[dev];
 }
 
-template <int D, bool KV4>
+template <int D, bool KV4, bool WIN = false>
 cudaError_t launch_tc_d(const AttnLaunch &a, cudaStream_t stream) {
-    TcOcc &occ = tc_occ<D, KV4>();
+    TcOcc &occ = tc_occ<D, KV4, WIN>();
     if (!occ.ok) return cudaErrorInvalidDevice;
     const int bs = 1 << a.bs_log2;
     const int box_rows = bs < kTileTokens ? bs : kTileTokens;
@@ -1176,7 +1206,7 @@ cudaError_t launch_tc_d(const AttnLaunch &a, cudaStream_t stream) {
     // one CTA per SM (its shared memory and TMEM allow no more)
     const int grid = a.n_tc_units < occ.sms ? a.n_tc_units : occ.sms;
     const int out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
-    attn_tc_kernel<D, KV4><<<grid, kTcThreads, TcCfg<D>::SMEM, stream>>>(km, vm, qm, a, box_rows, q_tma ? 1 : 0, out32);
+    attn_tc_kernel<D, KV4, WIN><<<grid, kTcThreads, TcCfg<D>::SMEM, stream>>>(km, vm, qm, a, box_rows, q_tma ? 1 : 0, out32);
     count_launch();
     return cudaGetLastError();
 }
@@ -1279,6 +1309,11 @@ bool tc_path_supported(int L, int NB, int Hkv, int bs) {
 cudaError_t launch_attention_tc(const AttnLaunch &a, cudaStream_t stream, int ctas_per_sm) {
     (void)ctas_per_sm;
     if (a.n_tc_units <= 0) return cudaSuccess;
+    if (a.win > 0 && !a.kv4) {
+        if (a.D == 64) return launch_tc_d<64, false, true>(a, stream);
+        if (a.D == 128) return launch_tc_d<128, false, true>(a, stream);
+        return cudaErrorInvalidValue;
+    }
     if (a.D == 64) return a.kv4 ? launch_tc_d<64, true>(a, stream) : launch_tc_d<64, false>(a, stream);
     if (a.D == 128) return a.kv4 ? launch_tc_d<128, true>(a, stream) : launch_tc_d<128, false>(a, stream);
     return cudaErrorInvalidValue;

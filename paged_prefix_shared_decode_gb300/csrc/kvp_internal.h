@@ -38,13 +38,16 @@ static_assert(sizeof(KvTile) == 32, "KvTile is 32 bytes");
 // A work item: KV tiles [tile_begin, tile_end) against the query rows of
 // n_members members (decode sequences or draft nodes) x the GQA group.
 // out_base < 0: the item covers every key of its rows and writes out / lse;
-// otherwise row r goes to partial row out_base + r.
+// otherwise row r goes to partial row out_base + r.  Window plans only: the
+// tiles [pre_begin, pre_begin + n_pre) come before them (the sink tokens').
 struct WorkItem {
     int32_t tile_begin, tile_end;
     int32_t member_off, n_members;
     int32_t out_base;
-    int32_t pad[3];
+    int32_t pre_begin, n_pre;
+    int32_t pad;
 };
+static_assert(sizeof(WorkItem) == 32, "WorkItem is 32 bytes");
 
 // Per query token: merge entries[off .. off + cnt) are partial-row bases
 // (add the head's index within its group); cnt == 0 means written directly.
@@ -90,6 +93,10 @@ struct AttnLaunch {
     float *part_lse;
     int32_t n_units, n_tc_units, n_merge_q, P;
     int32_t wait_first;   // 1: the kernel before wrote the plan too; wait before reading anything
+    // sliding window (win > 0): query token q at position q_pos[q] sees keys
+    // up to its own position that are less than win behind it or are sinks
+    int32_t win, sinks;
+    const int32_t *q_pos;
 };
 
 // before/after: optional events recorded around the work-item kernel.

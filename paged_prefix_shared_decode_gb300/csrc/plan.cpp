@@ -26,6 +26,12 @@
 // reads the context in 64-token tiles seen by every node, then one
 // tree-masked tile with the draft tokens up to the tile's last node.
 //
+// Window plan (sliding window + sink tokens): for a decode batch the cascade
+// above, each segment cut to the keys that some member's window or sink range
+// holds; with several query tokens per sequence, units of consecutive query
+// tokens over one tile list per sequence, of which a unit takes the sinks'
+// tiles and the run that its window covers.  The kernels mask by position.
+//
 // The plan carries each tile's physical block ids, so the kernels read no
 // device block table; block tables are consumed here, on the host.
 #include <algorithm>
@@ -35,6 +41,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <numeric>
 #include <unordered_map>
 #include <vector>
@@ -58,6 +65,8 @@ struct HostPlan {
     std::vector<int32_t> members;
     std::vector<MergeDesc> merge;
     std::vector<int32_t> entries;
+    std::vector<int32_t> q_pos;       // window plans: position of each query token
+    int32_t win = 0, sinks = 0;
     int32_t n_row_tiles = 0, n_partial_rows = 0, n_units = 0, n_tc_units = 0;
     int32_t n_tree_q = 0;   // query tokens with a draft-tree mask (verify)
     int64_t unique_kv_bytes = 0;
@@ -69,6 +78,8 @@ struct HostPlan {
         members.clear();
         merge.clear();
         entries.clear();
+        q_pos.clear();
+        win = sinks = 0;
         n_row_tiles = n_partial_rows = n_units = n_tc_units = n_tree_q = 0;
         unique_kv_bytes = 0;
     }
@@ -540,6 +551,226 @@ int build_verify(const kvp_attn_desc &d, const int32_t *tables, const int32_t *c
     return KVP_OK;
 }
 
+// Tiles of the tokens [t0, t1) of a table row, the first cut short so that
+// the others start on a block boundary (whole tiles then go by TMA).
+int32_t aligned_end(int32_t t0, int32_t bs) {
+    return bs <= kTileTokens ? (t0 + kTileTokens) / bs * bs : (t0 / kTileTokens + 1) * kTileTokens;
+}
+void push_aligned(std::vector<KvTile> &kv, const TileSrc &src, int32_t row, int32_t t0, int32_t t1, int32_t lo,
+                  int32_t hi) {
+    if (t0 >= t1) return;
+    const int32_t e = std::min(t1, aligned_end(t0, src.bs));
+    push_range(kv, src, row, t0, e, lo, hi, 0);
+    push_range(kv, src, row, e, t1, lo, hi, 0);
+}
+
+// One query token per sequence: the cascade over the keys in view.
+void window_decode_protos(const kvp_attn_desc &d, const int32_t *tables, const int32_t *lens, int32_t S, int32_t MB,
+                          int32_t win, int32_t sinks) {
+    const int32_t bs = d.block_size, G = d.num_q_heads / d.num_kv_heads;
+    Scratch &sc = t_scratch;
+    TileSrc src{tables, MB, bs};
+    Protos &pr = sc.protos;
+    // the part of [t0, t1) that is a sink or at or behind `low`
+    auto push_view = [&](int32_t row, int32_t t0, int32_t t1, int32_t low, int32_t lo, int32_t hi) {
+        if (low <= sinks) {
+            push_aligned(pr.kv, src, row, t0, t1, lo, hi);
+            return;
+        }
+        push_aligned(pr.kv, src, row, t0, std::min(t1, sinks), lo, hi);
+        push_aligned(pr.kv, src, row, std::max(t0, low), t1, lo, hi);
+    };
+    auto lowest = [&](int32_t s) { return std::max(0, lens[s] - win); };
+    if (!d.use_sharing) {
+        for (int32_t s = 0; s < S; ++s) {
+            open_item(pr, &s, 1);
+            push_view(s, 0, lens[s], lowest(s), 0, 1);
+            close_item(pr);
+        }
+        return;
+    }
+    sc.nblk.resize(S);
+    for (int32_t s = 0; s < S; ++s) sc.nblk[s] = (lens[s] + bs - 1) / bs;
+    sc.order.clear();
+    sc.segs.clear();
+    sc.bounds.clear();
+    sc.members.resize(S);
+    std::iota(sc.members.begin(), sc.members.end(), 0);
+    Builder b{tables, lens, S, MB, bs, sc};
+    b.build(sc.members.data(), S, 0);
+    const int32_t per_tile = members_per_tile(G, tc_usable(d));
+    std::vector<std::vector<int32_t>> priv;   // per member: its own segments, in pre-order
+    for (int32_t lo = 0; lo < S; lo += per_tile) {
+        const int32_t hi = std::min(S, lo + per_tile);
+        priv.assign((size_t)(hi - lo), {});
+        open_item(pr, sc.order.data() + lo, hi - lo);
+        for (int32_t i = 0; i < (int32_t)sc.segs.size(); ++i) {
+            const Seg &sg = sc.segs[i];
+            const int32_t a = std::max(lo, sg.lo), e = std::min(hi, sg.hi);
+            if (a >= e) continue;
+            if (e - a == 1) {
+                priv[(size_t)(a - lo)].push_back(i);
+                continue;
+            }
+            int32_t low = INT32_MAX;
+            for (int32_t m = a; m < e; ++m) low = std::min(low, lowest(sc.order[m]));
+            push_view(sg.row, sg.tok0, sg.tok1, low, a - lo, e - lo);
+        }
+        close_item(pr);
+        for (int32_t m = lo; m < hi; ++m) {
+            open_item(pr, sc.order.data() + m, 1);
+            for (int32_t i : priv[(size_t)(m - lo)])
+                push_view(sc.segs[i].row, sc.segs[i].tok0, sc.segs[i].tok1, lowest(sc.order[m]), 0, 1);
+            close_item(pr);
+        }
+    }
+}
+
+// Several query tokens per sequence.  A sequence's tile list is the sinks'
+// tiles, then those from its first query's window on (one run from token 0
+// where the two meet); a unit takes tiles [pre] and a run of the others.
+// Units that alone would leave SMs idle, or hold more tiles than a kernel
+// stages, are cut into chunks whose partial rows are merged.
+void window_extend_plan(const kvp_attn_desc &d, const int32_t *tables, const int32_t *lens, const int32_t *q_lens,
+                        int32_t S, int32_t MB, int32_t win, int32_t sinks, int sms, HostPlan &hp) {
+    const int32_t bs = d.block_size, G = d.num_q_heads / d.num_kv_heads;
+    const int32_t lh = d.num_layers * d.num_kv_heads;
+    // (the tcgen05 kernel for every unit of more than 32 rows, whatever the
+    // head dimension)
+    const int thr = tc_path_supported(d.num_layers, d.num_blocks, d.num_kv_heads, bs) ? tc_row_threshold(128) : INT32_MAX;
+    const int32_t per = std::max(1, (thr != INT32_MAX ? kTcRows : kMmaMaxRows) / G);
+    TileSrc src{tables, MB, bs};
+    constexpr int32_t kAll = 0x7FFF;   // every member of a unit sees its tiles, as far as positions allow
+    struct Unit {
+        int32_t m0, n, pre0, n_pre, t0, t1;
+        bool tc;
+    };
+    std::vector<Unit> units;
+    int32_t q0 = 0;
+    int64_t n_tiles[2] = {0, 0}, n_units[2] = {0, 0};
+    for (int32_t s = 0; s < S; ++s) {
+        const int32_t n = lens[s], m = q_lens[s], p0 = n - m;
+        for (int32_t i = 0; i < m; ++i) {
+            hp.members.push_back(q0 + i);
+            hp.q_pos.push_back(p0 + i);
+        }
+        if (m > 0) {
+            int32_t low = std::max(0, p0 - win + 1);
+            const int32_t base = (int32_t)hp.tiles.size();
+            const int32_t n_sink = std::min(sinks, n);
+            int32_t n_pre;
+            if (low <= n_sink) {
+                low = 0;
+                n_pre = (n_sink + kTileTokens - 1) / kTileTokens;
+                push_range(hp.tiles, src, s, 0, n, 0, kAll, 0);
+            } else {
+                push_range(hp.tiles, src, s, 0, n_sink, 0, kAll, 0);
+                n_pre = (int32_t)hp.tiles.size() - base;
+                push_aligned(hp.tiles, src, s, low, n, 0, kAll);
+            }
+            const int32_t first = low == 0 ? 0 : n_pre;                     // tile of token `low`
+            const int32_t end1 = low == 0 ? kTileTokens : aligned_end(low, bs);   // its end
+            auto tile_of = [&](int32_t x) {
+                return base + first + (x < end1 ? 0 : 1 + (x - end1) / kTileTokens);
+            };
+            for (int32_t i0 = 0; i0 < m; i0 += per) {
+                const int32_t i1 = std::min(m, i0 + per);
+                Unit u{q0 + i0, i1 - i0, base, n_pre, tile_of(std::max(low, p0 + i0 - win + 1)),
+                       tile_of(p0 + i1 - 1) + 1, (i1 - i0) * G > thr};
+                if (u.t0 <= base + n_pre) {   // the window reaches the sinks' tiles
+                    u.t0 = base;
+                    u.n_pre = 0;
+                }
+                n_tiles[u.tc] += u.n_pre + u.t1 - u.t0;
+                n_units[u.tc] += 1;
+                units.push_back(u);
+            }
+        }
+        q0 += m;
+    }
+    hp.n_row_tiles = (int32_t)units.size();
+    int64_t chunk[2];
+    for (int k = 0; k < 2; ++k) {
+        const int64_t target = k ? sms : (int64_t)sms * attention_ctas_per_sm(d.head_dim);
+        chunk[k] = kMaxItemTiles;
+        if (n_units[k] * lh < target) {
+            const int64_t want = (n_tiles[k] * lh + target - 1) / target;
+            chunk[k] = std::max<int64_t>(4, std::min<int64_t>(chunk[k], want));
+        }
+    }
+    // longest first, as the queues want them
+    std::stable_sort(units.begin(), units.end(), [](const Unit &a, const Unit &b) {
+        return (int64_t)(a.n_pre + a.t1 - a.t0) * a.n > (int64_t)(b.n_pre + b.t1 - b.t0) * b.n;
+    });
+    int32_t P = 0;
+    std::vector<MergeDesc> merge((size_t)q0, MergeDesc{0, 0});
+    for (const Unit &u : units) {
+        const int64_t nt = u.n_pre + u.t1 - u.t0;
+        const int64_t nc = (nt + chunk[u.tc] - 1) / chunk[u.tc];
+        if (nc > 1)
+            for (int32_t m = 0; m < u.n; ++m) merge[u.m0 + m] = MergeDesc{(int32_t)(hp.entries.size() + m * nc), (int32_t)nc};
+        const size_t e0 = hp.entries.size();
+        if (nc > 1) hp.entries.resize(e0 + (size_t)(u.n * nc));
+        for (int64_t c = 0; c < nc; ++c) {
+            const int32_t b = (int32_t)(nt * c / nc), e = (int32_t)(nt * (c + 1) / nc);   // of pre, then the run
+            WorkItem it{};
+            it.pre_begin = u.pre0 + std::min(b, u.n_pre);
+            it.n_pre = std::min(e, u.n_pre) - std::min(b, u.n_pre);
+            it.tile_begin = u.t0 + std::max(0, b - u.n_pre);
+            it.tile_end = u.t0 + std::max(0, e - u.n_pre);
+            it.member_off = u.m0;
+            it.n_members = u.n;
+            it.out_base = -1;
+            if (nc > 1) {
+                it.out_base = P;
+                for (int32_t m = 0; m < u.n; ++m) hp.entries[e0 + (size_t)(m * nc + c)] = P + m * G;
+                P += u.n * G;
+            }
+            (u.tc ? hp.tc_items : hp.items).push_back(it);
+        }
+    }
+    if (P > 0) hp.merge = std::move(merge);
+    hp.n_partial_rows = P;
+    hp.n_units = (int32_t)hp.items.size() * lh;
+    hp.n_tc_units = (int32_t)hp.tc_items.size() * lh;
+}
+
+int build_window(const kvp_attn_desc &d, const int32_t *tables, const int32_t *lens, const int32_t *q_lens, int32_t S,
+                 int32_t MB, int32_t win, int32_t sinks, int sms, HostPlan &hp) {
+    const int32_t bs = d.block_size, G = d.num_q_heads / d.num_kv_heads;
+    int64_t T = 0;
+    bool single = true;
+    for (int32_t s = 0; s < S; ++s) {
+        const int32_t nq = q_lens ? q_lens[s] : 1;
+        if (lens[s] < 0 || nq < 0 || nq > lens[s]) return KVP_ERR_INVALID;
+        const int64_t nb = ((int64_t)lens[s] + bs - 1) / bs;
+        if (nb > MB) return KVP_ERR_INVALID;
+        for (int64_t j = 0; j < nb; ++j) {
+            const int32_t id = tables[(size_t)s * MB + j];
+            if (id < 0 || id >= d.num_blocks) return KVP_ERR_INVALID;
+        }
+        single = single && nq == 1;
+        T += nq;
+    }
+    if (T * d.num_q_heads > INT32_MAX / 4) return KVP_ERR_INVALID;
+    // a window longer than any sequence sees everything
+    const int32_t longest = *std::max_element(lens, lens + S);
+    hp.win = std::max(1, std::min(win, longest));
+    hp.sinks = std::min(sinks, longest);
+    if (T == 0) return KVP_OK;
+    if (single) {
+        Scratch &sc = t_scratch;
+        sc.protos.clear();
+        window_decode_protos(d, tables, lens, S, MB, hp.win, hp.sinks);
+        finish(hp, sc, G, S, d.num_layers * d.num_kv_heads, sms, attention_ctas_per_sm(d.head_dim),
+               tc_usable(d) ? tc_row_threshold(d.head_dim) : INT32_MAX);
+        for (int32_t s = 0; s < S; ++s) hp.q_pos.push_back(lens[s] - 1);
+    } else {
+        window_extend_plan(d, tables, lens, q_lens, S, MB, hp.win, hp.sinks, sms, hp);
+    }
+    return KVP_OK;
+}
+
 bool desc_ok(const kvp_attn_desc *d) {
     if (!d || d->num_layers <= 0 || d->num_q_heads <= 0 || d->num_kv_heads <= 0 ||
         d->num_q_heads % d->num_kv_heads != 0 || d->num_q_heads / d->num_kv_heads > 64 ||
@@ -560,7 +791,7 @@ int log2_int(int32_t x) {
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct WsLayout {
-    size_t items, tc_items, tiles, members, merge, entries, part_o, part_lse, tree_mask, total, plan_bytes;
+    size_t items, tc_items, tiles, members, merge, entries, q_pos, part_o, part_lse, tree_mask, total, plan_bytes;
 };
 
 WsLayout layout(const HostPlan &hp, const kvp_attn_desc &d) {
@@ -572,6 +803,7 @@ WsLayout layout(const HostPlan &hp, const kvp_attn_desc &d) {
     w.members = off; off = align256(off + sizeof(int32_t) * hp.members.size());
     w.merge = off;   off = align256(off + sizeof(MergeDesc) * hp.merge.size());
     w.entries = off; off = align256(off + sizeof(int32_t) * hp.entries.size());
+    w.q_pos = off;   off = align256(off + sizeof(int32_t) * hp.q_pos.size());
     w.plan_bytes = off;
     const size_t lh = (size_t)d.num_layers * d.num_kv_heads * (size_t)hp.n_partial_rows;
     w.part_o = off;  off = align256(off + sizeof(float) * lh * d.head_dim);
@@ -589,6 +821,7 @@ struct Packed {
     std::vector<unsigned char> image;
     WsLayout w{};
     int32_t n_units = 0, n_tc_units = 0, n_partial_rows = 0;
+    int32_t win = 0, sinks = 0;
 };
 
 void pack(const HostPlan &hp, const kvp_attn_desc &d, Packed &pk) {
@@ -611,6 +844,9 @@ void pack(const HostPlan &hp, const kvp_attn_desc &d, Packed &pk) {
     std::memcpy(img + w.members, hp.members.data(), sizeof(int32_t) * hp.members.size());
     std::memcpy(img + w.merge, hp.merge.data(), sizeof(MergeDesc) * hp.merge.size());
     std::memcpy(img + w.entries, hp.entries.data(), sizeof(int32_t) * hp.entries.size());
+    if (!hp.q_pos.empty()) std::memcpy(img + w.q_pos, hp.q_pos.data(), sizeof(int32_t) * hp.q_pos.size());
+    pk.win = hp.win;
+    pk.sinks = hp.sinks;
     pk.n_units = hp.n_units;
     pk.n_tc_units = hp.n_tc_units;
     pk.n_partial_rows = hp.n_partial_rows;
@@ -682,6 +918,9 @@ int launch_packed(const Packed &pk, const kvp_attn_desc &d, const void *q, const
     a.n_merge_q = pk.n_partial_rows > 0 ? nq : 0;
     a.P = pk.n_partial_rows;
     a.wait_first = uploaded ? 1 : 0;
+    a.win = pk.win;
+    a.sinks = pk.sinks;
+    a.q_pos = (const int32_t *)(base + w.q_pos);
     return launch_attention(a, stream, t_ev_before, t_ev_after) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
@@ -1107,6 +1346,41 @@ int tree_verify_attention(const void *q, const int32_t *tree_parent, int32_t n_d
     if (rc) return rc;
     return run(hp, *desc, q, k_pool, v_pool, batch * n_draft, tree_parent, n_draft, out, lse,
                workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+size_t kvp_window_workspace_size(const kvp_attn_desc *desc, const int32_t *block_tables, const int32_t *seq_lens,
+                                 const int32_t *q_lens, int32_t num_seqs, int32_t max_blocks, int32_t window,
+                                 int32_t sinks) try {
+    if (!desc_ok(desc) || desc->kv_format != KVP_KV_BF16 || num_seqs <= 0 || max_blocks <= 0 || !block_tables ||
+        !seq_lens || window <= 0 || sinks < 0)
+        return 0;
+    HostPlan &hp = t_plan;
+    hp.clear();
+    if (build_window(*desc, block_tables, seq_lens, q_lens, num_seqs, max_blocks, window, sinks, device_sm_count(), hp))
+        return 0;
+    return layout(hp, *desc).total;
+} catch (const std::bad_alloc &) {
+    return 0;
+}
+
+int paged_window_attention(const void *q, const int32_t *q_lens, const void *k_pool, const void *v_pool,
+                           const int32_t *block_tables, const int32_t *seq_lens, int32_t num_seqs, int32_t max_blocks,
+                           int32_t window, int32_t sinks, const kvp_attn_desc *desc, void *out, float *lse,
+                           void *workspace, size_t ws_bytes, void *stream) try {
+    if (!desc_ok(desc) || desc->kv_format != KVP_KV_BF16 || num_seqs <= 0 || max_blocks <= 0 || !block_tables ||
+        !seq_lens || window <= 0 || sinks < 0)
+        return KVP_ERR_INVALID;
+    HostPlan &hp = t_plan;
+    hp.clear();
+    int rc = build_window(*desc, block_tables, seq_lens, q_lens, num_seqs, max_blocks, window, sinks,
+                          device_sm_count(), hp);
+    if (rc) return rc;
+    if (stream_capturing((cudaStream_t)stream)) return KVP_ERR_STATE;
+    const int32_t T = (int32_t)hp.q_pos.size();
+    if (T == 0) return KVP_OK;
+    return run(hp, *desc, q, k_pool, v_pool, T, nullptr, 0, out, lse, workspace, ws_bytes, (cudaStream_t)stream);
+} catch (const std::bad_alloc &) {
+    return KVP_ERR_OOM;
 }
 
 int kvp_device_error(void *workspace, void *stream, int32_t *err_out) {
