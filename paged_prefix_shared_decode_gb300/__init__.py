@@ -191,7 +191,8 @@ def _dev(x):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of the time of a Stream object
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -558,29 +559,36 @@ def tree_verify_attention(q, tree_parent, n_draft: int, k_pool, v_pool, block_ta
 
 # ------------------------------------------------- bounded caches and drafts
 
-def _typed(name, x, dtype, shape=None):
-    """Checks a tensor argument's type, shape and device (None and integer
-    addresses pass) and returns it."""
+def _arg(name, x, dtype, shape, device):
+    """Device address of a tensor argument of the given type, shape and
+    device, contiguous (None and integer addresses pass unchecked)."""
     if x is None or isinstance(x, int):
         return x
-    import torch
-    if x.dtype != getattr(torch, dtype):
+    if x.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {x.dtype}")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.is_cuda and x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {x.device}, not the current device")
-    return x
+    if x.get_device() != device:
+        raise ValueError(f"{name}: on {x.device}, expected a tensor on the current device, cuda:{device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return x.data_ptr()
 
 
 def _batch_i32(name, a, n):
-    """A host int32 array of one entry per sequence, or None."""
+    """A host int32 array of one entry per sequence, or None, and its address."""
     if a is None:
         return None, None
     a, p = _host_i32(a)
     if a.shape != (n,):
         raise ValueError(f"{name}: expected {n} entries, got shape {a.shape}")
     return a, p
+
+
+def _torch():
+    """torch and the current device (0 before CUDA is in use: no tensor is on it)."""
+    import torch
+    return torch, torch.cuda.current_device() if torch.cuda.is_initialized() else 0
 
 
 def _pool_shape(d: AttnDesc):
@@ -607,15 +615,14 @@ def paged_window_attention(q, q_lens, k_pool, v_pool, block_tables, seq_lens, wi
     S = t.shape[0]
     ln, lp = _batch_i32("seq_lens", seq_lens, S)
     ql, qp = _batch_i32("q_lens", q_lens, S)
-    T = S if ql is None else int(ql.sum())
-    rows = (desc.num_layers, T, desc.num_q_heads)
-    _typed("q", q, "bfloat16", rows + (desc.head_dim,))
-    _typed("out", out, "bfloat16", rows + (desc.head_dim,))
-    _typed("lse", lse, "float32", rows)
-    _typed("k_pool", k_pool, "bfloat16", _pool_shape(desc))
-    _typed("v_pool", v_pool, "bfloat16", _pool_shape(desc))
-    _check(load().paged_window_attention(_dev(q), qp, _dev(k_pool), _dev(v_pool), tp, lp, S, t.shape[1], window,
-                                         sinks, ctypes.byref(desc), _dev(out), _dev(lse), _dev(workspace),
+    T = S if ql is None else sum(ql.tolist())
+    torch, dev = _torch()
+    bf16, rows = torch.bfloat16, (desc.num_layers, T, desc.num_q_heads)
+    pool, wide = _pool_shape(desc), (*rows, desc.head_dim)
+    _check(load().paged_window_attention(_arg("q", q, bf16, wide, dev), qp, _arg("k_pool", k_pool, bf16, pool, dev),
+                                         _arg("v_pool", v_pool, bf16, pool, dev), tp, lp, S, t.shape[1], window,
+                                         sinks, ctypes.byref(desc), _arg("out", out, bf16, wide, dev),
+                                         _arg("lse", lse, torch.float32, rows, dev), _dev(workspace),
                                          _ws_bytes(workspace, ws_bytes), _stream(stream)), "paged_window_attention")
 
 
@@ -641,18 +648,15 @@ def kvp_attention_mass(q, q_lens, lse, k_pool, block_tables, seq_lens, desc: Att
     ln, lp = _batch_i32("seq_lens", seq_lens, S)
     ql, qp = _batch_i32("q_lens", q_lens, S)
     pl, pp = _batch_i32("prev_lens", prev_lens, S)
-    T = S if ql is None else int(ql.sum())
-    d = desc
-    rows = (d.num_layers, T, d.num_q_heads)
-    stride = mass_out.shape[-1]
-    shape = (d.num_layers, S, d.num_kv_heads, stride)
-    _typed("q", q, "bfloat16", rows + (d.head_dim,))
-    _typed("lse", lse, "float32", rows)
-    _typed("k_pool", k_pool, "bfloat16", _pool_shape(d))
-    _typed("mass_in", mass_in, "float32", shape)
-    _typed("mass_out", mass_out, "float32", shape)
-    _check(load().kvp_attention_mass(_dev(q), qp, _dev(lse), _dev(k_pool), tp, lp, S, t.shape[1], ctypes.byref(desc),
-                                     decay, _dev(mass_in), pp, _dev(mass_out), stride, _dev(workspace),
+    T = S if ql is None else sum(ql.tolist())
+    torch, dev = _torch()
+    f32, rows, stride = torch.float32, (desc.num_layers, T, desc.num_q_heads), mass_out.shape[-1]
+    shape = (desc.num_layers, S, desc.num_kv_heads, stride)
+    _check(load().kvp_attention_mass(_arg("q", q, torch.bfloat16, (*rows, desc.head_dim), dev), qp,
+                                     _arg("lse", lse, f32, rows, dev),
+                                     _arg("k_pool", k_pool, torch.bfloat16, _pool_shape(desc), dev), tp, lp, S,
+                                     t.shape[1], ctypes.byref(desc), decay, _arg("mass_in", mass_in, f32, shape, dev),
+                                     pp, _arg("mass_out", mass_out, f32, shape, dev), stride, _dev(workspace),
                                      _ws_bytes(workspace, ws_bytes), _stream(stream)), "kvp_attention_mass")
 
 
@@ -670,15 +674,14 @@ def seq_evict(pool, seqs, mass, budget: int, n_sink: int, n_recent: int, kept, m
     [L][n][Hkv][stride] fp32; kept [L][n][Hkv][budget] int32 receives their
     positions, mass_out (like mass, mass itself or None) their weights."""
     s, sp = _host_i32(seqs)
-    stride = mass.shape[-1]
     if mass.dim() != 4 or mass.shape[1] != len(s):
         raise ValueError(f"mass: expected [L][{len(s)}][Hkv][stride], got shape {tuple(mass.shape)}")
-    _typed("mass", mass, "float32")
-    _typed("mass_out", mass_out, "float32", mass.shape)
-    _typed("kept", kept, "int32", (*mass.shape[:3], budget))
-    _check(load().seq_evict(pool, sp, len(s), _dev(mass), stride, budget, n_sink, n_recent, _dev(kept),
-                            _dev(mass_out), _dev(workspace), _ws_bytes(workspace, ws_bytes), _stream(stream)),
-           "seq_evict")
+    torch, dev = _torch()
+    f32, shape = torch.float32, mass.shape
+    _check(load().seq_evict(pool, sp, len(s), _arg("mass", mass, f32, shape, dev), shape[3], budget, n_sink, n_recent,
+                            _arg("kept", kept, torch.int32, (*shape[:3], budget), dev),
+                            _arg("mass_out", mass_out, f32, shape, dev), _dev(workspace),
+                            _ws_bytes(workspace, ws_bytes), _stream(stream)), "seq_evict")
 
 
 def kvp_draft_verify(target, draft, tree_parent, draft_tokens, u_accept, u_next, accepted, n_accepted, next_token,
@@ -688,32 +691,29 @@ def kvp_draft_verify(target, draft, tree_parent, draft_tokens, u_accept, u_next,
     drafts chosen outright) fp32 probabilities, their last dimension
     contiguous; tree_parent, draft_tokens int32 and u_accept fp32 [B][n];
     u_next [B]; the outputs int32 [B]."""
-    B, n = draft_tokens.shape
+    B, n = bn = draft_tokens.shape
     V = target.shape[-1]
+    torch, dev = _torch()
+    i32, f32 = torch.int32, torch.float32
 
     def rows(name, x, least):
         if x is None:
             return None, 0, 0
-        _typed(name, x, "float32")
-        if not x.is_cuda:
-            raise ValueError("expected a CUDA tensor")
+        if x.dtype is not f32 or x.get_device() != dev:
+            raise ValueError(f"{name}: expected a float32 tensor on cuda:{dev}, got {x.dtype} on {x.device}")
         if x.dim() != 3 or x.shape[0] != B or x.shape[1] < least or x.shape[2] != V or (V > 1 and x.stride(2) != 1):
             raise ValueError(f"{name}: expected [{B}][>= {least}][{V}] with contiguous rows, got shape "
                              f"{tuple(x.shape)}, strides {x.stride()}")
-        # a dimension of one entry is never stepped over
-        return x.data_ptr(), x.stride(0) if B > 1 else 0, x.stride(1) if x.shape[1] > 1 else V
+        return x.data_ptr(), x.stride(0), x.stride(1)
 
-    tp, tb, tr = rows("target", target, n + 1)
-    dp, db, dr = rows("draft", draft, n)
-    for name, x, dtype, shape in (("tree_parent", tree_parent, "int32", (B, n)),
-                                  ("draft_tokens", draft_tokens, "int32", (B, n)),
-                                  ("u_accept", u_accept, "float32", (B, n)), ("u_next", u_next, "float32", (B,)),
-                                  ("accepted", accepted, "int32", (B,)), ("n_accepted", n_accepted, "int32", (B,)),
-                                  ("next_token", next_token, "int32", (B,))):
-        _typed(name, x, dtype, shape)
-    _check(load().kvp_draft_verify(tp, tb, tr, dp, db, dr, _dev(tree_parent), _dev(draft_tokens), _dev(u_accept),
-                                   _dev(u_next), B, n, V, _dev(accepted), _dev(n_accepted), _dev(next_token),
-                                   _stream(stream)), "kvp_draft_verify")
+    _check(load().kvp_draft_verify(*rows("target", target, n + 1), *rows("draft", draft, n),
+                                   _arg("tree_parent", tree_parent, i32, bn, dev),
+                                   _arg("draft_tokens", draft_tokens, i32, bn, dev),
+                                   _arg("u_accept", u_accept, f32, bn, dev), _arg("u_next", u_next, f32, (B,), dev),
+                                   B, n, V, _arg("accepted", accepted, i32, (B,), dev),
+                                   _arg("n_accepted", n_accepted, i32, (B,), dev),
+                                   _arg("next_token", next_token, i32, (B,), dev), _stream(stream)),
+           "kvp_draft_verify")
 
 
 def kvp_device_error(workspace, stream=None) -> int:

@@ -18,17 +18,25 @@
 // What is decided here is a token, so a sum may not depend on how it was
 // split: weights are added as 64-bit fixed point (2^-60), in which addition
 // is exact and any order gives the same bits.  An fp32 value from 2^-37 up is
-// represented exactly, a smaller one is cut at 2^-60.  (Sums in fp32 picked
-// another token wherever v fell within 1e-6 of a boundary; fp64 has one
-// unit for 64 lanes on this part, and converting and adding there would take
-// ten times as long as reading the row.)
+// represented exactly, a smaller one is cut at 2^-60.  (fp32 sums would pick
+// another token wherever v falls within about 1e-6 of a boundary, and fp64
+// arithmetic runs at a small fraction of the integer rate on this part.)
 //
-// One cluster of kCtas CTAs per sequence: a row of the vocabulary is cut into
-// kCtas * kWarps contiguous runs, one per warp, whose sums meet through
-// distributed shared memory.  Warp 0 of every CTA walks the tree redundantly
-// on the same numbers (all nodes' p(x) and q(x) are gathered at the start), so
-// the walk needs no communication but the sums.  The last sum's runs tell
-// which warp holds the sampled token: only that run is read again.
+// One cluster of up to 8 CTAs per sequence: a row of the vocabulary is cut
+// into contiguous runs, one per warp of the cluster, and every warp stores its
+// run's sum into every CTA's shared memory, so that one cluster barrier ends a
+// pass.  Warp 0 of every CTA walks the tree redundantly on the same numbers
+// (all nodes' p(x) and q(x), and the tests of first children, are made ready
+// by one lane per node at the start), so the walk needs no communication but
+// the sums.  The last pass's run sums tell which run holds the sampled token:
+// its CTA's warps read that run alone once more.
+//
+// Measured: 6.6 us for one chain of 5 over 32000 tokens (launch, the gather,
+// one pass and the search, each a memory latency or two), 18.3 us for 8 trees
+// of 64 nodes over 32003 (up to 7 passes of about 2 us, one per rejection:
+// two barriers, reductions and an L2 latency each), 22.5 us for 64 chains
+// over 131072 (67 MB, 3.0 TB/s: the passes' issue slots, about 30
+// instructions a token, and the latencies around them).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -40,9 +48,9 @@
 namespace kvp {
 namespace {
 
-constexpr int kCtas = 8;        // portable cluster size
+constexpr int kMaxCtas = 8;     // portable cluster size
 constexpr int kWarps = 16;
-constexpr int kRuns = kCtas * kWarps;
+constexpr int kMaxRuns = kMaxCtas * kWarps;
 constexpr int kOne = 60;        // fixed-point fraction bits of a weight
 
 struct DraftVerifyArgs {
@@ -54,31 +62,39 @@ struct DraftVerifyArgs {
     int32_t *accepted, *count, *next;
 };
 
-// p as fixed point with `bits` fraction bits, cut below; p in [0, 1]
-__device__ __forceinline__ uint64_t to_fixed(float p, int bits) {
+// p in [0, 1] as fixed point with kOne (60) or 63 fraction bits, cut below:
+// the significand, its first bit at p = 1's place, shifted right by 127 minus
+// the exponent (PTX shifts clamp, so zeros and subnormals come out as 0).
+template <int BITS>
+__device__ __forceinline__ uint64_t to_fixed(float p) {
     const uint32_t b = __float_as_uint(p);
-    const int sh = (int)(b >> 23) - 150 + bits;
-    const uint64_t m = (b & 0x7fffffu) | 0x800000u;
-    return b < 0x00800000u ? 0u : sh >= 0 ? m << sh : sh > -24 ? m >> -sh : 0u;
+    const uint32_t m = b << 8 | 0x80000000u, r = 127u - (b >> 23);
+    const uint32_t hi = m >> (63 - BITS), lo = BITS == 63 ? 0u : m << (BITS - 31);
+    uint32_t h, l, far;
+    asm("shr.u32 %0, %1, %2;" : "=r"(h) : "r"(hi), "r"(r));
+    asm("shf.r.clamp.b32 %0, %1, %2, %3;" : "=r"(l) : "r"(lo), "r"(hi), "r"(r));
+    asm("shr.u32 %0, %1, %2;" : "=r"(far) : "r"(hi), "r"(r - 32u));
+    return (uint64_t)h << 32 | (r > 32u ? far : l);
 }
 // a probability: NaN and negative values count as 0, values above 1 as 1
-__device__ __forceinline__ float prob(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
+__device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 
 // The weight max(p - c q, 0) of one token: MODE 0 takes c = 0, 1 takes c = 1,
 // 2 any c as a 57-bit fraction.
 template <int MODE>
 __device__ __forceinline__ uint64_t weight(float p, float q, uint64_t c) {
-    const uint64_t a = to_fixed(prob(p), kOne);
+    const uint64_t a = to_fixed<kOne>(prob(p));
     if (MODE == 0) return a;
     uint64_t b;
     if (MODE == 1) {
-        b = to_fixed(prob(q), kOne);
+        b = to_fixed<kOne>(prob(q));
     } else {   // 57 + 63 fraction bits, 60 of them kept
-        const uint64_t f = to_fixed(prob(q), 63);
+        const uint64_t f = to_fixed<63>(prob(q));
         b = (__umul64hi(c, f) << 4) | ((c * f) >> 60);
     }
     return a > b ? a - b : 0u;
 }
+
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -93,20 +109,31 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {   // inclu
     return x;
 }
 
-// Sum of the weights of tokens [lo, hi) of one row, this lane's share.  VEC:
-// the rows are 16-byte aligned (lo always is a multiple of 32).
-template <int MODE, bool VEC>
-__device__ __forceinline__ uint64_t run_sum(const float *p, const float *q, uint64_t c, int lo, int hi, int lane) {
+// How a warp reads its run of a row: element by element; as 16-byte vectors
+// (aligned rows); or, for runs of at most 32 * kHeld tokens, once into
+// registers, where the passes after a node's second and later rejections find
+// the row again.
+enum { kScalar = 0, kVector = 1, kHold = 2 };
+constexpr int kHeld = 8;
+
+// Sum of the weights of tokens [lo, hi) of one row, this lane's share (lo is
+// a multiple of 32).
+template <int MODE, int READ>
+__device__ __forceinline__ uint64_t run_sum(const float *p, const float *q, uint64_t c, int lo, int hi, int lane,
+                                            const float (&hp)[kHeld], const float (&hq)[kHeld]) {
     uint64_t s = 0;
     int x = lo;
-    if (VEC) {
+    if (READ == kHold) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) s += weight<MODE>(hp[k], hq[k], c);
+    } else if (READ == kVector) {
 #pragma unroll 4
         for (x = lo + 4 * lane; x + 4 <= hi; x += 128) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p + x));
-            float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (MODE) b = __ldg(reinterpret_cast<const float4 *>(q + x));
-            s += weight<MODE>(a.x, b.x, c) + weight<MODE>(a.y, b.y, c) + weight<MODE>(a.z, b.z, c) +
-                 weight<MODE>(a.w, b.w, c);
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(p + x));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (MODE) v = __ldg(reinterpret_cast<const float4 *>(q + x));
+            s += weight<MODE>(u.x, v.x, c) + weight<MODE>(u.y, v.y, c) + weight<MODE>(u.z, v.z, c) +
+                 weight<MODE>(u.w, v.w, c);
         }
         for (; x < hi; ++x) s += weight<MODE>(__ldg(p + x), MODE ? __ldg(q + x) : 0.f, c);
     } else {
@@ -116,25 +143,47 @@ __device__ __forceinline__ uint64_t run_sum(const float *p, const float *q, uint
     return s;
 }
 
+constexpr uint64_t kOneZ = 1ull << 60, kOneC = 1ull << 57, kMaxC = 127ull << 57;
+
+// u q Z < p - c q, in 32 bits where that is beyond doubt (each side's error
+// is below 2^-20 of the terms, which are far from underflow), else in 64: fp64 is slow here and every
+// later sibling's test is on the walk's critical path.
+__device__ __forceinline__ bool accepts(float u, float p, float q, uint64_t c, uint64_t Z) {
+    const float cq = __ull2float_rn(c) * 0x1p-57f * q, uqz = u * q * (__ull2float_rn(Z) * 0x1p-60f);
+    const float gap = p - cq - uqz;
+    const float terms = p + cq + uqz;
+    if (terms > 1e-30f && fabsf(gap) > 0x1p-20f * terms) return gap > 0.f;
+    return (double)u * q * ((double)Z * 0x1p-60) < p - (double)c * 0x1p-57 * q;
+}
+
 struct Walk {              // what warp 0 tells its CTA
     const float *p, *q;    // the row last summed, or to sum
     uint64_t c;            // 57-bit fraction
     int mode;              // weight()'s
     int n_cut;             // without q: rejected tokens, in s_cut
     bool done;             // the sums at hand are the last
-    uint64_t before, at;   // sum of the CTAs before this one; the sampled token's place (~0: none)
+    uint64_t at;           // the sampled token's place in the running sum (~0: none)
 };
 
-template <bool VEC>
-__global__ void __launch_bounds__(32 * kWarps) draft_verify_kernel(const DraftVerifyArgs a) {
+// Inclusive scan over the cluster's run sums, four runs to a lane.
+__device__ __forceinline__ uint64_t scan_runs(const uint64_t *run, int lane, uint64_t (&v)[4]) {
+    uint64_t s = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s += v[k] = run[4 * lane + k];
+    return warp_scan(s, lane);
+}
+
+template <int READ>
+__global__ void __launch_bounds__(32 * kWarps, 2) draft_verify_kernel(const DraftVerifyArgs a) {
     __shared__ int s_par[kMaxDraft], s_tok[kMaxDraft], s_cut[kMaxDraft];
     __shared__ float s_p[kMaxDraft], s_q[kMaxDraft], s_u[kMaxDraft];
-    __shared__ uint64_t s_run[kWarps], s_cta[2];
+    __shared__ uint64_t s_run[2][kMaxRuns], s_part[kWarps];
     __shared__ Walk s_walk;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint32_t rank;
+    uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(rank));
-    const int b = blockIdx.x / kCtas;
+    asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(ctas));
+    const int b = blockIdx.x / ctas;
     const float *tb = a.target + b * a.t_batch;
     const float *db = a.draft ? a.draft + b * a.d_batch : nullptr;
     if (tid < a.n) {
@@ -149,17 +198,28 @@ __global__ void __launch_bounds__(32 * kWarps) draft_verify_kernel(const DraftVe
         s_p[tid] = ok ? prob(tb[(par + 1) * a.t_row + x]) : 0.f;
         s_q[tid] = ok && db ? prob(db[(par + 1) * a.d_row + x]) : 0.f;
     }
+    if (tid < 2 * kMaxRuns) s_run[0][tid] = 0;  // (runs that a smaller cluster lacks)
+    const float u_next = tid == 0 ? a.u_next[b] : 0.f;
     __syncthreads();
+    // every CTA has cleared its sums before another stores into them
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
 
     // warp 0's walk, the same in every CTA.  rest: children of cur still to
-    // be tried; summed: the sums at hand are those of cur's row and c
+    // be tried; first: nodes that are accepted when tried first (c = 0, Z =
+    // 1; a first rejection makes c 1); summed: the sums at hand are those of cur's row and c
     int cur = -1, cnt = 0, n_cut = 0;
-    double c = 0., Z = 1.;
+    uint64_t c = 0, Z = kOneZ;   // 57 and 60 fraction bits
     bool summed = false, plain = false;   // plain: sample from p itself
     int par0 = -2, par1 = -2;
+    uint64_t first = 0;
     if (warp == 0) {
-        if (lane < a.n && s_tok[lane] >= 0) par0 = s_par[lane];
-        if (lane + 32 < a.n && s_tok[lane + 32] >= 0) par1 = s_par[lane + 32];
+        auto test = [&](int i, int &par) -> bool {
+            if (i >= a.n || s_tok[i] < 0) return false;
+            par = s_par[i];
+            return db ? (double)s_u[i] * s_q[i] < s_p[i] : s_u[i] < s_p[i];
+        };
+        const bool t0 = test(lane, par0), t1 = test(lane + 32, par1);
+        first = (uint64_t)__ballot_sync(0xffffffffu, t0) | (uint64_t)__ballot_sync(0xffffffffu, t1) << 32;
     }
     auto children = [&](int node) -> uint64_t {
         return (uint64_t)__ballot_sync(0xffffffffu, par0 == node) |
@@ -170,24 +230,26 @@ __global__ void __launch_bounds__(32 * kWarps) draft_verify_kernel(const DraftVe
     const long long begin = (long long)(rank * kWarps + warp) * a.run;
     const int lo = (int)(begin < a.vocab ? begin : a.vocab);
     const int hi = (int)(begin + a.run < a.vocab ? begin + a.run : a.vocab);
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 
-    for (int pass = 0;; ++pass) {
+    float hp[kHeld], hq[kHeld];
+    int pass = 0;
+    for (;; ++pass) {
         if (warp == 0) {
             bool need = false;   // the walk waits for a sum
             while (rest != 0 && !need) {
                 const int i = __ffsll((long long)rest) - 1;
                 rest &= rest - 1;
-                const double u = s_u[i], p = s_p[i];
-                bool yes;
+                bool yes = (first >> i) & 1;
                 if (db) {
-                    const double q = s_q[i];
-                    yes = u * q * Z < p - c * q;
+                    if (c != 0) yes = accepts(s_u[i], s_p[i], s_q[i], c, Z);
                 } else {
                     bool cut = false;
                     for (int k = 0; k < n_cut; ++k) cut |= s_cut[k] == s_tok[i];
-                    yes = u * Z < (cut ? 0. : p);
+                    if (n_cut > 0) yes = (double)s_u[i] * ((double)Z * 0x1p-60) < (cut ? 0. : (double)s_p[i]);
                     if (!yes && !cut) {
-                        Z = fmax(Z - p, 0.);
+                        const uint64_t p = to_fixed<kOne>(s_p[i]);
+                        Z = Z > p ? Z - p : 0;
                         if (lane == 0) s_cut[n_cut] = s_tok[i];
                         __syncwarp();
                         ++n_cut;
@@ -196,13 +258,13 @@ __global__ void __launch_bounds__(32 * kWarps) draft_verify_kernel(const DraftVe
                 if (yes) {
                     cur = i;
                     ++cnt;
-                    c = 0.;
-                    Z = 1.;
+                    c = 0;
+                    Z = kOneZ;
                     n_cut = 0;
                     summed = false;
                     rest = children(cur);
                 } else if (db) {
-                    c = fmin(c + Z, 127.);
+                    c = min(c + (Z >> 3), kMaxC);
                     need = true;
                 }
             }
@@ -210,10 +272,10 @@ __global__ void __launch_bounds__(32 * kWarps) draft_verify_kernel(const DraftVe
             if (lane == 0) {
                 s_walk.done = done;
                 if (!done) {
-                    s_walk.mode = c == 0. || plain ? 0 : c == 1. ? 1 : 2;
+                    s_walk.mode = c == 0 || plain ? 0 : c == kOneC ? 1 : 2;
                     s_walk.p = tb + (cur + 1) * a.t_row;
                     s_walk.q = s_walk.mode ? db + (cur + 1) * a.d_row : nullptr;
-                    s_walk.c = (uint64_t)(c * 0x1p57);
+                    s_walk.c = c;
                     s_walk.n_cut = plain ? 0 : n_cut;
                 }
             }
@@ -221,41 +283,36 @@ __global__ void __launch_bounds__(32 * kWarps) draft_verify_kernel(const DraftVe
         __syncthreads();
         if (s_walk.done) break;
         const Walk w = s_walk;
-        uint64_t s = w.mode == 0   ? run_sum<0, VEC>(w.p, w.q, w.c, lo, hi, lane)
-                     : w.mode == 1 ? run_sum<1, VEC>(w.p, w.q, w.c, lo, hi, lane)
-                                   : run_sum<2, VEC>(w.p, w.q, w.c, lo, hi, lane);
+        if (READ == kHold && w.mode < 2) {   // (a third pass over a row finds it held)
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) {
+                const int x = lo + 32 * k + lane;
+                hp[k] = x < hi ? __ldg(w.p + x) : 0.f;
+                hq[k] = x < hi && w.mode ? __ldg(w.q + x) : 0.f;
+            }
+        }
+        uint64_t s = w.mode == 0   ? run_sum<0, READ>(w.p, w.q, w.c, lo, hi, lane, hp, hq)
+                     : w.mode == 1 ? run_sum<1, READ>(w.p, w.q, w.c, lo, hi, lane, hp, hq)
+                                   : run_sum<2, READ>(w.p, w.q, w.c, lo, hi, lane, hp, hq);
         s = warp_sum(s);
         // (the rejected tokens of a certain draft are distinct)
         for (int k = 0; k < w.n_cut; ++k) {
             const int x = s_cut[k];
             if (x >= lo && x < hi) s -= weight<0>(__ldg(w.p + x), 0.f, 0);
         }
-        if (lane == 0) s_run[warp] = s;
-        __syncthreads();
-        if (warp == 0) {
-            const uint64_t mine = warp_sum(lane < kWarps ? s_run[lane] : 0);
-            if (lane == 0) s_cta[pass & 1] = mine;
+        // lane r stores the sum into CTA r.  The next pass stores into the
+        // other array, and the one after it here again, when every CTA has
+        // been through the next pass's barrier and so has read this one
+        if (lane < ctas) {
+            uint32_t addr = (uint32_t)__cvta_generic_to_shared(&s_run[pass & 1][rank * kWarps + warp]);
+            asm volatile("mapa.shared::cluster.u32 %0, %0, %1;\n" : "+r"(addr) : "r"(lane));
+            asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(addr), "l"(s) : "memory");
         }
-        // the CTAs' sums meet.  The next pass writes the other word, and the
-        // one after it this word again, when every CTA has been through the
-        // next pass's barrier and so has read it
         asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         if (warp == 0) {
-            uint64_t v = 0;
-            if (lane < kCtas) {
-                uint32_t addr = (uint32_t)__cvta_generic_to_shared(&s_cta[pass & 1]);
-                asm volatile("mapa.shared::cluster.u32 %0, %0, %1;\n" : "+r"(addr) : "r"(lane));
-                asm volatile("ld.shared::cluster.u64 %0, [%1];\n" : "=l"(v) : "r"(addr) : "memory");
-            }
-            const uint64_t sc = warp_scan(v, lane);
-            const uint64_t total = __shfl_sync(0xffffffffu, sc, 31);
-            if (lane == (int)rank) {
-                float v1 = a.u_next[b];
-                v1 = v1 > 0.f ? fminf(v1, 1.f - 0x1p-24f) : 0.f;
-                s_walk.before = sc - v;
-                s_walk.at = total ? __umul64hi(to_fixed(v1, 64), total) : ~0ull;
-            }
-            Z = (double)total * 0x1p-60;
+            uint64_t v[4];
+            const uint64_t total = __shfl_sync(0xffffffffu, scan_runs(s_run[pass & 1], lane, v), 31);
+            Z = total;
             summed = true;
             if (rest == 0 && total == 0 && !plain) {
                 // nothing is left of p once its rejected part is taken off:
@@ -263,68 +320,84 @@ __global__ void __launch_bounds__(32 * kWarps) draft_verify_kernel(const DraftVe
                 plain = true;
                 summed = false;
             }
+            if (lane == 0) {
+                const float v1 = u_next > 0.f ? fminf(u_next, 1.f - 0x1p-24f) : 0.f;
+                // (v1 < 1, so 64 fraction bits fit)
+                s_walk.at = total ? __umul64hi(to_fixed<63>(v1) << 1, total) : ~0ull;
+            }
         }
     }
 
-    // the sampled token is the first whose running sum exceeds `at`
+    // the sampled token is the first whose running sum exceeds `at`: which
+    // run, then which part of it (one per warp of its CTA), lane and token
     const Walk w = s_walk;
     if (rank == 0 && tid == 0) {
         a.accepted[b] = cur;
         a.count[b] = cnt;
         if (w.at == ~0ull) a.next[b] = -1;   // p is zero everywhere
     }
-    const uint64_t mine = lane < kWarps ? s_run[lane] : 0;
-    const uint64_t upto = warp_scan(mine, lane);
-    const uint64_t end = w.before + __shfl_sync(0xffffffffu, upto, warp);
-    const uint64_t start = end - s_run[warp];
-    if (w.at != ~0ull && w.at >= start && w.at < end) {
-        const uint64_t t = w.at - start;
-        auto token_weight = [&](int x) -> uint64_t {
-            for (int k = 0; k < w.n_cut; ++k)
-                if (s_cut[k] == x) return 0;
-            const float p = __ldg(w.p + x);
-            return w.mode == 0 ? weight<0>(p, 0.f, 0)
-                               : w.mode == 1 ? weight<1>(p, __ldg(w.q + x), 0) : weight<2>(p, __ldg(w.q + x), w.c);
-        };
-        // which lane's share of the run, then which of its tokens
-        const int share = a.run / 32;
-        uint64_t s = 0;
-#pragma unroll 4
-        for (int k = 0; k < share; ++k) {
-            const int x = lo + lane * share + k;
-            if (x < hi) s += token_weight(x);
-        }
-        uint64_t inc = warp_scan(s, lane);
-        const int f = __ffs(__ballot_sync(0xffffffffu, inc > t)) - 1;
-        uint64_t base = __shfl_sync(0xffffffffu, inc - s, f);
-        for (int k = 0; k < share; k += 32) {
-            const int x = lo + f * share + k + lane;
-            inc = base + warp_scan(k + lane < share && x < hi ? token_weight(x) : 0, lane);
-            const uint32_t hit = __ballot_sync(0xffffffffu, inc > t);
-            if (hit) {
-                if (lane == 0) a.next[b] = lo + f * share + k + __ffs(hit) - 1;
-                break;
+    if (w.at != ~0ull) {
+        uint64_t v[4];
+        const uint64_t inc = scan_runs(s_run[(pass - 1) & 1], lane, v);
+        const int f = __ffs(__ballot_sync(0xffffffffu, inc > w.at)) - 1;
+        uint64_t start = inc - (v[0] + v[1] + v[2] + v[3]);
+        int run = 4 * lane;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (run == 4 * lane + k && start + v[k] <= w.at) {
+                start += v[k];
+                ++run;
             }
-            base = __shfl_sync(0xffffffffu, inc, 31);
+        start = __shfl_sync(0xffffffffu, start, f);
+        run = __shfl_sync(0xffffffffu, run, f);
+        if (run / kWarps == (int)rank) {   // (the same for the whole CTA)
+            auto token_weight = [&](int x) -> uint64_t {
+                for (int k = 0; k < w.n_cut; ++k)
+                    if (s_cut[k] == x) return 0;
+                const float p = __ldg(w.p + x);
+                return w.mode == 0   ? weight<0>(p, 0.f, 0)
+                       : w.mode == 1 ? weight<1>(p, __ldg(w.q + x), 0)
+                                     : weight<2>(p, __ldg(w.q + x), w.c);
+            };
+            const int part = a.run / kWarps, share = (part + 31) / 32;
+            const int x0 = run * a.run + warp * part;
+            const int xl = min(x0 + lane * share, a.vocab);
+            const int xe = min(min(xl + share, x0 + part), a.vocab);
+            uint64_t s = 0;
+#pragma unroll 4
+            for (int x = xl; x < xe; ++x) s += token_weight(x);
+            const uint64_t in_warp = warp_scan(s, lane);
+            if (lane == 31) s_part[warp] = in_warp;
+            __syncthreads();
+            for (int k = 0; k < warp; ++k) start += s_part[k];
+            uint64_t upto = start + in_warp - s;
+            if (w.at >= upto && w.at < upto + s) {   // one lane of the CTA
+                int x = xl;
+                for (; x < xe - 1; ++x) {
+                    upto += token_weight(x);
+                    if (upto > w.at) break;
+                }
+                a.next[b] = x;
+            }
         }
     }
-    // every CTA's sum has been read before any CTA ends
+    // no CTA ends while another may still store into it
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-template <bool VEC>
-cudaError_t launch_draft_verify(const DraftVerifyArgs &a, int32_t batch, cudaStream_t stream) {
+template <int READ>
+cudaError_t launch_draft_verify(const DraftVerifyArgs &a, int32_t batch, int ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)batch * kCtas);
+    cfg.gridDim = dim3((unsigned)batch * ctas);
     cfg.blockDim = dim3(32 * kWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, draft_verify_kernel<VEC>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, draft_verify_kernel<READ>, a);
     count_launch();
     return e;
 }
@@ -338,7 +411,7 @@ extern "C" int kvp_draft_verify(const float *target, int64_t target_batch_stride
                                 const float *u_next, int32_t batch, int32_t n_draft, int32_t vocab,
                                 int32_t *accepted, int32_t *n_accepted, int32_t *next_token, void *stream) {
     using namespace kvp;
-    if (!target || !u_next || !accepted || !n_accepted || !next_token || batch <= 0 || batch > INT32_MAX / kCtas ||
+    if (!target || !u_next || !accepted || !n_accepted || !next_token || batch <= 0 || batch > INT32_MAX / kMaxCtas ||
         n_draft < 0 || n_draft > kMaxDraft || vocab <= 0 || vocab > (1 << 30))
         return KVP_ERR_INVALID;
     if (n_draft > 0 && (!tree_parent || !draft_tokens || !u_accept)) return KVP_ERR_INVALID;
@@ -361,7 +434,12 @@ extern "C" int kvp_draft_verify(const float *target, int64_t target_batch_stride
     a.u_next = u_next;
     a.n = n_draft;
     a.vocab = vocab;
-    a.run = (int32_t)(((int64_t)vocab + 32 * kRuns - 1) / (32 * kRuns)) * 32;
+    // the largest cluster with which the batch still runs at once (two CTAs
+    // fit on an SM)
+    int ctas = kMaxCtas;
+    while (ctas > 1 && (int64_t)batch * ctas > 2LL * device_sm_count()) ctas /= 2;
+    const int64_t step = 32LL * kWarps * ctas;
+    a.run = (int32_t)((vocab + step - 1) / step) * 32;
     a.accepted = accepted;
     a.count = n_accepted;
     a.next = next_token;
@@ -370,7 +448,9 @@ extern "C" int kvp_draft_verify(const float *target, int64_t target_batch_stride
     };
     const bool v4 = vec(target, target_batch_stride, target_row_stride) &&
                     (!draft || vec(draft, draft_batch_stride, draft_row_stride));
-    const cudaError_t e = v4 ? launch_draft_verify<true>(a, batch, (cudaStream_t)stream)
-                             : launch_draft_verify<false>(a, batch, (cudaStream_t)stream);
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = a.run <= 32 * kHeld ? launch_draft_verify<kHold>(a, batch, ctas, st)
+                          : v4                ? launch_draft_verify<kVector>(a, batch, ctas, st)
+                                              : launch_draft_verify<kScalar>(a, batch, ctas, st);
     return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
