@@ -5,10 +5,14 @@
 // last `recent` tokens stay, and of the rest the k = budget - sink - recent
 // with the largest weight, equal weights by lowest position.  The k-th
 // largest is found by a radix select over the weights as ordered 32-bit keys
-// (11, 11 and 10 bits a pass, a histogram in shared memory), which reads the
-// row three times from L2 and compares nothing; a sort would move it.  Then
-// each warp takes a contiguous stretch of the row, so that one scan over the
-// 16 warps' counts gives every kept token its place in position order.
+// (11, 11 and 10 bits a pass, a histogram in shared memory).  Each warp holds
+// a contiguous stretch of the row, so that one scan over the 16 warps' counts
+// gives every kept token its place in position order.  Rows are read once and
+// stay in shared memory as keys (which also makes the weights' compaction safe
+// in place) as far as it reaches; longer ones are read again in every pass,
+// from L2.  (Keys in registers, 32 to a lane, needed every loop unrolled:
+// straight-line code that each CTA runs once waits for instruction fetches,
+// 27 to 35 us where this takes 23 us for rows of up to 16000.)
 //
 // Compaction: kept token j of a (layer, kv head) moves to slot j of the
 // sequence.  A row of K or V is d * 2 contiguous bytes and moves in 16-byte
@@ -25,6 +29,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include "kvp_internal.h"
 
@@ -34,16 +39,20 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kHoldKeys = 48 * 1024;   // keys of a row that fit in shared memory
 constexpr int kRowTile = 64;      // rows of K and of V per copy CTA
 constexpr int kMoveThreads = 256;
 constexpr int kInFlight = 8;      // 16-byte loads in flight per thread
 
-// Order of weights as unsigned keys: NaN below everything, -0 equal to 0.
+// Weights as unsigned keys of the same order: NaN below everything, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
-    if (x != x) return 0u;
-    const uint32_t b = __float_as_uint(x + 0.f);   // -0 + 0 = +0
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    const uint32_t b = __float_as_uint(x == x ? x + 0.f : __uint_as_float(0xffffffffu));
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float key_weight(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+constexpr uint32_t kStays = 0xffffffffu;   // sinks and recent tokens: above every weight's key
 
 __device__ __forceinline__ int scan_warp(int x, int lane) {   // inclusive
 #pragma unroll
@@ -54,130 +63,150 @@ __device__ __forceinline__ int scan_warp(int x, int lane) {   // inclusive
     return x;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLaunch a) {
-    __shared__ int s_bin[kBins];
+// HOLD: the row's keys are kept in (dynamic) shared memory.
+template <bool HOLD>
+__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const EvictLaunch a) {
+    __shared__ __align__(16) int s_bin[kBins];
     __shared__ int s_sum[kSelWarps], s_eq[kSelWarps];
     __shared__ int s_digit, s_left;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.Hkv, ls = blockIdx.x / a.Hkv;
-    const int s = ls % a.S;
-    const EvictSeq sq = a.seqs[s];
+    const EvictSeq sq = a.seqs[blockIdx.x / a.Hkv % a.S];
     const float *m = a.mass + (size_t)blockIdx.x * a.stride;
     float *mo = a.mass_out ? a.mass_out + (size_t)blockIdx.x * a.stride : nullptr;
     int32_t *kept = a.kept + (size_t)blockIdx.x * a.budget;
-    (void)h;
     if (sq.len <= a.budget) {   // everything stays where it is
         for (int j = tid; j < a.budget; j += kSelThreads) kept[j] = j < sq.len ? j : -1;
         if (mo && mo != m)
             for (int j = tid; j < sq.len; j += kSelThreads) mo[j] = m[j];
         return;
     }
-    // positions [lo, hi) compete for k places
-    const int lo = a.sink, hi = sq.len - a.recent;
-    const int k = a.budget - a.sink - a.recent;
-    uint32_t prefix = 0;   // the leading bits of the k-th largest key
-    int left = k;          // places left among the keys that share them
-    if (k > 0) {
-#pragma unroll 1
-        for (int p = 0; p < 3; ++p) {
-            const int shift = p == 0 ? 21 : p == 1 ? 10 : 0, bits = p == 2 ? 10 : 11;
-            for (int i = tid; i < kBins; i += kSelThreads) s_bin[i] = 0;
-            __syncthreads();
-#pragma unroll 8
-            for (int i = lo + tid; i < hi; i += kSelThreads) {
-                const uint32_t key = order_key(m[i]);
-                // (the shift by 32 of the first pass is split in two)
-                if ((key >> shift >> bits) == (p == 0 ? 0u : prefix >> shift >> bits))
-                    atomicAdd(&s_bin[(key >> shift) & ((1 << bits) - 1)], 1);
-            }
-            __syncthreads();
-            // from the largest digit down: thread i has digits 2047 - 4 i - {0..3}
-            int n[4], sum = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum += n[e] = s_bin[kBins - 1 - 4 * tid - e];
-            const int inc = scan_warp(sum, lane);
-            if (lane == 31) s_sum[warp] = inc;
-            __syncthreads();
-            int before = inc - sum;
-            for (int w = 0; w < warp; ++w) before += s_sum[w];
-            if (before < left && before + sum >= left) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (before < left && before + n[e] >= left) {
-                        s_digit = kBins - 1 - 4 * tid - e;
-                        s_left = left - before;
-                        break;
-                    }
-                    before += n[e];
-                }
-            }
-            __syncthreads();
-            prefix |= (uint32_t)s_digit << shift;
-            left = s_left;
-            __syncthreads();
-        }
-    }
-    // stretch of this warp; its tokens above the k-th largest (and the sinks
-    // and recent ones), and those equal to it
+    // this warp's stretch: tokens b0 + lane + 32 k below b1.  A token that
+    // stays by its position has the highest key, and one past the end the
+    // lowest (a NaN's, but behind it), so the `budget` first keys by (key,
+    // position) are the kept tokens and nothing below looks at positions.
     const int per = ((sq.len + kSelWarps - 1) / kSelWarps + 31) & ~31;
     const int b0 = min(warp * per, sq.len), b1 = min(b0 + per, sq.len);
-    auto kind = [&](int i) -> int {   // 2: stays, 1: equal, 0: goes
-        if (i < lo || i >= hi) return 2;
-        if (k == 0) return 0;
-        const uint32_t key = order_key(m[i]);
-        return key > prefix ? 2 : key == prefix ? 1 : 0;
+    const int lo = a.sink, hi = sq.len - a.recent;
+    auto key_at = [&](int i, float x) -> uint32_t {
+        return i >= b1 ? 0u : (unsigned)(i - lo) < (unsigned)(hi - lo) ? order_key(x) : kStays;
     };
-    int above = 0, equal = 0;
+    extern __shared__ uint32_t s_key[];
+    if (HOLD) {   // (each lane reads back its own)
+#pragma unroll 8
+        for (int i = b0 + lane; i < b1; i += 32) s_key[i] = key_at(i, m[i]);
+    }
+    // f(i, key) for the lane's tokens in ascending order, the whole warp at
+    // every step
+    auto each = [&](auto f) {
 #pragma unroll 4
-    for (int i = b0 + lane; i < b1; i += 32) {
-        const int c = kind(i);
-        above += c == 2;
-        equal += c == 1;
-    }
+        for (int i = b0 + lane; i - lane < b1; i += 32)
+            f(i, i >= b1 ? 0u : HOLD ? s_key[i] : key_at(i, m[i]));
+    };
+    uint32_t prefix = 0;      // the leading bits of the last kept key
+    int left = a.budget;      // places left among the keys that share them
+#pragma unroll 1
+    for (int p = 0; p < 3; ++p) {
+        const int shift = p == 0 ? 21 : p == 1 ? 10 : 0, bits = p == 2 ? 10 : 11;
+        for (int i = tid; i < kBins / 4; i += kSelThreads) reinterpret_cast<int4 *>(s_bin)[i] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        if (p == 0) {
+            each([&](int, uint32_t key) { atomicAdd(&s_bin[key >> 21], 1); });
+        } else {
+            const uint32_t mask = ~0u << (shift + bits);
+            each([&](int, uint32_t key) {
+                if (((key ^ prefix) & mask) == 0) atomicAdd(&s_bin[(key >> shift) & ((1 << bits) - 1)], 1);
+            });
+        }
+        __syncthreads();
+        // from the largest digit down: thread i has digits 2047 - 4 i - {0..3}
+        int4 q = make_int4(0, 0, 0, 0);
+        if (tid < kBins / 4) q = reinterpret_cast<const int4 *>(s_bin)[kBins / 4 - 1 - tid];
+        const int n[4] = {q.w, q.z, q.y, q.x};
+        const int sum = n[0] + n[1] + n[2] + n[3];
+        const int inc = scan_warp(sum, lane);
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        int before = inc - sum + (int)__reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
+        if (before < left && before + sum >= left) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        above += __shfl_xor_sync(0xffffffffu, above, o);
-        equal += __shfl_xor_sync(0xffffffffu, equal, o);
+            for (int e = 0; e < 4; ++e) {
+                if (before < left && before + n[e] >= left) {
+                    s_digit = kBins - 1 - 4 * tid - e;
+                    s_left = left - before;
+                    break;
+                }
+                before += n[e];
+            }
+        }
+        __syncthreads();
+        prefix |= (uint32_t)s_digit << shift;
+        left = s_left;
     }
+    // keys above the last kept one stay, of those equal to it the first
+    // `left`: how many of each lie before this warp's stretch
+    int above = 0, equal = 0;
+    each([&](int i, uint32_t key) {
+        above += key > prefix;
+        equal += key == prefix;
+    });
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane == 0) {
         s_sum[warp] = above;
         s_eq[warp] = equal;
     }
     __syncthreads();
-    int n_above = 0, n_equal = 0;
-    for (int w = 0; w < warp; ++w) {
-        n_above += s_sum[w];
-        n_equal += s_eq[w];
-    }
-    for (int i0 = b0; i0 < b1; i0 += 32) {
-        const int i = i0 + lane;
-        const int c = i < b1 ? kind(i) : 0;
-        const uint32_t up = __ballot_sync(0xffffffffu, c == 2), eq = __ballot_sync(0xffffffffu, c == 1);
-        const uint32_t mask = (1u << lane) - 1u;
-        const int eq_before = n_equal + __popc(eq & mask);
-        // (k == 0: nothing is equal)
-        if (c == 2 || (c == 1 && eq_before < left))
-            kept[n_above + __popc(up & mask) + min(eq_before, left)] = i;
-        n_above += __popc(up);
-        n_equal += __popc(eq);
+    int n_above = __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
+    int n_equal = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
+    const uint32_t mask = (1u << lane) - 1u;
+    // (with the keys held, no weight is read again but those of tokens that
+    // stay by position: sinks keep their place, recent ones are moved below)
+    const bool write = HOLD && mo;
+    if (equal == 0 || n_equal >= left) {   // no key of the stretch is kept as an equal
+        int j0 = n_above + min(n_equal, left);
+        each([&](int i, uint32_t key) {
+            const uint32_t up = __ballot_sync(0xffffffffu, key > prefix);
+            const int j = j0 + __popc(up & mask);
+            if (key > prefix) {
+                kept[j] = i;
+                if (write && key != kStays) mo[j] = key_weight(key);
+            }
+            j0 += __popc(up);
+        });
+    } else {
+        each([&](int i, uint32_t key) {
+            const uint32_t up = __ballot_sync(0xffffffffu, key > prefix), eq = __ballot_sync(0xffffffffu, key == prefix);
+            const int eq_before = n_equal + __popc(eq & mask);
+            if (key > prefix || (key == prefix && eq_before < left)) {
+                const int j = n_above + __popc(up & mask) + min(eq_before, left);
+                kept[j] = i;
+                if (write && key != kStays) mo[j] = key_weight(key);
+            }
+            n_above += __popc(up);
+            n_equal += __popc(eq);
+        });
     }
     if (!mo) return;
-    // the kept weights, in place if need be: a run is read before any of it
-    // is written, and later runs lie at or behind their places
+    // the weights not yet in place: all of them, or the recent tokens' (whose
+    // sources lie behind every place written so far).  In place if need be: a
+    // run is read before any of it is written, and later runs lie at or
+    // behind their places
     __syncthreads();
+    if (HOLD && mo != m)
+        for (int j = tid; j < lo; j += kSelThreads) mo[j] = m[j];
     constexpr int U = 4;
-    for (int j0 = 0; j0 < a.budget; j0 += kSelThreads * U) {
-        float v[U];
+    for (int j0 = HOLD ? a.budget - a.recent : 0; j0 < a.budget; j0 += kSelThreads * U) {
+        float w[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int j = j0 + u * kSelThreads + tid;
-            v[u] = j < a.budget ? m[kept[j]] : 0.f;
+            w[u] = j < a.budget ? m[kept[j]] : 0.f;
         }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int j = j0 + u * kSelThreads + tid;
-            if (j < a.budget) mo[j] = v[u];
+            if (j < a.budget) mo[j] = w[u];
         }
     }
 }
@@ -262,10 +291,29 @@ __global__ void __launch_bounds__(kMoveThreads) evict_pack_kernel(const EvictLau
     }
 }
 
+// Per device: the selection kernel's shared-memory limit is raised once.
+bool select_ready() {
+    static bool ok[kMaxDevices];
+    static std::once_flag once[kMaxDevices];
+    const int dev = current_device();
+    if (dev < 0) return false;
+    std::call_once(once[dev], [dev] {
+        ok[dev] = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kHoldKeys * 4) == cudaSuccess;
+    });
+    return ok[dev];
+}
+
 }  // namespace
 
-cudaError_t launch_evict(const EvictLaunch &a, bool copies, bool packs, cudaStream_t stream) {
-    evict_select_kernel<<<(unsigned)(a.L * a.S * a.Hkv), kSelThreads, 0, stream>>>(a);
+cudaError_t launch_evict(const EvictLaunch &a, int max_len, bool copies, bool packs, cudaStream_t stream) {
+    const unsigned rows = (unsigned)(a.L * a.S * a.Hkv);
+    if (max_len <= kHoldKeys) {
+        if (!select_ready()) return cudaErrorInvalidDevice;
+        evict_select_kernel<true><<<rows, kSelThreads, (size_t)max_len * 4, stream>>>(a);
+    } else {
+        evict_select_kernel<false><<<rows, kSelThreads, 0, stream>>>(a);
+    }
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

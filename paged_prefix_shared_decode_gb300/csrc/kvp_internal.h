@@ -289,7 +289,8 @@ struct EvictLaunch {
     int32_t L, S, Hkv, NB, bs, CH;   // CH: 16-byte chunks per row
     int32_t budget, sink, recent;
 };
-cudaError_t launch_evict(const EvictLaunch &a, bool copies, bool packs, cudaStream_t stream);
+// max_len: the longest sequence.
+cudaError_t launch_evict(const EvictLaunch &a, int max_len, bool copies, bool packs, cudaStream_t stream);
 
 // A descriptor that the attention entry points accept.
 bool attn_desc_ok(const kvp_attn_desc *d);

@@ -417,11 +417,12 @@ int seq_evict(kvp_pool *p, const int32_t *seqs, int32_t n, const float *mass, in
     std::vector<std::vector<int32_t>> pages((size_t)n);   // the new tables
     std::vector<int32_t> taken;
     taken.reserve((size_t)need);
-    int32_t at = 0;
+    int32_t at = 0, max_len = 0;
     bool copies = false, packs = false;
     for (int32_t i = 0; i < n; ++i) {
         const auto &t = p->tables[seqs[i]];
         const int32_t len = p->lens[seqs[i]], keep = (std::min(len, budget) + bs - 1) / bs;
+        max_len = std::max(max_len, len);
         pages[i].assign(t.begin(), t.begin() + keep);
         int32_t how = kvp::kEvictKeep;
         if (len > budget) {
@@ -473,7 +474,7 @@ int seq_evict(kvp_pool *p, const int32_t *seqs, int32_t n, const float *mass, in
     a.stride = mass_stride;
     a.L = d.num_layers; a.S = n; a.Hkv = d.num_kv_heads; a.NB = d.num_blocks; a.bs = bs; a.CH = d.head_dim / 8;
     a.budget = budget; a.sink = n_sink; a.recent = n_recent;
-    return kvp::launch_evict(a, copies, packs, st) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+    return kvp::launch_evict(a, max_len, copies, packs, st) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 } catch (const std::bad_alloc &) {
     return KVP_ERR_OOM;
 }
