@@ -542,7 +542,8 @@ int paged_window_attention(const void *q, const int32_t *q_lens, const void *k_p
  * K is read once, V not at all.  Pages must be bf16; block_tables, seq_lens,
  * desc (use_sharing is not used) and workspace as for
  * paged_decode_attention, ws_bytes >= kvp_mass_workspace_size().  Cached keys
- * must be finite.  KVP_ERR_STATE while `stream` is being captured.
+ * must be finite.  KVP_ERR_INVALID also for layers * kv heads above 65535;
+ * KVP_ERR_STATE while `stream` is being captured.
  */
 size_t kvp_mass_workspace_size(const kvp_attn_desc *desc, const int32_t *block_tables,
                                const int32_t *seq_lens, const int32_t *q_lens, int32_t num_seqs,

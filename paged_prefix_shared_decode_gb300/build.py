@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libkvp.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 SOURCES = ["pool.cpp", "radix.cpp", "plan.cpp", "attn_kernels.cu", "attn_tc.cu", "kv_kernels.cu", "kv4_kernels.cu", "no_alloc.cu",
-           "mass_kernels.cu", "evict_kernels.cu", "draft_verify.cu"]
+           "mass_kernels.cu", "mass_tc.cu", "evict_kernels.cu", "draft_verify.cu"]
 
 
 def _nvcc() -> str:

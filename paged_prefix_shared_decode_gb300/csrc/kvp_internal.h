@@ -251,8 +251,8 @@ struct Kv4Move {
 };
 cudaError_t launch_kv4_move(const Kv4Move &m, cudaStream_t stream);
 
-// Accumulated attention weight per cached token (mass_kernels.cu).
-struct MassSeq {
+// Accumulated attention weight per cached token (mass_kernels.cu, mass_tc.cu).
+struct alignas(16) MassSeq {
     int32_t len, nq, q0;   // cached tokens, query tokens, first query row of q
     int32_t prev;          // tokens whose weight mass_in holds
     int64_t table;         // offset of its block table in tables
@@ -267,10 +267,18 @@ struct MassLaunch {
     int32_t L, S, T, Hq, Hkv, G, D, NB, bs_log2;
     int32_t tiles, chunks;   // set by launch_mass: 128-token steps per CTA, CTAs per sequence
     float scale_log2, decay;
+    // tcgen05 kernel: first tile of each CTA ((layer, kv head), sequence,
+    // position) and how many; the device error word
+    const int4 *starts;
+    int32_t *err;
 };
-// max_len, max_rows: the longest sequence, and the most query rows (queries
-// x GQA group) of one.
-cudaError_t launch_mass(const MassLaunch &a, int max_len, int max_rows, cudaStream_t stream);
+// The kernel for at most 16 query rows (queries x GQA group) a sequence.
+cudaError_t launch_mass(const MassLaunch &a, int max_len, cudaStream_t stream);
+// The tcgen05 kernel: its CTAs' runs of tiles (returns their number, at most
+// ctas_max), whether it can address the pool, the launch.
+int mass_tc_starts(const MassLaunch &a, const MassSeq *seqs, int32_t ctas_max, std::vector<int4> &starts);
+bool mass_tc_fits(const MassLaunch &a);
+cudaError_t launch_mass_tc(const MassLaunch &a, int ctas, cudaStream_t stream);
 
 // Eviction by accumulated weight (evict_kernels.cu).
 enum { kEvictKeep = 0, kEvictCopy = 1, kEvictPack = 2 };   // pages stay; fresh pages; some filled in place

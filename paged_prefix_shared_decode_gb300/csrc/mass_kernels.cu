@@ -16,10 +16,9 @@
 // by HBM needs.  Every row of scores is turned into weights and added up in
 // registers; the sum over the rows ends in a transposing reduction that
 // leaves lane x with token x, so the store is one 128-byte line.
-//   - at most 16 query rows (a decode step): Q's fragments stay in registers
-//     and the warp walks `tiles` groups of 32 tokens with them;
-//   - more rows (a prompt's last queries): 64 rows at a time go through
-//     shared memory and serve the CTA's four warps.
+// This kernel takes at most 16 query rows a sequence (a decode step), whose
+// fragments stay in registers while the warp walks `tiles` groups of 32
+// tokens; more rows go to the tcgen05 kernel (mass_tc.cu).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,8 +37,9 @@ namespace {
 
 constexpr int kMassWarps = 4;
 constexpr int kMassTok = 32;    // tokens per warp and step
-constexpr int kStageRows = 64;  // query rows in shared memory
 
+// (volatile: products in program order leave the tile's loads ahead of them;
+// reordered ones measured 255 instead of 219 us over 32 x about 9000 tokens)
 __device__ __forceinline__ void mass_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -51,18 +51,6 @@ __device__ __forceinline__ float mass_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
-}
-
-// 16 bytes.  This and the products are volatile, so that a warp's loads are
-// all issued before its first product (left to itself the compiler sinks them
-// to their use, which measured 255 instead of 220 us over 32 sequences of
-// about 9000 tokens).
-__device__ __forceinline__ uint4 load16(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
 }
 
 // K rows of 32 tokens: group g (8 tokens), chunk c (32 dims) of lane (t, j).
@@ -89,7 +77,7 @@ __device__ __forceinline__ void load_k(KTile<D> &kt, const MassLaunch &a, const 
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             kt.k[g][c] = make_uint4(0u, 0u, 0u, 0u);
-            if (in) kt.k[g][c] = load16(src + 32 * c);
+            if (in) kt.k[g][c] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * c));
         }
     }
 }
@@ -117,18 +105,14 @@ __device__ __forceinline__ void add_tile(float (&acc)[8], const KTile<D> &kt, co
     const int j2 = 2 * (lane & 3);
     // warps whose every row sees all 32 tokens skip the selects
     const bool whole = __all_sync(0xffffffffu, n0 >= kMassTok && n1 >= kMassTok);
-    // four independent accumulators, so that the products overlap
-    float sg[4][4] = {};
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) mass_mma(sg[g], qf[2 * c], kt.k[g][c].x, kt.k[g][c].y);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) mass_mma(sg[g], qf[2 * c + 1], kt.k[g][c].z, kt.k[g][c].w);
-    }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        const float(&s)[4] = sg[g];
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            mass_mma(s, qf[2 * c], kt.k[g][c].x, kt.k[g][c].y);
+            mass_mma(s, qf[2 * c + 1], kt.k[g][c].z, kt.k[g][c].w);
+        }
         float e[4] = {mass_exp2(fmaf(s[0], sc, -l0)), mass_exp2(fmaf(s[1], sc, -l0)), mass_exp2(fmaf(s[2], sc, -l1)),
                       mass_exp2(fmaf(s[3], sc, -l1))};
         if (!whole) {   // selects: a masked score may be anything
@@ -174,7 +158,7 @@ __device__ __forceinline__ void store_mass(const MassLaunch &a, size_t row, int 
     a.mass_out[row + pos] = v;
 }
 
-template <int D, bool FEW>
+template <int D>
 __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(const MassLaunch a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
@@ -198,94 +182,49 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(const MassLaunch 
         const float v = r < rows ? a.lse[row_of(r)] : INFINITY;
         return v == -INFINITY ? INFINITY : v * 1.4426950408889634f;
     };
-    if constexpr (FEW) {
-        uint4 x0[D / 32], x1[D / 32];
+    uint4 x0[D / 32], x1[D / 32];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            x0[c] = x1[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (t < rows) x0[c] = __ldg(reinterpret_cast<const uint4 *>(qb + row_of(t) * D + 32 * c + 8 * j));
-            if (t + 8 < rows) x1[c] = __ldg(reinterpret_cast<const uint4 *>(qb + row_of(t + 8) * D + 32 * c + 8 * j));
-        }
-        uint32_t qf[D / 16][4];
-        q_frags<D>(qf, x0, x1);
-        const float l0 = lse2(t), l1 = lse2(t + 8);
-        const int see0 = t < rows ? sq.len - sq.nq + t / G + 1 : 0;
-        const int see1 = t + 8 < rows ? sq.len - sq.nq + (t + 8) / G + 1 : 0;
-        for (int i = 0; i < a.tiles; ++i) {
-            const int pos0 = first + (i * kMassWarps + warp) * kMassTok;
-            if (pos0 >= sq.len) break;
-            KTile<D> kt;
-            load_k<D>(kt, a, table, pos0, sq.len, head_base, lane);
-            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            add_tile<D>(acc, kt, qf, sc, l0, l1, see0 - pos0, see1 - pos0, lane);
-            store_mass(a, out_row, pos0 + lane, sq.len, sq.prev, spread(acc, lane));
-        }
-    } else {
-        // staged rows: chunk c of a row's 32-dim chunks, 16 bytes per j, in
-        // the order the lanes read them
-        __shared__ uint4 s_q[kStageRows][D / 8];
-        __shared__ float s_l[kStageRows];
-        const int pos0 = first + warp * kMassTok;
+    for (int c = 0; c < D / 32; ++c) {
+        x0[c] = x1[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < rows) x0[c] = __ldg(reinterpret_cast<const uint4 *>(qb + row_of(t) * D + 32 * c + 8 * j));
+        if (t + 8 < rows) x1[c] = __ldg(reinterpret_cast<const uint4 *>(qb + row_of(t + 8) * D + 32 * c + 8 * j));
+    }
+    uint32_t qf[D / 16][4];
+    q_frags<D>(qf, x0, x1);
+    const float l0 = lse2(t), l1 = lse2(t + 8);
+    const int see0 = t < rows ? sq.len - sq.nq + t / G + 1 : 0;
+    const int see1 = t + 8 < rows ? sq.len - sq.nq + (t + 8) / G + 1 : 0;
+    for (int i = 0; i < a.tiles; ++i) {
+        const int pos0 = first + (i * kMassWarps + warp) * kMassTok;
+        if (pos0 >= sq.len) break;
         KTile<D> kt;
         load_k<D>(kt, a, table, pos0, sq.len, head_base, lane);
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int r0 = 0; r0 < rows; r0 += kStageRows) {
-            // rows whose query sees none of the CTA's tokens are skipped
-            if (sq.len - sq.nq + min(rows - 1, r0 + kStageRows - 1) / G < first) continue;
-            __syncthreads();
-            for (int x = threadIdx.x; x < kStageRows * (D / 8); x += 32 * kMassWarps) {
-                const int r = x / (D / 8), c = x % (D / 8);
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (r0 + r < rows) v = __ldg(reinterpret_cast<const uint4 *>(qb + row_of(r0 + r) * D + 8 * c));
-                s_q[r][c ^ (r & 7)] = v;
-            }
-            if (threadIdx.x < kStageRows) s_l[threadIdx.x] = lse2(r0 + threadIdx.x);
-            __syncthreads();
-            if (pos0 >= sq.len) continue;
-#pragma unroll 1
-            for (int b = 0; b < kStageRows && r0 + b < rows; b += 16) {
-                const int ra = r0 + b + t, rb = ra + 8;
-                const int see0 = ra < rows ? sq.len - sq.nq + ra / G + 1 - pos0 : 0;
-                const int see1 = rb < rows ? sq.len - sq.nq + rb / G + 1 - pos0 : 0;
-                if (!__any_sync(0xffffffffu, see0 > 0 || see1 > 0)) continue;
-                uint4 x0[D / 32], x1[D / 32];
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    x0[c] = s_q[b + t][(4 * c + j) ^ (t & 7)];
-                    x1[c] = s_q[b + t + 8][(4 * c + j) ^ (t & 7)];
-                }
-                uint32_t qf[D / 16][4];
-                q_frags<D>(qf, x0, x1);
-                add_tile<D>(acc, kt, qf, sc, s_l[b + t], s_l[b + t + 8], see0, see1, lane);
-            }
-        }
+        add_tile<D>(acc, kt, qf, sc, l0, l1, see0 - pos0, see1 - pos0, lane);
         store_mass(a, out_row, pos0 + lane, sq.len, sq.prev, spread(acc, lane));
     }
 }
 
 template <int D>
-cudaError_t launch_mass_d(MassLaunch a, int max_len, int max_rows, cudaStream_t stream) {
-    const bool few = max_rows <= 16;
+cudaError_t launch_mass_d(MassLaunch a, int max_len, cudaStream_t stream) {
     const int step = kMassWarps * kMassTok;
     const int64_t tiles = ((int64_t)max_len + step - 1) / step;
-    // a CTA of few rows walks several tiles of tokens once there are CTAs
-    // enough to fill the GPU eight times over
+    // a CTA walks several tiles of tokens once there are CTAs enough to fill
+    // the GPU eight times over (one each measured 313 instead of 255 us)
     const int64_t ctas = tiles * a.S * a.L * a.Hkv;
-    a.tiles = few ? (int)std::max<int64_t>(1, std::min<int64_t>(8, ctas / (8LL * 8 * device_sm_count()))) : 1;
+    a.tiles = (int)std::max<int64_t>(1, std::min<int64_t>(8, ctas / (8LL * 8 * device_sm_count())));
     a.chunks = (int)((tiles + a.tiles - 1) / a.tiles);
     if ((int64_t)a.chunks * a.S > INT32_MAX) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)(a.chunks * a.S), (unsigned)(a.L * a.Hkv));
-    if (few) mass_kernel<D, true><<<grid, 32 * kMassWarps, 0, stream>>>(a);
-    else mass_kernel<D, false><<<grid, 32 * kMassWarps, 0, stream>>>(a);
+    mass_kernel<D><<<dim3((unsigned)(a.chunks * a.S), (unsigned)(a.L * a.Hkv)), 32 * kMassWarps, 0, stream>>>(a);
     count_launch();
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_mass(const MassLaunch &a, int max_len, int max_rows, cudaStream_t stream) {
-    if (a.D == 64) return launch_mass_d<64>(a, max_len, max_rows, stream);
-    if (a.D == 128) return launch_mass_d<128>(a, max_len, max_rows, stream);
+cudaError_t launch_mass(const MassLaunch &a, int max_len, cudaStream_t stream) {
+    if (a.D == 64) return launch_mass_d<64>(a, max_len, stream);
+    if (a.D == 128) return launch_mass_d<128>(a, max_len, stream);
     return cudaErrorInvalidValue;
 }
 
@@ -296,11 +235,11 @@ using namespace kvp;
 namespace {
 
 struct MassLayout {
-    size_t seqs, tables, total;
+    size_t seqs, starts, tables, total;
 };
 
 // Checks the batch and lays out its image: a zero header (the error word),
-// the sequences, then their block tables.
+// the sequences, a start per SM, then the sequences' block tables.
 bool mass_layout(const kvp_attn_desc &d, const int32_t *tables, const int32_t *lens, const int32_t *q_lens, int32_t S,
                  int32_t MB, MassLayout &w) {
     int64_t blocks = 0, rows = 0;
@@ -316,12 +255,23 @@ bool mass_layout(const kvp_attn_desc &d, const int32_t *tables, const int32_t *l
         blocks += nb;
         rows += nq;
     }
-    if (rows > INT32_MAX / 2) return false;
+    // (query rows of one kv head, and 128-token tiles over all of them, are
+    // counted in 32 bits)
+    if (rows * d.num_q_heads > INT32_MAX / 2 ||
+        (blocks + S) * (d.block_size / 16) * d.num_layers * d.num_kv_heads > INT32_MAX)
+        return false;
     w.seqs = 256;
-    w.tables = (w.seqs + sizeof(MassSeq) * (size_t)S + 255) & ~(size_t)255;
+    w.starts = (w.seqs + sizeof(MassSeq) * (size_t)S + 255) & ~(size_t)255;
+    w.tables = (w.starts + sizeof(int4) * (size_t)device_sm_count() + 255) & ~(size_t)255;
     w.total = (w.tables + sizeof(int32_t) * (size_t)blocks + 255) & ~(size_t)255;
     return true;
 }
+
+// More than 16 query rows go to the tcgen05 kernel (256 rows over 2 x about
+// 7000 tokens: 20 us; the same rows as 16-row tiles on mma.sync took 62 us).
+// Up to 16 the register kernel is faster (4 rows over 32 x about 9000 tokens:
+// 219 us against 260 us) and starts sooner.
+bool use_tc(const MassLaunch &a, int32_t max_q) { return (int64_t)max_q * a.G > 16; }
 
 bool mass_args_ok(const kvp_attn_desc *d, const int32_t *tables, const int32_t *lens, int32_t S, int32_t MB) {
     return attn_desc_ok(d) && d->kv_format == KVP_KV_BF16 && (int64_t)d->num_layers * d->num_kv_heads <= 65535 &&
@@ -369,6 +319,28 @@ int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, c
     cudaStream_t st = (cudaStream_t)stream;
     if (stream_capturing(st)) return KVP_ERR_STATE;
     if (max_len == 0) return KVP_OK;
+    const unsigned char *base = static_cast<const unsigned char *>(workspace);
+    MassLaunch a{};
+    a.q = q;
+    a.k_pool = k_pool;
+    a.lse = lse;
+    a.mass_in = mass_in;
+    a.mass_out = mass_out;
+    a.seqs = reinterpret_cast<const MassSeq *>(base + w.seqs);
+    a.starts = reinterpret_cast<const int4 *>(base + w.starts);
+    a.tables = reinterpret_cast<const int32_t *>(base + w.tables);
+    a.err = reinterpret_cast<int32_t *>(workspace);
+    a.stride = mass_stride;
+    a.L = desc->num_layers; a.S = S; a.T = (int32_t)T;
+    a.Hq = desc->num_q_heads; a.Hkv = desc->num_kv_heads; a.G = desc->num_q_heads / desc->num_kv_heads;
+    a.D = desc->head_dim; a.NB = desc->num_blocks;
+    while ((1 << a.bs_log2) < bs) ++a.bs_log2;
+    const float scale = desc->scale > 0.f ? desc->scale : 1.0f / std::sqrt((float)desc->head_dim);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.decay = decay;
+    const bool tc = use_tc(a, max_q);
+    if (tc && !mass_tc_fits(a)) return KVP_ERR_INVALID;
+    int ctas = 0;
     try {
         thread_local std::vector<unsigned char> image;
         image.assign(w.total, 0);
@@ -384,32 +356,19 @@ int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, c
             at += nb;
             q0 += nq;
         }
+        if (tc) {
+            thread_local std::vector<int4> starts;
+            ctas = mass_tc_starts(a, seqs, device_sm_count(), starts);
+            std::copy(starts.begin(), starts.end(), reinterpret_cast<int4 *>(image.data() + w.starts));
+        }
         // pageable source: the copy is staged before the call returns
         if (cudaMemcpyAsync(workspace, image.data(), w.total, cudaMemcpyHostToDevice, st) != cudaSuccess)
             return KVP_ERR_CUDA;
     } catch (const std::bad_alloc &) {
         return KVP_ERR_OOM;
     }
-    const unsigned char *base = static_cast<const unsigned char *>(workspace);
-    MassLaunch a{};
-    a.q = q;
-    a.k_pool = k_pool;
-    a.lse = lse;
-    a.mass_in = mass_in;
-    a.mass_out = mass_out;
-    a.seqs = reinterpret_cast<const MassSeq *>(base + w.seqs);
-    a.tables = reinterpret_cast<const int32_t *>(base + w.tables);
-    a.stride = mass_stride;
-    a.L = desc->num_layers; a.S = S; a.T = (int32_t)T;
-    a.Hq = desc->num_q_heads; a.Hkv = desc->num_kv_heads; a.G = desc->num_q_heads / desc->num_kv_heads;
-    a.D = desc->head_dim; a.NB = desc->num_blocks;
-    while ((1 << a.bs_log2) < bs) ++a.bs_log2;
-    const float scale = desc->scale > 0.f ? desc->scale : 1.0f / std::sqrt((float)desc->head_dim);
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.decay = decay;
-    const int64_t max_rows = (int64_t)max_q * a.G;
-    return launch_mass(a, max_len, (int)std::min<int64_t>(max_rows, INT32_MAX), st) == cudaSuccess ? KVP_OK
-                                                                                                  : KVP_ERR_CUDA;
+    const cudaError_t e = tc ? launch_mass_tc(a, ctas, st) : launch_mass(a, max_len, st);
+    return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 }  // extern "C"
