@@ -225,6 +225,27 @@ __device__ __forceinline__ void p_pass(uint32_t s_tm, float nm, float sc, int nv
         }
     }
 }
+// The same for a step whose scores are all valid: no masks, and each 32
+// columns of S are loaded while the 32 before them are turned into P.
+__device__ __forceinline__ void p_pass_whole(uint32_t s_tm, float nm, float sc, uint32_t (&pk)[64], float &ls) {
+    uint32_t x[32], y[32];
+    tmem_ld32(s_tm, x);
+    tmem_wait_ld();
+    tmem_ld32(s_tm + 32, y);
+    exp_pack16<false>(x, 0, sc, nm, 0, pk, ls);
+    exp_pack16<false>(x, 16, sc, nm, 0, pk + 8, ls);
+    tmem_wait_ld();
+    tmem_ld32(s_tm + 64, x);
+    exp_pack16<false>(y, 0, sc, nm, 0, pk + 16, ls);
+    exp_pack16<false>(y, 16, sc, nm, 0, pk + 24, ls);
+    tmem_wait_ld();
+    tmem_ld32(s_tm + 96, y);
+    exp_pack16<false>(x, 0, sc, nm, 0, pk + 32, ls);
+    exp_pack16<false>(x, 16, sc, nm, 0, pk + 40, ls);
+    tmem_wait_ld();
+    exp_pack16<false>(y, 0, sc, nm, 0, pk + 48, ls);
+    exp_pack16<false>(y, 16, sc, nm, 0, pk + 56, ls);
+}
 // P overwrites the first 64 S columns (all scores are read by then)
 __device__ __forceinline__ void p_store(uint32_t s_tm, const uint32_t (&pk)[64]) {
     tmem_st32(s_tm, *reinterpret_cast<const uint32_t(*)[32]>(pk));
@@ -641,135 +662,147 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // the whole warp, converged; one elected lane issues
+        {
             constexpr uint32_t IDESC_S = idesc_bf16(128, kStepTokens, false);
             constexpr uint32_t IDESC_PV = idesc_bf16(128, D, true);
+            const uint32_t lead = elect_one();
+            auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, wait(b, parity));
+            };
             uint32_t gk = 0, gv = 0;        // steps taken from the K / V rings
             uint32_t np0 = 0, np1 = 0;      // P_FULL phases consumed per group
             for (int uc = 0;; ++uc) {
                 const int slot = uc & 1;
-                if (!wait(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1)) break;
-                const int unit = s_unit[slot];
+                if (!wait_all(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1)) break;
+                const int unit = uniform(s_unit[slot]);
                 if (unit < 0) break;
                 const WorkItem it = a.tc_items[unit % n_items];
-                const int ntile = item_tiles<WIN>(it);
+                const int ntile = uniform(item_tiles<WIN>(it));
                 const int nsteps = (ntile + 1) >> 1;
-                const bool pair = it.n_members * G > 128;
-                bool ok = wait(bar(C::B_Q_FULL), uc & 1);
+                const bool pair = uniform(it.n_members * G) > 128;
+                bool ok = wait_all(bar(C::B_Q_FULL), uc & 1);
                 // Q was written through the generic proxy (cp.async)
                 fence_async_smem();
                 tc_after();
-                auto issue_s = [&](int t) -> bool {
+                // Waits for K of step t / V of step t.  Both are made well
+                // ahead of the products that need them: a wait costs this
+                // thread 100 to 250 cycles even when there is nothing to wait
+                // for, and the tensor cores' queue holds only a few products,
+                // so between P's arrival and the products nothing else may
+                // stand (8192 queries over a 4096 window: 510 to 486 us; the
+                // converged issue brought it to 399).
+                auto wait_k = [&](int t) -> bool {
                     const uint32_t g = gk + t, st = g % C::NK;
-                    if (!wait(bar(C::B_K_FULL + st), (g / C::NK) & 1)) return false;
+                    if (!wait_all(bar(C::B_K_FULL + st), (g / C::NK) & 1)) return false;
                     fence_async_smem();
                     tc_after();
-                    const uint32_t kst = k_smem + st * C::OPER;
-                    const uint32_t d_tm = tmem + C::S_COL + (t & 1) * kStepTokens;
-                    const uint64_t qd = sdesc(q_smem, 16, 1024), kd = sdesc(kst, 16, 1024);
+                    return true;
+                };
+                auto wait_v = [&](int t) -> bool {
+                    const uint32_t g = gv + t, st = g % C::NV;
+                    if (!wait_all(bar(C::B_V_FULL + st), (g / C::NV) & 1)) return false;
+                    fence_async_smem();
+                    tc_after();
+                    return true;
+                };
+                // S of step t for query tile tq into S buffer b
+                auto issue_s = [&](int t, int tq, int b) {
+                    const uint32_t st = (gk + t) % C::NK;
+                    const uint32_t kst = k_smem + st * C::OPER, qs = q_smem + tq * C::OPER;
+                    const uint32_t d_tm = tmem + C::S_COL + b * kStepTokens;
+                    const uint64_t qd = sdesc(qs, 16, 1024), kd = sdesc(kst, 16, 1024);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t o = ((uint32_t)(k >> 2) * C::SLAB + (uint32_t)(k & 3) * 32) >> 4;
-                        umma_ss(d_tm, qd + o, kd + o, IDESC_S, k > 0 ? 1u : 0u);
+                        umma_ss(d_tm, qd + o, kd + o, IDESC_S, k > 0 ? 1u : 0u, lead);
                     }
-                    umma_commit(bar(C::B_S_FULL + (t & 1)));
-                    umma_commit(bar(C::B_K_EMPTY + st));
+                    umma_commit(bar(C::B_S_FULL + b), lead);
+                };
+                auto free_k = [&](int t) { umma_commit(bar(C::B_K_EMPTY + (gk + t) % C::NK), lead); };
+                // O_b += P_b V of step t
+                auto issue_pv = [&](int t, int b, bool first) {
+                    const uint32_t st = (gv + t) % C::NV;
+                    const uint64_t vd = sdesc(v_smem + st * C::OPER, C::SLAB, 1024);
+                    const uint32_t o_tm = tmem + C::O_COL + b * D, p_tm = tmem + C::S_COL + b * kStepTokens;
+                    // an odd last tile leaves rows 64..127 of V unwritten: skip them
+                    const int ksteps = 2 * t + 1 < ntile ? kStepTokens / 16 : kTileTokens / 16;
+#pragma unroll
+                    for (int k = 0; k < kStepTokens / 16; ++k)
+                        if (k < ksteps)
+                            umma_ts(o_tm, p_tm + k * 8, vd + k * (2048 >> 4), IDESC_PV, !first || k > 0 ? 1u : 0u, lead);
+                };
+                auto free_v = [&](int t) { umma_commit(bar(C::B_V_EMPTY + (gv + t) % C::NV), lead); };
+                auto wait_p = [&](int b) -> bool {
+                    if (!wait_all(bar(C::B_P_FULL + b), (b ? np1 : np0) & 1)) return false;
+                    if (b) ++np1; else ++np0;
+                    tc_after();
                     return true;
                 };
                 if (pair) {
                     // Two 128-row tiles over the same K/V: each step serves both,
                     // S_g and O_g belong to tile g, and group g takes every step.
-                    auto wait_k = [&](int t) -> bool {
-                        const uint32_t g = gk + t, st = g % C::NK;
-                        if (!wait(bar(C::B_K_FULL + st), (g / C::NK) & 1)) return false;
-                        fence_async_smem();
-                        tc_after();
-                        return true;
-                    };
-                    auto issue_sp = [&](int t, int tq) {
-                        const uint32_t st = (gk + t) % C::NK;
-                        const uint32_t kst = k_smem + st * C::OPER, qs = q_smem + tq * C::OPER;
-                        const uint32_t d_tm = tmem + C::S_COL + tq * kStepTokens;
-                        const uint64_t qd = sdesc(qs, 16, 1024), kd = sdesc(kst, 16, 1024);
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t o = ((uint32_t)(k >> 2) * C::SLAB + (uint32_t)(k & 3) * 32) >> 4;
-                            umma_ss(d_tm, qd + o, kd + o, IDESC_S, k > 0 ? 1u : 0u);
-                        }
-                        umma_commit(bar(C::B_S_FULL + tq));
-                        if (tq == 1) umma_commit(bar(C::B_K_EMPTY + st));
-                    };
                     if (ok && nsteps > 0) {
                         ok = wait_k(0);
                         if (ok) {
-                            issue_sp(0, 0);
-                            issue_sp(0, 1);
+                            issue_s(0, 0, 0);
+                            issue_s(0, 1, 1);
+                            free_k(0);
                         }
                     }
-                    if (ok) ok = wait(bar(C::B_O_EMPTY), (uc & 1) ^ 1);
+                    if (ok) ok = wait_all(bar(C::B_O_EMPTY), (uc & 1) ^ 1);
                     tc_after();
+                    if (ok && nsteps > 0) ok = wait_v(0);
+                    if (ok && nsteps > 1) ok = wait_k(1);
                     for (int t = 0; ok && t < nsteps; ++t) {
-                        const uint32_t g = gv + t, st = g % C::NV;
-                        const uint32_t vst = v_smem + st * C::OPER;
-                        const int ksteps = 2 * t + 1 < ntile ? kStepTokens / 16 : kTileTokens / 16;
                         for (int tq = 0; ok && tq < 2; ++tq) {
-                            if (!wait(bar(C::B_P_FULL + tq), (tq ? np1 : np0) & 1)) { ok = false; break; }
-                            if (tq) ++np1; else ++np0;
-                            if (tq == 0 && !wait(bar(C::B_V_FULL + st), (g / C::NV) & 1)) { ok = false; break; }
-                            if (tq == 0) fence_async_smem();
-                            tc_after();
-                            const uint64_t vd = sdesc(vst, C::SLAB, 1024);
-                            const uint32_t o_tm = tmem + C::O_COL + tq * D, p_tm = tmem + C::S_COL + tq * kStepTokens;
-#pragma unroll
-                            for (int k = 0; k < kStepTokens / 16; ++k)
-                                if (k < ksteps)
-                                    umma_ts(o_tm, p_tm + k * 8, vd + k * (2048 >> 4), IDESC_PV,
-                                            (t > 0 || k > 0) ? 1u : 0u);
-                            if (tq == 1) umma_commit(bar(C::B_V_EMPTY + st));
-                            if (t + 1 < nsteps) {
-                                if (tq == 0 && !wait_k(t + 1)) { ok = false; break; }
-                                issue_sp(t + 1, tq);
-                            }
+                            ok = wait_p(tq);
+                            if (!ok) break;
+                            issue_pv(t, tq, t == 0);
+                            if (t + 1 < nsteps) issue_s(t + 1, tq, tq);
                         }
+                        if (!ok) break;
+                        free_v(t);
+                        if (t + 1 < nsteps) {
+                            free_k(t + 1);
+                            ok = wait_v(t + 1);
+                        }
+                        if (ok && t + 2 < nsteps) ok = wait_k(t + 2);
                     }
                 } else {
-                if (ok && nsteps > 0) ok = issue_s(0);
-                if (ok && nsteps > 1) ok = issue_s(1);
-                // the previous unit's epilogue has read O_0 and O_1
-                if (ok) ok = wait(bar(C::B_O_EMPTY), (uc & 1) ^ 1);
-                tc_after();
-                for (int t = 0; ok && t < nsteps; ++t) {
-                    const int grp = t & 1;
-                    if (!wait(bar(C::B_P_FULL + grp), (grp ? np1 : np0) & 1)) { ok = false; break; }
-                    if (grp) ++np1; else ++np0;
-                    const uint32_t g = gv + t, st = g % C::NV;
-                    if (!wait(bar(C::B_V_FULL + st), (g / C::NV) & 1)) { ok = false; break; }
-                    fence_async_smem();
+                    for (int t = 0; ok && t < 2 && t < nsteps; ++t) {
+                        ok = wait_k(t);
+                        if (!ok) break;
+                        issue_s(t, 0, t & 1);
+                        free_k(t);
+                    }
+                    // the previous unit's epilogue has read O_0 and O_1
+                    if (ok) ok = wait_all(bar(C::B_O_EMPTY), (uc & 1) ^ 1);
                     tc_after();
-                    const uint32_t vst = v_smem + st * C::OPER;
-                    // an odd last tile leaves rows 64..127 of V unwritten: skip them
-                    const int ksteps = 2 * t + 1 < ntile ? kStepTokens / 16 : kTileTokens / 16;
-                    const uint64_t vd = sdesc(vst, C::SLAB, 1024);
-                    const uint32_t o_tm = tmem + C::O_COL + grp * D, p_tm = tmem + C::S_COL + grp * kStepTokens;
-#pragma unroll
-                    for (int k = 0; k < kStepTokens / 16; ++k)
-                        if (k < ksteps)
-                            umma_ts(o_tm, p_tm + k * 8, vd + k * (2048 >> 4), IDESC_PV, (t >= 2 || k > 0) ? 1u : 0u);
-                    umma_commit(bar(C::B_V_EMPTY + st));
-                    if (t + 2 < nsteps && !issue_s(t + 2)) { ok = false; break; }
-                }
+                    if (ok && nsteps > 0) ok = wait_v(0);
+                    if (ok && nsteps > 2) ok = wait_k(2);
+                    for (int t = 0; ok && t < nsteps; ++t) {
+                        ok = wait_p(t & 1);
+                        if (!ok) break;
+                        issue_pv(t, t & 1, t < 2);
+                        if (t + 2 < nsteps) issue_s(t + 2, 0, t & 1);
+                        free_v(t);
+                        if (t + 2 < nsteps) free_k(t + 2);
+                        if (t + 1 < nsteps) ok = wait_v(t + 1);
+                        if (ok && t + 3 < nsteps) ok = wait_k(t + 3);
+                    }
                 }
                 if (!ok) break;
                 // (with steps, the softmax thread that sees the unit's last S
                 // releases Q)
-                if (nsteps == 0) umma_commit(bar(C::B_Q_EMPTY));
+                if (nsteps == 0) umma_commit(bar(C::B_Q_EMPTY), lead);
                 gk += nsteps;
                 gv += nsteps;
-                umma_commit(bar(C::B_O_FULL));
-                mbar_arrive(bar(C::B_UNIT_EMPTY + slot));
+                umma_commit(bar(C::B_O_FULL), lead);
+                if (lead) mbar_arrive(bar(C::B_UNIT_EMPTY + slot));
             }
-            // every MMA this thread issued completes before TMEM is freed
-            umma_commit(bar(C::B_DRAIN));
+            // every MMA that was issued completes before TMEM is freed
+            umma_commit(bar(C::B_DRAIN), lead);
             settle(bar(C::B_DRAIN), 0);
         }
         __syncwarp();
@@ -806,6 +839,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (has) qt = __ldg(a.members + it.member_off + mem);
             const uint64_t tmask = !WIN && has && a.tree_mask ? a.tree_mask[qt] : ~0ull;
             const int pos = WIN && has ? __ldg(a.q_pos + qt) : 0;
+            int pos_lo = 0, pos_hi = 0;   // over the warp's rows
+            if (WIN) {
+                pos_lo = __reduce_min_sync(0xffffffffu, has ? pos : INT32_MAX);
+                pos_hi = __reduce_max_sync(0xffffffffu, has ? pos : INT32_MIN);
+            }
             // a warp none of whose 32 rows is in the unit (a half-filled
             // 128-row tile) only keeps the group's barriers: the rows of P it
             // would write are never read back into an output row, since every
@@ -814,6 +852,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
             float m = -INFINITY, lsum = 0.f;
             for (int t = pair ? 0 : grp; t < nsteps; t += pair ? 1 : 2) {
+                // what the rows see of the step's two tiles, while S is on its way
+                int nv0 = 0, nv1 = 0;
+                bool tr0 = false, tr1 = false;
+                uint64_t m0 = tmask, m1 = tmask;
+                const KvTile &k0 = tiles[2 * t], &k1 = tiles[2 * t + 1 < ntile ? 2 * t + 1 : 2 * t];
+                auto seen = [&](const KvTile &k) {   // the row's keys of a tile, before any mask
+                    return has && mem >= (k.members & 0xFFFF) && mem < k.members >> 16 ? (k.ntok_flags & 0xFFFF) : 0;
+                };
+                // WIN: a step inside the windows of all the warp's rows needs no
+                // masks; otherwise the masks alone say what is valid
+                bool whole = false;
+                if (WIN) {
+                    auto inside = [&](const KvTile &k) {
+                        return (k.ntok_flags & 0xFFFF) == kTileTokens && (k.members & 0xFFFF) == 0 &&
+                               k.members >> 16 >= it.n_members && k.tok0 + kTileTokens - 1 <= pos_lo &&
+                               (k.tok0 > pos_hi - a.win || k.tok0 + kTileTokens <= a.sinks);
+                    };
+                    whole = 2 * t + 1 < ntile && inside(k0) && inside(k1);
+                    if (!whole) {
+                        const int n0 = seen(k0), n1 = 2 * t + 1 < ntile ? seen(k1) : 0;
+                        m0 = n0 > 0 ? window_bits(k0.tok0, n0, pos, a.win, a.sinks) : 0ull;
+                        m1 = n1 > 0 ? window_bits(k1.tok0, n1, pos, a.win, a.sinks) : 0ull;
+                        tr0 = tr1 = true;
+                    }
+                    nv0 = nv1 = kTileTokens;
+                } else {
+                    nv0 = seen(k0);
+                    tr0 = (k0.ntok_flags >> 16) & kTileTree;
+                    if (2 * t + 1 < ntile) {
+                        nv1 = seen(k1);
+                        tr1 = (k1.ntok_flags >> 16) & kTileTree;
+                    }
+                }
                 ok = wait(bar(C::B_S_FULL + grp), ns & 1) && ok;
                 ns += 1;
                 // the unit's last S is done with Q: one thread of the group
@@ -827,29 +898,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_before();
                     mbar_arrive(bar(C::B_P_FULL + grp));
                     continue;
-                }
-                int nv0 = 0, nv1 = 0;
-                bool tr0 = false, tr1 = false;
-                uint64_t m0 = tmask, m1 = tmask;
-                {
-                    const KvTile &k0 = tiles[2 * t];
-                    const int mlo = k0.members & 0xFFFF, mhi = k0.members >> 16;
-                    nv0 = has && mem >= mlo && mem < mhi ? (k0.ntok_flags & 0xFFFF) : 0;
-                    tr0 = (k0.ntok_flags >> 16) & kTileTree;
-                    if (WIN) m0 = nv0 > 0 ? window_bits(k0.tok0, nv0, pos, a.win, a.sinks) : 0ull;
-                }
-                if (2 * t + 1 < ntile) {
-                    const KvTile &k1 = tiles[2 * t + 1];
-                    const int mlo = k1.members & 0xFFFF, mhi = k1.members >> 16;
-                    nv1 = has && mem >= mlo && mem < mhi ? (k1.ntok_flags & 0xFFFF) : 0;
-                    tr1 = (k1.ntok_flags >> 16) & kTileTree;
-                    if (WIN) m1 = nv1 > 0 ? window_bits(k1.tok0, nv1, pos, a.win, a.sinks) : 0ull;
-                } else if (WIN) {
-                    m1 = 0ull;
-                }
-                if (WIN) {   // the masks alone say what is valid
-                    nv0 = nv1 = kTileTokens;
-                    tr0 = tr1 = true;
                 }
                 // A row's running max m is raised only when the step's P would
                 // sum to more than 2^32, so every p <= 2^32, well inside bf16
@@ -865,8 +913,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 float ls = 0.f;
                 uint32_t pk[64];
-                p_pass(s_tm, m == -INFINITY ? 0.f : -m, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
-                const bool some = WIN ? (m0 | m1) != 0 : nv0 > 0 || nv1 > 0;
+                if (WIN && whole) p_pass_whole(s_tm, m == -INFINITY ? 0.f : -m, sc, pk, ls);
+                else p_pass(s_tm, m == -INFINITY ? 0.f : -m, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
+                const bool some = WIN ? (whole ? has : (m0 | m1) != 0) : nv0 > 0 || nv1 > 0;
                 const bool bad = m == -INFINITY ? some : !(ls <= kSlackSum);
                 if (!__any_sync(0xffffffffu, bad)) {
                     p_store(s_tm, pk);

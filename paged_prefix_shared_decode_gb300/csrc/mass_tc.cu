@@ -215,36 +215,38 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            uint32_t i = 0, steps[2] = {0, 0};
-            bool ok = true;
-            for (; ok && w.left > 0; w.next(), ++i) {
-                const int st = i % C::NK;
-                ok = wait(bar(C::B_K_FULL + st), (i / C::NK) & 1);
-                uint32_t step = i & 1 ? steps[1] : steps[0];
-                for (int c = w.c0; ok && c < w.c1; ++c, ++step) {
-                    const int b = c & 1, sb = 2 * (i & 1) + (step & 1);
-                    ok = wait(bar(C::B_Q_FULL + sb), (step >> 1) & 1);
-                    if (ok) ok = wait(bar(C::B_S_EMPTY + sb), ((step >> 1) & 1) ^ 1);
-                    if (!ok) break;
-                    fence_async_smem();   // Q came through the generic proxy (cp.async)
-                    tc_after();
-                    const int n = min(kChunk, w.rows - c * kChunk);
-                    const uint32_t idesc = idesc_bf16(kTok, max(16, (n + 15) & ~15), false);
-                    const uint64_t kd = sdesc(k_smem + st * C::OPER, 16, 1024), qd = sdesc(q_smem + b * C::OPER, 16, 1024);
+        // the whole warp, converged; one elected lane issues
+        const uint32_t lead = elect_one();
+        auto wait_all = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
+        uint32_t i = 0, steps[2] = {0, 0};
+        bool ok = true;
+        for (; ok && w.left > 0; w.next(), ++i) {
+            const int st = i % C::NK;
+            ok = wait_all(bar(C::B_K_FULL + st), (i / C::NK) & 1);
+            uint32_t step = i & 1 ? steps[1] : steps[0];
+            const int c1 = uniform(w.c1), rows = uniform(w.rows);
+            for (int c = uniform(w.c0); ok && c < c1; ++c, ++step) {
+                const int b = c & 1, sb = 2 * (i & 1) + (step & 1);
+                ok = wait_all(bar(C::B_Q_FULL + sb), (step >> 1) & 1);
+                if (ok) ok = wait_all(bar(C::B_S_EMPTY + sb), ((step >> 1) & 1) ^ 1);
+                if (!ok) break;
+                fence_async_smem();   // Q came through the generic proxy (cp.async)
+                tc_after();
+                const int n = min(kChunk, rows - c * kChunk);
+                const uint32_t idesc = idesc_bf16(kTok, max(16, (n + 15) & ~15), false);
+                const uint64_t kd = sdesc(k_smem + st * C::OPER, 16, 1024), qd = sdesc(q_smem + b * C::OPER, 16, 1024);
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t o = ((uint32_t)(x >> 2) * C::SLAB + (uint32_t)(x & 3) * 32) >> 4;
-                        umma_ss(tmem + sb * kChunk, kd + o, qd + o, idesc, x > 0 ? 1u : 0u);
-                    }
-                    umma_commit(bar(C::B_S_FULL + sb));
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t o = ((uint32_t)(x >> 2) * C::SLAB + (uint32_t)(x & 3) * 32) >> 4;
+                    umma_ss(tmem + sb * kChunk, kd + o, qd + o, idesc, x > 0 ? 1u : 0u, lead);
                 }
-                (i & 1 ? steps[1] : steps[0]) = step;
-                umma_commit(bar(C::B_K_EMPTY + st));
+                umma_commit(bar(C::B_S_FULL + sb), lead);
             }
-            umma_commit(bar(C::B_DRAIN));
-            settle(bar(C::B_DRAIN), 0);
+            (i & 1 ? steps[1] : steps[0]) = step;
+            umma_commit(bar(C::B_K_EMPTY + st), lead);
         }
+        umma_commit(bar(C::B_DRAIN), lead);
+        settle(bar(C::B_DRAIN), 0);
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------ queries
