@@ -753,21 +753,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (ok) ok = wait_all(bar(C::B_O_EMPTY), (uc & 1) ^ 1);
                     tc_after();
                     if (ok && nsteps > 0) ok = wait_v(0);
-                    if (ok && nsteps > 1) ok = wait_k(1);
+                    // K of the next step is waited for behind P_0 V, V of it
+                    // behind P_1 V, as late as the queue allows: the rings are
+                    // short, and waits half a step earlier made this 1.6 times
+                    // slower
                     for (int t = 0; ok && t < nsteps; ++t) {
-                        for (int tq = 0; ok && tq < 2; ++tq) {
-                            ok = wait_p(tq);
-                            if (!ok) break;
-                            issue_pv(t, tq, t == 0);
-                            if (t + 1 < nsteps) issue_s(t + 1, tq, tq);
-                        }
+                        ok = wait_p(0);
                         if (!ok) break;
+                        issue_pv(t, 0, t == 0);
+                        if (t + 1 < nsteps) {
+                            ok = wait_k(t + 1);
+                            if (!ok) break;
+                            issue_s(t + 1, 0, 0);
+                        }
+                        ok = wait_p(1);
+                        if (!ok) break;
+                        issue_pv(t, 1, t == 0);
                         free_v(t);
                         if (t + 1 < nsteps) {
-                            free_k(t + 1);
                             ok = wait_v(t + 1);
+                            if (!ok) break;
+                            issue_s(t + 1, 1, 1);
+                            free_k(t + 1);
                         }
-                        if (ok && t + 2 < nsteps) ok = wait_k(t + 2);
                     }
                 } else {
                     for (int t = 0; ok && t < 2 && t < nsteps; ++t) {
@@ -860,22 +868,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 auto seen = [&](const KvTile &k) {   // the row's keys of a tile, before any mask
                     return has && mem >= (k.members & 0xFFFF) && mem < k.members >> 16 ? (k.ntok_flags & 0xFFFF) : 0;
                 };
-                // WIN: a step inside the windows of all the warp's rows needs no
-                // masks; otherwise the masks alone say what is valid
-                bool whole = false;
-                if (WIN) {
-                    auto inside = [&](const KvTile &k) {
-                        return (k.ntok_flags & 0xFFFF) == kTileTokens && (k.members & 0xFFFF) == 0 &&
-                               k.members >> 16 >= it.n_members && k.tok0 + kTileTokens - 1 <= pos_lo &&
-                               (k.tok0 > pos_hi - a.win || k.tok0 + kTileTokens <= a.sinks);
-                    };
-                    whole = 2 * t + 1 < ntile && inside(k0) && inside(k1);
-                    if (!whole) {
-                        const int n0 = seen(k0), n1 = 2 * t + 1 < ntile ? seen(k1) : 0;
-                        m0 = n0 > 0 ? window_bits(k0.tok0, n0, pos, a.win, a.sinks) : 0ull;
-                        m1 = n1 > 0 ? window_bits(k1.tok0, n1, pos, a.win, a.sinks) : 0ull;
-                        tr0 = tr1 = true;
-                    }
+                // a step of whole tiles that all the unit's rows see (WIN: inside
+                // the windows of all the warp's rows) needs no masks
+                auto inside = [&](const KvTile &k) {
+                    return k.ntok_flags == kTileTokens && (k.members & 0xFFFF) == 0 &&
+                           k.members >> 16 >= it.n_members &&
+                           (!WIN || (k.tok0 + kTileTokens - 1 <= pos_lo &&
+                                     (k.tok0 > pos_hi - a.win || k.tok0 + kTileTokens <= a.sinks)));
+                };
+                const bool whole = 2 * t + 1 < ntile && inside(k0) && inside(k1);
+                if (whole) {
+                    nv0 = nv1 = kTileTokens;
+                } else if (WIN) {   // the masks alone say what is valid
+                    const int n0 = seen(k0), n1 = 2 * t + 1 < ntile ? seen(k1) : 0;
+                    m0 = n0 > 0 ? window_bits(k0.tok0, n0, pos, a.win, a.sinks) : 0ull;
+                    m1 = n1 > 0 ? window_bits(k1.tok0, n1, pos, a.win, a.sinks) : 0ull;
+                    tr0 = tr1 = true;
                     nv0 = nv1 = kTileTokens;
                 } else {
                     nv0 = seen(k0);
@@ -913,9 +921,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 float ls = 0.f;
                 uint32_t pk[64];
-                if (WIN && whole) p_pass_whole(s_tm, m == -INFINITY ? 0.f : -m, sc, pk, ls);
+                if (whole) p_pass_whole(s_tm, m == -INFINITY ? 0.f : -m, sc, pk, ls);
                 else p_pass(s_tm, m == -INFINITY ? 0.f : -m, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
-                const bool some = WIN ? (whole ? has : (m0 | m1) != 0) : nv0 > 0 || nv1 > 0;
+                const bool some = whole ? has : WIN ? (m0 | m1) != 0 : nv0 > 0 || nv1 > 0;
                 const bool bad = m == -INFINITY ? some : !(ls <= kSlackSum);
                 if (!__any_sync(0xffffffffu, bad)) {
                     p_store(s_tm, pk);
