@@ -1136,7 +1136,11 @@ cudaError_t launch_d(const AttnLaunch &a, cudaStream_t stream, cudaEvent_t befor
             return cudaErrorUnknown;
         mma_stream = side.s;
     }
-    cudaError_t e = launch_attention_tc(a, stream, fork ? 1 : 0);
+    // A window call's mma.sync units are few and short (single query tokens
+    // beside prompt chunks): launched first they run while the persistent
+    // tcgen05 CTAs start, instead of after these end
+    const bool tc_last = fork && a.win > 0;
+    cudaError_t e = tc_last ? cudaSuccess : launch_attention_tc(a, stream, 1);
     if (e != cudaSuccess) return e;
     if (a.n_units > 0 && a.kv4) {
         Occupancy &o4 = occupancy<D, true>();
@@ -1167,6 +1171,10 @@ cudaError_t launch_d(const AttnLaunch &a, cudaStream_t stream, cudaEvent_t befor
         e = launch_pdl(attn_item_kernel<D, false, false>, dim3(grid), dim3(kThreads), C::SMEM, mma_stream, a);
         count_launch();
         if (e == cudaSuccess) e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (tc_last) {
+        e = launch_attention_tc(a, stream, 1);
         if (e != cudaSuccess) return e;
     }
     if (mma_stream != stream) {

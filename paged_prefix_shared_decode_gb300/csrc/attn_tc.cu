@@ -30,8 +30,8 @@
 //               other group's P V and next S.  The two groups' (m, l, O) are
 //               merged when the unit ends.  In a pair unit group g takes
 //               every step for the rows of tile g and writes them alone.
-// P (bf16 pairs) overwrites the S columns it came from, so it never passes
-// through shared memory.  The running max is raised only when a step's P
+// P (bf16 pairs) overwrites the S columns it came from (at d = 64 it has
+// columns of its own), so it never passes through shared memory.  The running max is raised only when a step's P
 // would sum to more than 2^32, so every p <= 2^32; O_g is then rescaled in
 // TMEM.
 // Every wait is bounded; on a timeout the CTA sets bit 4 of the workspace
@@ -40,8 +40,9 @@
 // lets its MMAs complete (bounded waits too).  Softmax warps none of whose
 // rows is in the unit (a half-filled tile) keep only the barriers.
 //
-// TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + d),
-// O_1 [256 + d, 256 + 2d).
+// TMEM columns, d = 128: S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1
+// [384, 512), P over S; d = 64: S_0, S_1, P_0 [256, 320), P_1 [320, 384), O_0
+// [384, 448), O_1 [448, 512).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -114,10 +115,15 @@ struct TcCfg {
                          B_V_FULL = B_K_EMPTY + NK, B_V_EMPTY = B_V_FULL + NV, B_S_FULL = B_V_EMPTY + NV,
                          B_P_FULL = B_S_FULL + 2, B_Q_FULL = B_P_FULL + 2, B_Q_EMPTY = B_Q_FULL + 1,
                          B_O_FULL = B_Q_EMPTY + 1, B_O_EMPTY = B_O_FULL + 1, B_DRAIN = B_O_EMPTY + 1,
-                         N_BARS = B_DRAIN + 1;
+                         B_PV_DONE = B_DRAIN + 1,   // APART: per group
+                         N_BARS = B_PV_DONE + 2;
     static constexpr int MISC_OFF = BAR_OFF + N_BARS * 8;   // tmem address, abort flag
     static constexpr int SMEM = MISC_OFF + 16 + 1024;       // + slack to align the base to 1024
-    static constexpr int S_COL = 0, O_COL = 2 * kStepTokens;
+    // D = 64 leaves room for P beside S, so that the next S need not wait for
+    // this step's P V; at D = 128 P overwrites S
+    static constexpr bool APART = D == 64;
+    static constexpr int S_COL = 0, P_COL = APART ? 2 * kStepTokens : 0, P_STRIDE = APART ? kStepTokens / 2 : kStepTokens,
+                         O_COL = APART ? 3 * kStepTokens : 2 * kStepTokens;
 };
 static_assert(TcCfg<64>::SMEM <= 227 * 1024 && TcCfg<128>::SMEM <= 227 * 1024, "shared memory");
 
@@ -246,7 +252,7 @@ __device__ __forceinline__ void p_pass_whole(uint32_t s_tm, float nm, float sc, 
     exp_pack16<false>(y, 0, sc, nm, 0, pk + 48, ls);
     exp_pack16<false>(y, 16, sc, nm, 0, pk + 56, ls);
 }
-// P overwrites the first 64 S columns (all scores are read by then)
+// (all scores are read by then: P may overwrite the first 64 S columns)
 __device__ __forceinline__ void p_store(uint32_t s_tm, const uint32_t (&pk)[64]) {
     tmem_st32(s_tm, *reinterpret_cast<const uint32_t(*)[32]>(pk));
     tmem_st32(s_tm + 32, *reinterpret_cast<const uint32_t(*)[32]>(pk + 32));
@@ -267,14 +273,14 @@ __device__ __forceinline__ float step_max(uint32_t s_tm, int nv0, bool tr0, int 
 // The slow path, kept out of line so that its registers do not add to the
 // common path's: the step's max, the new running max (raised for the rows
 // marked bad), P again, stored.  Returns (new m, sum of P).
-__device__ __noinline__ float2 recompute_step(uint32_t s_tm, float m, float sc, int nv0, bool tr0, int nv1, bool tr1,
+__device__ __noinline__ float2 recompute_step(uint32_t s_tm, uint32_t p_tm, float m, float sc, int nv0, bool tr0, int nv1, bool tr1,
                                               uint64_t m0, uint64_t m1, bool bad) {
     const float tmx = step_max(s_tm, nv0, tr0, nv1, tr1, m0, m1) * sc;
     const float m_new = bad ? fmaxf(m, tmx) : m;
     float ls = 0.f;
     uint32_t pk[64];
     p_pass(s_tm, m_new == -INFINITY ? 0.f : -m_new, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
-    p_store(s_tm, pk);
+    p_store(p_tm, pk);
     return make_float2(m_new, ls);
 }
 
@@ -304,6 +310,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(bar(C::B_UNIT_EMPTY + s), 1 + kSoftThreads + kProdWarps);
             mbar_init(bar(C::B_S_FULL + s), 1);
             mbar_init(bar(C::B_P_FULL + s), kGroupThreads);
+            mbar_init(bar(C::B_PV_DONE + s), 1);
         }
         for (int s = 0; s < C::NK; ++s) {
             mbar_init(bar(C::B_K_FULL + s), 32);
@@ -724,13 +731,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 auto issue_pv = [&](int t, int b, bool first) {
                     const uint32_t st = (gv + t) % C::NV;
                     const uint64_t vd = sdesc(v_smem + st * C::OPER, C::SLAB, 1024);
-                    const uint32_t o_tm = tmem + C::O_COL + b * D, p_tm = tmem + C::S_COL + b * kStepTokens;
+                    const uint32_t o_tm = tmem + C::O_COL + b * D, p_tm = tmem + C::P_COL + b * C::P_STRIDE;
                     // an odd last tile leaves rows 64..127 of V unwritten: skip them
                     const int ksteps = 2 * t + 1 < ntile ? kStepTokens / 16 : kTileTokens / 16;
 #pragma unroll
                     for (int k = 0; k < kStepTokens / 16; ++k)
                         if (k < ksteps)
                             umma_ts(o_tm, p_tm + k * 8, vd + k * (2048 >> 4), IDESC_PV, !first || k > 0 ? 1u : 0u, lead);
+                    if (C::APART) umma_commit(bar(C::B_PV_DONE + b), lead);
                 };
                 auto free_v = [&](int t) { umma_commit(bar(C::B_V_EMPTY + (gv + t) % C::NV), lead); };
                 auto wait_p = [&](int b) -> bool {
@@ -758,23 +766,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // short, and waits half a step earlier made this 1.6 times
                     // slower
                     for (int t = 0; ok && t < nsteps; ++t) {
+                        const bool more = t + 1 < nsteps;
                         ok = wait_p(0);
                         if (!ok) break;
-                        issue_pv(t, 0, t == 0);
-                        if (t + 1 < nsteps) {
+                        if (!C::APART) issue_pv(t, 0, t == 0);
+                        if (more) {
                             ok = wait_k(t + 1);
                             if (!ok) break;
                             issue_s(t + 1, 0, 0);
                         }
+                        if (C::APART) issue_pv(t, 0, t == 0);
                         ok = wait_p(1);
                         if (!ok) break;
-                        issue_pv(t, 1, t == 0);
-                        free_v(t);
-                        if (t + 1 < nsteps) {
-                            ok = wait_v(t + 1);
-                            if (!ok) break;
+                        if (C::APART && more) {
                             issue_s(t + 1, 1, 1);
                             free_k(t + 1);
+                        }
+                        issue_pv(t, 1, t == 0);
+                        free_v(t);
+                        if (more) {
+                            ok = wait_v(t + 1);
+                            if (!ok) break;
+                            if (!C::APART) {
+                                issue_s(t + 1, 1, 1);
+                                free_k(t + 1);
+                            }
                         }
                     }
                 } else {
@@ -792,10 +808,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int t = 0; ok && t < nsteps; ++t) {
                         ok = wait_p(t & 1);
                         if (!ok) break;
-                        issue_pv(t, t & 1, t < 2);
+                        if (!C::APART) issue_pv(t, t & 1, t < 2);
                         if (t + 2 < nsteps) issue_s(t + 2, 0, t & 1);
+                        if (C::APART) {
+                            if (t + 2 < nsteps) free_k(t + 2);
+                            issue_pv(t, t & 1, t < 2);
+                        }
                         free_v(t);
-                        if (t + 2 < nsteps) free_k(t + 2);
+                        if (!C::APART && t + 2 < nsteps) free_k(t + 2);
                         if (t + 1 < nsteps) ok = wait_v(t + 1);
                         if (ok && t + 3 < nsteps) ok = wait_k(t + 3);
                     }
@@ -821,6 +841,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int r = quarter * 32 + lane;        // query row in the unit
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_tm = tmem + lane_base + C::S_COL + grp * kStepTokens;
+        const uint32_t p_tm = tmem + lane_base + C::P_COL + grp * C::P_STRIDE;
         const uint32_t o_tm = tmem + lane_base + C::O_COL;
         const float sc = a.scale_log2;
         uint32_t ns = 0;   // S_FULL phases consumed by this group
@@ -925,13 +946,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 else p_pass(s_tm, m == -INFINITY ? 0.f : -m, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
                 const bool some = whole ? has : WIN ? (m0 | m1) != 0 : nv0 > 0 || nv1 > 0;
                 const bool bad = m == -INFINITY ? some : !(ls <= kSlackSum);
+                // (ns steps of this group are seen: the products of the one
+                // before have read their P, and completed O_g)
+                if (C::APART && ns > 1) ok = wait(bar(C::B_PV_DONE + grp), ns & 1) && ok;
                 if (!__any_sync(0xffffffffu, bad)) {
-                    p_store(s_tm, pk);
+                    p_store(p_tm, pk);
                 } else {
-                    const float2 r2 = recompute_step(s_tm, m, sc, nv0, tr0, nv1, tr1, m0, m1, bad);
+                    const float2 r2 = recompute_step(s_tm, p_tm, m, sc, nv0, tr0, nv1, tr1, m0, m1, bad);
                     const bool resc = r2.x != m && m != -INFINITY;
                     if (__any_sync(0xffffffffu, resc)) {
-                        // O_g holds P V up to step t-2, complete since S(t) is
+                        // O_g holds P V up to the group's step before, complete
+                        // (APART: waited for above; else since S(t) is)
                         const float f = resc ? exp2_sfu(m - r2.x) : 1.f;
 #pragma unroll
                         for (int c0 = 0; c0 < D; c0 += 32) {

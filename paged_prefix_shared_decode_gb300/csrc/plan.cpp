@@ -693,7 +693,9 @@ void window_extend_plan(const kvp_attn_desc &d, const int32_t *tables, const int
     for (int k = 0; k < 2; ++k) {
         const int64_t target = k ? sms : (int64_t)sms * attention_ctas_per_sm(d.head_dim);
         chunk[k] = kMaxItemTiles;
-        if (n_units[k] * lh < target) {
+        // (a few rows beside tcgen05 units are done long before these, and
+        // whole units need no merge)
+        if (n_units[k] * lh < target && (k == 1 || n_units[1] == 0)) {
             const int64_t want = (n_tiles[k] * lh + target - 1) / target;
             chunk[k] = std::max<int64_t>(4, std::min<int64_t>(chunk[k], want));
         }
