@@ -3,7 +3,7 @@
 // segments read by many sequences, MCTS tree levels and draft-tree
 // verification.
 //
-// One persistent CTA of 12 warps per SM.  A work unit is (item, layer, kv
+// One persistent CTA of 20 warps per SM.  A work unit is (item, layer, kv
 // head): up to 128 query rows (the item's members x the GQA group of the kv
 // head), or a pair unit of up to 256 rows as two 128-row tiles over one K/V
 // stream, against the item's 64-token KV tiles, taken two at a time as
@@ -23,8 +23,9 @@
 //               TMA boxes of whole rows (the G heads of consecutive query
 //               tokens) when the unit's members are consecutive tokens, else
 //               by a cp.async gather.
-//   warps 4-7   softmax group 0 (even steps), warps 8-11 group 1 (odd
-//               steps), one thread per query row.  Each group keeps its own
+//   warps 4-11  softmax group 0 (even steps), warps 12-19 group 1 (odd
+//               steps), two threads per query row, one for each of a step's
+//               two tiles.  Each group keeps its own
 //               running max m_g, sum l_g and accumulator O_g, so while one
 //               group turns step t's scores into P the tensor cores run the
 //               other group's P V and next S.  The two groups' (m, l, O) are
@@ -64,24 +65,35 @@ constexpr int kProdWarps = 2;        // warp 0: K, warp 1: V
 constexpr int kVWarp = 1;
 constexpr int kMmaWarp = 2;
 constexpr int kUnitWarp = 3;         // claims units, stages descriptors and Q
-constexpr int kSoftWarp0 = 4;        // warps 4-7: group 0, 8-11: group 1
-constexpr int kTcThreads = 384;      // 12 warps: 3 per SM sub-partition
-constexpr int kSoftThreads = 256;
-constexpr int kGroupThreads = 128;
+constexpr int kSoftWarp0 = 4;        // warps 4-11: group 0, 12-19: group 1
+constexpr int kTcThreads = 640;      // 20 warps: 5 per SM sub-partition
+constexpr int kSoftThreads = 512;
+constexpr int kGroupThreads = 256;
 constexpr int kStepTokens = 2 * kTileTokens;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kSlackSum = 4294967296.f;   // 2^32: bound on a step's sum of p
 
-// Named barrier 1 over the 256 softmax threads with an OR reduction, so that
-// all of them take the same branch.
+// Named barriers with an OR reduction, so that all their threads take the same
+// branch: 1 over the softmax threads, 2 + i over the two warps that share the
+// rows of quarter i % 4 of group i / 4.
 __device__ __forceinline__ bool soft_bar_or(bool v) {
     uint32_t r;
     asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, 1, 256, q;\n"
+        "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, 1, 512, q;\n"
         "selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(r)
         : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool row_bar_or(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 q, %2, 0;\nbar.red.or.pred p, %1, 64, q;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)v)
         : "memory");
     return r != 0;
 }
@@ -108,8 +120,9 @@ struct TcCfg {
     static constexpr int STG4_BUF = CODE4 + kTileTokens;
     static constexpr int STG4_OFF = V_OFF + NV * OPER;
     static constexpr int DESC_OFF = STG4_OFF + 2 * 2 * STG4_BUF;                      // [2][kMaxItemTiles]
-    static constexpr int ML_OFF = DESC_OFF + 2 * kMaxItemTiles * (int)sizeof(KvTile);  // [2][128] float2
-    static constexpr int UNIT_OFF = ML_OFF + 2 * 128 * 8;                           // [2] ints
+    static constexpr int ML_OFF = DESC_OFF + 2 * kMaxItemTiles * (int)sizeof(KvTile);  // [2][2][128] float2
+    static constexpr int XCH_OFF = ML_OFF + 4 * 128 * 8;                            // the same
+    static constexpr int UNIT_OFF = XCH_OFF + 4 * 128 * 8;                          // [2] ints
     static constexpr int BAR_OFF = UNIT_OFF + 16;
     static constexpr int B_UNIT_FULL = 0, B_UNIT_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = B_K_FULL + NK,
                          B_V_FULL = B_K_EMPTY + NK, B_V_EMPTY = B_V_FULL + NV, B_S_FULL = B_V_EMPTY + NV,
@@ -204,84 +217,36 @@ __device__ __forceinline__ void exp_pack16(const uint32_t (&x)[32], int j0, floa
     sum += s0 + s1;
 }
 
-// P = 2^(s * sc + nm) of one step, packed into pk (word i holds scores 2i,
-// 2i + 1); adds the sum of P to ls.  S is only read.
-// (m0, m1: masks of the step's two tiles, used where tr0 / tr1 are set.)
-__device__ __forceinline__ void p_pass(uint32_t s_tm, float nm, float sc, int nv0, bool tr0, int nv1, bool tr1,
-                                       uint64_t m0, uint64_t m1, uint32_t (&pk)[64], float &ls) {
+// P = 2^(s * sc + nm) of one 64-token tile, packed into pk (word i holds scores
+// 2i, 2i + 1); adds the sum of P to ls.  S is only read.  WHOLE: all scores
+// are valid; else nv, tree and mask say which are (valid_bits).
+template <bool WHOLE>
+__device__ __forceinline__ void p_pass(uint32_t s_tm, float nm, float sc, int nv, bool tree, uint64_t mask,
+                                       uint32_t (&pk)[32], float &ls) {
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-        uint32_t x[32], y[32];
-        tmem_ld32(s_tm + 64 * hh, x);
-        tmem_ld32(s_tm + 64 * hh + 32, y);
+    for (int h = 0; h < 2; ++h) {
+        uint32_t x[32];
+        tmem_ld32(s_tm + 32 * h, x);
         tmem_wait_ld();
-        const uint32_t vx = valid_bits(hh ? nv1 : nv0, hh ? tr1 : tr0, hh ? m1 : m0, 0);
-        const uint32_t vy = valid_bits(hh ? nv1 : nv0, hh ? tr1 : tr0, hh ? m1 : m0, 32);
-        uint32_t *q = pk + 32 * hh;
-        if (__all_sync(0xffffffffu, (vx & vy) == 0xffffffffu)) {
-            exp_pack16<false>(x, 0, sc, nm, vx, q, ls);
-            exp_pack16<false>(x, 16, sc, nm, vx, q + 8, ls);
-            exp_pack16<false>(y, 0, sc, nm, vy, q + 16, ls);
-            exp_pack16<false>(y, 16, sc, nm, vy, q + 24, ls);
+        const uint32_t v = WHOLE ? 0u : valid_bits(nv, tree, mask, 32 * h);
+        if (WHOLE || __all_sync(0xffffffffu, v == 0xffffffffu)) {
+            exp_pack16<false>(x, 0, sc, nm, v, pk + 16 * h, ls);
+            exp_pack16<false>(x, 16, sc, nm, v, pk + 16 * h + 8, ls);
         } else {
-            exp_pack16<true>(x, 0, sc, nm, vx, q, ls);
-            exp_pack16<true>(x, 16, sc, nm, vx, q + 8, ls);
-            exp_pack16<true>(y, 0, sc, nm, vy, q + 16, ls);
-            exp_pack16<true>(y, 16, sc, nm, vy, q + 24, ls);
+            exp_pack16<true>(x, 0, sc, nm, v, pk + 16 * h, ls);
+            exp_pack16<true>(x, 16, sc, nm, v, pk + 16 * h + 8, ls);
         }
     }
 }
-// The same for a step whose scores are all valid: no masks, and each 32
-// columns of S are loaded while the 32 before them are turned into P.
-__device__ __forceinline__ void p_pass_whole(uint32_t s_tm, float nm, float sc, uint32_t (&pk)[64], float &ls) {
-    uint32_t x[32], y[32];
+// Row max of one tile's valid raw scores (-inf if none).
+__device__ __forceinline__ float tile_max(uint32_t s_tm, int nv, bool tree, uint64_t mask) {
+    uint32_t x[32];
     tmem_ld32(s_tm, x);
     tmem_wait_ld();
-    tmem_ld32(s_tm + 32, y);
-    exp_pack16<false>(x, 0, sc, nm, 0, pk, ls);
-    exp_pack16<false>(x, 16, sc, nm, 0, pk + 8, ls);
+    const float mx = max32(x, valid_bits(nv, tree, mask, 0));
+    tmem_ld32(s_tm + 32, x);
     tmem_wait_ld();
-    tmem_ld32(s_tm + 64, x);
-    exp_pack16<false>(y, 0, sc, nm, 0, pk + 16, ls);
-    exp_pack16<false>(y, 16, sc, nm, 0, pk + 24, ls);
-    tmem_wait_ld();
-    tmem_ld32(s_tm + 96, y);
-    exp_pack16<false>(x, 0, sc, nm, 0, pk + 32, ls);
-    exp_pack16<false>(x, 16, sc, nm, 0, pk + 40, ls);
-    tmem_wait_ld();
-    exp_pack16<false>(y, 0, sc, nm, 0, pk + 48, ls);
-    exp_pack16<false>(y, 16, sc, nm, 0, pk + 56, ls);
-}
-// (all scores are read by then: P may overwrite the first 64 S columns)
-__device__ __forceinline__ void p_store(uint32_t s_tm, const uint32_t (&pk)[64]) {
-    tmem_st32(s_tm, *reinterpret_cast<const uint32_t(*)[32]>(pk));
-    tmem_st32(s_tm + 32, *reinterpret_cast<const uint32_t(*)[32]>(pk + 32));
-}
-// Row max of one step's valid raw scores (-inf if none).
-__device__ __forceinline__ float step_max(uint32_t s_tm, int nv0, bool tr0, int nv1, bool tr1, uint64_t m0,
-                                          uint64_t m1) {
-    uint32_t x[32], y[32];
-    tmem_ld32(s_tm, x);
-    tmem_ld32(s_tm + 32, y);
-    tmem_wait_ld();
-    float mx = fmaxf(max32(x, valid_bits(nv0, tr0, m0, 0)), max32(y, valid_bits(nv0, tr0, m0, 32)));
-    tmem_ld32(s_tm + 64, x);
-    tmem_ld32(s_tm + 96, y);
-    tmem_wait_ld();
-    return fmaxf(mx, fmaxf(max32(x, valid_bits(nv1, tr1, m1, 0)), max32(y, valid_bits(nv1, tr1, m1, 32))));
-}
-// The slow path, kept out of line so that its registers do not add to the
-// common path's: the step's max, the new running max (raised for the rows
-// marked bad), P again, stored.  Returns (new m, sum of P).
-__device__ __noinline__ float2 recompute_step(uint32_t s_tm, uint32_t p_tm, float m, float sc, int nv0, bool tr0, int nv1, bool tr1,
-                                              uint64_t m0, uint64_t m1, bool bad) {
-    const float tmx = step_max(s_tm, nv0, tr0, nv1, tr1, m0, m1) * sc;
-    const float m_new = bad ? fmaxf(m, tmx) : m;
-    float ls = 0.f;
-    uint32_t pk[64];
-    p_pass(s_tm, m_new == -INFINITY ? 0.f : -m_new, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
-    p_store(p_tm, pk);
-    return make_float2(m_new, ls);
+    return fmaxf(mx, max32(x, valid_bits(nv, tree, mask, 32)));
 }
 
 template <int D, bool KV4, bool WIN>
@@ -295,6 +260,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     KvTile *s_desc = reinterpret_cast<KvTile *>(smem + C::DESC_OFF);
     float2 *s_ml = reinterpret_cast<float2 *>(smem + C::ML_OFF);
+    float2 *s_xch = reinterpret_cast<float2 *>(smem + C::XCH_OFF);
     volatile int *s_unit = reinterpret_cast<volatile int *>(smem + C::UNIT_OFF);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
@@ -673,7 +639,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         {
             constexpr uint32_t IDESC_S = idesc_bf16(128, kStepTokens, false);
             constexpr uint32_t IDESC_PV = idesc_bf16(128, D, true);
-            const uint32_t lead = elect_one();
+            const bool lead = elect_one();
+            const uint32_t tm = uniform(tmem), qs0 = uniform(q_smem), ks0 = uniform(k_smem), vs0 = uniform(v_smem);
             auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, wait(b, parity));
             };
@@ -716,31 +683,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // S of step t for query tile tq into S buffer b
                 auto issue_s = [&](int t, int tq, int b) {
                     const uint32_t st = (gk + t) % C::NK;
-                    const uint32_t kst = k_smem + st * C::OPER, qs = q_smem + tq * C::OPER;
-                    const uint32_t d_tm = tmem + C::S_COL + b * kStepTokens;
-                    const uint64_t qd = sdesc(qs, 16, 1024), kd = sdesc(kst, 16, 1024);
+                    const uint32_t d_tm = tm + C::S_COL + b * kStepTokens;
+                    const uint64_t qd = sdesc(qs0 + tq * C::OPER, 16, 1024), kd = sdesc(ks0 + st * C::OPER, 16, 1024);
+                    if (lead) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t o = ((uint32_t)(k >> 2) * C::SLAB + (uint32_t)(k & 3) * 32) >> 4;
-                        umma_ss(d_tm, qd + o, kd + o, IDESC_S, k > 0 ? 1u : 0u, lead);
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t o = ((uint32_t)(k >> 2) * C::SLAB + (uint32_t)(k & 3) * 32) >> 4;
+                            umma_ss(d_tm, qd + o, kd + o, IDESC_S, k > 0 ? 1u : 0u);
+                        }
+                        umma_commit(bar(C::B_S_FULL + b));
                     }
-                    umma_commit(bar(C::B_S_FULL + b), lead);
                 };
-                auto free_k = [&](int t) { umma_commit(bar(C::B_K_EMPTY + (gk + t) % C::NK), lead); };
+                auto free_k = [&](int t) {
+                    if (lead) umma_commit(bar(C::B_K_EMPTY + (gk + t) % C::NK));
+                };
                 // O_b += P_b V of step t
                 auto issue_pv = [&](int t, int b, bool first) {
                     const uint32_t st = (gv + t) % C::NV;
-                    const uint64_t vd = sdesc(v_smem + st * C::OPER, C::SLAB, 1024);
-                    const uint32_t o_tm = tmem + C::O_COL + b * D, p_tm = tmem + C::P_COL + b * C::P_STRIDE;
+                    const uint64_t vd = sdesc(vs0 + st * C::OPER, C::SLAB, 1024);
+                    const uint32_t o_tm = tm + C::O_COL + b * D, p_tm = tm + C::P_COL + b * C::P_STRIDE;
                     // an odd last tile leaves rows 64..127 of V unwritten: skip them
-                    const int ksteps = 2 * t + 1 < ntile ? kStepTokens / 16 : kTileTokens / 16;
+                    const bool both = 2 * t + 1 < ntile;
+                    if (lead) {
 #pragma unroll
-                    for (int k = 0; k < kStepTokens / 16; ++k)
-                        if (k < ksteps)
-                            umma_ts(o_tm, p_tm + k * 8, vd + k * (2048 >> 4), IDESC_PV, !first || k > 0 ? 1u : 0u, lead);
-                    if (C::APART) umma_commit(bar(C::B_PV_DONE + b), lead);
+                        for (int k = 0; k < kTileTokens / 16; ++k)
+                            umma_ts(o_tm, p_tm + k * 8, vd + k * (2048 >> 4), IDESC_PV, !first || k > 0 ? 1u : 0u);
+                        if (both) {
+#pragma unroll
+                            for (int k = kTileTokens / 16; k < kStepTokens / 16; ++k)
+                                umma_ts(o_tm, p_tm + k * 8, vd + k * (2048 >> 4), IDESC_PV, 1u);
+                        }
+                        if (C::APART) umma_commit(bar(C::B_PV_DONE + b));
+                    }
                 };
-                auto free_v = [&](int t) { umma_commit(bar(C::B_V_EMPTY + (gv + t) % C::NV), lead); };
+                auto free_v = [&](int t) {
+                    if (lead) umma_commit(bar(C::B_V_EMPTY + (gv + t) % C::NV));
+                };
                 auto wait_p = [&](int b) -> bool {
                     if (!wait_all(bar(C::B_P_FULL + b), (b ? np1 : np0) & 1)) return false;
                     if (b) ++np1; else ++np0;
@@ -823,25 +801,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!ok) break;
                 // (with steps, the softmax thread that sees the unit's last S
                 // releases Q)
-                if (nsteps == 0) umma_commit(bar(C::B_Q_EMPTY), lead);
+                if (lead && nsteps == 0) umma_commit(bar(C::B_Q_EMPTY));
                 gk += nsteps;
                 gv += nsteps;
-                umma_commit(bar(C::B_O_FULL), lead);
+                if (lead) umma_commit(bar(C::B_O_FULL));
                 if (lead) mbar_arrive(bar(C::B_UNIT_EMPTY + slot));
             }
             // every MMA that was issued completes before TMEM is freed
-            umma_commit(bar(C::B_DRAIN), lead);
+            if (lead) umma_commit(bar(C::B_DRAIN));
             settle(bar(C::B_DRAIN), 0);
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        const int grp = (warp - kSoftWarp0) >> 2;
+        const int grp = (warp - kSoftWarp0) >> 3;
+        const int half = ((warp - kSoftWarp0) >> 2) & 1;   // the step's tile that this warp takes
         const int quarter = warp & 3;             // TMEM lanes this warp may access
         const int r = quarter * 32 + lane;        // query row in the unit
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t s_tm = tmem + lane_base + C::S_COL + grp * kStepTokens;
-        const uint32_t p_tm = tmem + lane_base + C::P_COL + grp * C::P_STRIDE;
+        const uint32_t s_tm = tmem + lane_base + C::S_COL + grp * kStepTokens + 64 * half;
+        const uint32_t p_tm = tmem + lane_base + C::P_COL + grp * C::P_STRIDE + 32 * half;
+        const int row_bar = 2 + grp * 4 + quarter;
+        float2 *mine = s_xch + (grp * 2 + half) * 128 + r, *other = s_xch + (grp * 2 + 1 - half) * 128 + r;
         const uint32_t o_tm = tmem + lane_base + C::O_COL;
         const float sc = a.scale_log2;
         uint32_t ns = 0;   // S_FULL phases consumed by this group
@@ -881,46 +862,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
             float m = -INFINITY, lsum = 0.f;
             for (int t = pair ? 0 : grp; t < nsteps; t += pair ? 1 : 2) {
-                // what the rows see of the step's two tiles, while S is on its way
-                int nv0 = 0, nv1 = 0;
-                bool tr0 = false, tr1 = false;
-                uint64_t m0 = tmask, m1 = tmask;
-                const KvTile &k0 = tiles[2 * t], &k1 = tiles[2 * t + 1 < ntile ? 2 * t + 1 : 2 * t];
-                auto seen = [&](const KvTile &k) {   // the row's keys of a tile, before any mask
-                    return has && mem >= (k.members & 0xFFFF) && mem < k.members >> 16 ? (k.ntok_flags & 0xFFFF) : 0;
-                };
-                // a step of whole tiles that all the unit's rows see (WIN: inside
-                // the windows of all the warp's rows) needs no masks
-                auto inside = [&](const KvTile &k) {
-                    return k.ntok_flags == kTileTokens && (k.members & 0xFFFF) == 0 &&
-                           k.members >> 16 >= it.n_members &&
-                           (!WIN || (k.tok0 + kTileTokens - 1 <= pos_lo &&
-                                     (k.tok0 > pos_hi - a.win || k.tok0 + kTileTokens <= a.sinks)));
-                };
-                const bool whole = 2 * t + 1 < ntile && inside(k0) && inside(k1);
+                // what the rows see of this warp's tile, while S is on its way
+                const bool there = 2 * t + half < ntile;
+                const KvTile &kt = tiles[there ? 2 * t + half : 2 * t];
+                // keys before any mask
+                const int n = there && has && mem >= (kt.members & 0xFFFF) && mem < kt.members >> 16
+                                  ? (kt.ntok_flags & 0xFFFF)
+                                  : 0;
+                // a whole tile that all the unit's rows see (WIN: inside the
+                // windows of all the warp's rows) needs no masks
+                const bool whole = there && kt.ntok_flags == kTileTokens && (kt.members & 0xFFFF) == 0 &&
+                                   kt.members >> 16 >= it.n_members &&
+                                   (!WIN || (kt.tok0 + kTileTokens - 1 <= pos_lo &&
+                                             (kt.tok0 > pos_hi - a.win || kt.tok0 + kTileTokens <= a.sinks)));
+                int nv = n;
+                bool tree = (kt.ntok_flags >> 16) & kTileTree;
+                uint64_t mask = tmask;
                 if (whole) {
-                    nv0 = nv1 = kTileTokens;
-                } else if (WIN) {   // the masks alone say what is valid
-                    const int n0 = seen(k0), n1 = 2 * t + 1 < ntile ? seen(k1) : 0;
-                    m0 = n0 > 0 ? window_bits(k0.tok0, n0, pos, a.win, a.sinks) : 0ull;
-                    m1 = n1 > 0 ? window_bits(k1.tok0, n1, pos, a.win, a.sinks) : 0ull;
-                    tr0 = tr1 = true;
-                    nv0 = nv1 = kTileTokens;
-                } else {
-                    nv0 = seen(k0);
-                    tr0 = (k0.ntok_flags >> 16) & kTileTree;
-                    if (2 * t + 1 < ntile) {
-                        nv1 = seen(k1);
-                        tr1 = (k1.ntok_flags >> 16) & kTileTree;
-                    }
+                    nv = kTileTokens;
+                    tree = false;
+                } else if (WIN) {   // the mask alone says what is valid
+                    mask = n > 0 ? window_bits(kt.tok0, n, pos, a.win, a.sinks) : 0ull;
+                    nv = kTileTokens;
+                    tree = true;
                 }
+                const bool some = whole ? has : WIN ? mask != 0 : nv > 0;
                 ok = wait(bar(C::B_S_FULL + grp), ns & 1) && ok;
                 ns += 1;
                 // the unit's last S is done with Q: one thread of the group
                 // that takes it releases Q for the next unit's load, as soon
                 // as that S is seen (measured slightly faster than releasing
                 // it with an MMA commit)
-                if (t == nsteps - 1 && grp == (pair ? 1 : (t & 1)) && quarter == 0 && lane == 0)
+                if (t == nsteps - 1 && grp == (pair ? 1 : (t & 1)) && half == 0 && quarter == 0 && lane == 0)
                     mbar_arrive(bar(C::B_Q_EMPTY));
                 tc_after();
                 if (idle) {
@@ -928,38 +901,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_arrive(bar(C::B_P_FULL + grp));
                     continue;
                 }
-                // A row's running max m is raised only when the step's P would
-                // sum to more than 2^32, so every p <= 2^32, well inside bf16
-                // and the fp32 sums.  A step therefore reads S once and forms P
-                // with the current m, in registers; only a row whose sum breaks
-                // the bound, or that has valid scores but no m yet, takes the
-                // slow path (the step's max, O_g and l rescaled, P again)
-                // before P overwrites S.
-                if (__all_sync(0xffffffffu, m == -INFINITY)) {
-                    // this group's first step of the unit: find m first
-                    // (scale > 0: max of scaled scores = scale * max of raw scores)
-                    m = step_max(s_tm, nv0, tr0, nv1, tr1, m0, m1) * sc;
-                }
-                float ls = 0.f;
-                uint32_t pk[64];
-                if (whole) p_pass_whole(s_tm, m == -INFINITY ? 0.f : -m, sc, pk, ls);
-                else p_pass(s_tm, m == -INFINITY ? 0.f : -m, sc, nv0, tr0, nv1, tr1, m0, m1, pk, ls);
-                const bool some = whole ? has : WIN ? (m0 | m1) != 0 : nv0 > 0 || nv1 > 0;
-                const bool bad = m == -INFINITY ? some : !(ls <= kSlackSum);
+                // A row's running max m is raised only when a tile's P would sum
+                // to more than 2^32, so every p <= 2^32, well inside bf16 and
+                // the fp32 sums.  A step therefore reads S once and forms P with
+                // the current m, in registers; only a row whose sum breaks the
+                // bound, or that has valid scores but no m yet, takes the slow
+                // path (the two warps' max, O_g and l rescaled, P again).  The
+                // two warps of a row meet once a step: they take the same
+                // path, and P may go into columns that the first one's S came
+                // from.
                 // (ns steps of this group are seen: the products of the one
-                // before have read their P, and completed O_g)
+                // before have read their P, and completed O_g; where P
+                // overwrites S they have anyway, since this S came after them)
                 if (C::APART && ns > 1) ok = wait(bar(C::B_PV_DONE + grp), ns & 1) && ok;
-                if (!__any_sync(0xffffffffu, bad)) {
-                    p_store(p_tm, pk);
-                } else {
-                    const float2 r2 = recompute_step(s_tm, p_tm, m, sc, nv0, tr0, nv1, tr1, m0, m1, bad);
-                    const bool resc = r2.x != m && m != -INFINITY;
+                float ls = 0.f;
+                bool bad = some, slow = true;
+                if (!__all_sync(0xffffffffu, m == -INFINITY) || !__any_sync(0xffffffffu, some)) {
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    uint32_t pk[32];
+                    if (whole) p_pass<true>(s_tm, nm, sc, nv, tree, mask, pk, ls);
+                    else p_pass<false>(s_tm, nm, sc, nv, tree, mask, pk, ls);
+                    if (m != -INFINITY) bad = !(ls <= kSlackSum);
+                    slow = row_bar_or(row_bar, bad);
+                    if (!slow) tmem_st32(p_tm, pk);
+                } else {   // the rows' first keys: straight to the slow path
+                    row_bar_or(row_bar, true);
+                }
+                if (slow) {
+                    // (scale > 0: max of scaled scores = scale * max of raw scores)
+                    const float tmx = tile_max(s_tm, nv, tree, mask) * sc;
+                    *mine = make_float2(tmx, bad ? 1.f : 0.f);
+                    row_bar_or(row_bar, false);
+                    const float2 o2 = *other;
+                    const float m_new = bad || o2.y != 0.f ? fmaxf(m, fmaxf(tmx, o2.x)) : m;
+                    const bool resc = m_new != m && m != -INFINITY;
                     if (__any_sync(0xffffffffu, resc)) {
-                        // O_g holds P V up to the group's step before, complete
-                        // (APART: waited for above; else since S(t) is)
-                        const float f = resc ? exp2_sfu(m - r2.x) : 1.f;
-#pragma unroll
-                        for (int c0 = 0; c0 < D; c0 += 32) {
+                        // each warp rescales half of O_g's columns
+                        const float f = resc ? exp2_sfu(m - m_new) : 1.f;
+#pragma unroll 1
+                        for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                             uint32_t x[32];
                             tmem_ld32(o_tm + grp * D + c0, x);
                             tmem_wait_ld();
@@ -969,42 +949,50 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         lsum *= f;
                     }
-                    m = r2.x;
-                    ls = r2.y;
+                    m = m_new;
+                    ls = 0.f;
+                    uint32_t pk[32];
+                    p_pass<false>(s_tm, m == -INFINITY ? 0.f : -m, sc, nv, tree, mask, pk, ls);
+                    row_bar_or(row_bar, false);   // both have read S (and the other's max)
+                    tmem_st32(p_tm, pk);
                 }
                 lsum += ls;
                 tmem_wait_st();
                 tc_before();
                 mbar_arrive(bar(C::B_P_FULL + grp));
             }
-            // epilogue: one tile merges the two groups' (m, l, O) and each
-            // group writes half of the columns; in a pair unit each group
-            // writes its own tile's rows from its own O
+            // epilogue: one tile merges the two groups' (m, l, O) and the four
+            // warps of a row split its columns; in a pair unit each group's two
+            // warps write their own tile's rows from its own O
             ok = wait(bar(C::B_O_FULL), uc & 1) && ok;
             tc_after();
-            s_ml[grp * 128 + r] = make_float2(m, lsum);
+            s_ml[(grp * 2 + half) * 128 + r] = make_float2(m, lsum);
             if (soft_bar_or(!ok || *s_abort)) break;
             float w0, w1, lse2;
             int ca, cb;
+            // the two warps of a row share m
+            const float l0 = s_ml[r].y + s_ml[128 + r].y, l1 = s_ml[256 + r].y + s_ml[384 + r].y;
             if (!pair) {
-                const float2 a0 = s_ml[r], a1 = s_ml[128 + r];
-                const float c = fmaxf(a0.x, a1.x);
-                const float f0 = a0.x == -INFINITY ? 0.f : exp2_sfu(a0.x - c);
-                const float f1 = a1.x == -INFINITY ? 0.f : exp2_sfu(a1.x - c);
-                const float ltot = a0.y * f0 + a1.y * f1;
+                const float m0 = s_ml[r].x, m1 = s_ml[256 + r].x;
+                const float c = fmaxf(m0, m1);
+                const float f0 = m0 == -INFINITY ? 0.f : exp2_sfu(m0 - c);
+                const float f1 = m1 == -INFINITY ? 0.f : exp2_sfu(m1 - c);
+                const float ltot = l0 * f0 + l1 * f1;
                 const float inv = ltot > 0.f ? 1.f / ltot : 0.f;
                 lse2 = ltot > 0.f ? c + __log2f(ltot) : -INFINITY;
                 w0 = f0 * inv;
                 w1 = f1 * inv;
-                ca = grp * (D / 2);
-                cb = ca + D / 2;
+                // 32 columns a warp (D = 64: the second warps have none)
+                ca = D == 128 ? grp * 64 + half * 32 : grp * 32;
+                cb = D == 128 || half == 0 ? ca + 32 : ca;
             } else {
-                const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-                lse2 = lsum > 0.f ? m + __log2f(lsum) : -INFINITY;
+                const float lg = grp ? l1 : l0;
+                const float inv = lg > 0.f ? 1.f / lg : 0.f;
+                lse2 = lg > 0.f ? m + __log2f(lg) : -INFINITY;
                 w0 = grp == 0 ? inv : 0.f;
                 w1 = grp == 1 ? inv : 0.f;
-                ca = 0;
-                cb = D;
+                ca = half * (D / 2);
+                cb = ca + D / 2;
             }
             const bool write = has && nsteps > 0;
             for (int c0 = ca; !idle && c0 < cb; c0 += 32) {
@@ -1073,7 +1061,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                      : "memory");
                 }
             }
-            if (write && (pair || grp == 0)) {
+            if (write && half == 0 && (pair || grp == 0)) {
                 if (it.out_base < 0) {
                     if (a.lse) a.lse[((size_t)l * a.nq + qt) * a.Hq + kvh * G + rr % G] = lse2 * 0.6931471805599453f;
                 } else {

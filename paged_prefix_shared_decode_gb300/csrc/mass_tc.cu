@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
         // the whole warp, converged; one elected lane issues
-        const uint32_t lead = elect_one();
+        const bool lead = elect_one();
+        const uint32_t tm = uniform(tmem), ks0 = uniform(k_smem), qs0 = uniform(q_smem);
         auto wait_all = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
         uint32_t i = 0, steps[2] = {0, 0};
         bool ok = true;
@@ -234,18 +235,21 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 tc_after();
                 const int n = min(kChunk, rows - c * kChunk);
                 const uint32_t idesc = idesc_bf16(kTok, max(16, (n + 15) & ~15), false);
-                const uint64_t kd = sdesc(k_smem + st * C::OPER, 16, 1024), qd = sdesc(q_smem + b * C::OPER, 16, 1024);
+                const uint64_t kd = sdesc(ks0 + st * C::OPER, 16, 1024), qd = sdesc(qs0 + b * C::OPER, 16, 1024);
+                const uint32_t d_tm = tm + sb * kChunk;
+                if (lead) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t o = ((uint32_t)(x >> 2) * C::SLAB + (uint32_t)(x & 3) * 32) >> 4;
-                    umma_ss(tmem + sb * kChunk, kd + o, qd + o, idesc, x > 0 ? 1u : 0u, lead);
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint32_t o = ((uint32_t)(x >> 2) * C::SLAB + (uint32_t)(x & 3) * 32) >> 4;
+                        umma_ss(d_tm, kd + o, qd + o, idesc, x > 0 ? 1u : 0u);
+                    }
+                    umma_commit(bar(C::B_S_FULL + sb));
                 }
-                umma_commit(bar(C::B_S_FULL + sb), lead);
             }
             (i & 1 ? steps[1] : steps[0]) = step;
-            umma_commit(bar(C::B_K_EMPTY + st), lead);
+            if (lead) umma_commit(bar(C::B_K_EMPTY + st));
         }
-        umma_commit(bar(C::B_DRAIN), lead);
+        if (lead) umma_commit(bar(C::B_DRAIN));
         settle(bar(C::B_DRAIN), 0);
         __syncwarp();
     } else if (warp == 2) {

@@ -101,39 +101,37 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major)
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// The MMA warp runs converged and issues under the predicate `lead` of one
-// elected lane, so that descriptors and addresses stay in uniform registers:
-// issued from inside `if (lane == 0)` a 64-cycle product took 66 to 73 cycles
-// with other warps at work beside it, this way 64.  (Its loop bounds must be
-// uniform too: uniform().)
-__device__ __forceinline__ uint32_t elect_one() {
+// The MMA warp runs converged and issues from inside `if (lead)` of one elected
+// lane, so that descriptors and addresses stay in uniform registers: issuing
+// an MMA takes 34 cycles this way, 66 from inside `if (lane == 0)` (and an
+// M = N = 128 MMA runs for 64).  What the operands are computed from has to
+// be uniform too: uniform().
+__device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n.reg .pred P;\nelect.sync _|P, 0xffffffff;\nselp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
-    return p;
+    return p != 0;
 }
 // A value that is the same in every lane, in a uniform register.
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 // D (TMEM) (+)= A (shared memory) * B (shared memory)
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate, uint32_t lead) {
+                                        uint32_t accumulate) {
     asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead));
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 // D (TMEM) (+)= A (TMEM) * B (shared memory)
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate, uint32_t lead) {
+                                        uint32_t accumulate) {
     asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead));
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
 }
-__device__ __forceinline__ void umma_commit(uint32_t bar, uint32_t lead) {
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
     asm volatile(
-        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
-        "r"(lead)
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
         : "memory");
 }
 
