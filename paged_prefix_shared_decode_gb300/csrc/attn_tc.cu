@@ -739,8 +739,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (ok) ok = wait_all(bar(C::B_O_EMPTY), (uc & 1) ^ 1);
                     tc_after();
                     if (ok && nsteps > 0) ok = wait_v(0);
-                    // K of the next step is waited for behind P_0 V, V of it
-                    // behind P_1 V, as late as the queue allows: the rings are
+                    // K of the next step is waited for behind P_0 V and V of it
+                    // at the end, as late as the queue allows: the rings are
                     // short, and waits half a step earlier made this 1.6 times
                     // slower
                     for (int t = 0; ok && t < nsteps; ++t) {
@@ -756,20 +756,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (C::APART) issue_pv(t, 0, t == 0);
                         ok = wait_p(1);
                         if (!ok) break;
-                        if (C::APART && more) {
+                        if (!C::APART) {
+                            issue_pv(t, 1, t == 0);
+                            free_v(t);
+                        }
+                        if (more) {
                             issue_s(t + 1, 1, 1);
                             free_k(t + 1);
                         }
-                        issue_pv(t, 1, t == 0);
-                        free_v(t);
-                        if (more) {
-                            ok = wait_v(t + 1);
-                            if (!ok) break;
-                            if (!C::APART) {
-                                issue_s(t + 1, 1, 1);
-                                free_k(t + 1);
-                            }
+                        if (C::APART) {
+                            issue_pv(t, 1, t == 0);
+                            free_v(t);
                         }
+                        if (more) ok = wait_v(t + 1);
                     }
                 } else {
                     for (int t = 0; ok && t < 2 && t < nsteps; ++t) {
