@@ -29,6 +29,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 #include "kvp_internal.h"
@@ -63,14 +64,29 @@ __device__ __forceinline__ int scan_warp(int x, int lane) {   // inclusive
     return x;
 }
 
+// The sequences and the tables: from the workspace, or from the image in the
+// kernel's parameters.
+template <class Image>
+__device__ __forceinline__ const EvictSeq *seqs_of(const EvictLaunch &a, const Image &image) {
+    return std::is_same<Image, InlineImage>::value ? reinterpret_cast<const EvictSeq *>(&image) : a.seqs;
+}
+template <class Image>
+__device__ __forceinline__ const int32_t *tables_of(const EvictLaunch &a, const Image &image) {
+    return std::is_same<Image, InlineImage>::value
+               ? reinterpret_cast<const int32_t *>(reinterpret_cast<const unsigned char *>(&image) + a.tables_at)
+               : a.tables;
+}
+
 // HOLD: the row's keys are kept in (dynamic) shared memory.
-template <bool HOLD>
-__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const EvictLaunch a) {
+template <bool HOLD, class Image>
+__global__ void __launch_bounds__(kSelThreads, 3)
+    evict_select_kernel(const EvictLaunch a, const __grid_constant__ Image image) {
     __shared__ __align__(16) int s_bin[kBins];
     __shared__ int s_sum[kSelWarps], s_eq[kSelWarps];
     __shared__ int s_digit, s_left;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const EvictSeq sq = a.seqs[blockIdx.x / a.Hkv % a.S];
+    if (blockIdx.x == 0 && tid == 0) *a.err = 0;
+    const EvictSeq sq = seqs_of(a, image)[blockIdx.x / a.Hkv % a.S];
     const float *m = a.mass + (size_t)blockIdx.x * a.stride;
     float *mo = a.mass_out ? a.mass_out + (size_t)blockIdx.x * a.stride : nullptr;
     int32_t *kept = a.kept + (size_t)blockIdx.x * a.budget;
@@ -217,12 +233,14 @@ __device__ __forceinline__ int64_t chunk_at(const EvictLaunch &a, const int32_t 
     return ((((int64_t)l * a.NB + blk) * a.Hkv + h) * a.bs + pos % a.bs) * a.CH + c;
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictLaunch a, int row_tiles) {
+template <class Image>
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_copy_kernel(const EvictLaunch a, int row_tiles, const __grid_constant__ Image image) {
     const int s = blockIdx.x / row_tiles, r0 = (blockIdx.x % row_tiles) * kRowTile;
-    const EvictSeq sq = a.seqs[s];
+    const EvictSeq sq = seqs_of(a, image)[s];
     if (sq.how != kEvictCopy) return;
     const int h = blockIdx.y % a.Hkv, l = blockIdx.y / a.Hkv;
-    const int32_t *src = a.tables + sq.src, *dst = a.tables + sq.dst;
+    const int32_t *src = tables_of(a, image) + sq.src, *dst = tables_of(a, image) + sq.dst;
     const int32_t *kept = a.kept + (((size_t)l * a.S + s) * a.Hkv + h) * a.budget;
     const uint4 *kp = static_cast<const uint4 *>(a.k_pool), *vp = static_cast<const uint4 *>(a.v_pool);
     uint4 *ko = static_cast<uint4 *>(a.k_pool), *vo = static_cast<uint4 *>(a.v_pool);
@@ -255,17 +273,19 @@ __global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictLau
 
 // One CTA per (in-place sequence, layer, kv head, K or V, column slice of
 // `width` chunks).
-__global__ void __launch_bounds__(kMoveThreads) evict_pack_kernel(const EvictLaunch a, int width) {
+template <class Image>
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_pack_kernel(const EvictLaunch a, int width, const __grid_constant__ Image image) {
     const int slices = a.CH / width;
     int x = blockIdx.x;
     const int slice = x % slices;
     x /= slices;
     uint4 *pool = static_cast<uint4 *>(x % 2 ? a.v_pool : a.k_pool);
     const int s = x / 2;
-    const EvictSeq sq = a.seqs[s];
+    const EvictSeq sq = seqs_of(a, image)[s];
     if (sq.how != kEvictPack) return;
     const int h = blockIdx.y % a.Hkv, l = blockIdx.y / a.Hkv;
-    const int32_t *src = a.tables + sq.src, *dst = a.tables + sq.dst;
+    const int32_t *src = tables_of(a, image) + sq.src, *dst = tables_of(a, image) + sq.dst;
     const int32_t *kept = a.kept + (((size_t)l * a.S + s) * a.Hkv + h) * a.budget;
     const int per = kMoveThreads / width;   // rows per step of the CTA
     const int row = threadIdx.x / width, c = slice * width + threadIdx.x % width;
@@ -291,28 +311,29 @@ __global__ void __launch_bounds__(kMoveThreads) evict_pack_kernel(const EvictLau
     }
 }
 
-// Per device: the selection kernel's shared-memory limit is raised once.
+// Per device: the selection kernels' shared-memory limit is raised once.
 bool select_ready() {
     static bool ok[kMaxDevices];
     static std::once_flag once[kMaxDevices];
     const int dev = current_device();
     if (dev < 0) return false;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kHoldKeys * 4) == cudaSuccess;
+        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        ok[dev] = cudaFuncSetAttribute(evict_select_kernel<true, NoImage>, attr, kHoldKeys * 4) == cudaSuccess &&
+                  cudaFuncSetAttribute(evict_select_kernel<true, InlineImage>, attr, kHoldKeys * 4) == cudaSuccess;
     });
     return ok[dev];
 }
 
-}  // namespace
-
-cudaError_t launch_evict(const EvictLaunch &a, int max_len, bool copies, bool packs, cudaStream_t stream) {
+template <class Image>
+cudaError_t launch_evict_with(const EvictLaunch &a, int max_len, bool copies, bool packs, const Image &image,
+                              cudaStream_t stream) {
     const unsigned rows = (unsigned)(a.L * a.S * a.Hkv);
     if (max_len <= kHoldKeys) {
         if (!select_ready()) return cudaErrorInvalidDevice;
-        evict_select_kernel<true><<<rows, kSelThreads, (size_t)max_len * 4, stream>>>(a);
+        evict_select_kernel<true><<<rows, kSelThreads, (size_t)max_len * 4, stream>>>(a, image);
     } else {
-        evict_select_kernel<false><<<rows, kSelThreads, 0, stream>>>(a);
+        evict_select_kernel<false><<<rows, kSelThreads, 0, stream>>>(a, image);
     }
     count_launch();
     cudaError_t e = cudaGetLastError();
@@ -320,18 +341,31 @@ cudaError_t launch_evict(const EvictLaunch &a, int max_len, bool copies, bool pa
     const unsigned lh = (unsigned)(a.L * a.Hkv);
     if (copies) {
         const int tiles = (a.budget + kRowTile - 1) / kRowTile;
-        evict_copy_kernel<<<dim3((unsigned)(tiles * a.S), lh), kMoveThreads, 0, stream>>>(a, tiles);
+        evict_copy_kernel<<<dim3((unsigned)(tiles * a.S), lh), kMoveThreads, 0, stream>>>(a, tiles, image);
         count_launch();
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (packs) {
         const int width = a.CH % 4 == 0 ? 4 : 1;
-        evict_pack_kernel<<<dim3((unsigned)(2 * a.S * (a.CH / width)), lh), kMoveThreads, 0, stream>>>(a, width);
+        evict_pack_kernel<<<dim3((unsigned)(2 * a.S * (a.CH / width)), lh), kMoveThreads, 0, stream>>>(a, width, image);
         count_launch();
         e = cudaGetLastError();
     }
     return e;
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictLaunch &a0, int max_len, bool copies, bool packs, const unsigned char *image,
+                         size_t bytes, size_t tables_at, cudaStream_t stream) {
+    EvictLaunch a = a0;
+    if (!image) return launch_evict_with(a, max_len, copies, packs, NoImage{}, stream);
+    if (bytes > kInlineMax) return cudaErrorInvalidValue;
+    a.tables_at = (int32_t)tables_at;
+    InlineImage in;
+    std::memcpy(in.b, image, bytes);
+    return launch_evict_with(a, max_len, copies, packs, in, stream);
 }
 
 }  // namespace kvp

@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
 #include <vector>
 
 #include <cuda.h>
@@ -251,6 +252,19 @@ struct Kv4Move {
 };
 cudaError_t launch_kv4_move(const Kv4Move &m, cudaStream_t stream);
 
+// A call's host image (its sequences and block tables) carried in the kernel
+// parameters when it is small, instead of a copy into the workspace: the copy
+// costs the host 3.5 us and the stream an operation of its own, as much as
+// the smallest calls' kernels.  (Read through the parameter itself: such an
+// address is no global one.)
+constexpr size_t kInlineMax = 3584;
+struct InlineImage {
+    alignas(16) unsigned char b[kInlineMax];
+};
+struct NoImage {
+    char none;
+};
+
 // Accumulated attention weight per cached token (mass_kernels.cu, mass_tc.cu).
 struct alignas(16) MassSeq {
     int32_t len, nq, q0;   // cached tokens, query tokens, first query row of q
@@ -271,9 +285,13 @@ struct MassLaunch {
     // position) and how many; the device error word
     const int4 *starts;
     int32_t *err;
+    int32_t tables_at;     // offset of the tables in an image carried in the parameters
 };
 // The kernel for at most 16 query rows (queries x GQA group) a sequence.
-cudaError_t launch_mass(const MassLaunch &a, int max_len, cudaStream_t stream);
+// image: the host image if it goes with the launch (a.seqs and a.tables are
+// then null), its tables at byte `tables_at`.
+cudaError_t launch_mass(const MassLaunch &a, int max_len, const unsigned char *image, size_t bytes, size_t tables_at,
+                        cudaStream_t stream);
 // The tcgen05 kernel: its CTAs' runs of tiles (returns their number, at most
 // ctas_max), whether it can address the pool, the launch.
 int mass_tc_starts(const MassLaunch &a, const MassSeq *seqs, int32_t ctas_max, std::vector<int4> &starts);
@@ -293,12 +311,15 @@ struct EvictLaunch {
     int32_t *kept;
     const EvictSeq *seqs;
     const int32_t *tables;
+    int32_t *err;          // the workspace's error word
+    int32_t tables_at;     // offset of the tables in an image carried in the parameters
     int64_t stride;
     int32_t L, S, Hkv, NB, bs, CH;   // CH: 16-byte chunks per row
     int32_t budget, sink, recent;
 };
-// max_len: the longest sequence.
-cudaError_t launch_evict(const EvictLaunch &a, int max_len, bool copies, bool packs, cudaStream_t stream);
+// max_len: the longest sequence; image: as for launch_mass.
+cudaError_t launch_evict(const EvictLaunch &a, int max_len, bool copies, bool packs, const unsigned char *image,
+                         size_t bytes, size_t tables_at, cudaStream_t stream);
 
 // A descriptor that the attention entry points accept.
 bool attn_desc_ok(const kvp_attn_desc *d);

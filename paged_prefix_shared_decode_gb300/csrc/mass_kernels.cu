@@ -26,6 +26,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <new>
 #include <vector>
 
@@ -71,7 +72,7 @@ __device__ __forceinline__ void load_k(KTile<D> &kt, const MassLaunch &a, const 
     for (int g = 0; g < 4; ++g) {
         const int pos = pos0 + 8 * g + t;
         const bool in = pos < len;
-        const int blk = in ? __ldg(table + (pos >> a.bs_log2)) : 0;
+        const int blk = in ? table[pos >> a.bs_log2] : 0;   // (may lie in the kernel's parameters)
         const __nv_bfloat16 *src =
             pool + head_base + (size_t)blk * block_stride + (size_t)(pos & ((1 << a.bs_log2) - 1)) * D + 8 * j;
 #pragma unroll
@@ -158,15 +159,19 @@ __device__ __forceinline__ void store_mass(const MassLaunch &a, size_t row, int 
     a.mass_out[row + pos] = v;
 }
 
-template <int D>
-__global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(const MassLaunch a) {
+template <int D, class Image>
+__global__ void __launch_bounds__(32 * kMassWarps)
+    mass_kernel(const MassLaunch a, const __grid_constant__ Image image) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
     const int kvh = blockIdx.y % a.Hkv, l = blockIdx.y / a.Hkv;
-    const MassSeq sq = a.seqs[s];
+    constexpr bool INLINE = std::is_same<Image, InlineImage>::value;
+    const unsigned char *img = reinterpret_cast<const unsigned char *>(&image);
+    if (INLINE && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.err = 0;
+    const MassSeq sq = INLINE ? reinterpret_cast<const MassSeq *>(img)[s] : a.seqs[s];
     const int first = chunk * a.tiles * kMassWarps * kMassTok;
     if (first >= sq.len) return;
-    const int32_t *table = a.tables + sq.table;
+    const int32_t *table = (INLINE ? reinterpret_cast<const int32_t *>(img + a.tables_at) : a.tables) + sq.table;
     const size_t head_base = (((size_t)l * a.NB * a.Hkv + kvh) << a.bs_log2) * D;
     const size_t out_row = (((size_t)l * a.S + s) * a.Hkv + kvh) * (size_t)a.stride;
     const int G = a.G, rows = sq.nq * G;
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(const MassLaunch 
 }
 
 template <int D>
-cudaError_t launch_mass_d(MassLaunch a, int max_len, cudaStream_t stream) {
+cudaError_t launch_mass_d(MassLaunch a, int max_len, const unsigned char *image, size_t bytes, cudaStream_t stream) {
     const int step = kMassWarps * kMassTok;
     const int64_t tiles = ((int64_t)max_len + step - 1) / step;
     // a CTA walks several tiles of tokens once there are CTAs enough to fill
@@ -215,16 +220,27 @@ cudaError_t launch_mass_d(MassLaunch a, int max_len, cudaStream_t stream) {
     a.tiles = (int)std::max<int64_t>(1, std::min<int64_t>(8, ctas / (8LL * 8 * device_sm_count())));
     a.chunks = (int)((tiles + a.tiles - 1) / a.tiles);
     if ((int64_t)a.chunks * a.S > INT32_MAX) return cudaErrorInvalidValue;
-    mass_kernel<D><<<dim3((unsigned)(a.chunks * a.S), (unsigned)(a.L * a.Hkv)), 32 * kMassWarps, 0, stream>>>(a);
+    const dim3 grid((unsigned)(a.chunks * a.S), (unsigned)(a.L * a.Hkv));
+    if (image) {
+        InlineImage in;
+        std::memcpy(in.b, image, bytes);
+        mass_kernel<D, InlineImage><<<grid, 32 * kMassWarps, 0, stream>>>(a, in);
+    } else {
+        mass_kernel<D, NoImage><<<grid, 32 * kMassWarps, 0, stream>>>(a, NoImage{});
+    }
     count_launch();
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_mass(const MassLaunch &a, int max_len, cudaStream_t stream) {
-    if (a.D == 64) return launch_mass_d<64>(a, max_len, stream);
-    if (a.D == 128) return launch_mass_d<128>(a, max_len, stream);
+cudaError_t launch_mass(const MassLaunch &a0, int max_len, const unsigned char *image, size_t bytes, size_t tables_at,
+                        cudaStream_t stream) {
+    MassLaunch a = a0;
+    a.tables_at = (int32_t)tables_at;
+    if (image && bytes > kInlineMax) return cudaErrorInvalidValue;
+    if (a.D == 64) return launch_mass_d<64>(a, max_len, image, bytes, stream);
+    if (a.D == 128) return launch_mass_d<128>(a, max_len, image, bytes, stream);
     return cudaErrorInvalidValue;
 }
 
@@ -361,13 +377,21 @@ int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, c
             ctas = mass_tc_starts(a, seqs, device_sm_count(), starts);
             std::copy(starts.begin(), starts.end(), reinterpret_cast<int4 *>(image.data() + w.starts));
         }
+        // sequences and tables, without the header and the starts
+        const size_t head = w.starts - w.seqs, need = head + sizeof(int32_t) * (size_t)at;
+        if (!tc && need <= kInlineMax) {
+            std::copy(tabs, tabs + at, reinterpret_cast<int32_t *>(image.data() + w.starts));
+            a.seqs = nullptr;
+            a.tables = nullptr;
+            return launch_mass(a, max_len, image.data() + w.seqs, need, head, st) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+        }
         // pageable source: the copy is staged before the call returns
         if (cudaMemcpyAsync(workspace, image.data(), w.total, cudaMemcpyHostToDevice, st) != cudaSuccess)
             return KVP_ERR_CUDA;
     } catch (const std::bad_alloc &) {
         return KVP_ERR_OOM;
     }
-    const cudaError_t e = tc ? launch_mass_tc(a, ctas, st) : launch_mass(a, max_len, st);
+    const cudaError_t e = tc ? launch_mass_tc(a, ctas, st) : launch_mass(a, max_len, nullptr, 0, 0, st);
     return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 

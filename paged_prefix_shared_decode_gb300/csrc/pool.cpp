@@ -448,8 +448,11 @@ int seq_evict(kvp_pool *p, const int32_t *seqs, int32_t n, const float *mass, in
     // (room for every block that goes back, so that nothing below throws)
     p->free_.reserve((size_t)d.num_blocks);
     cudaStream_t st = (cudaStream_t)stream;
-    // pageable source: the copy is staged before the call returns
-    if (cudaMemcpyAsync(workspace, image.data(), bytes, cudaMemcpyHostToDevice, st) != cudaSuccess)
+    // a small image goes with the kernels' parameters; else (pageable source)
+    // the copy is staged before the call returns
+    const size_t words = tables_at - 256 + sizeof(int32_t) * (size_t)at;
+    const bool small = words <= kvp::kInlineMax;
+    if (!small && cudaMemcpyAsync(workspace, image.data(), bytes, cudaMemcpyHostToDevice, st) != cudaSuccess)
         return KVP_ERR_CUDA;
 
     for (int32_t b : taken) p->ref[b] = 1;
@@ -474,7 +477,11 @@ int seq_evict(kvp_pool *p, const int32_t *seqs, int32_t n, const float *mass, in
     a.stride = mass_stride;
     a.L = d.num_layers; a.S = n; a.Hkv = d.num_kv_heads; a.NB = d.num_blocks; a.bs = bs; a.CH = d.head_dim / 8;
     a.budget = budget; a.sink = n_sink; a.recent = n_recent;
-    return kvp::launch_evict(a, max_len, copies, packs, st) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+    a.err = (int32_t *)workspace;
+    return kvp::launch_evict(a, max_len, copies, packs, small ? image.data() + 256 : nullptr, words, tables_at - 256,
+                             st) == cudaSuccess
+               ? KVP_OK
+               : KVP_ERR_CUDA;
 } catch (const std::bad_alloc &) {
     return KVP_ERR_OOM;
 }
