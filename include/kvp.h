@@ -502,14 +502,15 @@ int kvp_decode_step_run(kvp_step_plan *plan, const kvp_step_io *io, void *worksp
  * position p sees the keys j <= p with j > p - window or j < sinks;
  *   out = softmax(q k^T * scale) v over them, lse the natural log-sum-exp.
  * window >= 1 (one at least as long as the sequence gives causal attention),
- * sinks >= 0.  q, out: [L][T][Hq][d] bf16 and lse: [L][T][Hq] fp32 (or NULL),
- * sequence after sequence, T = sum of q_lens.  block_tables, seq_lens, desc,
- * workspace and errors as for paged_decode_attention, ws_bytes >=
- * kvp_window_workspace_size() for the same arguments; pages must be bf16.
+ * sinks >= 0, lengths below 2^31 - 128.  q, out: [L][T][Hq][d] bf16 and lse:
+ * [L][T][Hq] fp32 (or NULL), sequence after sequence, T = sum of q_lens.
+ * block_tables, seq_lens, desc, workspace and errors as for
+ * paged_decode_attention, ws_bytes >= kvp_window_workspace_size() for the
+ * same arguments; pages must be bf16.
  * With desc->use_sharing, batches of one query token per sequence read a
- * block that several of them share and see once.  Only tokens that some query of the
- * call sees are read; those must hold finite K and V (a query's masked
- * neighbours enter its products with weight 0).  A sequence may have no
+ * block that several of them share and see once.  Tokens that no query of the
+ * call sees do not matter; those that one sees must hold finite K and V (for
+ * the others they enter the products with weight 0).  A sequence may have no
  * cached token (q_lens[s] = 0 then).  KVP_ERR_STATE while `stream` is being
  * captured: the plan is uploaded from host memory.
  */
@@ -535,7 +536,8 @@ int paged_window_attention(const void *q, const int32_t *q_lens, const void *k_p
  * of attention over every cached token up to the query's own) hold them
  * sequence after sequence, T = sum of q_lens.  A row whose lse is -inf adds
  * nothing.  mass_in and mass_out are device fp32, [L][num_seqs][Hkv]
- * [mass_stride], mass_stride >= the longest sequence; they may be one buffer.
+ * [mass_stride], mass_stride >= the longest sequence; they are one buffer or
+ * do not overlap.
  * mass_in holds the first prev_lens[s] tokens (host; NULL: seq_lens - q_lens,
  * the tokens before this step's); later ones count as 0, and with mass_in
  * NULL all do.  Entries of mass_out from seq_lens[s] on are left as they are.
@@ -567,7 +569,9 @@ int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, c
  * mass_out (device, laid out like mass; NULL: not wanted; mass itself or
  * apart from it) their weights in the first `budget` entries.  A sequence of
  * at most `budget` tokens stays as it is: kept = 0, 1, ... then -1, its
- * weights copied.
+ * weights copied.  A slot of an evicted sequence is no token position any
+ * more: attention over all of it is what it was, but its blocks do not belong
+ * in a prefix cache, and a sliding window over it counts slots.
  * Pages that another sequence or the prefix cache also holds are not written:
  * the sequence gets fresh blocks for them, except for pages that hold sink
  * tokens alone, which stay shared.  Sharing is judged at the start of the

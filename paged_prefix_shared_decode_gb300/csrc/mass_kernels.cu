@@ -332,6 +332,11 @@ int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, c
         T += nq;
     }
     if (mass_stride < max_len || (T > 0 && (!q || !lse))) return KVP_ERR_INVALID;
+    if (mass_in && mass_in != mass_out) {   // in place, or apart
+        const uintptr_t x = (uintptr_t)mass_in, y = (uintptr_t)mass_out;
+        const uintptr_t n = (uintptr_t)desc->num_layers * desc->num_kv_heads * S * (uintptr_t)mass_stride * 4;
+        if (x < y + n && y < x + n) return KVP_ERR_INVALID;
+    }
     cudaStream_t st = (cudaStream_t)stream;
     if (stream_capturing(st)) return KVP_ERR_STATE;
     if (max_len == 0) return KVP_OK;

@@ -744,7 +744,8 @@ int build_window(const kvp_attn_desc &d, const int32_t *tables, const int32_t *l
     bool single = true;
     for (int32_t s = 0; s < S; ++s) {
         const int32_t nq = q_lens ? q_lens[s] : 1;
-        if (lens[s] < 0 || nq < 0 || nq > lens[s]) return KVP_ERR_INVALID;
+        // (positions plus a tile stay in 32 bits)
+        if (lens[s] < 0 || lens[s] > INT32_MAX - 2 * kTileTokens || nq < 0 || nq > lens[s]) return KVP_ERR_INVALID;
         const int64_t nb = ((int64_t)lens[s] + bs - 1) / bs;
         if (nb > MB) return KVP_ERR_INVALID;
         for (int64_t j = 0; j < nb; ++j) {

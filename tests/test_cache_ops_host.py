@@ -21,6 +21,7 @@ def mass(desc=None, q=A, q_lens=None, lse=A, k=A, tables=((0, 1),), lens=(20,), 
 @pytest.mark.parametrize("bad", [
     dict(q=None), dict(lse=None), dict(k=None), dict(out=None), dict(ws=None), dict(ws=A + 128), dict(ws_bytes=256),
     dict(q=A + 8), dict(k=A + 8), dict(lse=A + 2), dict(out=A + 1), dict(mass_in=A + 2),
+    dict(mass_in=A + 4),        # overlaps the output without being it
     dict(lens=(33,)), dict(lens=(-1,)), dict(lens=(0,)), dict(q_lens=(21,)), dict(q_lens=(-1,)),
     dict(prev=(21,)), dict(prev=(-1,)), dict(stride=19), dict(tables=((0, 8),)), dict(tables=((0, -1),)),
     dict(decay=float("inf")), dict(decay=float("nan")),

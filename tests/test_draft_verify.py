@@ -96,6 +96,13 @@ def test_against_the_walk(B, n, V, tree, draft):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("B,n,V", [(60, 3, 6001), (100, 3, 20001), (200, 2, 20000), (200, 2, 9001), (400, 1, 300)])
+def test_batches_on_smaller_clusters(B, n, V, draft):
+    check(inputs(B + V, B, n, V, True), draft)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("draft", [True, False])
 def test_many_siblings(draft):
     # 40 children of the root, most of them rejected, equal tokens among them
     d = inputs(5, 6, 40, 300)

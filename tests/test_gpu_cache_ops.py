@@ -89,6 +89,8 @@ def run_mass(desc, q, qlens, lse, k, tables, lens, decay, mass_in, prev, out):
     (4, 2, 16, 2, [0, 90, 5, 300, 64], [0, 5, 5, 33, 0]),
     (2, 2, 32, 1, [700, 140], [140, 140]),             # queries over several stages
     (64, 1, 16, 1, [77], [3]),
+    (4, 2, 128, 1, [500, 129, 128], [20, 129, 5]),     # blocks as long as a tile of tokens, and longer
+    (3, 2, 256, 2, [700, 256, 1], [50, 7, 1]),
 ])
 def test_mass(d, G, Hkv, bs, L, lens, qlens):
     ql = qlens or [1] * len(lens)
@@ -105,6 +107,24 @@ def test_mass(d, G, Hkv, bs, L, lens, qlens):
         err = (out[:, s, :, :n].double() - w).abs()
         # + the sum over rows (at most rows roundings) and the last fma
         assert (err <= (rtol + (ql[s] * G + 2) * 2.0 ** -24) * w).all(), (s, float((err / w.clamp(min=1e-300)).max()))
+
+
+@pytest.mark.parametrize("d,G,L,Hkv", [(64, 8, 3, 3), (128, 4, 2, 5), (128, 5, 1, 2)])
+def test_mass_many_sequences(d, G, L, Hkv):
+    """More tiles than CTAs, every run of them crossing sequences and heads of
+    one to many row chunks, some without queries or tokens."""
+    g = np.random.default_rng(d + G)
+    lens = [int(x) for x in g.integers(0, 1500, 30)]
+    ql = [min(n, int(g.choice([0, 1, 3, 40, 150]))) for n in lens]
+    desc, q, lse, k, tables, want, rtol = mass_case(d, G, Hkv, 16, L, lens, ql, seed=5)
+    old = torch.rand(L, 30, Hkv, 1500, device="cuda")
+    out = torch.full_like(old, -5.0)
+    for _ in range(2):      # the workspace and its barriers are used again
+        run_mass(desc, q, ql, lse, k, tables, lens, 0.5, old, None, out)
+    for s, n in enumerate(lens):
+        w = want[s] + 0.5 * old[:, s, :, :n].double() * (torch.arange(n, device="cuda") < n - ql[s])
+        assert ((out[:, s, :, :n].double() - w).abs() <= (rtol + (ql[s] * G + 2) * 2.0 ** -24) * w).all(), s
+        assert (out[:, s, :, n:] == -5).all()
 
 
 def test_mass_in_place_prev_and_none():
@@ -338,6 +358,37 @@ def test_evict_odd_weights_and_mass_in_place(same):
     check_evicted(pool, k, v, [s], before, ref, budget, 2, 3, kept, mo, 16)
     if not same:
         assert torch.equal(mass.nan_to_num(9.0), ref.nan_to_num(9.0))
+    kvp.kv_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("same", [True, False])
+def test_evict_long_rows(same):
+    # past what a CTA holds of a row's weights
+    n, budget = 70001, 20000
+    pool, k, v = make_pool(1, -(-n // 64) + 1, 1, 64, 8)
+    s = kvp.seq_alloc(pool)
+    kvp.seq_reserve(pool, s, n)
+    mass = weights(1, 1, 1, n)
+    before, ref = snapshot(pool, k, v, [s], 64), mass.clone()
+    kept, mo = evict(pool, [s], mass, budget, 4, 100, mass if same else None)
+    check_evicted(pool, k, v, [s], before, ref, budget, 4, 100, kept, mo, 64)
+    kvp.kv_pool_destroy(pool)
+
+
+def test_evict_many_sequences():
+    # an image of sequences and tables too long for the kernel parameters
+    pool, k, v = make_pool(1, 1500, 2, 16, 64, seqs=40)
+    seqs = [kvp.seq_alloc(pool) for _ in range(20)]
+    for i, s in enumerate(seqs):
+        kvp.seq_reserve(pool, s, 300 + 37 * i)
+    seqs += [kvp.seq_fork(pool, s) for s in seqs[:5]]
+    before = snapshot(pool, k, v, seqs, 16)
+    mass = weights(1, 25, 2, 1100)
+    kept, mo = evict(pool, seqs, mass, 333, 17, 40)
+    check_evicted(pool, k, v, seqs, before, mass, 333, 17, 40, kept, mo, 16)
+    for s in seqs:
+        kvp.seq_free(pool, s)
+    assert kvp.kvp_free_block_count(pool) == 1500
     kvp.kv_pool_destroy(pool)
 
 

@@ -137,6 +137,12 @@ def test_layers_scale_and_peaked_rows():
     check(64, 8, 2, 16, 3, [600, 90], [1, 1], 250, 7, scale=0.3, mul=4.0)
 
 
+@pytest.mark.parametrize("win,sinks", [(2 ** 31 - 1, 0), (1, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_longest_window_and_sinks(win, sinks):
+    check(64, 8, 2, 16, 1, [700, 65], [300, 1], win, sinks)
+    check(128, 4, 2, 16, 1, [700, 65], [1, 1], win, sinks)
+
+
 def test_unshared_plan():
     check(64, 8, 2, 16, 1, [400, 300, 64], [1, 1, 1], 100, 20, share=0)
 

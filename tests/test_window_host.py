@@ -45,3 +45,15 @@ def test_workspace_does_not_grow_with_the_cache():
     for bad in (dict(window=0, sinks=0), dict(window=4, sinks=-1)):
         with pytest.raises(kvp.KvpError):
             kvp.kvp_window_workspace_size(desc, t, [1000], [1], **bad)
+
+
+def test_longest_window_and_sinks():
+    # (the plan is made on the host: no sum of a position and a window overflows)
+    desc = kvp.AttnDesc(1, 32, 8, 128, 16, 200, 0.0, 1)
+    t = np.arange(200, dtype=np.int32)[None]
+    top = 2 ** 31 - 1
+    for n, q in ((1000, 1), (1000, 300), (3200, 3200), (1, 1), (0, 0)):
+        size = lambda w, s: kvp.kvp_window_workspace_size(desc, t, [n], [q], w, s)
+        assert size(top, 0) == size(5000, 0) and size(top, top) == size(5000, 5000) == size(5000, 0), (n, q)
+        assert size(1, top) == size(1, 5000)
+    assert call(lens=(top,), tables=np.zeros((1, 2 ** 27), np.int32)) == kvp.KVP_ERR_INVALID
