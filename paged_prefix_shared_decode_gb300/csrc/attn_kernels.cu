@@ -1136,8 +1136,8 @@ cudaError_t launch_d(const AttnLaunch &a, cudaStream_t stream, cudaEvent_t befor
             return cudaErrorUnknown;
         mma_stream = side.s;
     }
-    // A window call's mma.sync units are few and short (single query tokens
-    // beside prompt chunks): launched first they run while the persistent
+    // A window call's mma.sync units are short (many tokens decoding over short
+    // windows beside a prompt chunk): launched first they run while the persistent
     // tcgen05 CTAs start, instead of after these end
     const bool tc_last = fork && a.win > 0;
     cudaError_t e = tc_last ? cudaSuccess : launch_attention_tc(a, stream, 1);

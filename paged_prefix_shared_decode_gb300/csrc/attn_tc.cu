@@ -328,6 +328,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
 
     const int n_items = a.n_tc_units / (a.L * a.Hkv);
+    // unit -> item, layer and kv head.  Under a window the items run from the
+    // longest to the shortest, so that the last units, which leave SMs idle,
+    // are the shortest of all heads.
+    auto item_of = [&](int unit) { return WIN ? unit / (a.L * a.Hkv) : unit % n_items; };
+    auto head_of = [&](int unit) { return WIN ? unit % (a.L * a.Hkv) : unit / n_items; };
     const int G = a.G;
     const uint32_t q_smem = saddr(smem + C::Q_OFF);
     const uint32_t k_smem = saddr(smem + C::K_OFF);
@@ -364,8 +369,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool okw = wait_warp(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1);
             const int unit = okw ? s_unit[slot] : -1;
             if (unit < 0) break;
-            const int item_idx = unit % n_items;
-            const int lk = unit / n_items;
+            const int item_idx = item_of(unit);
+            const int lk = head_of(unit);
             const int kvh = lk % a.Hkv, l = lk / a.Hkv;
             const WorkItem it = a.tc_items[item_idx];
             const int ntile = item_tiles<WIN>(it);
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool done = !ok || unit >= a.n_tc_units || __shfl_sync(0xffffffffu, *s_abort, 0);
             WorkItem it{};
             if (!done) {
-                it = a.tc_items[unit % n_items];
+                it = a.tc_items[item_of(unit)];
                 const int ntile = item_tiles<WIN>(it);
                 const int4 *src = reinterpret_cast<const int4 *>(a.tiles + it.tile_begin);
                 int4 *dst = reinterpret_cast<int4 *>(s_desc + slot * kMaxItemTiles);
@@ -565,7 +570,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // Q of this unit, once the previous unit's S MMAs are done with it
             ok = wait_warp(bar(C::B_Q_EMPTY), (uc & 1) ^ 1);
             if (!ok) break;
-            const int lk = unit / n_items;
+            const int lk = head_of(unit);
             const int kvh = lk % a.Hkv, l = lk / a.Hkv;
             // (one 128-row tile, or two for a pair unit)
             const int rows = it.n_members * G;
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!wait_all(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1)) break;
                 const int unit = uniform(s_unit[slot]);
                 if (unit < 0) break;
-                const WorkItem it = a.tc_items[unit % n_items];
+                const WorkItem it = a.tc_items[item_of(unit)];
                 const int ntile = uniform(item_tiles<WIN>(it));
                 const int nsteps = (ntile + 1) >> 1;
                 const bool pair = uniform(it.n_members * G) > 128;
@@ -830,8 +835,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             bool ok = wait(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1);
             const int unit = ok ? s_unit[slot] : -1;
             if (soft_bar_or(!ok || unit < 0 || *s_abort)) break;
-            const int item_idx = unit % n_items;
-            const int lk = unit / n_items;
+            const int item_idx = item_of(unit);
+            const int lk = head_of(unit);
             const int kvh = lk % a.Hkv, l = lk / a.Hkv;
             const WorkItem it = a.tc_items[item_idx];
             const int ntile = item_tiles<WIN>(it);

@@ -689,6 +689,18 @@ void window_extend_plan(const kvp_attn_desc &d, const int32_t *tables, const int
         q0 += m;
     }
     hp.n_row_tiles = (int32_t)units.size();
+    // Units of few rows (decoding sequences, short chunks) beside tcgen05 units
+    // go with these when they are few or long: the mma.sync kernel beside the
+    // persistent CTAs takes SMs from them (7 decoding and 500 chunk tokens
+    // over windows of 4096, d = 64: 141 to 66 us; 63 and 100: 130 to 100).
+    // Many short ones are better off there (200 and 64 over 128: 29 us against
+    // 49; 63 and 100 over 512, d = 128: 63 against 72).
+    if (n_units[1] > 0 && (n_units[0] * lh <= sms || n_tiles[0] >= 12 * n_units[0])) {
+        for (Unit &u : units) u.tc = true;
+        n_units[1] += n_units[0];
+        n_tiles[1] += n_tiles[0];
+        n_units[0] = n_tiles[0] = 0;
+    }
     int64_t chunk[2];
     for (int k = 0; k < 2; ++k) {
         const int64_t target = k ? sms : (int64_t)sms * attention_ctas_per_sm(d.head_dim);
@@ -701,9 +713,30 @@ void window_extend_plan(const kvp_attn_desc &d, const int32_t *tables, const int
         }
     }
     // longest first, as the queues want them
-    std::stable_sort(units.begin(), units.end(), [](const Unit &a, const Unit &b) {
-        return (int64_t)(a.n_pre + a.t1 - a.t0) * a.n > (int64_t)(b.n_pre + b.t1 - b.t0) * b.n;
-    });
+    auto sort_units = [&] {
+        std::stable_sort(units.begin(), units.end(), [](const Unit &a, const Unit &b) {
+            return (int64_t)(a.n_pre + a.t1 - a.t0) * a.n > (int64_t)(b.n_pre + b.t1 - b.t0) * b.n;
+        });
+    };
+    sort_units();
+    // A last round of the tcgen05 queue that at most half of the SMs have a
+    // unit of is made of units of half the rows: one takes about 2/3 of the
+    // time of a pair (five ragged sequences of up to 777 queries over windows
+    // of 1000, with the queue in order of length over all heads: 84 to 76 us).
+    const int64_t rest = n_units[1] * lh % sms;
+    if (n_units[1] * lh > sms && rest > 0 && 2 * rest <= sms) {
+        int64_t left = (rest + lh - 1) / lh;
+        for (size_t i = units.size(); i-- > 0 && left > 0;) {
+            if (!units[i].tc || units[i].n * G <= 128) continue;
+            Unit half = units[i];
+            units[i].n = half.n / 2;
+            half.m0 += units[i].n;
+            half.n -= units[i].n;
+            units.push_back(half);
+            --left;
+        }
+        sort_units();
+    }
     int32_t P = 0;
     std::vector<MergeDesc> merge((size_t)q0, MergeDesc{0, 0});
     for (const Unit &u : units) {
