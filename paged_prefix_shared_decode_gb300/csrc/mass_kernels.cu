@@ -284,7 +284,7 @@ bool mass_layout(const kvp_attn_desc &d, const int32_t *tables, const int32_t *l
 }
 
 // More than 16 query rows go to the tcgen05 kernel (256 rows over 2 x about
-// 7000 tokens: 20 us; the same rows as 16-row tiles on mma.sync took 62 us).
+// 7000 tokens: 19 us; the same rows as 16-row tiles on mma.sync took 62 us).
 // Up to 16 the register kernel is faster (4 rows over 32 x about 9000 tokens:
 // 219 us against 260 us) and starts sooner.
 bool use_tc(const MassLaunch &a, int32_t max_q) { return (int64_t)max_q * a.G > 16; }

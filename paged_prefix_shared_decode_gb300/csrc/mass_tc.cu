@@ -26,9 +26,9 @@
 // Each group has two S buffers in TMEM (all 512 columns), so the tensor cores
 // work ahead of both.  Every wait is bounded, as in the attention kernel.
 //
-// What bounds it: the exponentials, 128 x 128 a step at 16 a clock and SM, and
+// What bounds it: the exponentials, 128 x 128 a step at 32 a clock and SM, and
 // on short runs the first loads.  256 rows over 2 x about 7000 tokens, 8 kv
-// heads of 128 (32 MB, 7 GFLOP): 20 us, 6 us of them exponentials.
+// heads of 128 (32 MB, 7 GFLOP): 19 us, 3 us of them exponentials.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
