@@ -2,7 +2,7 @@
 // sm_103a) for work items with more than 32 query rows: shared-prefix
 // segments read by many sequences, MCTS tree levels, draft-tree verification
 // and the prompt chunks of sliding-window attention (8192 queries over 4096
-// keys at d = 128: 385 us, 1.4 PFLOP/s).
+// keys at d = 128: 379 us, 1.45 PFLOP/s).
 //
 // One persistent CTA of 20 warps per SM.  A work unit is (item, layer, kv
 // head): up to 128 query rows (the item's members x the GQA group of the kv
@@ -19,7 +19,7 @@
 //               TMEM buffer g = step parity, and O_g += P_g V (M=128, N=d,
 //               K=128) with P_g read from TMEM.
 //   warp 3      claims units from an atomic counter, stages their tile
-//               descriptors in shared memory (two slots), and loads each
+//               descriptors and members in shared memory (two slots), and loads each
 //               unit's Q as soon as the previous unit's last S is done: by
 //               TMA boxes of whole rows (the G heads of consecutive query
 //               tokens) when the unit's members are consecutive tokens, else
@@ -27,15 +27,16 @@
 //   warps 4-11  softmax group 0 (even steps), warps 12-19 group 1 (odd
 //               steps), two threads per query row, one for each of a step's
 //               two tiles.  Each group keeps its own
-//               running max m_g, sum l_g and accumulator O_g, so while one
+//               reference m_g, sum l_g and accumulator O_g, so while one
 //               group turns step t's scores into P the tensor cores run the
 //               other group's P V and next S.  The two groups' (m, l, O) are
 //               merged when the unit ends.  In a pair unit group g takes
 //               every step for the rows of tile g and writes them alone.
 // P (bf16 pairs) overwrites the S columns it came from (at d = 64 it has
-// columns of its own), so it never passes through shared memory.  The running
-// max is raised only when a tile's P would sum to more than 2^32, so every
-// p <= 2^32; O_g is then rescaled in TMEM.
+// columns of its own), so it never passes through shared memory.  P is
+// formed with a reference that starts at 0 and is moved, with O_g rescaled in
+// TMEM, only when a tile's P would sum to more than 2^32 or a row's first
+// keys' to less than 2^-16: whole passes over S for a maximum are rare.
 // Every wait is bounded; on a timeout the CTA sets bit 4 of the workspace
 // error word and all roles leave their loops; before the CTA frees its TMEM
 // and ends, the producers let the copies they issued land and the MMA thread
@@ -74,6 +75,7 @@ constexpr int kStepTokens = 2 * kTileTokens;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kSlackSum = 4294967296.f;   // 2^32: bound on a step's sum of p
+constexpr float kLeastSum = 1.f / 65536.f;  // 2^-16: what a row's first keys give at least
 
 // Named barriers with an OR reduction, so that all their threads take the same
 // branch: 1 over the softmax threads, 2 + i over the two warps that share the
@@ -104,6 +106,13 @@ __device__ __forceinline__ int item_tiles(const WorkItem &it) {
     return it.tile_end - it.tile_begin + (WIN ? it.n_pre : 0);
 }
 
+// What the softmax threads need of a unit's member.
+struct RowInfo {
+    int32_t qt, pos;   // query token, its position (WIN)
+    uint64_t tree;     // ancestors-or-self among the draft nodes
+};
+constexpr int kMaxRows = 256;        // a pair unit's
+
 template <int D>
 struct TcCfg {
     static constexpr int NSLAB = D / 64;               // 64-column slabs (128-byte rows)
@@ -123,14 +132,19 @@ struct TcCfg {
     static constexpr int DESC_OFF = STG4_OFF + 2 * 2 * STG4_BUF;                      // [2][kMaxItemTiles]
     static constexpr int ML_OFF = DESC_OFF + 2 * kMaxItemTiles * (int)sizeof(KvTile);  // [2][2][128] float2
     static constexpr int XCH_OFF = ML_OFF + 4 * 128 * 8;                            // the same
-    static constexpr int UNIT_OFF = XCH_OFF + 4 * 128 * 8;                          // [2] ints
-    static constexpr int BAR_OFF = UNIT_OFF + 16;
+    static constexpr int UNIT_OFF = XCH_OFF + 4 * 128 * 8;                          // [2] ints, [2] items
+    static constexpr int ITEM_OFF = UNIT_OFF + 16;
+    static constexpr int BAR_OFF = ITEM_OFF + 2 * (int)sizeof(WorkItem);
+    static_assert(BAR_OFF % 8 == 0, "barriers on 8 bytes");
+    // bf16 pages stage no codes: the units' members lie there
+    static constexpr int ROW_OFF = STG4_OFF;                                        // [2][kMaxRows]
+    static_assert(2 * kMaxRows * (int)sizeof(RowInfo) <= 4 * STG4_BUF, "members over the 4-bit staging");
     static constexpr int B_UNIT_FULL = 0, B_UNIT_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = B_K_FULL + NK,
                          B_V_FULL = B_K_EMPTY + NK, B_V_EMPTY = B_V_FULL + NV, B_S_FULL = B_V_EMPTY + NV,
                          B_P_FULL = B_S_FULL + 2, B_Q_FULL = B_P_FULL + 2, B_Q_EMPTY = B_Q_FULL + 1,
                          B_O_FULL = B_Q_EMPTY + 1, B_O_EMPTY = B_O_FULL + 1, B_DRAIN = B_O_EMPTY + 1,
                          B_PV_DONE = B_DRAIN + 1,   // APART: per group
-                         N_BARS = B_PV_DONE + 2;
+                         B_ROWS_FULL = B_PV_DONE + 2, N_BARS = B_ROWS_FULL + 2;
     static constexpr int MISC_OFF = BAR_OFF + N_BARS * 8;   // tmem address, abort flag
     static constexpr int SMEM = MISC_OFF + 16 + 1024;       // + slack to align the base to 1024
     // D = 64 leaves room for P beside S, so that the next S need not wait for
@@ -263,6 +277,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     float2 *s_ml = reinterpret_cast<float2 *>(smem + C::ML_OFF);
     float2 *s_xch = reinterpret_cast<float2 *>(smem + C::XCH_OFF);
     volatile int *s_unit = reinterpret_cast<volatile int *>(smem + C::UNIT_OFF);
+    WorkItem *s_item = reinterpret_cast<WorkItem *>(smem + C::ITEM_OFF);
+    RowInfo *s_row = reinterpret_cast<RowInfo *>(smem + C::ROW_OFF);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
     const uint32_t bar0 = saddr(smem + C::BAR_OFF);
@@ -273,11 +289,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(C::B_UNIT_FULL + s), 1);
-            // unit slot free: MMA thread + softmax threads + K and V warps
-            mbar_init(bar(C::B_UNIT_EMPTY + s), 1 + kSoftThreads + kProdWarps);
+            // unit slot free: MMA, softmax, K and V warps
+            mbar_init(bar(C::B_UNIT_EMPTY + s), 1 + kSoftThreads / 32 + kProdWarps);
             mbar_init(bar(C::B_S_FULL + s), 1);
             mbar_init(bar(C::B_P_FULL + s), kGroupThreads);
             mbar_init(bar(C::B_PV_DONE + s), 1);
+            mbar_init(bar(C::B_ROWS_FULL + s), 1);
         }
         for (int s = 0; s < C::NK; ++s) {
             mbar_init(bar(C::B_K_FULL + s), 32);
@@ -290,7 +307,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(bar(C::B_Q_FULL), 32);
         mbar_init(bar(C::B_Q_EMPTY), 1);
         mbar_init(bar(C::B_O_FULL), 1);
-        mbar_init(bar(C::B_O_EMPTY), kSoftThreads);
+        mbar_init(bar(C::B_O_EMPTY), kSoftThreads / 32);
         mbar_init(bar(C::B_DRAIN), 1);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -370,11 +387,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool okw = wait_warp(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1);
             const int unit = okw ? s_unit[slot] : -1;
             if (unit < 0) break;
-            const int item_idx = item_of(unit);
             const int lk = head_of(unit);
             const int kvh = lk % a.Hkv, l = lk / a.Hkv;
-            const WorkItem it = a.tc_items[item_idx];
-            const int ntile = item_tiles<WIN>(it);
+            const int ntile = item_tiles<WIN>(s_item[slot]);
             const int nsteps = (ntile + 1) >> 1;
             const size_t layer_base = (size_t)l * a.NB * block_stride + (size_t)kvh * head_stride;
             const int row_base_lh = (l * a.NB) * a.Hkv + kvh;   // row of block b = (row_base_lh + b*Hkv) * bs
@@ -564,10 +579,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int i = lane; i < ntile * 2; i += 32) dst[i] = src[i];
                 }
             }
-            if (lane == 0) s_unit[slot] = done ? -1 : unit;
+            if (lane == 0) {
+                s_unit[slot] = done ? -1 : unit;
+                s_item[slot] = it;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_UNIT_FULL + slot));
             if (done) break;
+            // its members, for the softmax threads (who would otherwise go
+            // through two dependent loads at each unit's start: 1800 cycles)
+            if (!KV4) {
+                for (int i = lane; i < it.n_members; i += 32) {
+                    const int qt = __ldg(a.members + it.member_off + i);
+                    s_row[slot * kMaxRows + i] = RowInfo{qt, WIN ? __ldg(a.q_pos + qt) : 0,
+                                                         !WIN && a.tree_mask ? __ldg(a.tree_mask + qt) : ~0ull};
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_ROWS_FULL + slot));
+            }
             // Q of this unit, once the previous unit's S MMAs are done with it
             ok = wait_warp(bar(C::B_Q_EMPTY), (uc & 1) ^ 1);
             if (!ok) break;
@@ -657,10 +686,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!wait_all(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1)) break;
                 const int unit = uniform(s_unit[slot]);
                 if (unit < 0) break;
-                const WorkItem it = a.tc_items[item_of(unit)];
-                const int ntile = uniform(item_tiles<WIN>(it));
+                const int ntile = uniform(item_tiles<WIN>(s_item[slot]));
                 const int nsteps = (ntile + 1) >> 1;
-                const bool pair = uniform(it.n_members * G) > 128;
+                const bool pair = uniform(s_item[slot].n_members * G) > 128;
                 bool ok = wait_all(bar(C::B_Q_FULL), uc & 1);
                 // Q was written through the generic proxy (cp.async)
                 fence_async_smem();
@@ -782,24 +810,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         issue_s(t, 0, t & 1);
                         free_k(t);
                     }
+                    // K of step t + 2 is waited for behind P V of step t, and V is
+                    // freed before its S: the rings hold two steps at d = 128,
+                    // and either half a step later delays loads (8 x 2048 keys,
+                    // 64 rows: 5 % slower)
                     // the previous unit's epilogue has read O_0 and O_1
                     if (ok) ok = wait_all(bar(C::B_O_EMPTY), (uc & 1) ^ 1);
                     tc_after();
                     if (ok && nsteps > 0) ok = wait_v(0);
-                    if (ok && nsteps > 2) ok = wait_k(2);
+                    if (C::APART && ok && nsteps > 2) ok = wait_k(2);
                     for (int t = 0; ok && t < nsteps; ++t) {
                         ok = wait_p(t & 1);
                         if (!ok) break;
-                        if (!C::APART) issue_pv(t, t & 1, t < 2);
+                        if (!C::APART) {
+                            issue_pv(t, t & 1, t < 2);
+                            free_v(t);
+                            if (t + 2 < nsteps) ok = wait_k(t + 2);
+                            if (!ok) break;
+                        }
                         if (t + 2 < nsteps) issue_s(t + 2, 0, t & 1);
                         if (C::APART) {
                             if (t + 2 < nsteps) free_k(t + 2);
                             issue_pv(t, t & 1, t < 2);
+                            free_v(t);
                         }
-                        free_v(t);
                         if (!C::APART && t + 2 < nsteps) free_k(t + 2);
                         if (t + 1 < nsteps) ok = wait_v(t + 1);
-                        if (ok && t + 3 < nsteps) ok = wait_k(t + 3);
+                        if (C::APART && ok && t + 3 < nsteps) ok = wait_k(t + 3);
                     }
                 }
                 if (!ok) break;
@@ -830,15 +867,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t o_tm = tmem + lane_base + C::O_COL;
         const float sc = a.scale_log2;
         uint32_t ns = 0;   // S_FULL phases consumed by this group
-        for (int uc = 0;; ++uc) {
+        // one arrival a warp, behind what all its lanes did
+        auto arrive_warp = [&](uint32_t b) {
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        // the number of the unit in a slot (-1: no more)
+        auto take_unit = [&](int uc, bool &ok) -> int {
             const int slot = uc & 1;
-            bool ok = wait(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1);
-            const int unit = ok ? s_unit[slot] : -1;
-            if (soft_bar_or(!ok || unit < 0 || *s_abort)) break;
-            const int item_idx = item_of(unit);
+            ok = wait(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1) && ok;
+            const int u = ok ? s_unit[slot] : -1;
+            if (!KV4 && u >= 0) ok = wait(bar(C::B_ROWS_FULL + slot), (uc >> 1) & 1) && ok;
+            return u;
+        };
+        bool ok = true;
+        int unit = take_unit(0, ok);
+        if (soft_bar_or(!ok || *s_abort)) unit = -1;
+        for (int uc = 0; unit >= 0; ++uc) {
+            const int slot = uc & 1;
             const int lk = head_of(unit);
             const int kvh = lk % a.Hkv, l = lk / a.Hkv;
-            const WorkItem it = a.tc_items[item_idx];
+            const WorkItem it = s_item[slot];
             const int ntile = item_tiles<WIN>(it);
             const int nsteps = (ntile + 1) >> 1;
             const KvTile *tiles = s_desc + slot * kMaxItemTiles;
@@ -849,10 +899,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int rr = pair ? 128 * grp + r : r;
             const bool has = rr < rows;
             const int mem = rr / G;
-            int qt = 0;
-            if (has) qt = __ldg(a.members + it.member_off + mem);
-            const uint64_t tmask = !WIN && has && a.tree_mask ? a.tree_mask[qt] : ~0ull;
-            const int pos = WIN && has ? __ldg(a.q_pos + qt) : 0;
+            RowInfo row{0, 0, ~0ull};
+            if (has && !KV4) row = s_row[slot * kMaxRows + mem];
+            if (has && KV4) {
+                row.qt = __ldg(a.members + it.member_off + mem);
+                if (a.tree_mask) row.tree = a.tree_mask[row.qt];
+            }
+            const int qt = row.qt, pos = row.pos;
+            const uint64_t tmask = row.tree;
             int pos_lo = 0, pos_hi = 0;   // over the warp's rows
             if (WIN) {
                 pos_lo = __reduce_min_sync(0xffffffffu, has ? pos : INT32_MAX);
@@ -864,7 +918,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // row of O depends on its own row of P alone
             const bool idle = !__any_sync(0xffffffffu, has);
 
-            float m = -INFINITY, lsum = 0.f;
+            float m = 0.f, lsum = 0.f;
+            bool fresh = true;   // none of this thread's keys has gone into l yet
             for (int t = pair ? 0 : grp; t < nsteps; t += pair ? 1 : 2) {
                 // what the rows see of this warp's tile, while S is on its way
                 const bool there = 2 * t + half < ntile;
@@ -905,40 +960,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_arrive(bar(C::B_P_FULL + grp));
                     continue;
                 }
-                // A row's running max m is raised only when a tile's P would sum
-                // to more than 2^32, so every p <= 2^32, well inside bf16 and
-                // the fp32 sums.  A step therefore reads S once and forms P with
-                // the current m, in registers; only a row whose sum breaks the
-                // bound, or that has valid scores but no m yet, takes the slow
-                // path (the two warps' max, O_g and l rescaled, P again).  The
-                // two warps of a row meet once a step: they take the same
-                // path, and P may go into columns that the first one's S came
-                // from.
+                // P is formed with a reference m that need not be the row's
+                // running max: it starts at 0, and is moved only when a
+                // tile's P would sum to more than 2^32, or the row's first
+                // keys' to less than 2^-16 (all p then lie well inside bf16,
+                // and l and O inside the fp32 sums).  A step therefore reads
+                // S once and forms P in registers; only a row that breaks a
+                // bound takes the slow path (the two warps' max, O_g and l
+                // rescaled, P again).  The two warps of a row meet once a
+                // step: they take the same path, and P may go into columns
+                // that the first one's S came from.
                 // (ns steps of this group are seen: the products of the one
                 // before have read their P, and completed O_g; where P
                 // overwrites S they have anyway, since this S came after them)
                 if (C::APART && ns > 1) ok = wait(bar(C::B_PV_DONE + grp), ns & 1) && ok;
-                float ls = 0.f;
-                bool bad = some, slow = true;
-                if (!__all_sync(0xffffffffu, m == -INFINITY) || !__any_sync(0xffffffffu, some)) {
-                    const float nm = m == -INFINITY ? 0.f : -m;
+                float ls = 0.f, mx = -INFINITY;
+                bool bad, slow;
+                {
                     uint32_t pk[32];
-                    if (whole) p_pass<true>(s_tm, nm, sc, nv, tree, mask, pk, ls);
-                    else p_pass<false>(s_tm, nm, sc, nv, tree, mask, pk, ls);
-                    if (m != -INFINITY) bad = !(ls <= kSlackSum);
+                    if (whole) p_pass<true>(s_tm, -m, sc, nv, tree, mask, pk, ls);
+                    else p_pass<false>(s_tm, -m, sc, nv, tree, mask, pk, ls);
+                    bad = some && !(ls <= kSlackSum && (!fresh || ls >= kLeastSum));
                     slow = row_bar_or(row_bar, bad);
                     if (!slow) tmem_st32(p_tm, pk);
-                } else {   // the rows' first keys: straight to the slow path
-                    row_bar_or(row_bar, true);
                 }
                 if (slow) {
                     // (scale > 0: max of scaled scores = scale * max of raw scores)
-                    const float tmx = tile_max(s_tm, nv, tree, mask) * sc;
-                    *mine = make_float2(tmx, bad ? 1.f : 0.f);
+                    mx = tile_max(s_tm, nv, tree, mask) * sc;
+                    *mine = make_float2(mx, (bad ? 1.f : 0.f) + (fresh ? 2.f : 0.f));
                     row_bar_or(row_bar, false);
                     const float2 o2 = *other;
-                    const float m_new = bad || o2.y != 0.f ? fmaxf(m, fmaxf(tmx, o2.x)) : m;
-                    const bool resc = m_new != m && m != -INFINITY;
+                    mx = fmaxf(mx, o2.x);   // the row's
+                    const bool first = fresh && o2.y >= 2.f;   // l and O_g are still 0
+                    float m_new = m;
+                    if (bad || o2.y == 1.f || o2.y == 3.f) m_new = !first ? fmaxf(m, mx) : mx == -INFINITY ? 0.f : mx;
+                    const bool resc = m_new != m && !first;
                     if (__any_sync(0xffffffffu, resc)) {
                         // each warp rescales half of O_g's columns
                         const float f = resc ? exp2_sfu(m - m_new) : 1.f;
@@ -956,10 +1012,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     m = m_new;
                     ls = 0.f;
                     uint32_t pk[32];
-                    p_pass<false>(s_tm, m == -INFINITY ? 0.f : -m, sc, nv, tree, mask, pk, ls);
+                    p_pass<false>(s_tm, -m, sc, nv, tree, mask, pk, ls);
                     row_bar_or(row_bar, false);   // both have read S (and the other's max)
                     tmem_st32(p_tm, pk);
                 }
+                // (scores that are all -inf leave the row as it was)
+                fresh = fresh && !(some && (ls != 0.f || mx > -INFINITY));
                 lsum += ls;
                 tmem_wait_st();
                 tc_before();
@@ -970,6 +1028,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // warps write their own tile's rows from its own O
             ok = wait(bar(C::B_O_FULL), uc & 1) && ok;
             tc_after();
+            // (the next unit is known well before this one's end: one barrier
+            // settles both)
+            const int next = take_unit(uc + 1, ok);
             s_ml[(grp * 2 + half) * 128 + r] = make_float2(m, lsum);
             if (soft_bar_or(!ok || *s_abort)) break;
             float w0, w1, lse2;
@@ -977,7 +1038,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // the two warps of a row share m
             const float l0 = s_ml[r].y + s_ml[128 + r].y, l1 = s_ml[256 + r].y + s_ml[384 + r].y;
             if (!pair) {
-                const float m0 = s_ml[r].x, m1 = s_ml[256 + r].x;
+                const float m0 = l0 > 0.f ? s_ml[r].x : -INFINITY, m1 = l1 > 0.f ? s_ml[256 + r].x : -INFINITY;
                 const float c = fmaxf(m0, m1);
                 const float f0 = m0 == -INFINITY ? 0.f : exp2_sfu(m0 - c);
                 const float f1 = m1 == -INFINITY ? 0.f : exp2_sfu(m1 - c);
@@ -1004,7 +1065,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (pair) {   // this group's own tile: its O alone
                     tmem_ld32(o_tm + grp * D + c0, x);
                     tmem_wait_ld();
-                    if (!write) continue;
                     const float w = grp ? w1 : w0;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -1014,7 +1074,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tmem_ld32(o_tm + c0, x);
                     tmem_ld32(o_tm + D + c0, y);
                     tmem_wait_ld();
-                    if (!write) continue;
                     // an O with weight 0 may never have been written (a group
                     // with no steps or no valid key): select, do not multiply
 #pragma unroll
@@ -1024,37 +1083,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         x[j] = __float_as_uint(v0 + v1);
                     }
                 }
-                if (it.out_base < 0 && !out32) {
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                         (((size_t)l * a.nq + qt) * a.Hq + kvh * G + rr % G) * D + c0;
+                if (it.out_base < 0) {
+                    if (write) {
+                        // 32-byte stores when the output is 32-byte aligned (a row
+                        // of D bf16 is a multiple of 128 bytes and c0 of 32
+                        // columns): half the store instructions of 16-byte ones
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                                             (((size_t)l * a.nq + qt) * a.Hq + kvh * G + rr % G) * D + c0;
+                        uint32_t w[16];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        uint4 v;
-                        v.x = pack_bf16x2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-                        v.y = pack_bf16x2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
-                        v.z = pack_bf16x2(__uint_as_float(x[j + 4]), __uint_as_float(x[j + 5]));
-                        v.w = pack_bf16x2(__uint_as_float(x[j + 6]), __uint_as_float(x[j + 7]));
-                        *reinterpret_cast<uint4 *>(dst + j) = v;
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = pack_bf16x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+                        if (out32) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 8)
+                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst + 2 * j),
+                                             "r"(w[j]), "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]),
+                                             "r"(w[j + 5]), "r"(w[j + 6]), "r"(w[j + 7])
+                                             : "memory");
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<uint4 *>(dst + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                        }
                     }
-                } else if (it.out_base < 0) {
-                    // 32-byte stores when the output is 32-byte aligned (a row
-                    // of D bf16 is a multiple of 128 bytes and c0 of 32
-                    // columns): half the store instructions of 16-byte ones
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                         (((size_t)l * a.nq + qt) * a.Hq + kvh * G + rr % G) * D + c0;
-#pragma unroll
-                    for (int j = 0; j < 32; j += 16)
-                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst + j),
-                                     "r"(pack_bf16x2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]))),
-                                     "r"(pack_bf16x2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]))),
-                                     "r"(pack_bf16x2(__uint_as_float(x[j + 4]), __uint_as_float(x[j + 5]))),
-                                     "r"(pack_bf16x2(__uint_as_float(x[j + 6]), __uint_as_float(x[j + 7]))),
-                                     "r"(pack_bf16x2(__uint_as_float(x[j + 8]), __uint_as_float(x[j + 9]))),
-                                     "r"(pack_bf16x2(__uint_as_float(x[j + 10]), __uint_as_float(x[j + 11]))),
-                                     "r"(pack_bf16x2(__uint_as_float(x[j + 12]), __uint_as_float(x[j + 13]))),
-                                     "r"(pack_bf16x2(__uint_as_float(x[j + 14]), __uint_as_float(x[j + 15])))
-                                     : "memory");
-                } else {
+                } else if (write) {
                     // the workspace is 256-byte aligned: 32-byte stores
                     float *dst = a.part_o + (((size_t)l * a.Hkv + kvh) * a.P + it.out_base + rr) * D + c0;
 #pragma unroll
@@ -1072,9 +1125,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     a.part_lse[((size_t)l * a.Hkv + kvh) * a.P + it.out_base + rr] = lse2;
                 }
             }
-            tc_before();
-            mbar_arrive(bar(C::B_O_EMPTY));
-            mbar_arrive(bar(C::B_UNIT_EMPTY + slot));
+            arrive_warp(bar(C::B_O_EMPTY));
+            if (lane == 0) mbar_arrive(bar(C::B_UNIT_EMPTY + slot));
+            unit = next;
         }
     }
     tc_before();

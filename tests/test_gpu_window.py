@@ -143,6 +143,55 @@ def test_longest_window_and_sinks(win, sinks):
     check(128, 4, 2, 16, 1, [700, 65], [1, 1], win, sinks)
 
 
+SCORES = {   # of 320 keys, 64-token tiles
+    "all far down": lambda j: -300,
+    "all far up": lambda j: 300,
+    "first tile far down": lambda j: -300 if j < 64 else 0,
+    "second tile far down": lambda j: -300 if 64 <= j < 128 else 0,
+    "odd tiles far down": lambda j: -200 if j // 64 % 2 else -3,
+    "even tiles far down": lambda j: -3 if j // 64 % 2 else -200,
+    "rising": lambda j: j - 250,
+    "falling": lambda j: 100 - j,
+    "around the bounds": lambda j: (-12, 22, -11, 23, -14)[j // 64],
+    "down, then up": lambda j: -256 if j < 250 else 256,
+}
+
+
+@pytest.mark.parametrize("name", SCORES)
+@pytest.mark.parametrize("d,m", [(64, 20), (64, 10), (128, 30), (128, 12)])
+def test_prescribed_scores(name, d, m):
+    """Rows whose scores lie far from 0 or jump between tiles, in units of one
+    and of two row tiles."""
+    n, G, bs = 320, 8, 16
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    k = torch.zeros(1, n // bs, 1, bs, d, device="cuda", dtype=torch.bfloat16)
+    v = torch.randn(1, n // bs, 1, bs, d, device="cuda", generator=gen).to(torch.bfloat16)
+    score = torch.tensor([float(SCORES[name](j)) for j in range(n)], device="cuda")
+    k[0, :, 0, :, 0] = score.view(n // bs, bs).to(torch.bfloat16)
+    q = torch.zeros(1, m, G, d, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = 1
+    score = k[0, :, 0, :, 0].reshape(n).double()
+    desc = kvp.AttnDesc(1, G, 1, d, bs, n // bs, 1.0, 1)
+    tables = np.arange(n // bs, dtype=np.int32)[None]
+    see = torch.arange(n, device="cuda") <= torch.arange(n - m, n, device="cuda")[:, None]
+    for win, sinks in ((n, 0), (100, 70)):
+        vis = see & ((torch.arange(n, device="cuda") > torch.arange(n - m, n, device="cuda")[:, None] - win)
+                     | (torch.arange(n, device="cuda") < sinks))
+        x = score.expand(m, n).masked_fill(~vis, -math.inf)
+        want = torch.softmax(x, -1) @ v[0].double().view(n, d)
+        ws = torch.empty(kvp.kvp_window_workspace_size(desc, tables, [n], [m], win, sinks), dtype=torch.uint8,
+                         device="cuda")
+        out, lse = torch.empty_like(q), torch.empty(1, m, G, device="cuda")
+        kvp.paged_window_attention(q, [m], k, v, tables, [n], win, sinks, desc, out, lse, ws)
+        assert kvp.kvp_device_error(ws) == 0
+        # P and out in bf16 (2^-9 each, doubled); scores of up to 433 in base 2
+        # round by 433 * 2^-24, which the lse carries
+        err = (out[0].double() - want[:, None]).abs()
+        assert (err <= 2.0 ** -8 * (v.double().abs().max() + want[:, None].abs())).all(), (win, float(err.max()))
+        lw = torch.logsumexp(x, -1)[:, None]
+        assert ((lse[0].double() - lw).abs() <= 2.0 ** -18 * (1 + lw.abs())).all(), win
+
+
 def test_unshared_plan():
     check(64, 8, 2, 16, 1, [400, 300, 64], [1, 1, 1], 100, 20, share=0)
 
