@@ -630,9 +630,11 @@ void window_decode_protos(const kvp_attn_desc &d, const int32_t *tables, const i
 // tiles, then those from its first query's window on (one run from token 0
 // where the two meet); a unit takes tiles [pre] and a run of the others.
 // Units that alone would leave SMs idle, or hold more tiles than a kernel
-// stages, are cut into chunks whose partial rows are merged.
-void window_extend_plan(const kvp_attn_desc &d, const int32_t *tables, const int32_t *lens, const int32_t *q_lens,
-                        int32_t S, int32_t MB, int32_t win, int32_t sinks, int sms, HostPlan &hp) {
+// stages, are cut into chunks whose partial rows are merged.  KVP_ERR_INVALID
+// when its units or partial rows do not fit 32 bits (a prompt of 2^20 tokens
+// under a causal window has about 64 partial rows to a query row).
+int window_extend_plan(const kvp_attn_desc &d, const int32_t *tables, const int32_t *lens, const int32_t *q_lens,
+                       int32_t S, int32_t MB, int32_t win, int32_t sinks, int sms, HostPlan &hp) {
     const int32_t bs = d.block_size, G = d.num_q_heads / d.num_kv_heads;
     const int32_t lh = d.num_layers * d.num_kv_heads;
     // (the tcgen05 kernel for every unit of more than 32 rows, whatever the
@@ -737,11 +739,18 @@ void window_extend_plan(const kvp_attn_desc &d, const int32_t *tables, const int
         }
         sort_units();
     }
+    auto chunks_of = [&](const Unit &u) { return (u.n_pre + u.t1 - u.t0 + chunk[u.tc] - 1) / chunk[u.tc]; };
+    int64_t partial = 0, n_items = 0;
+    for (const Unit &u : units) {
+        const int64_t nc = chunks_of(u);
+        n_items += nc;
+        if (nc > 1) partial += nc * u.n * G;
+    }
+    if (partial > INT32_MAX || n_items * lh > INT32_MAX) return KVP_ERR_INVALID;
     int32_t P = 0;
     std::vector<MergeDesc> merge((size_t)q0, MergeDesc{0, 0});
     for (const Unit &u : units) {
-        const int64_t nt = u.n_pre + u.t1 - u.t0;
-        const int64_t nc = (nt + chunk[u.tc] - 1) / chunk[u.tc];
+        const int64_t nt = u.n_pre + u.t1 - u.t0, nc = chunks_of(u);
         if (nc > 1)
             for (int32_t m = 0; m < u.n; ++m) merge[u.m0 + m] = MergeDesc{(int32_t)(hp.entries.size() + m * nc), (int32_t)nc};
         const size_t e0 = hp.entries.size();
@@ -768,6 +777,7 @@ void window_extend_plan(const kvp_attn_desc &d, const int32_t *tables, const int
     hp.n_partial_rows = P;
     hp.n_units = (int32_t)hp.items.size() * lh;
     hp.n_tc_units = (int32_t)hp.tc_items.size() * lh;
+    return KVP_OK;
 }
 
 int build_window(const kvp_attn_desc &d, const int32_t *tables, const int32_t *lens, const int32_t *q_lens, int32_t S,
@@ -801,10 +811,9 @@ int build_window(const kvp_attn_desc &d, const int32_t *tables, const int32_t *l
         finish(hp, sc, G, S, d.num_layers * d.num_kv_heads, sms, attention_ctas_per_sm(d.head_dim),
                tc_usable(d) ? tc_row_threshold(d.head_dim) : INT32_MAX);
         for (int32_t s = 0; s < S; ++s) hp.q_pos.push_back(lens[s] - 1);
-    } else {
-        window_extend_plan(d, tables, lens, q_lens, S, MB, hp.win, hp.sinks, sms, hp);
+        return KVP_OK;
     }
-    return KVP_OK;
+    return window_extend_plan(d, tables, lens, q_lens, S, MB, hp.win, hp.sinks, sms, hp);
 }
 
 bool desc_ok(const kvp_attn_desc *d) {

@@ -57,3 +57,17 @@ def test_longest_window_and_sinks():
         assert size(top, 0) == size(5000, 0) and size(top, top) == size(5000, 5000) == size(5000, 0), (n, q)
         assert size(1, top) == size(1, 5000)
     assert call(lens=(top,), tables=np.zeros((1, 2 ** 27), np.int32)) == kvp.KVP_ERR_INVALID
+
+
+@pytest.mark.parametrize("G", [32, 64])
+def test_more_partial_rows_than_32_bits_hold_are_refused(G):
+    # a causal prompt: a query row has one partial row per 8192 keys that it sees
+    desc = kvp.AttnDesc(1, G, 1, 128, 16, 1 << 16, 0.0, 1)
+    t = np.arange(1 << 16, dtype=np.int32)[None]
+    size = lambda n: kvp.kvp_window_workspace_size(desc, t, [n], [n], n, 0)
+    n = 1 << 17
+    rows = G * sum((p // 256 * 256 + 256 + 8191) // 8192 if p >= 8192 else 0 for p in range(0, n, 256)) * 256
+    assert size(n) >= rows * 129 * 4
+    with pytest.raises(kvp.KvpError):
+        size(1 << 20)
+    assert call(desc=desc, tables=t, lens=(1 << 20,), q_lens=(1 << 20,), win=1 << 20) == kvp.KVP_ERR_INVALID
