@@ -19,7 +19,7 @@ __all__ = [
     "KvpError", "PoolDesc", "AttnDesc", "load", "lib_path",
     "kv_pool_create", "kv_pool_create_kv4", "kv_pool_destroy", "seq_alloc", "seq_fork", "seq_free", "seq_append",
     "seq_append_batch", "seq_reserve", "seq_block_table", "seq_len", "block_refcount",
-    "kvp_free_block_count", "kvp_cow_count", "kvp_gather_tables", "kvp_export_tables",
+    "kvp_free_block_count", "kvp_cow_count", "kvp_pool_shape", "kvp_gather_tables", "kvp_export_tables",
     "kvp_decode_workspace_size", "paged_decode_attention", "kvp_verify_workspace_size",
     "tree_verify_attention", "kvp_device_error", "kvp_decode_plan_stats", "kvp_strerror",
     "kvp_set_kernel_events", "kvp_kernel_launches", "paged_decode_attention_noalloc",
@@ -103,6 +103,7 @@ _SIGS = {
     "block_refcount": ([_P, _I32, _I32P], ctypes.c_int),
     "kvp_free_block_count": ([_P, _I32P], ctypes.c_int),
     "kvp_cow_count": ([_P, ctypes.POINTER(ctypes.c_int64)], ctypes.c_int),
+    "kvp_pool_shape": ([_P, _P, _P], ctypes.c_int),
     "kvp_gather_tables": ([_P, _P, _I32, _I32, _P, _P], ctypes.c_int),
     "kvp_export_tables": ([_P, _P, _I32, _I32, _P, _P, _P], ctypes.c_int),
     "kvp_decode_workspace_size": ([ctypes.POINTER(AttnDesc), _P, _P, _I32, _I32], ctypes.c_size_t),
@@ -312,6 +313,13 @@ def kvp_cow_count(pool) -> int:
     n = ctypes.c_int64()
     _check(load().kvp_cow_count(pool, ctypes.byref(n)), "kvp_cow_count")
     return n.value
+
+
+def kvp_pool_shape(pool):
+    """The pool's layers and kv heads."""
+    layers, heads = _I32(), _I32()
+    _check(load().kvp_pool_shape(pool, ctypes.byref(layers), ctypes.byref(heads)), "kvp_pool_shape")
+    return layers.value, heads.value
 
 
 def kvp_gather_tables(pool, seqs, width: int):
@@ -671,13 +679,15 @@ def seq_evict_workspace_size(pool, seqs, budget: int) -> int:
 def seq_evict(pool, seqs, mass, budget: int, n_sink: int, n_recent: int, kept, mass_out, workspace, ws_bytes=None,
               stream=None):
     """Keeps `budget` tokens of each sequence by accumulated weight mass
-    [L][n][Hkv][stride] fp32; kept [L][n][Hkv][budget] int32 receives their
-    positions, mass_out (like mass, mass itself or None) their weights."""
+    [L][n][Hkv][stride] fp32 (L, Hkv: the pool's); kept [L][n][Hkv][budget]
+    int32 receives their positions, mass_out (like mass, mass itself or None)
+    their weights."""
     s, sp = _host_i32(seqs)
-    if mass.dim() != 4 or mass.shape[1] != len(s):
-        raise ValueError(f"mass: expected [L][{len(s)}][Hkv][stride], got shape {tuple(mass.shape)}")
+    layers, heads = kvp_pool_shape(pool)
+    if mass.dim() != 4:
+        raise ValueError(f"mass: expected [{layers}][{len(s)}][{heads}][stride], got shape {tuple(mass.shape)}")
     torch, dev = _torch()
-    f32, shape = torch.float32, mass.shape
+    f32, shape = torch.float32, (layers, len(s), heads, mass.shape[3])
     _check(load().seq_evict(pool, sp, len(s), _arg("mass", mass, f32, shape, dev), shape[3], budget, n_sink, n_recent,
                             _arg("kept", kept, torch.int32, (*shape[:3], budget), dev),
                             _arg("mass_out", mass_out, f32, shape, dev), _dev(workspace),

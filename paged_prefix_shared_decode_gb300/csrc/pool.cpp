@@ -592,6 +592,13 @@ int kvp_cow_count(const kvp_pool *p, int64_t *n_out) {
     return KVP_OK;
 }
 
+int kvp_pool_shape(const kvp_pool *p, int32_t *layers_out, int32_t *kv_heads_out) {
+    if (!p || !layers_out || !kv_heads_out) return KVP_ERR_INVALID;
+    *layers_out = p->desc.num_layers;
+    *kv_heads_out = p->desc.num_kv_heads;
+    return KVP_OK;
+}
+
 int kvp_gather_tables(const kvp_pool *p, const int32_t *seqs, int32_t n, int32_t width,
                       int32_t *h_tables, int32_t *h_lens) {
     if (!p || n < 0 || width < 0 || (n > 0 && !seqs)) return KVP_ERR_INVALID;

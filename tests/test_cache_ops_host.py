@@ -91,3 +91,57 @@ def test_evict_workspace():
         with pytest.raises(kvp.KvpError):
             kvp.seq_evict_workspace_size(p, seqs, budget)
     kvp.kv_pool_destroy(p)
+
+
+class Tensor:
+    """What the binding asks of a tensor on the current device, at an address that nothing here may reach."""
+
+    def __init__(self, dtype, *shape, device=0):
+        import torch
+        self.dtype, self.shape, self.device = dtype, torch.Size(shape), device
+        self.is_cuda = True
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return 4
+
+    def data_ptr(self):
+        return A
+
+
+@pytest.mark.parametrize("wrong", ["mass", "kept", "mass_out"])
+@pytest.mark.parametrize("shape", [(1, 1, 3, 128), (2, 1, 1, 128), (2, 1, 2, 128), (3, 1, 3, 128), (2, 1, 4, 128),
+                                   (2, 2, 3, 128), (2, 3, 128)])
+def test_evict_weights_are_of_the_pool_s_layers_and_heads(wrong, shape):
+    import torch
+    p = kvp.kv_pool_create(kvp.PoolDesc(2, 16, 16, 3, 64, 4, 8, 0), A, A)
+    s = kvp.seq_alloc(p)
+    kvp.seq_reserve(p, s, 100)
+    good = dict(mass=(2, 1, 3, 128), kept=(2, 1, 3, 40), mass_out=(2, 1, 3, 128))
+    # one tensor too small or too large, and all of them of the same wrong layers and heads
+    for names in ([wrong], list(good)):
+        sh = {**good, **{n: shape[:-1] + good[n][-1:] for n in names}}
+        with pytest.raises(ValueError, match="expected"):
+            kvp.seq_evict(p, [s], Tensor(torch.float32, *sh["mass"]), 40, 4, 8, Tensor(torch.int32, *sh["kept"]),
+                          Tensor(torch.float32, *sh["mass_out"]), A, 1 << 16, stream=0)
+    assert kvp.seq_len(p, s) == 100 and kvp.kvp_free_block_count(p) == 9
+    kvp.kv_pool_destroy(p)
+
+
+def test_pool_shape():
+    p = kvp.kv_pool_create(kvp.PoolDesc(2, 16, 16, 3, 64, 4, 8, 0))
+    assert kvp.kvp_pool_shape(p) == (2, 3)
+    kvp.kv_pool_destroy(p)
+    for bad in ((None, A, A), (A, None, A), (A, A, None)):
+        assert kvp.load().kvp_pool_shape(*bad) == kvp.KVP_ERR_INVALID
