@@ -89,8 +89,9 @@ __device__ __forceinline__ uint64_t weight(float p, float q, uint64_t c) {
     if (MODE == 1) {
         b = to_fixed<kOne>(prob(q));
     } else {   // 57 + 63 fraction bits, 60 of them kept
-        const uint64_t f = to_fixed<63>(prob(q));
-        b = (__umul64hi(c, f) << 4) | ((c * f) >> 60);
+        const uint64_t f = to_fixed<63>(prob(q)), hi = __umul64hi(c, f);
+        if (hi >> 56) return 0u;   // c q >= 1 >= p (c reaches 127, and from c q = 16 on 64 bits would not hold it)
+        b = hi << 4 | (c * f) >> 60;
     }
     return a > b ? a - b : 0u;
 }

@@ -113,6 +113,54 @@ def test_many_siblings(draft):
     assert (got[:, 1] <= 1).all()
 
 
+def sharp_siblings(n, V, pairs, u_next):
+    """n children of the root, all of one token that the draft row is nearly
+    certain of and the target rejects: c q(x) grows past n / 2.  pairs: (p, q)
+    of that token, one per sequence; the rest of p lies on one other token."""
+    B = len(pairs)
+    d = dict(p=np.zeros((B, n + 1, V), np.float32), q=np.zeros((B, n, V), np.float32),
+             par=np.full((B, n), -1, np.int32), tok=np.zeros((B, n), np.int32),
+             u=np.full((B, n), 1.0 - 2.0 ** -24, np.float32), un=np.full(B, u_next, np.float32))
+    for b, (p, q) in enumerate(pairs):
+        x, y = (7 * b + 3) % V, (V - 1 - 5 * b) % V
+        d["tok"][b] = x
+        d["p"][b, 0, x], d["p"][b, 0, y] = p, np.float32(1) - np.float32(p)
+        d["q"][b, 0, x], d["q"][b, 0, y] = q, np.float32(1) - np.float32(q)
+    return d
+
+
+# rows held in registers (up to 32768 tokens a sequence of a small batch), read
+# as vectors (a length that is a multiple of 4) and element by element
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [40, 301, 40000, 40001])
+@pytest.mark.parametrize("n,p,q", [(17, 1 / 16, 1.0), (31, 0.5, 1.0), (61, 0.75, 1.0), (64, 1 / 16, 1.0),
+                                   (64, 0.25, 0.96875), (24, 0.125, 0.9375)])
+def test_many_siblings_under_a_sharp_draft(V, n, p, q):
+    # c q(x) reaches 16 and more: the token is spent, its residual stays 0
+    for un in (0.0, 0.03, 0.4):
+        d = sharp_siblings(n, V, [(p, q), (p / 2, q), (p, 1.0)], un)
+        got = check(d)
+        assert (got[:, 1] == 0).all() and (got[:, 2] != d["tok"][:, 0]).all()
+
+
+@pytest.mark.gpu
+def test_sharp_siblings_over_random_rows():
+    # p(x) of 0.05 to 0.3 and q(x) of 0.9 to 0.99 on one token, the rest spread
+    g = np.random.default_rng(11)
+    B, n, V = 24, 64, 33
+    d = sharp_siblings(n, V, [(0.1, 0.9)] * B, 0.5)
+    for b in range(B):
+        x = d["tok"][b, 0]
+        for name, top in (("p", g.uniform(0.05, 0.3)), ("q", g.uniform(0.9, 0.99))):
+            r = g.random(V)
+            r[x] = 0
+            r *= (1 - top) / r.sum()
+            r[x] = top
+            d[name][b, 0] = r
+    d["un"] = g.random(B).astype(np.float32)
+    check(d)
+
+
 @pytest.mark.gpu
 def test_no_drafts_is_sampling():
     d = inputs(6, 5, 3, 777)
