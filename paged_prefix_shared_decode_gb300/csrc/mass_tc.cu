@@ -21,8 +21,8 @@
 //               for the MMA issuer
 //   warps 3-10  epilogue, two groups of four warps that take turns with the
 //               tiles, one thread per token: w = 2^(s * scale - lse) over the
-//               chunk's columns, masked by position, added up in fp32; after
-//               the last chunk out = decay * in + sum
+//               chunk's columns, masked by position, added up in fp32 (the
+//               chunks with compensation); after the last out = decay * in + sum
 // Each group has two S buffers in TMEM (all 512 columns), so the tensor cores
 // work ahead of both.  Every wait is bounded, as in the attention kernel.
 //
@@ -355,8 +355,11 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             const size_t at = ((((size_t)(w.lh / a.Hkv) * a.S + w.s) * a.Hkv + w.lh % a.Hkv)) * (size_t)a.stride + pos;
             float old = 0.f;
             if (in && a.mass_in && pos < w.sq.prev) old = a.mass_in[at];
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            // the chunks' sums are added up with their roundings carried along
+            // (one running sum over 131072 equal weights was off by 3e-4)
+            float sum = 0.f, rest = 0.f;
             for (int c = w.c0; c < w.c1; ++c, ++step) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
                 const int b = c & 1, sb = 2 * grp + (step & 1);
                 ok = wait(bar(C::B_Q_FULL + sb), (step >> 1) & 1) && ok;   // (the rows' lse)
                 ok = wait(bar(C::B_S_FULL + sb), (step >> 1) & 1) && ok;
@@ -398,8 +401,11 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 }
                 tc_before();
                 mbar_arrive(bar(C::B_S_EMPTY + sb));
+                const float x = (acc[0] + acc[1]) + (acc[2] + acc[3]), up = sum + x;
+                rest += sum < x ? (x - up) + sum : (sum - up) + x;   // (both are positive)
+                sum = up;
             }
-            if (ok && in) a.mass_out[at] = fmaf(a.decay, old, (acc[0] + acc[1]) + (acc[2] + acc[3]));
+            if (ok && in) a.mass_out[at] = fmaf(a.decay, old, isfinite(sum) ? sum + rest : sum);
         }
     }
     tc_before();

@@ -109,6 +109,40 @@ def test_mass(d, G, Hkv, bs, L, lens, qlens):
         assert (err <= (rtol + (ql[s] * G + 2) * 2.0 ** -24) * w).all(), (s, float((err / w.clamp(min=1e-300)).max()))
 
 
+@pytest.mark.parametrize("d,G,lse", [(64, 16, 9.0), (128, 16, 7.3), (64, 5, 11.7)])
+def test_mass_of_a_long_chunk_of_equal_weights(d, G, lse):
+    """Up to 131072 rows give a token the same weight: roundings of one running sum all go the same way and add up."""
+    lens, ql = [8200, 300], [8192, 300]
+    desc, q, z, k, tables, _, _ = mass_case(d, 1, 1, 16, 1, lens, [1, 1])
+    desc.num_q_heads = G
+    q = torch.zeros(1, sum(ql), G, d, device="cuda", dtype=torch.bfloat16)      # every score is 0
+    z = torch.full((1, sum(ql), G), lse, device="cuda")
+    out = torch.full((1, 2, 1, 8200), -5.0, device="cuda")
+    run_mass(desc, q, ql, z, k, tables, lens, 1.0, None, None, out)
+    w = float(torch.exp(-z.double()[0, 0, 0]))
+    # the exponent's argument: log2 e and its product with lse, half a step each
+    # (relative 2^-24, of |lse| as a natural exponent); exp2 itself 2^-21; the
+    # sum: 32 terms to an accumulator, two steps to join them, and the sum over
+    # the chunks and its last step, whatever the number of rows
+    tol = lse * 2.0 ** -23 + 2.0 ** -21 + 38 * 2.0 ** -24
+    for s, (n, m) in enumerate(zip(lens, ql)):
+        pos = torch.arange(n, device="cuda")
+        want = (n - pos.clamp(min=n - m)).double() * G * w
+        err = (out[0, s, 0, :n].double() - want).abs() / want
+        assert (err <= tol).all(), (s, float(err.max()), tol)
+        assert (out[0, s, 0, n:] == -5).all()
+
+
+def test_mass_of_a_long_chunk():
+    lens, ql = [4400, 1000], [4096, 999]
+    desc, q, lse, k, tables, want, rtol = mass_case(128, 4, 1, 16, 1, lens, ql, seed=3)
+    out = torch.zeros(1, 2, 1, 4400, device="cuda")
+    run_mass(desc, q, ql, lse, k, tables, lens, 1.0, None, None, out)
+    for s, n in enumerate(lens):
+        err = (out[:, s, :, :n].double() - want[s]).abs()
+        assert (err <= (rtol + 38 * 2.0 ** -24) * want[s]).all(), s
+
+
 @pytest.mark.parametrize("d,G,L,Hkv", [(64, 8, 3, 3), (128, 4, 2, 5), (128, 5, 1, 2)])
 def test_mass_many_sequences(d, G, L, Hkv):
     """More tiles than CTAs, every run of them crossing sequences and heads of
