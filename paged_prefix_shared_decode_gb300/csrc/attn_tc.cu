@@ -4,11 +4,11 @@
 // and the prompt chunks of sliding-window attention (8192 queries over 4096
 // keys at d = 128: 379 us, 1.45 PFLOP/s).
 //
-// One persistent CTA of 20 warps per SM.  A work unit is (item, layer, kv
-// head): up to 128 query rows (the item's members x the GQA group of the kv
-// head), or a pair unit of up to 256 rows as two 128-row tiles over one K/V
-// stream, against the item's 64-token KV tiles, taken two at a time as
-// 128-token steps.
+// One persistent CTA of 12 warps per SM (20 under a window).  A work unit is
+// (item, layer, kv head): up to 128 query rows (the item's members x the GQA
+// group of the kv head), or a pair unit of up to 256 rows as two 128-row tiles
+// over one K/V stream, against the item's 64-token KV tiles, taken two at a
+// time as 128-token steps.
 //   warp 0      K producer, warp 1 V producer.  Each fills its own ring, since
 //               K is released as soon as S = Q K^T is computed and V only once
 //               P V is.  Whole tiles whose blocks start on a box boundary are
@@ -19,19 +19,21 @@
 //               TMEM buffer g = step parity, and O_g += P_g V (M=128, N=d,
 //               K=128) with P_g read from TMEM.
 //   warp 3      claims units from an atomic counter, stages their tile
-//               descriptors and members in shared memory (two slots), and loads each
-//               unit's Q as soon as the previous unit's last S is done: by
-//               TMA boxes of whole rows (the G heads of consecutive query
-//               tokens) when the unit's members are consecutive tokens, else
-//               by a cp.async gather.
-//   warps 4-11  softmax group 0 (even steps), warps 12-19 group 1 (odd
-//               steps), two threads per query row, one for each of a step's
-//               two tiles.  Each group keeps its own
-//               reference m_g, sum l_g and accumulator O_g, so while one
-//               group turns step t's scores into P the tensor cores run the
-//               other group's P V and next S.  The two groups' (m, l, O) are
-//               merged when the unit ends.  In a pair unit group g takes
-//               every step for the rows of tile g and writes them alone.
+//               descriptors and members in shared memory (two slots), and
+//               loads each unit's Q as soon as the previous unit's last S is
+//               done: by TMA boxes of whole rows (the G heads of consecutive
+//               query tokens, their coordinates worked out before) when the
+//               unit's members are consecutive tokens, else by a cp.async
+//               gather.
+//   then        softmax group 0 (even steps) and group 1 (odd steps), four
+//               warps each, one thread per query row; under a window eight
+//               each, two threads per row, one for each of a step's two
+//               tiles.  Each group keeps its own reference m_g, sum l_g and
+//               accumulator O_g, so while one group turns step t's scores
+//               into P the tensor cores run the other group's P V and next S.
+//               The two groups' (m, l, O) are merged when the unit ends.  In
+//               a pair unit group g takes every step for the rows of tile g
+//               and writes them alone.
 // P (bf16 pairs) overwrites the S columns it came from (at d = 64 it has
 // columns of its own), so it never passes through shared memory.  P is
 // formed with a reference that starts at 0 and is moved, with O_g rescaled in
@@ -67,10 +69,20 @@ constexpr int kProdWarps = 2;        // warp 0: K, warp 1: V
 constexpr int kVWarp = 1;
 constexpr int kMmaWarp = 2;
 constexpr int kUnitWarp = 3;         // claims units, stages descriptors and Q
-constexpr int kSoftWarp0 = 4;        // warps 4-11: group 0, 12-19: group 1
-constexpr int kTcThreads = 640;      // 20 warps: 5 per SM sub-partition
-constexpr int kSoftThreads = 512;
-constexpr int kGroupThreads = 256;
+constexpr int kSoftWarp0 = 4;        // group 0's first warp; group 1 follows
+// Softmax threads per query row: one that takes both tiles of a step (up to
+// 168 registers), or under a window two that take one each.  Two hide more of
+// the masks' work there (d = 64: 64 sequences of 3 queries and one of 300 over
+// 1024 keys 42 us against 51, five ragged chunks 75 against 82; d = 128 within
+// 1%), but meet at a barrier every step and share 96 registers: without masks
+// one thread is faster (tree verify, B = 32 of 8192 tokens, 16 / 32 / 64
+// drafts: 5.32 / 5.49 / 6.61 ms against 5.54 / 5.69 / 6.81; MCTS on 4-bit
+// pages, whose producers need the issue slots, 1.79 ms against 1.83).
+constexpr int threads_per_row(bool win) { return win ? 2 : 1; }
+// Threads of one softmax group, of both and of the CTA.
+constexpr int group_threads(bool win) { return 128 * threads_per_row(win); }
+constexpr int soft_threads(bool win) { return 2 * group_threads(win); }
+constexpr int tc_threads(bool win) { return 32 * kSoftWarp0 + soft_threads(win); }
 constexpr int kStepTokens = 2 * kTileTokens;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -80,13 +92,14 @@ constexpr float kLeastSum = 1.f / 65536.f;  // 2^-16: what a row's first keys gi
 // Named barriers with an OR reduction, so that all their threads take the same
 // branch: 1 over the softmax threads, 2 + i over the two warps that share the
 // rows of quarter i % 4 of group i / 4.
+template <int THREADS>
 __device__ __forceinline__ bool soft_bar_or(bool v) {
     uint32_t r;
     asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, 1, 512, q;\n"
+        "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, 1, %2, q;\n"
         "selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "n"(THREADS)
         : "memory");
     return r != 0;
 }
@@ -265,7 +278,7 @@ __device__ __forceinline__ float tile_max(uint32_t s_tm, int nv, bool tree, uint
 }
 
 template <int D, bool KV4, bool WIN>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(tc_threads(WIN), 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap, const AttnLaunch a, const int box_rows,
                    const int q_tma, const int out32) {
@@ -290,9 +303,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(C::B_UNIT_FULL + s), 1);
             // unit slot free: MMA, softmax, K and V warps
-            mbar_init(bar(C::B_UNIT_EMPTY + s), 1 + kSoftThreads / 32 + kProdWarps);
+            mbar_init(bar(C::B_UNIT_EMPTY + s), 1 + soft_threads(WIN) / 32 + kProdWarps);
             mbar_init(bar(C::B_S_FULL + s), 1);
-            mbar_init(bar(C::B_P_FULL + s), kGroupThreads);
+            mbar_init(bar(C::B_P_FULL + s), group_threads(WIN));
             mbar_init(bar(C::B_PV_DONE + s), 1);
             mbar_init(bar(C::B_ROWS_FULL + s), 1);
         }
@@ -307,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(bar(C::B_Q_FULL), 32);
         mbar_init(bar(C::B_Q_EMPTY), 1);
         mbar_init(bar(C::B_O_FULL), 1);
-        mbar_init(bar(C::B_O_EMPTY), kSoftThreads / 32);
+        mbar_init(bar(C::B_O_EMPTY), soft_threads(WIN) / 32);
         mbar_init(bar(C::B_DRAIN), 1);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -586,43 +599,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_UNIT_FULL + slot));
             if (done) break;
-            // its members, for the softmax threads (who would otherwise go
-            // through two dependent loads at each unit's start: 1800 cycles)
-            if (!KV4) {
-                for (int i = lane; i < it.n_members; i += 32) {
-                    const int qt = __ldg(a.members + it.member_off + i);
-                    s_row[slot * kMaxRows + i] = RowInfo{qt, WIN ? __ldg(a.q_pos + qt) : 0,
-                                                         !WIN && a.tree_mask ? __ldg(a.tree_mask + qt) : ~0ull};
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_ROWS_FULL + slot));
-            }
-            // Q of this unit, once the previous unit's S MMAs are done with it
-            ok = wait_warp(bar(C::B_Q_EMPTY), (uc & 1) ^ 1);
-            if (!ok) break;
             const int lk = head_of(unit);
             const int kvh = lk % a.Hkv, l = lk / a.Hkv;
             // (one 128-row tile, or two for a pair unit)
             const int rows = it.n_members * G;
             const int ntq = rows > 128 ? 2 : 1;
-            last_q = uc;
-            // By TMA when every box's members are consecutive query tokens: a
-            // box is the kv head's G query heads of max(1, 8 / G) consecutive
-            // tokens, i.e. max(8, G) whole rows of one 64-column slab, so each
-            // lands on a 1024-byte boundary of the 128-byte swizzle; boxes
-            // past the unit's members are read out of range (zero fill).
-            // Otherwise lane j gathers rows j + 32 i by cp.async.
-            if (q_tma) {
-                const int tpb = G < 8 ? 8 / G : 1;       // tokens per box
-                const int nbox = ntq * (128 / (tpb * G)) * C::NSLAB;
-                const int z_oob = a.L * a.nq;
+            // Q of this unit.  By TMA when every box's members are
+            // consecutive query tokens: a box is the kv head's G query heads of
+            // max(1, 8 / G) consecutive tokens, i.e. max(8, G) whole rows of
+            // one 64-column slab, so each lands on a 1024-byte boundary of the
+            // 128-byte swizzle; boxes past the unit's members are read out of
+            // range (zero fill).  Otherwise lane j gathers rows j + 32 i by
+            // cp.async.
+            const int tpb = G < 8 ? 8 / G : 1;       // tokens per box
+            const int nbox = ntq * (128 / (tpb * G)) * C::NSLAB;
+            bool by_tma = q_tma && nbox <= 64;
+            int zc[2] = {a.L * a.nq, a.L * a.nq};
+            if (by_tma) {
                 bool consec = true;
-                int zc[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int b = lane + 32 * j;
                     const int m0 = (b / C::NSLAB) * tpb;   // first member of the box
-                    zc[j] = z_oob;
                     if (b < nbox && m0 < it.n_members) {
                         const int q0 = __ldg(a.members + it.member_off + m0);
                         for (int k = 1; k < tpb && m0 + k < it.n_members; ++k)
@@ -630,23 +628,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         zc[j] = l * a.nq + q0;
                     }
                 }
-                if (__all_sync(0xffffffffu, consec) && nbox <= 64) {
-                    if (lane == 0) mbar_expect_tx(bar(C::B_Q_FULL), (uint32_t)(ntq * C::OPER));
-                    __syncwarp();
+                by_tma = __all_sync(0xffffffffu, consec);
+            }
+            // its members, for the softmax threads (who would otherwise go
+            // through two dependent loads at each unit's start: 1800 cycles)
+            auto stage_rows = [&] {
+                for (int i = lane; i < it.n_members; i += 32) {
+                    const int qt = __ldg(a.members + it.member_off + i);
+                    s_row[slot * kMaxRows + i] = RowInfo{qt, WIN ? __ldg(a.q_pos + qt) : 0,
+                                                         !WIN && a.tree_mask ? __ldg(a.tree_mask + qt) : ~0ull};
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_ROWS_FULL + slot));
+            };
+            // Q goes as soon as the previous unit's S MMAs are done with it;
+            // what it needs, and the members, are at hand by then (members
+            // behind Q: B = 32 of 512 tokens, 32 drafts, 0.658 ms against
+            // 0.598).  The first unit's Q goes ahead of them
+            if (!KV4 && uc > 0) stage_rows();
+            ok = wait_warp(bar(C::B_Q_EMPTY), (uc & 1) ^ 1);
+            if (!ok) break;
+            last_q = uc;
+            if (by_tma) {
+                if (lane == 0) mbar_expect_tx(bar(C::B_Q_FULL), (uint32_t)(ntq * C::OPER));
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int b = lane + 32 * j;
-                        if (b < nbox) {
-                            const int cb = b % C::NSLAB, row = (b / C::NSLAB) * tpb * G;   // unit row
-                            tma_load_3d(q_smem + (row >> 7) * C::OPER + cb * C::SLAB + (row & 127) * 128, &qmap,
-                                        cb * 64, kvh * G, zc[j], bar(C::B_Q_FULL));
-                        }
+                for (int j = 0; j < 2; ++j) {
+                    const int b = lane + 32 * j;
+                    if (b < nbox) {
+                        const int cb = b % C::NSLAB, row = (b / C::NSLAB) * tpb * G;   // unit row
+                        tma_load_3d(q_smem + (row >> 7) * C::OPER + cb * C::SLAB + (row & 127) * 128, &qmap, cb * 64,
+                                    kvh * G, zc[j], bar(C::B_Q_FULL));
                     }
-                    cp_async_arrive(bar(C::B_Q_FULL));
-                    continue;
                 }
             }
-            for (int tq = 0; tq < ntq; ++tq) {
+            for (int tq = 0; !by_tma && tq < ntq; ++tq) {
                 int qt[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -664,6 +680,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             cp_async_arrive(bar(C::B_Q_FULL));
+            if (!KV4 && uc == 0) stage_rows();
         }
         // the last Q load lands before the CTA ends (at once after a normal run)
         if (lane == 0 && last_q >= 0) settle(bar(C::B_Q_FULL), last_q & 1);
@@ -855,8 +872,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        const int grp = (warp - kSoftWarp0) >> 3;
-        const int half = ((warp - kSoftWarp0) >> 2) & 1;   // the step's tile that this warp takes
+        constexpr int TPR = threads_per_row(WIN);
+        constexpr int NT = 3 - TPR;               // tiles of a step that a thread takes
+        const int grp = (warp - kSoftWarp0) >> (TPR == 2 ? 3 : 2);
+        const int half = TPR == 2 ? ((warp - kSoftWarp0) >> 2) & 1 : 0;   // the first of them
         const int quarter = warp & 3;             // TMEM lanes this warp may access
         const int r = quarter * 32 + lane;        // query row in the unit
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -867,6 +886,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t o_tm = tmem + lane_base + C::O_COL;
         const float sc = a.scale_log2;
         uint32_t ns = 0;   // S_FULL phases consumed by this group
+        // whether v holds for a thread of the warp, or of the two that share
+        // its rows
+        auto row_any = [&](bool v) -> bool {
+            return TPR == 2 ? row_bar_or(row_bar, v) : (bool)__any_sync(0xffffffffu, v);
+        };
         // one arrival a warp, behind what all its lanes did
         auto arrive_warp = [&](uint32_t b) {
             tc_before();
@@ -877,13 +901,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         auto take_unit = [&](int uc, bool &ok) -> int {
             const int slot = uc & 1;
             ok = wait(bar(C::B_UNIT_FULL + slot), (uc >> 1) & 1) && ok;
-            const int u = ok ? s_unit[slot] : -1;
-            if (!KV4 && u >= 0) ok = wait(bar(C::B_ROWS_FULL + slot), (uc >> 1) & 1) && ok;
-            return u;
+            return ok ? s_unit[slot] : -1;
         };
         bool ok = true;
         int unit = take_unit(0, ok);
-        if (soft_bar_or(!ok || *s_abort)) unit = -1;
+        if (soft_bar_or<soft_threads(WIN)>(!ok || *s_abort)) unit = -1;
         for (int uc = 0; unit >= 0; ++uc) {
             const int slot = uc & 1;
             const int lk = head_of(unit);
@@ -900,6 +922,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool has = rr < rows;
             const int mem = rr / G;
             RowInfo row{0, 0, ~0ull};
+            if (!KV4) ok = wait(bar(C::B_ROWS_FULL + slot), (uc >> 1) & 1) && ok;
             if (has && !KV4) row = s_row[slot * kMaxRows + mem];
             if (has && KV4) {
                 row.qt = __ldg(a.members + it.member_off + mem);
@@ -921,31 +944,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float m = 0.f, lsum = 0.f;
             bool fresh = true;   // none of this thread's keys has gone into l yet
             for (int t = pair ? 0 : grp; t < nsteps; t += pair ? 1 : 2) {
-                // what the rows see of this warp's tile, while S is on its way
-                const bool there = 2 * t + half < ntile;
-                const KvTile &kt = tiles[there ? 2 * t + half : 2 * t];
-                // keys before any mask
-                const int n = there && has && mem >= (kt.members & 0xFFFF) && mem < kt.members >> 16
-                                  ? (kt.ntok_flags & 0xFFFF)
-                                  : 0;
-                // a whole tile that all the unit's rows see (WIN: inside the
-                // windows of all the warp's rows) needs no masks
-                const bool whole = there && kt.ntok_flags == kTileTokens && (kt.members & 0xFFFF) == 0 &&
-                                   kt.members >> 16 >= it.n_members &&
-                                   (!WIN || (kt.tok0 + kTileTokens - 1 <= pos_lo &&
-                                             (kt.tok0 > pos_hi - a.win || kt.tok0 + kTileTokens <= a.sinks)));
-                int nv = n;
-                bool tree = (kt.ntok_flags >> 16) & kTileTree;
-                uint64_t mask = tmask;
-                if (whole) {
-                    nv = kTileTokens;
-                    tree = false;
-                } else if (WIN) {   // the mask alone says what is valid
-                    mask = n > 0 ? window_bits(kt.tok0, n, pos, a.win, a.sinks) : 0ull;
-                    nv = kTileTokens;
-                    tree = true;
+                // what the rows see of this warp's tiles, while S is on its way
+                int nv[NT];
+                bool whole[NT], tree[NT], some = false;
+                uint64_t mask[NT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const bool there = 2 * t + half + i < ntile;
+                    const KvTile &kt = tiles[there ? 2 * t + half + i : 2 * t];
+                    // keys before any mask
+                    const int n = there && has && mem >= (kt.members & 0xFFFF) && mem < kt.members >> 16
+                                      ? (kt.ntok_flags & 0xFFFF)
+                                      : 0;
+                    // a whole tile that all the unit's rows see (WIN: inside
+                    // the windows of all the warp's rows) needs no masks
+                    whole[i] = there && kt.ntok_flags == kTileTokens && (kt.members & 0xFFFF) == 0 &&
+                               kt.members >> 16 >= it.n_members &&
+                               (!WIN || (kt.tok0 + kTileTokens - 1 <= pos_lo &&
+                                         (kt.tok0 > pos_hi - a.win || kt.tok0 + kTileTokens <= a.sinks)));
+                    nv[i] = n;
+                    tree[i] = (kt.ntok_flags >> 16) & kTileTree;
+                    mask[i] = tmask;
+                    if (whole[i]) {
+                        nv[i] = kTileTokens;
+                        tree[i] = false;
+                    } else if (WIN) {   // the mask alone says what is valid
+                        mask[i] = n > 0 ? window_bits(kt.tok0, n, pos, a.win, a.sinks) : 0ull;
+                        nv[i] = kTileTokens;
+                        tree[i] = true;
+                    }
+                    some = some || (whole[i] ? has : WIN ? mask[i] != 0 : nv[i] > 0);
                 }
-                const bool some = whole ? has : WIN ? mask != 0 : nv > 0;
+                // P of the thread's tiles with reference m, and its sum
+                auto form_p = [&](bool use_whole, uint32_t (&pk)[NT][32], float &ls) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        if (use_whole && whole[i])
+                            p_pass<true>(s_tm + 64 * i, -m, sc, nv[i], tree[i], mask[i], pk[i], ls);
+                        else
+                            p_pass<false>(s_tm + 64 * i, -m, sc, nv[i], tree[i], mask[i], pk[i], ls);
+                    }
+                };
+                auto store_p = [&](const uint32_t (&pk)[NT][32]) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) tmem_st32(p_tm + 32 * i, pk[i]);
+                };
                 ok = wait(bar(C::B_S_FULL + grp), ns & 1) && ok;
                 ns += 1;
                 // the unit's last S is done with Q: one thread of the group
@@ -962,12 +1005,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 // P is formed with a reference m that need not be the row's
                 // running max: it starts at 0, and is moved only when a
-                // tile's P would sum to more than 2^32, or the row's first
+                // thread's P would sum to more than 2^32, or the row's first
                 // keys' to less than 2^-16 (all p then lie well inside bf16,
                 // and l and O inside the fp32 sums).  A step therefore reads
                 // S once and forms P in registers; only a row that breaks a
-                // bound takes the slow path (the two warps' max, O_g and l
-                // rescaled, P again).  The two warps of a row meet once a
+                // bound takes the slow path (the row's max, O_g and l
+                // rescaled, P again).  Two warps that share rows meet once a
                 // step: they take the same path, and P may go into columns
                 // that the first one's S came from.
                 // (ns steps of this group are seen: the products of the one
@@ -977,29 +1020,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 float ls = 0.f, mx = -INFINITY;
                 bool bad, slow;
                 {
-                    uint32_t pk[32];
-                    if (whole) p_pass<true>(s_tm, -m, sc, nv, tree, mask, pk, ls);
-                    else p_pass<false>(s_tm, -m, sc, nv, tree, mask, pk, ls);
+                    uint32_t pk[NT][32];
+                    form_p(true, pk, ls);
                     bad = some && !(ls <= kSlackSum && (!fresh || ls >= kLeastSum));
-                    slow = row_bar_or(row_bar, bad);
-                    if (!slow) tmem_st32(p_tm, pk);
+                    slow = row_any(bad);
+                    if (!slow) store_p(pk);
                 }
                 if (slow) {
                     // (scale > 0: max of scaled scores = scale * max of raw scores)
-                    mx = tile_max(s_tm, nv, tree, mask) * sc;
-                    *mine = make_float2(mx, (bad ? 1.f : 0.f) + (fresh ? 2.f : 0.f));
-                    row_bar_or(row_bar, false);
-                    const float2 o2 = *other;
-                    mx = fmaxf(mx, o2.x);   // the row's
-                    const bool first = fresh && o2.y >= 2.f;   // l and O_g are still 0
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        mx = fmaxf(mx, tile_max(s_tm + 64 * i, nv[i], tree[i], mask[i]) * sc);
+                    bool first = fresh, move = bad;   // l and O_g are still 0; the row's reference moves
+                    if (TPR == 2) {
+                        *mine = make_float2(mx, (bad ? 1.f : 0.f) + (fresh ? 2.f : 0.f));
+                        row_bar_or(row_bar, false);
+                        const float2 o2 = *other;
+                        mx = fmaxf(mx, o2.x);   // the row's
+                        first = first && o2.y >= 2.f;
+                        move = move || o2.y == 1.f || o2.y == 3.f;
+                    }
                     float m_new = m;
-                    if (bad || o2.y == 1.f || o2.y == 3.f) m_new = !first ? fmaxf(m, mx) : mx == -INFINITY ? 0.f : mx;
+                    if (move) m_new = !first ? fmaxf(m, mx) : mx == -INFINITY ? 0.f : mx;
                     const bool resc = m_new != m && !first;
                     if (__any_sync(0xffffffffu, resc)) {
-                        // each warp rescales half of O_g's columns
+                        // (two warps that share rows rescale half of O_g's columns each)
                         const float f = resc ? exp2_sfu(m - m_new) : 1.f;
 #pragma unroll 1
-                        for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+                        for (int c0 = half * (D / TPR); c0 < (half + 1) * (D / TPR); c0 += 32) {
                             uint32_t x[32];
                             tmem_ld32(o_tm + grp * D + c0, x);
                             tmem_wait_ld();
@@ -1011,20 +1059,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     m = m_new;
                     ls = 0.f;
-                    uint32_t pk[32];
-                    p_pass<false>(s_tm, -m, sc, nv, tree, mask, pk, ls);
-                    row_bar_or(row_bar, false);   // both have read S (and the other's max)
-                    tmem_st32(p_tm, pk);
+                    uint32_t pk[NT][32];
+                    form_p(false, pk, ls);
+                    if (TPR == 2) row_bar_or(row_bar, false);   // both have read S (and the other's max)
+                    store_p(pk);
                 }
-                // (scores that are all -inf leave the row as it was)
+                // scores that are all -inf leave the row as it was
                 fresh = fresh && !(some && (ls != 0.f || mx > -INFINITY));
                 lsum += ls;
                 tmem_wait_st();
                 tc_before();
                 mbar_arrive(bar(C::B_P_FULL + grp));
             }
-            // epilogue: one tile merges the two groups' (m, l, O) and the four
-            // warps of a row split its columns; in a pair unit each group's two
+            // epilogue: one tile merges the two groups' (m, l, O) and all the
+            // warps of a row split its columns; in a pair unit each group's
             // warps write their own tile's rows from its own O
             ok = wait(bar(C::B_O_FULL), uc & 1) && ok;
             tc_after();
@@ -1032,11 +1080,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // settles both)
             const int next = take_unit(uc + 1, ok);
             s_ml[(grp * 2 + half) * 128 + r] = make_float2(m, lsum);
-            if (soft_bar_or(!ok || *s_abort)) break;
+            if (soft_bar_or<soft_threads(WIN)>(!ok || *s_abort)) break;
             float w0, w1, lse2;
             int ca, cb;
-            // the two warps of a row share m
-            const float l0 = s_ml[r].y + s_ml[128 + r].y, l1 = s_ml[256 + r].y + s_ml[384 + r].y;
+            // the warps of a row and group share m
+            float l0 = s_ml[r].y, l1 = s_ml[256 + r].y;
+            if (TPR == 2) {
+                l0 += s_ml[128 + r].y;
+                l1 += s_ml[384 + r].y;
+            }
             if (!pair) {
                 const float m0 = l0 > 0.f ? s_ml[r].x : -INFINITY, m1 = l1 > 0.f ? s_ml[256 + r].x : -INFINITY;
                 const float c = fmaxf(m0, m1);
@@ -1047,17 +1099,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 lse2 = ltot > 0.f ? c + __log2f(ltot) : -INFINITY;
                 w0 = f0 * inv;
                 w1 = f1 * inv;
-                // 32 columns a warp (D = 64: the second warps have none)
-                ca = D == 128 ? grp * 64 + half * 32 : grp * 32;
-                cb = D == 128 || half == 0 ? ca + 32 : ca;
+                // (D = 64: 32 columns, so second warps have none)
+                ca = grp * (D / 2) + half * 32;
+                cb = min(ca + (D == 128 && TPR == 1 ? 64 : 32), (grp + 1) * (D / 2));
             } else {
                 const float lg = grp ? l1 : l0;
                 const float inv = lg > 0.f ? 1.f / lg : 0.f;
                 lse2 = lg > 0.f ? m + __log2f(lg) : -INFINITY;
                 w0 = grp == 0 ? inv : 0.f;
                 w1 = grp == 1 ? inv : 0.f;
-                ca = half * (D / 2);
-                cb = ca + D / 2;
+                ca = half * (D / TPR);
+                cb = ca + D / TPR;
             }
             const bool write = has && nsteps > 0;
             for (int c0 = ca; !idle && c0 < cb; c0 += 32) {
@@ -1184,7 +1236,8 @@ cudaError_t launch_tc_d(const AttnLaunch &a, cudaStream_t stream) {
     // one CTA per SM (its shared memory and TMEM allow no more)
     const int grid = a.n_tc_units < occ.sms ? a.n_tc_units : occ.sms;
     const int out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
-    attn_tc_kernel<D, KV4, WIN><<<grid, kTcThreads, TcCfg<D>::SMEM, stream>>>(km, vm, qm, a, box_rows, q_tma ? 1 : 0, out32);
+    attn_tc_kernel<D, KV4, WIN>
+        <<<grid, tc_threads(WIN), TcCfg<D>::SMEM, stream>>>(km, vm, qm, a, box_rows, q_tma ? 1 : 0, out32);
     count_launch();
     return cudaGetLastError();
 }

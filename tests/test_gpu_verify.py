@@ -152,3 +152,50 @@ def test_verify_partly_filled_pair_unit():
     # tile's output rows are written row by row), over a context that ends
     # inside a block
     run_verify(W.verify_tree(2, layers=1, ctx=1000, n_draft=40))
+
+
+@pytest.mark.parametrize("late", [True, False])
+@pytest.mark.parametrize("n", [16, 20, 32])
+def test_verify_growing_scores_of_one_row_tile(n, late):
+    # one 128-row tile a unit (n x G 4 rows), whose steps two groups of softmax
+    # threads take in turn: scores far above the reference in the context's
+    # second half, or in its first, so that each group moves its own
+    def kv(w, i):
+        k, v = W.append_kv(w, i)
+        ntok = w.ops[i][2]
+        if ntok > w.info["n_draft"]:
+            kf = W.bf16_bits_to_f32(k)
+            half = slice(ntok // 2, None) if late else slice(0, ntok // 2)
+            kf[:, half] *= 30.0
+            k = W.f32_to_bf16_bits(kf)
+        return k, v
+
+    w = W.verify_tree(2, layers=1, ctx=700, n_draft=n)
+    r = PoolRunner(w, alloc_seed=1)
+    r.run_ops(kv_fn=kv)
+    call = VerifyCall(r)
+    q = W.verify_q(w)
+    call(bf16_tensor(q))
+    torch.cuda.synchronize()
+    rw = oracle.replay(w, alloc_seed=1, kv_fn=kv)
+    t, ln = rw.tables(w.batch, w.max_blocks_per_seq)
+    want_o, want_l = oracle.verify_attention(q, rw.k_pool, rw.v_pool, t, ln - n, w.info["parents"])
+    check_close(to_f64(call.out), want_o, max_abs_tol=peaked_max_abs(want_o, bf16_absmax(rw.v_pool)))
+    check_lse(to_f64(call.lse), want_l)
+    assert kvp.kvp_device_error(call.ws) == 0
+
+
+@pytest.mark.parametrize("n", [16, 32, 64])
+def test_verify_twice_gives_the_same_bits(n):
+    # units are claimed in any order, but each is computed in one way
+    w = W.verify_tree(3, layers=2, ctx=1500, n_draft=n)
+    r = PoolRunner(w)
+    r.run_ops()
+    call = VerifyCall(r)
+    q = bf16_tensor(W.verify_q(w))
+    call(q)
+    o, z = call.out.clone(), call.lse.clone()
+    for _ in range(5):
+        call.out.fill_(7)
+        call(q)
+        assert torch.equal(call.out.view(torch.int16), o.view(torch.int16)) and torch.equal(call.lse, z)

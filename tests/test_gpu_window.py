@@ -244,3 +244,17 @@ def test_forced_kernels(path):
     r = subprocess.run([sys.executable, "-c", code], env={**os.environ, "KVP_ATTN_PATH": path}, capture_output=True,
                        text=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("d,lens,qlens", [(128, [3000, 900], [1, 1]), (64, [3000, 900, 70], [777, 1, 70]),
+                                          (128, [3000, 900], [1000, 40])])
+def test_twice_gives_the_same_bits(d, lens, qlens):
+    desc, q, k, v, tables = case(d, 8, 2, 16, 2, lens, qlens, 500, 4)
+    ws = torch.empty(kvp.kvp_window_workspace_size(desc, tables, lens, qlens, 500, 4), dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(5):
+        out = torch.full_like(q, 7.0)
+        lse = torch.zeros(q.shape[:3], device="cuda")
+        kvp.paged_window_attention(q, qlens, k, v, tables, lens, 500, 4, desc, out, lse, ws)
+        first = first or (out, lse)
+        assert torch.equal(out.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
