@@ -583,6 +583,8 @@ int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, c
  * nothing: KVP_ERR_OOM (no free blocks), KVP_ERR_INVALID and KVP_ERR_STATE (a
  * pool without K/V storage or of 4-bit pages, or a stream being captured)
  * change nothing; after KVP_ERR_CUDA from a launch the bookkeeping stands.
+ * (For this and the two calls above, the legacy default stream counts as
+ * captured while a stream that synchronises with it is.)
  */
 size_t seq_evict_workspace_size(const kvp_pool *pool, const int32_t *seqs, int32_t n, int32_t budget);
 int seq_evict(kvp_pool *pool, const int32_t *seqs, int32_t n, const float *mass, int64_t mass_stride,

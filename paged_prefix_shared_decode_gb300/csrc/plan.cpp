@@ -1046,9 +1046,14 @@ bool attn_desc_ok(const kvp_attn_desc *d) { return desc_ok(d); }
 
 bool stream_capturing(cudaStream_t stream) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    // (the legacy default stream cannot be captured; asked about it while
-    // another stream captures, the runtime returns an error)
-    return cudaStreamIsCapturing(stream, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(stream, &st);
+    if (e == cudaErrorStreamCaptureImplicit) {
+        // the legacy default stream while a stream that waits for it is
+        // captured: any work on it would fail, and end that capture
+        cudaGetLastError();
+        return true;
+    }
+    return e == cudaSuccess && st != cudaStreamCaptureStatusNone;
 }
 
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }

@@ -505,3 +505,44 @@ def test_decode_with_a_bounded_cache():
         kvp.seq_free(pool, s)
     assert kvp.kvp_free_block_count(pool) == 120
     kvp.kv_pool_destroy(pool)
+
+
+def test_default_stream_beside_a_capture_is_refused_whole():
+    """The legacy default stream cannot be used while a stream that synchronises with it is captured: the calls say
+    so before anything changes, and the capture goes on."""
+    import ctypes
+    pool, k, v = make_pool(1, 12, 1, 16, 64)
+    a = kvp.seq_alloc(pool)
+    kvp.seq_reserve(pool, a, 100)
+    mass = weights(1, 1, 1, 100)
+    kept = torch.zeros(1, 1, 1, 50, dtype=torch.int32, device="cuda")
+    t, ln = kvp.kvp_gather_tables(pool, [a], 8)
+    desc = kvp.AttnDesc(1, 2, 1, 64, 16, 12, 0.0, 1)
+    q = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    z = torch.zeros(1, 1, 2, device="cuda")
+    out = torch.zeros_like(q)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    cu = ctypes.CDLL("libcuda.so.1")
+    s, g = ctypes.c_void_p(), ctypes.c_void_p()
+    assert cu.cuStreamCreate(ctypes.byref(s), 0) == 0
+    assert cu.cuStreamBeginCapture_v2(s, 1) == 0         # a capture of this thread's
+    codes = []
+    for call in (lambda: kvp.seq_evict(pool, [a], mass, 50, 0, 0, kept, None, ws, stream=0),
+                 lambda: kvp.kvp_attention_mass(q, None, z, k, t, ln, desc, 1.0, None, None, mass, ws, stream=0),
+                 lambda: kvp.paged_window_attention(q, None, k, v, t, ln, 8, 0, desc, out, z, ws, stream=0)):
+        try:
+            call()
+            codes.append(kvp.KVP_OK)
+        except kvp.KvpError as e:
+            codes.append(e.code)
+    ended = cu.cuStreamEndCapture(s, ctypes.byref(g))
+    assert cu.cuGraphDestroy(g) == 0 if ended == 0 else True
+    assert cu.cuStreamDestroy_v2(s) == 0
+    assert codes == [kvp.KVP_ERR_STATE] * 3 and kvp.seq_len(pool, a) == 100
+    assert ended == 0
+    torch.cuda.synchronize()
+    kvp.seq_evict(pool, [a], mass, 50, 0, 0, kept, None, ws, stream=0)
+    torch.cuda.synchronize()
+    assert kvp.seq_len(pool, a) == 50
+    kvp.kv_pool_destroy(pool)
