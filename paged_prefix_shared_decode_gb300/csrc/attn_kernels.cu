@@ -1142,7 +1142,7 @@ cudaError_t launch_d(const AttnLaunch &a, cudaStream_t stream, cudaEvent_t befor
     // windows beside a prompt chunk): launched first they run while the persistent
     // tcgen05 CTAs start, instead of after these end
     const bool tc_last = fork && a.win > 0;
-    cudaError_t e = tc_last ? cudaSuccess : launch_attention_tc(a, stream, 1);
+    cudaError_t e = tc_last ? cudaSuccess : launch_attention_tc(a, stream);
     if (e != cudaSuccess) return e;
     if (a.n_units > 0 && a.kv4) {
         Occupancy &o4 = occupancy<D, true>();
@@ -1176,7 +1176,7 @@ cudaError_t launch_d(const AttnLaunch &a, cudaStream_t stream, cudaEvent_t befor
         if (e != cudaSuccess) return e;
     }
     if (tc_last) {
-        e = launch_attention_tc(a, stream, 1);
+        e = launch_attention_tc(a, stream);
         if (e != cudaSuccess) return e;
     }
     if (mma_stream != stream) {

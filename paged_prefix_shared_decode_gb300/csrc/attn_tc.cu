@@ -1337,8 +1337,7 @@ bool tc_path_supported(int L, int NB, int Hkv, int bs) {
     return (long long)L * NB * Hkv * bs < (1LL << 31);
 }
 
-cudaError_t launch_attention_tc(const AttnLaunch &a, cudaStream_t stream, int ctas_per_sm) {
-    (void)ctas_per_sm;
+cudaError_t launch_attention_tc(const AttnLaunch &a, cudaStream_t stream) {
     if (a.n_tc_units <= 0) return cudaSuccess;
     if (a.win > 0 && !a.kv4) {
         if (a.D == 64) return launch_tc_d<64, false, true>(a, stream);

@@ -103,9 +103,8 @@ struct AttnLaunch {
 // before/after: optional events recorded around the work-item kernel.
 cudaError_t launch_attention(const AttnLaunch &a, cudaStream_t stream, cudaEvent_t before,
                              cudaEvent_t after);
-// tcgen05 kernel over a.tc_items (no-op when there are none); at most
-// `ctas_per_sm` CTAs per SM (0: as many as fit).
-cudaError_t launch_attention_tc(const AttnLaunch &a, cudaStream_t stream, int ctas_per_sm);
+// tcgen05 kernel over a.tc_items (no-op when there are none).
+cudaError_t launch_attention_tc(const AttnLaunch &a, cudaStream_t stream);
 // Whether the tcgen05 kernel can address this pool (32-bit TMA row index).
 bool tc_path_supported(int L, int NB, int Hkv, int bs);
 // TMA view of a K or V pool as rows = L*NB*Hkv*bs token rows of D bf16

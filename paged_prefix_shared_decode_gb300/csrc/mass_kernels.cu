@@ -131,7 +131,7 @@ __device__ __forceinline__ void add_tile(float (&acc)[8], const KTile<D> &kt, co
 // Three halving steps over t: after them lane (t, j) holds acc index
 // b = (t & 1) * 4 + (t & 2) + (t >> 2), i.e. token 8 (b >> 1) + 2 j + (b & 1).
 __device__ __forceinline__ float spread(const float (&acc)[8], int lane) {
-    const int t = lane >> 2, j = lane & 3;
+    const int t = lane >> 2;
     float a4[4], a2[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -148,7 +148,6 @@ __device__ __forceinline__ float spread(const float (&acc)[8], int lane) {
     // token x = lane's own: held by the lane with b >> 1 = x / 8, j = (x % 8) / 2, b & 1 = x % 2
     const int b = 2 * (lane >> 3) + (lane & 1);
     const int ts = (b >> 2) | (b & 2) | ((b & 1) << 2);
-    (void)j;
     return __shfl_sync(0xffffffffu, v, ts * 4 + ((lane & 7) >> 1));
 }
 
