@@ -508,6 +508,11 @@ int kvp_decode_step_run(kvp_step_plan *plan, const kvp_step_io *io, void *worksp
  * block_tables, seq_lens, desc, workspace and errors as for
  * paged_decode_attention, ws_bytes >= kvp_window_workspace_size() for the
  * same arguments; pages must be bf16.
+ * Weights are rounded to bf16 before they meet V, as in the other attention
+ * calls; their sum and the log-sum-exp are not.  The workspace grows with the
+ * keys in view; where queries see more than 8192 of them it holds d + 1 floats
+ * per 8192 keys, query token, head and layer, and KVP_ERR_INVALID says that
+ * 2^31 such rows or more would be needed for one layer and kv head.
  * With desc->use_sharing, batches of one query token per sequence read a
  * block that several of them share and see once.  Tokens that no query of the
  * call sees do not matter; those that one sees must hold finite K and V (for
@@ -568,9 +573,9 @@ int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, c
  * sequence's), and the blocks past them are released.  kept (device int32
  * [L][n][Hkv][budget]) receives the positions that the kept tokens had,
  * mass_out (device, laid out like mass; NULL: not wanted; mass itself or
- * apart from it) their weights in the first `budget` entries.  A sequence of
- * at most `budget` tokens stays as it is: kept = 0, 1, ... then -1, its
- * weights copied.  A slot of an evicted sequence is no token position any
+ * apart from it) their weights in the first `budget` entries (0 for -0, and any
+ * NaN for a NaN).  A sequence of at most `budget` tokens stays as it is: kept =
+ * 0, 1, ... then -1, its weights copied.  A slot of an evicted sequence is no token position any
  * more: attention over all of it is what it was, but its blocks do not belong
  * in a prefix cache, and a sliding window over it counts slots.
  * Pages that another sequence or the prefix cache also holds are not written:
@@ -616,7 +621,7 @@ int seq_evict(kvp_pool *pool, const int32_t *seqs, int32_t n, const float *mass,
  * n_accepted [B]: how many; next_token [B] (-1 if a row of p is all zero).
  *
  * target / draft: device fp32 probabilities (each row sums to about 1; NaN
- * and negative entries count as 0), element (b, r, x) at b * batch_stride +
+ * and negative entries count as 0, entries above 1 as 1), element (b, r, x) at b * batch_stride +
  * r * row_stride + x, strides >= 0 (0: one distribution for all).
  * tree_parent, draft_tokens, u_* in [0, 1), and the outputs: device, int32
  * and fp32.  A parent outside [-1, i) makes a root; a node whose token is

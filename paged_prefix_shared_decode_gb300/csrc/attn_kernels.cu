@@ -15,7 +15,7 @@
 // the tile's end and draft tokens that are not ancestors-or-self of a node
 // are masked, and in sliding-window calls (WIN) keys outside a row's window
 // that are no sinks.  (64 sequences decoding over windows of 4096, d = 128:
-// 724 us, 5.9 TB/s, 87% of the copy peak.)  With at most 16 rows the four warps split each tile's tokens
+// 732 us, 5.9 TB/s, 86% of the copy peak.)  With at most 16 rows the four warps split each tile's tokens
 // four ways (with at most 32 rows at head dim 128, two ways) and combine
 // their (m, l, o) through shared memory.
 //

@@ -2,7 +2,7 @@
 // sm_103a) for work items with more than 32 query rows: shared-prefix
 // segments read by many sequences, MCTS tree levels, draft-tree verification
 // and the prompt chunks of sliding-window attention (8192 queries over 4096
-// keys at d = 128: 379 us, 1.45 PFLOP/s).
+// keys at d = 128: 385 us, 1.43 PFLOP/s).
 //
 // One persistent CTA of 12 warps per SM (20 under a window).  A work unit is
 // (item, layer, kv head): up to 128 query rows (the item's members x the GQA
@@ -38,7 +38,10 @@
 // columns of its own), so it never passes through shared memory.  P is
 // formed with a reference that starts at 0 and is moved, with O_g rescaled in
 // TMEM, only when a tile's P would sum to more than 2^32 or a row's first
-// keys' to less than 2^-16: whole passes over S for a maximum are rare.
+// keys' to less than 2^-16: whole passes over S for a maximum are rare.  P is
+// rounded to bf16 because both operands of a product have one type and V's is
+// bf16 (relative 2^-8 of each p, averaged over the keys: about as much as the
+// bf16 output's own rounding); l adds the unrounded p.
 // Every wait is bounded; on a timeout the CTA sets bit 4 of the workspace
 // error word and all roles leave their loops; before the CTA frees its TMEM
 // and ends, the producers let the copies they issued land and the MMA thread
@@ -642,9 +645,10 @@ __global__ void __launch_bounds__(tc_threads(WIN), 1)
                 if (lane == 0) mbar_arrive(bar(C::B_ROWS_FULL + slot));
             };
             // Q goes as soon as the previous unit's S MMAs are done with it;
-            // what it needs, and the members, are at hand by then (members
-            // behind Q: B = 32 of 512 tokens, 32 drafts, 0.658 ms against
-            // 0.598).  The first unit's Q goes ahead of them
+            // its coordinates, and the members, are at hand by then (B = 32 of
+            // 512 tokens, 32 drafts: 0.598 ms; with the coordinates worked out
+            // only then 0.629, and the members behind that 0.658).  The first
+            // unit's Q goes ahead of the members
             if (!KV4 && uc > 0) stage_rows();
             ok = wait_warp(bar(C::B_Q_EMPTY), (uc & 1) ^ 1);
             if (!ok) break;

@@ -35,8 +35,9 @@
 // one pass and the search, each a memory latency or two), 18.3 us for 8 trees
 // of 64 nodes over 32003 (up to 7 passes of about 2 us, one per rejection:
 // two barriers, reductions and an L2 latency each), 22.5 us for 64 chains
-// over 131072 (67 MB, 3.0 TB/s: the passes' issue slots, about 30
-// instructions a token, and the latencies around them).
+// over 131072 (67 MB, 3.0 TB/s: load latency and barriers, 7.5 and 4.2 warps
+// waiting per issue, and 256 CTAs that put two on 104 SMs and one on 48; the
+// passes' issue slots, about 30 instructions a token, make 6 us of it).
 #include <cuda_runtime.h>
 
 #include <climits>

@@ -45,7 +45,8 @@ constexpr int kRowTile = 64;      // rows of K and of V per copy CTA
 constexpr int kMoveThreads = 256;
 constexpr int kInFlight = 8;      // 16-byte loads in flight per thread
 
-// Weights as unsigned keys of the same order: NaN below everything, -0 as 0.
+// Weights as unsigned keys of the same order: NaN below everything, -0 as 0
+// (a kept weight written from its key is 0 and one NaN for all of those).
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t b = __float_as_uint(x == x ? x + 0.f : __uint_as_float(0xffffffffu));
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);

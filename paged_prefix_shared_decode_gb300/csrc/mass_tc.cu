@@ -26,9 +26,11 @@
 // Each group has two S buffers in TMEM (all 512 columns), so the tensor cores
 // work ahead of both.  Every wait is bounded, as in the attention kernel.
 //
-// What bounds it: the exponentials, 128 x 128 a step at 32 a clock and SM, and
-// on short runs the first loads.  256 rows over 2 x about 7000 tokens, 8 kv
-// heads of 128 (32 MB, 7 GFLOP): 19 us, 3 us of them exponentials.
+// What bounds it: on long runs the exponentials, 128 x 128 a step at 32 a clock
+// and SM.  256 rows over 2 x about 7000 tokens, 8 kv heads of 128 (936 tiles,
+// 6.2 a CTA; 32 MB, 7 GFLOP) take 19 us, of which the exponentials need 3 and
+// the loads 5; where the rest goes has not been taken apart (the first tile
+// waits for the plan's copy and three dependent loads).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
