@@ -575,9 +575,10 @@ int kvp_attention_mass(const void *q, const int32_t *q_lens, const float *lse, c
  * mass_out (device, laid out like mass; NULL: not wanted; mass itself or
  * apart from it) their weights in the first `budget` entries (0 for -0, and any
  * NaN for a NaN).  A sequence of at most `budget` tokens stays as it is: kept =
- * 0, 1, ... then -1, its weights copied.  A slot of an evicted sequence is no token position any
- * more: attention over all of it is what it was, but its blocks do not belong
- * in a prefix cache, and a sliding window over it counts slots.
+ * 0, 1, ... then -1, its weights copied.  A slot of an evicted sequence is no
+ * token position any more: attention over all of it is what it was, but its
+ * blocks do not belong in a prefix cache, and a sliding window over it counts
+ * slots.
  * Pages that another sequence or the prefix cache also holds are not written:
  * the sequence gets fresh blocks for them, except for pages that hold sink
  * tokens alone, which stay shared.  Sharing is judged at the start of the
