@@ -628,7 +628,8 @@ int seq_evict(kvp_pool *pool, const int32_t *seqs, int32_t n, const float *mass,
  * and fp32.  A parent outside [-1, i) makes a root; a node whose token is
  * outside [0, vocab) is left out.  Sums over the vocabulary are exact to
  * 2^-60 an entry (a residual of smaller entries alone is nothing left), so the
- * result does not depend on the row's split over the GPU.  One kernel, no workspace; may be captured into a graph.
+ * result does not depend on the row's split over the GPU.  One kernel, no
+ * workspace; may be captured into a graph.
  */
 int kvp_draft_verify(const float *target, int64_t target_batch_stride, int64_t target_row_stride,
                      const float *draft, int64_t draft_batch_stride, int64_t draft_row_stride,
