@@ -637,6 +637,169 @@ int kvp_draft_verify(const float *target, int64_t target_batch_stride, int64_t t
                      const float *u_next, int32_t batch, int32_t n_draft, int32_t vocab,
                      int32_t *accepted, int32_t *n_accepted, int32_t *next_token, void *stream);
 
+/* --------------------------------- rotated appends, beams, sparse attention */
+
+/*
+ * The rotation of keys and queries by position: of each head's d values the
+ * first rot_dim (even, 2 .. min(d, 256)) are rot_dim / 2 pairs, pair i being
+ * dims (i, i + rot_dim / 2) or, with `interleaved`, (2 i, 2 i + 1).  At
+ * position p it becomes
+ *   (x cos a - y sin a, y cos a + x sin a) * scale,   a = p * freq_i,
+ * freq_i = freqs[i] (host, radians per position, rot_dim / 2 of them; read
+ * during the call) or, with freqs NULL, base ^ (-2 i / rot_dim).  The other
+ * dims stay as they are.  scale 0 counts as 1.  Angles are reduced exactly
+ * (positions are whole numbers: p * freq / 2 pi modulo 1 in 64-bit fixed
+ * point), so far positions lose nothing.
+ */
+typedef struct {
+    int32_t rot_dim;
+    int32_t interleaved;
+    const double *freqs;
+    double base;
+    float scale;
+} kvp_rope_desc;
+
+/*
+ * seq_append_batch with the rotation on the way: the keys go into their pages
+ * rotated (in 32 bits, rounded to bf16 once; 4-bit pages quantise those bf16
+ * keys as seq_append would), the values as they are, and q (device bf16
+ * [L][sum ntoks][num_q_heads][d], or NULL) is rotated into q_out (q itself or
+ * apart from it).  positions: device int32 [sum ntoks], any values (evicted
+ * caches, whose slots are no positions; draft trees, whose nodes share
+ * depths), or NULL: the slots that the tokens take in their sequences.
+ * Semantics, copy-on-write and errors of seq_append_batch, all or nothing;
+ * KVP_ERR_INVALID also for a rotation outside the above.  One kernel for
+ * appends of up to 512 sequences and 4096 pages, no workspace.  A batch whose
+ * ntoks are all 0 does nothing.  After KVP_ERR_CUDA from a launch the
+ * bookkeeping stands.
+ */
+int seq_append_rope(kvp_pool *pool, int32_t nseq, const int32_t *seqs, const int32_t *ntoks, const void *k,
+                    const void *v, const kvp_rope_desc *rope, const int32_t *positions, const void *q, void *q_out,
+                    int32_t num_q_heads, void *stream);
+
+/* Beam search's reordering of sequences: sequence dst[i] becomes a
+ * copy-on-write fork of what sequence src[i] was before the call (host arrays
+ * of n live sequences; each dst at most once, a src as often as wanted, dst
+ * and src may name the same sequences; dst[i] == src[i] leaves it as it is).
+ * Host bookkeeping only, no K/V moves.  What the dst sequences held before is
+ * released, the last of them first, each table from its last entry.
+ * KVP_ERR_INVALID changes nothing. */
+int seq_reorder(kvp_pool *pool, const int32_t *dst, const int32_t *src, int32_t n);
+
+/*
+ * Attention over pages that a cheap score selects for each query.  The four
+ * calls below take the batch on the DEVICE: block_tables int32 [num_seqs]
+ * [max_blocks] and seq_lens int32 [num_seqs] as kvp_export_tables leaves
+ * them, so that they need no plan and no workspace, synchronise nothing and
+ * may be captured into a graph, which then follows tables and lengths as they
+ * change.  Query rows: q_start NULL means one query token a sequence, num_q =
+ * num_seqs; else q_start (device int32 [num_seqs + 1], ascending from 0) gives
+ * sequence s the rows q_start[s] .. q_start[s + 1] - 1, which are its last
+ * cached tokens (append first); rows from q_start[num_seqs] up to num_q (a
+ * padded batch) are left as they are.  A query at position p sees the tokens
+ * up to p, in the pages 0 .. p / bs of its sequence; page j is table entry j.
+ * A length above max_blocks * bs counts as that.  desc as for
+ * paged_decode_attention (bf16 pages; use_sharing is not used).
+ *
+ * kvp_page_bounds: for every layer, kv head and page that holds one of the
+ * last n_new tokens of a sequence (n_new >= its length: every page), the
+ * smallest and the largest key value per dim over the page's tokens, into
+ * bounds, device bf16 [L][NB][Hkv][2][d] (smallest, then largest), indexed by
+ * block like the pool: pages that sequences share have their bounds once.
+ * Call it after every append (n_new = tokens appended) and after
+ * seq_accept_draft, seq_evict.  NaN keys give NaN bounds.  A page listed
+ * with different lengths (a shared page that one sequence was cut back in)
+ * must be refreshed by the longer one's call last.  Table entries outside
+ * [0, NB) are passed over.
+ */
+int kvp_page_bounds(const void *k_pool, const int32_t *block_tables, const int32_t *seq_lens, int32_t num_seqs,
+                    int32_t max_blocks, int32_t n_new, const kvp_attn_desc *desc, void *bounds, void *stream);
+
+/*
+ * kvp_page_scores: for each layer l, query row t, kv head h and page j that
+ * the query sees,
+ *   scores[l][t][h][j] = scale * sum over the query heads of h and the dims i
+ *                        of max(q_i * smallest_i, q_i * largest_i),
+ * which no sum of the group's scaled scores over a key of the page exceeds.
+ * q: bf16 [L][num_q][Hq][d]; scores: fp32 [L][num_q][Hkv][score_stride],
+ * score_stride >= max_blocks; entries of other pages are left as they are.
+ * The query values are summed in 32 bits and enter the products whole.
+ * Pages whose table entry is outside [0, NB) score -inf; queries or bounds
+ * that are not finite give scores that are not.
+ */
+int kvp_page_scores(const void *q, const int32_t *q_start, int32_t num_q, const void *bounds,
+                    const int32_t *block_tables, const int32_t *seq_lens, int32_t num_seqs, int32_t max_blocks,
+                    const kvp_attn_desc *desc, float *scores, int64_t score_stride, void *stream);
+
+/*
+ * kvp_page_select: for each layer, query row and kv head, `budget` pages out
+ * of those that the query sees: the first n_sink, the last n_recent and, of
+ * the others, those with the highest scores, among equal ones the lowest page
+ * (a NaN is higher than anything, so that it shows).  selected: int32
+ * [L][num_q][Hkv][budget], the pages in ascending order, then -1 where the
+ * query sees fewer.  n_sink + n_recent <= budget.  scores may come from
+ * anywhere; those of pages that the query does not see are not read.
+ */
+int kvp_page_select(const float *scores, int64_t score_stride, const int32_t *q_start, int32_t num_q,
+                    const int32_t *seq_lens, int32_t num_seqs, int32_t max_blocks, const kvp_attn_desc *desc,
+                    int32_t budget, int32_t n_sink, int32_t n_recent, int32_t *selected, void *stream);
+
+/*
+ * paged_sparse_attention: out = softmax(q k^T * scale) v over the tokens up
+ * to the query's own in the pages selected[l][t][h][0 .. budget), lse the
+ * natural log-sum-exp.  Entries that are negative, or name a page that the
+ * query does not see or whose table entry is outside [0, NB), are passed
+ * over; their order does not matter, and a page named twice counts twice.  A
+ * row without keys gives out 0 and lse -inf.  q, out: bf16 [L][num_q][Hq][d];
+ * lse: fp32 [L][num_q][Hq] or NULL.  A NaN among the keys and values that a
+ * row sees shows in its results (they should be finite); other slots do not
+ * matter, whatever they hold.  Sums and
+ * weights are held in 32 bits (a weight meets V as two bf16 parts), and
+ * repeated calls give equal bits.
+ */
+int paged_sparse_attention(const void *q, const int32_t *q_start, int32_t num_q, const void *k_pool,
+                           const void *v_pool, const int32_t *block_tables, const int32_t *seq_lens,
+                           int32_t num_seqs, int32_t max_blocks, const int32_t *selected, int32_t budget,
+                           const kvp_attn_desc *desc, void *out, float *lse, void *stream);
+
+/*
+ * Beam search's selection: for each of `groups` requests the n_out best
+ * continuations out of beams x vocab, best first.  Row r = group * beams +
+ * beam of logits (device, type KVP_F32 / KVP_BF16 / KVP_F16, element x of row
+ * r at r * row_stride + x) and scores[r] (fp32, the log-probability so far)
+ * give
+ *   score(r, x) = scores[r] + logits[r][x] - log(sum over y of exp(logits[r][y]));
+ * equal scores go by the lower row, then the higher logit, then the lower x.
+ * finished (bytes [groups][beams], or NULL): a row with a nonzero byte goes
+ * on with pad_token alone at its score as it is; its logits are not read.  A
+ * row whose scores[r] is not finite, or whose logits hold a NaN, +inf or
+ * nothing above -inf, gives no continuation, nor does a logit of -inf (a
+ * masked token).  out_scores fp32, out_rows (r) and out_tokens (x) int32, all
+ * [groups][n_out]; where there are fewer than n_out continuations: -inf, -1
+ * and -1.  1 <= beams <= 128, 1 <= n_out <= 128.  Log-sum-exps and the
+ * comparison are in 64 bits (exponentials in 32), the results rounded to fp32.
+ * workspace: 16-byte aligned, ws_bytes >= kvp_beam_workspace_size() (0 on
+ * invalid input), its content does not matter; one call at a time.  May be
+ * captured into a graph.
+ */
+enum { KVP_F32 = 0, KVP_BF16 = 1, KVP_F16 = 2 };
+size_t kvp_beam_workspace_size(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out);
+int kvp_beam_select(const void *logits, int32_t logits_type, int64_t row_stride, const float *scores,
+                    const uint8_t *finished, int32_t pad_token, int32_t groups, int32_t beams, int32_t vocab,
+                    int32_t n_out, float *out_scores, int32_t *out_rows, int32_t *out_tokens, void *workspace,
+                    size_t ws_bytes, void *stream);
+
+/*
+ * The beams' states after kvp_beam_select: dst[o][i] = src[o][index[i]] for o
+ * < outer, i < n_dst, rows of row_bytes bytes, src [outer][n_src] and dst
+ * [outer][n_dst] rows (token histories, kvp_attention_mass weights, recurrent
+ * states; sequences of the pool go through seq_reorder).  index: device int32
+ * [n_dst]; a row whose index is outside [0, n_src) is left as it is.  src and
+ * dst do not overlap.
+ */
+int kvp_state_reorder(const void *src, void *dst, const int32_t *index, int64_t outer, int32_t n_src, int32_t n_dst,
+                      int64_t row_bytes, void *stream);
+
 /* Reads (and clears) the device error word that the last attention call on
  * this workspace left; synchronises `stream`.  *err_out = 0 when clean. */
 int kvp_device_error(void *workspace, void *stream, int32_t *err_out);

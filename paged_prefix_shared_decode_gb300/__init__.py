@@ -11,6 +11,7 @@ is missing.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -29,6 +30,9 @@ __all__ = [
     "kvp_decode_step_plan", "kvp_decode_step_run", "StepPlan",
     "KVP_STATIC_WORKSPACE_BYTES",
     "kvp_window_workspace_size", "paged_window_attention", "kvp_mass_workspace_size", "kvp_attention_mass", "seq_evict_workspace_size", "seq_evict", "kvp_draft_verify",
+    "RopeDesc", "rope_desc", "seq_append_rope", "seq_reorder",
+    "kvp_page_bounds", "kvp_page_scores", "kvp_page_select", "paged_sparse_attention",
+    "kvp_beam_workspace_size", "kvp_beam_select", "kvp_state_reorder", "KVP_F32", "KVP_BF16", "KVP_F16",
     "KVP_OK", "KVP_ERR_INVALID", "KVP_ERR_OOM", "KVP_ERR_STATE", "KVP_ERR_CUDA", "KVP_ERR_DEVICE",
     "KVP_ERR_WORKSPACE",
 ]
@@ -36,6 +40,7 @@ __all__ = [
 KVP_OK, KVP_ERR_INVALID, KVP_ERR_OOM, KVP_ERR_STATE, KVP_ERR_CUDA, KVP_ERR_DEVICE = 0, -1, -2, -3, -4, -5
 KVP_ERR_WORKSPACE = -6
 KVP_KV_BF16, KVP_KV_4BIT = 0, 1   # page formats (kvp_attn_desc.kv_format)
+KVP_F32, KVP_BF16, KVP_F16 = 0, 1, 2   # logits of kvp_beam_select
 KVP_STATIC_WORKSPACE_BYTES = 32 << 20   # size of the library's own workspace (include/kvp.h)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -73,6 +78,11 @@ class AttnDesc(ctypes.Structure):
                 ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("use_sharing", ctypes.c_int32),
                 ("kv_format", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("freqs", ctypes.c_void_p),
+                ("base", ctypes.c_double), ("scale", ctypes.c_float)]
 
 
 class StepIO(ctypes.Structure):
@@ -145,6 +155,19 @@ _SIGS = {
                   ctypes.c_int),
     "kvp_draft_verify": ([_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P,
                           _I32, _I32, _I32, _P, _P, _P, _P], ctypes.c_int),
+    "seq_append_rope": ([_P, _I32, _P, _P, _P, _P, ctypes.POINTER(RopeDesc), _P, _P, _P, _I32, _P], ctypes.c_int),
+    "seq_reorder": ([_P, _P, _P, _I32], ctypes.c_int),
+    "kvp_page_bounds": ([_P, _P, _P, _I32, _I32, _I32, ctypes.POINTER(AttnDesc), _P, _P], ctypes.c_int),
+    "kvp_page_scores": ([_P, _P, _I32, _P, _P, _P, _I32, _I32, ctypes.POINTER(AttnDesc), _P, ctypes.c_int64, _P],
+                        ctypes.c_int),
+    "kvp_page_select": ([_P, ctypes.c_int64, _P, _I32, _P, _I32, _I32, ctypes.POINTER(AttnDesc), _I32, _I32, _I32, _P,
+                         _P], ctypes.c_int),
+    "paged_sparse_attention": ([_P, _P, _I32, _P, _P, _P, _P, _I32, _I32, _P, _I32, ctypes.POINTER(AttnDesc), _P, _P,
+                                _P], ctypes.c_int),
+    "kvp_beam_workspace_size": ([_I32, _I32, _I32, _I32], ctypes.c_size_t),
+    "kvp_beam_select": ([_P, _I32, ctypes.c_int64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
+                         ctypes.c_size_t, _P], ctypes.c_int),
+    "kvp_state_reorder": ([_P, _P, _P, ctypes.c_int64, _I32, _I32, ctypes.c_int64, _P], ctypes.c_int),
     "kvp_radix_create": ([_P, ctypes.POINTER(_P)], ctypes.c_int),
     "kvp_radix_destroy": ([_P], ctypes.c_int),
     "kvp_radix_match": ([_P, _P, _I32, _P, _I32, _I32P, _I32P], ctypes.c_int),
@@ -724,6 +747,170 @@ def kvp_draft_verify(target, draft, tree_parent, draft_tokens, u_accept, u_next,
                                    _arg("n_accepted", n_accepted, i32, (B,), dev),
                                    _arg("next_token", next_token, i32, (B,), dev), _stream(stream)),
            "kvp_draft_verify")
+
+
+# ------------------------------------ rotated appends, beams, sparse attention
+
+def rope_desc(rot_dim: int, base: float = 10000.0, freqs=None, interleaved: bool = False,
+              scale: float = 1.0) -> RopeDesc:
+    """The rotation of the first rot_dim dims: frequencies base ** (-2 i /
+    rot_dim), or freqs (radians per position, rot_dim / 2 of them)."""
+    d = RopeDesc(rot_dim, int(interleaved), None, base, scale)
+    if freqs is not None:
+        d.keep = np.ascontiguousarray(freqs, dtype=np.float64)
+        if d.keep.shape != (rot_dim // 2,):
+            raise ValueError(f"freqs: expected {rot_dim // 2} entries, got shape {d.keep.shape}")
+        d.freqs = d.keep.ctypes.data
+    return d
+
+
+def seq_append_rope(pool, seqs, ntoks, k, v, rope: RopeDesc, positions=None, q=None, q_out=None, stream=None):
+    """seq_append_batch with k rotated into the pages, and q [L][T][Hq][d]
+    into q_out (q itself or apart).  k, v [L][T][Hkv][d] bf16, T = sum of
+    ntoks; positions: device int32 [T], or None (the cache's)."""
+    s, sp = _host_i32(seqs)
+    n, np_ = _batch_i32("ntoks", ntoks, len(s))
+    torch, dev = _torch()
+    layers, heads = kvp_pool_shape(pool)
+    T, bf16 = sum(n.tolist()), torch.bfloat16
+    hq = 0
+    if k is not None and not isinstance(k, int):
+        d = k.shape[-1]
+        k, v = (_arg(nm, x, bf16, (layers, T, heads, d), dev) for nm, x in (("k", k), ("v", v)))
+        if q is not None:
+            hq = q.shape[-2]
+            q, q_out = (_arg(nm, x, bf16, (layers, T, hq, d), dev) for nm, x in (("q", q), ("q_out", q_out)))
+    _check(load().seq_append_rope(pool, len(s), sp, np_, k, v, ctypes.byref(rope),
+                                  _arg("positions", positions, torch.int32, (T,), dev), q, q_out, hq,
+                                  _stream(stream)), "seq_append_rope")
+
+
+def seq_reorder(pool, dst, src):
+    """Sequence dst[i] becomes a fork of what sequence src[i] was."""
+    d, dp = _host_i32(dst)
+    s, sp = _batch_i32("src", src, len(d))
+    _check(load().seq_reorder(pool, dp, sp, len(d)), "seq_reorder")
+
+
+def _batch(desc, block_tables, seq_lens, q_start, torch, dev):
+    """Addresses and sizes of a batch held on the device."""
+    S = seq_lens.shape[0]
+    i32, mb = torch.int32, None
+    if block_tables is not None:
+        mb = block_tables.shape[-1]
+        block_tables = _arg("block_tables", block_tables, i32, (S, mb), dev)
+    return (S, mb, block_tables, _arg("seq_lens", seq_lens, i32, (S,), dev),
+            _arg("q_start", q_start, i32, (S + 1,), dev))
+
+
+def kvp_page_bounds(k_pool, block_tables, seq_lens, n_new: int, desc: AttnDesc, bounds, stream=None):
+    """Smallest and largest key per dim of the pages that hold one of the last
+    n_new tokens of a sequence, into bounds [L][NB][Hkv][2][d] bf16.
+    block_tables [S][MB], seq_lens [S]: device int32."""
+    torch, dev = _torch()
+    S, mb, tp, lp, _ = _batch(desc, block_tables, seq_lens, None, torch, dev)
+    bf16, shape = torch.bfloat16, (desc.num_layers, desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim)
+    _check(load().kvp_page_bounds(_arg("k_pool", k_pool, bf16, _pool_shape(desc), dev), tp, lp, S, mb, n_new,
+                                  ctypes.byref(desc), _arg("bounds", bounds, bf16, shape, dev), _stream(stream)),
+           "kvp_page_bounds")
+
+
+def kvp_page_scores(q, q_start, bounds, block_tables, seq_lens, desc: AttnDesc, scores, stream=None):
+    """Scores [L][T][Hkv][stride] fp32 of the pages that each query row of q
+    [L][T][Hq][d] sees; q_start: device int32 [S + 1], or None (one row a
+    sequence)."""
+    torch, dev = _torch()
+    S, mb, tp, lp, sp = _batch(desc, block_tables, seq_lens, q_start, torch, dev)
+    L, T, heads, d = desc.num_layers, q.shape[1], desc.num_kv_heads, desc.head_dim
+    stride = scores.shape[-1]
+    _check(load().kvp_page_scores(_arg("q", q, torch.bfloat16, (L, T, desc.num_q_heads, d), dev), sp, T,
+                                  _arg("bounds", bounds, torch.bfloat16, (L, desc.num_blocks, heads, 2, d), dev), tp,
+                                  lp, S, mb, ctypes.byref(desc),
+                                  _arg("scores", scores, torch.float32, (L, T, heads, stride), dev), stride,
+                                  _stream(stream)), "kvp_page_scores")
+
+
+def kvp_page_select(scores, q_start, seq_lens, desc: AttnDesc, n_sink: int, n_recent: int, selected, max_blocks=None,
+                    stream=None):
+    """The best selected.shape[-1] pages of each row of scores
+    [L][T][Hkv][stride] into selected [L][T][Hkv][budget] int32, ascending;
+    max_blocks (None: as long as the scores' rows): the tables' width."""
+    torch, dev = _torch()
+    S, _, _, lp, sp = _batch(desc, None, seq_lens, q_start, torch, dev)
+    L, T, heads = desc.num_layers, scores.shape[1], desc.num_kv_heads
+    stride, budget = scores.shape[-1], selected.shape[-1]
+    _check(load().kvp_page_select(_arg("scores", scores, torch.float32, (L, T, heads, stride), dev), stride, sp, T, lp,
+                                  S, stride if max_blocks is None else max_blocks, ctypes.byref(desc), budget, n_sink,
+                                  n_recent, _arg("selected", selected, torch.int32, (L, T, heads, budget), dev),
+                                  _stream(stream)), "kvp_page_select")
+
+
+def paged_sparse_attention(q, q_start, k_pool, v_pool, block_tables, seq_lens, selected, desc: AttnDesc, out, lse,
+                           stream=None):
+    """Attention of each query row over its selected [L][T][Hkv][budget]
+    pages; out like q [L][T][Hq][d] bf16, lse [L][T][Hq] fp32 or None."""
+    torch, dev = _torch()
+    S, mb, tp, lp, sp = _batch(desc, block_tables, seq_lens, q_start, torch, dev)
+    T, budget, bf16 = q.shape[1], selected.shape[-1], torch.bfloat16
+    rows = (desc.num_layers, T, desc.num_q_heads)
+    wide, pool = (*rows, desc.head_dim), _pool_shape(desc)
+    _check(load().paged_sparse_attention(_arg("q", q, bf16, wide, dev), sp, T, _arg("k_pool", k_pool, bf16, pool, dev),
+                                         _arg("v_pool", v_pool, bf16, pool, dev), tp, lp, S, mb,
+                                         _arg("selected", selected, torch.int32,
+                                              (desc.num_layers, T, desc.num_kv_heads, budget), dev), budget,
+                                         ctypes.byref(desc), _arg("out", out, bf16, wide, dev),
+                                         _arg("lse", lse, torch.float32, rows, dev), _stream(stream)),
+           "paged_sparse_attention")
+
+
+def kvp_beam_workspace_size(groups: int, beams: int, vocab: int, n_out: int) -> int:
+    n = load().kvp_beam_workspace_size(groups, beams, vocab, n_out)
+    if n == 0:
+        raise KvpError(KVP_ERR_INVALID, "kvp_beam_workspace_size")
+    return n
+
+
+def kvp_beam_select(logits, scores, finished, pad_token: int, out_scores, out_rows, out_tokens, workspace,
+                    ws_bytes=None, stream=None):
+    """The best continuations of each request's beams: logits [G][B][V] fp32,
+    bf16 or fp16 (last dimension contiguous, rows evenly spaced), scores [G][B]
+    fp32, finished [G][B] bool or uint8 (or None); out_scores fp32, out_rows
+    and out_tokens int32 [G][n]."""
+    torch, dev = _torch()
+    G, B, V = logits.shape
+    types = {torch.float32: KVP_F32, torch.bfloat16: KVP_BF16, torch.float16: KVP_F16}
+    if logits.dtype not in types or logits.get_device() != dev:
+        raise ValueError(f"logits: expected float32, bfloat16 or float16 on cuda:{dev}, got {logits.dtype} on "
+                         f"{logits.device}")
+    row = logits.stride(1) if B > 1 else logits.stride(0) if G > 1 else V
+    if (V > 1 and logits.stride(2) != 1) or (G > 1 and logits.stride(0) != B * row):
+        raise ValueError(f"logits: expected evenly spaced contiguous rows, got strides {logits.stride()}")
+    if finished is not None and finished.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"finished: expected bool or uint8, got {finished.dtype}")
+    n, i32 = out_scores.shape[-1], torch.int32
+    _check(load().kvp_beam_select(logits.data_ptr(), types[logits.dtype], row,
+                                  _arg("scores", scores, torch.float32, (G, B), dev),
+                                  finished if finished is None else
+                                  _arg("finished", finished, finished.dtype, (G, B), dev), pad_token, G, B, V, n,
+                                  _arg("out_scores", out_scores, torch.float32, (G, n), dev),
+                                  _arg("out_rows", out_rows, i32, (G, n), dev),
+                                  _arg("out_tokens", out_tokens, i32, (G, n), dev), _dev(workspace),
+                                  _ws_bytes(workspace, ws_bytes), _stream(stream)), "kvp_beam_select")
+
+
+def kvp_state_reorder(src, dst, index, dim: int = 0, stream=None):
+    """dst row i = src row index[i] along dimension `dim` (the ones before it
+    are outer); index: device int32, as many as dst has rows, in any shape."""
+    torch, dev = _torch()
+    outer, inner = src.shape[:dim], src.shape[dim + 1:]
+    n_src, n_dst = src.shape[dim], dst.shape[dim]
+    if index.numel() != n_dst:
+        raise ValueError(f"index: expected {n_dst} entries, got {index.numel()}")
+    size = src.element_size()
+    _check(load().kvp_state_reorder(_arg("src", src, src.dtype, src.shape, dev),
+                                    _arg("dst", dst, src.dtype, (*outer, n_dst, *inner), dev),
+                                    _arg("index", index, torch.int32, index.shape, dev), math.prod(outer), n_src, n_dst,
+                                    math.prod(inner) * size, _stream(stream)), "kvp_state_reorder")
 
 
 def kvp_device_error(workspace, stream=None) -> int:

@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libkvp.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 SOURCES = ["pool.cpp", "radix.cpp", "plan.cpp", "attn_kernels.cu", "attn_tc.cu", "kv_kernels.cu", "kv4_kernels.cu", "no_alloc.cu",
-           "mass_kernels.cu", "mass_tc.cu", "evict_kernels.cu", "draft_verify.cu"]
+           "mass_kernels.cu", "mass_tc.cu", "evict_kernels.cu", "draft_verify.cu", "rope_kernels.cu", "page_kernels.cu",
+           "sparse_attn.cu", "beam_kernels.cu"]
 
 
 def _nvcc() -> str:

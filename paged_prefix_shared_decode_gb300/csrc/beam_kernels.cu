@@ -1,0 +1,484 @@
+// Beam search's selection (sm_103a): the n best of score + log-softmax over
+// beams x vocabulary, in one pass over the logits, and the gather that gives
+// the new beams their parents' states.
+//
+//   score(r, x) = scores[r] + logits[r][x] - log sum_y exp(logits[r][y])
+//
+// beam_part_kernel: a CTA per (row, chunk of the row).  A chunk's logits are
+// read once into registers; its maximum, its sum of exponentials and its n
+// best logits go to the workspace.  Within a row scores order like logits, so
+// a row's n best scores are among its chunks' n best logits.  The n best of a
+// chunk: the n-th largest of the threads' own maxima is a lower bound that
+// few more than n logits reach; those are ranked against one another.  (More
+// reach it where many are equal, or the large ones lie in few threads: then
+// one after the other is taken.)
+// beam_join_kernel: a CTA per request joins the sums (in 64 bits), scores the
+// candidates and ranks them the same way.
+// Bound by HBM for large batches (every logit read once), by latency for one
+// request.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/kvp.h"
+#include "kvp_internal.h"
+
+namespace kvp {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kPer = 32;                       // logits per thread
+constexpr int kChunk = kThreads * kPer;
+constexpr int kMaxOut = 128, kMaxBeams = 128;
+constexpr int kCap = 1024;                     // candidates ranked at once
+
+// A chunk's part of its row.
+struct PartHead {
+    float top;         // largest logit; +inf or NaN where the row is not to be used
+    int32_t count;     // candidates (descending)
+    double sum;        // of exp(logit - top)
+};
+
+struct BeamArgs {
+    const void *logits;
+    int64_t row_stride;
+    const float *scores;
+    const uint8_t *finished;
+    int32_t pad, groups, beams, vocab, n, chunks;
+    int32_t vec;                  // rows may be read 16 bytes at a time
+    float *out_scores;
+    int32_t *out_rows, *out_tokens;
+    PartHead *heads;              // [rows][chunks]
+    float *cand;                  // [rows][chunks][n]
+    int32_t *cand_at;
+};
+
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+
+// Thread i's k-th logit of a chunk sits at (k / V) * V * kThreads + i * V + k % V.
+template <class T> constexpr int kVec = 16 / sizeof(T);
+template <class T>
+__device__ __forceinline__ int place(int tid, int k) { return (k / kVec<T>) * kVec<T> * kThreads + tid * kVec<T> + k % kVec<T>; }
+
+__device__ __forceinline__ double sum_block(double x, double *s, int warp, int lane) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) s[warp] = x;
+    __syncthreads();
+    double r = 0;
+    for (int w = 0; w < kWarps; ++w) r += s[w];
+    return r;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) beam_part_kernel(const BeamArgs a) {
+    __shared__ double s_sum[kWarps];
+    __shared__ float s_max[kThreads];
+    __shared__ float s_c[kCap];
+    __shared__ int s_at[kCap];
+    __shared__ float s_bound;
+    __shared__ int s_count, s_best[kWarps];
+    __shared__ float s_bestv[kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
+    if (a.finished && a.finished[row]) return;
+    const int x0 = chunk * kChunk, len = min(kChunk, a.vocab - x0);
+    const T *src = static_cast<const T *>(a.logits) + row * a.row_stride + x0;
+    float v[kPer];
+    if (a.vec) {
+        uint4 raw[kPer / kVec<T>];
+#pragma unroll
+        for (int i = 0; i < kPer / kVec<T>; ++i) {
+            const int at = place<T>(tid, i * kVec<T>);
+            if (at + kVec<T> <= len) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + at));
+        }
+#pragma unroll
+        for (int i = 0; i < kPer / kVec<T>; ++i) {
+            const int at = place<T>(tid, i * kVec<T>);
+            const T *e = reinterpret_cast<const T *>(&raw[i]);
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k)
+                v[i * kVec<T> + k] = at + kVec<T> <= len ? as_float(e[k]) : at + k < len ? as_float(src[at + k]) : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int at = place<T>(tid, k);
+            v[k] = at < len ? as_float(src[at]) : -INFINITY;
+        }
+    }
+    float top = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        top = fmaxf(top, v[k]);
+        nan |= v[k] != v[k];
+    }
+    if (nan) top = INFINITY;             // as +inf does: the row has no log-sum-exp
+    s_max[tid] = top;
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    // rank of this thread's maximum among all of them
+    int rank = 0;
+    float all = -INFINITY;
+    for (int i = 0; i < kThreads; ++i) {
+        const float y = s_max[i];
+        rank += y > top || (y == top && i < tid);
+        all = fmaxf(all, y);
+    }
+    if (rank == min(a.n, kThreads) - 1) s_bound = top;
+    PartHead *head = a.heads + (int64_t)row * a.chunks + chunk;
+    float *cand = a.cand + ((int64_t)row * a.chunks + chunk) * a.n;
+    int32_t *cand_at = a.cand_at + ((int64_t)row * a.chunks + chunk) * a.n;
+    if (!(all < INFINITY) || all == -INFINITY) {       // nothing here, or nothing in the row
+        if (tid == 0) *head = PartHead{all, 0, 0.0};
+        return;
+    }
+    float part = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) part += expf(v[k] - all);
+    const double sum = sum_block((double)part, s_sum, warp, lane);     // (its barrier: s_bound is there)
+    const float bound = s_bound;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        if (v[k] >= bound && v[k] > -INFINITY) {
+            const int i = atomicAdd(&s_count, 1);
+            if (i < kCap) {
+                s_c[i] = v[k];
+                s_at[i] = place<T>(tid, k);
+            }
+        }
+    __syncthreads();
+    const int found = s_count;
+    if (found <= kCap) {
+        for (int i = tid; i < found; i += kThreads) {
+            const float x = s_c[i];
+            const int at = s_at[i];
+            int r = 0;
+            for (int j = 0; j < found; ++j) r += s_c[j] > x || (s_c[j] == x && s_at[j] < at);
+            if (r < a.n) {
+                cand[r] = x;
+                cand_at[r] = x0 + at;
+            }
+        }
+        if (tid == 0) *head = PartHead{all, min(found, a.n), sum};
+        return;
+    }
+    // one after the other: the largest logit behind the last one taken
+    float last = INFINITY;
+    int last_at = -1;
+    for (int r = 0; r < a.n; ++r) {
+        float best = -INFINITY;
+        int at = INT_MAX;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int p = place<T>(tid, k);
+            const bool open = v[k] < last || (v[k] == last && p > last_at);
+            if (open && (v[k] > best || (v[k] == best && p < at)) && v[k] > -INFINITY) {
+                best = v[k];
+                at = p;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float y = __shfl_xor_sync(0xffffffffu, best, o);
+            const int p = __shfl_xor_sync(0xffffffffu, at, o);
+            if (y > best || (y == best && p < at)) {
+                best = y;
+                at = p;
+            }
+        }
+        __syncthreads();
+        if (lane == 0) {
+            s_bestv[warp] = best;
+            s_best[warp] = at;
+        }
+        __syncthreads();
+        best = s_bestv[0];
+        at = s_best[0];
+        for (int w = 1; w < kWarps; ++w)
+            if (s_bestv[w] > best || (s_bestv[w] == best && s_best[w] < at)) {
+                best = s_bestv[w];
+                at = s_best[w];
+            }
+        last = best;
+        last_at = at;
+        if (tid == 0) {
+            cand[r] = best;
+            cand_at[r] = x0 + at;
+        }
+    }
+    if (tid == 0) *head = PartHead{all, a.n, sum};     // (more than kCap >= n of them)
+}
+
+// A candidate's place in the order: score, then row, then logit, then token.
+struct Entry {
+    double score;
+    float logit;
+    int32_t beam, at;
+};
+__device__ __forceinline__ bool before(const Entry &x, const Entry &y) {
+    if (x.score != y.score) return x.score > y.score;
+    if (x.beam != y.beam) return x.beam < y.beam;
+    if (x.logit != y.logit) return x.logit > y.logit;
+    return x.at < y.at;
+}
+
+__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
+    __shared__ double s_add[kMaxBeams];     // score - log-sum-exp; -inf: no candidates
+    __shared__ Entry s_e[kCap];
+    __shared__ double s_max[kThreads], s_bound;
+    __shared__ int s_count;
+    __shared__ Entry s_best[kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = blockIdx.x;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    for (int b = warp; b < a.beams; b += kWarps) {
+        const int row = g * a.beams + b;
+        const float cum = a.scores[row];
+        double add = -INFINITY;
+        if (isfinite(cum)) {
+            if (a.finished && a.finished[row]) {
+                add = (double)cum;
+            } else {
+                const PartHead *h = a.heads + (int64_t)row * a.chunks;
+                float top = -INFINITY;
+                for (int c = lane; c < a.chunks; c += 32) top = fmaxf(top, h[c].top);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                double sum = 0;
+                if (top < INFINITY && top > -INFINITY) {
+                    for (int c = lane; c < a.chunks; c += 32)
+                        if (h[c].top > -INFINITY) sum += h[c].sum * exp((double)h[c].top - (double)top);
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    add = (double)cum - ((double)top + log(sum));
+                }
+            }
+        }
+        if (lane == 0) s_add[b] = add;
+    }
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    // candidate i: (beam, chunk, place); finished beams have one, in chunk 0
+    const int64_t per_beam = (int64_t)a.chunks * a.n, total = per_beam * a.beams;
+    auto entry = [&](int64_t i, Entry &e) -> bool {
+        const int b = (int)(i / per_beam), row = g * a.beams + b;
+        const double add = s_add[b];
+        if (add == -INFINITY) return false;
+        const int64_t in = i % per_beam;
+        if (a.finished && a.finished[row]) {
+            if (in) return false;
+            e = Entry{add, 0.f, b, a.pad};
+            return true;
+        }
+        if ((int)(in % a.n) >= a.heads[(int64_t)row * a.chunks + in / a.n].count) return false;
+        const int64_t at = row * per_beam + in;
+        e.logit = a.cand[at];
+        e.score = add + (double)e.logit;
+        e.beam = b;
+        e.at = a.cand_at[at];
+        return true;
+    };
+    double top = -INFINITY;
+    Entry e;
+    for (int64_t i = tid; i < total; i += kThreads)
+        if (entry(i, e)) top = fmax(top, e.score);
+    s_max[tid] = top;
+    __syncthreads();
+    int rank = 0;
+    for (int i = 0; i < kThreads; ++i) rank += s_max[i] > top || (s_max[i] == top && i < tid);
+    if (rank == a.n - 1) s_bound = top;
+    __syncthreads();
+    const double bound = s_bound;
+    for (int64_t i = tid; i < total; i += kThreads)
+        if (entry(i, e) && e.score >= bound) {
+            const int k = atomicAdd(&s_count, 1);
+            if (k < kCap) s_e[k] = e;
+        }
+    __syncthreads();
+    const int found = s_count;
+    float *os = a.out_scores + (int64_t)g * a.n;
+    int32_t *orow = a.out_rows + (int64_t)g * a.n, *ot = a.out_tokens + (int64_t)g * a.n;
+    auto put = [&](int r, const Entry &x) {
+        os[r] = (float)x.score;
+        orow[r] = g * a.beams + x.beam;
+        ot[r] = x.at;
+    };
+    if (found <= kCap) {
+        for (int i = tid; i < found; i += kThreads) {
+            const Entry x = s_e[i];
+            int r = 0;
+            for (int j = 0; j < found; ++j) r += before(s_e[j], x);
+            if (r < a.n) put(r, x);
+        }
+        for (int r = found + tid; r < a.n; r += kThreads) {
+            os[r] = -INFINITY;
+            orow[r] = ot[r] = -1;
+        }
+        return;
+    }
+    // one after the other, each the best behind the last one
+    Entry last{INFINITY, INFINITY, -1, -1};
+    for (int r = 0; r < a.n; ++r) {
+        Entry best{-INFINITY, -INFINITY, INT_MAX, INT_MAX};
+        for (int64_t i = tid; i < total; i += kThreads)
+            if (entry(i, e) && before(last, e) && before(e, best)) best = e;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            Entry y;
+            y.score = __shfl_xor_sync(0xffffffffu, best.score, o);
+            y.logit = __shfl_xor_sync(0xffffffffu, best.logit, o);
+            y.beam = __shfl_xor_sync(0xffffffffu, best.beam, o);
+            y.at = __shfl_xor_sync(0xffffffffu, best.at, o);
+            if (before(y, best)) best = y;
+        }
+        __syncthreads();
+        if (lane == 0) s_best[warp] = best;
+        __syncthreads();
+        best = s_best[0];
+        for (int w = 1; w < kWarps; ++w)
+            if (before(s_best[w], best)) best = s_best[w];
+        last = best;
+        if (tid == 0) put(r, best);
+    }
+}
+
+// ------------------------------------------------------------------ states
+
+constexpr int kCopyThreads = 256, kInFlight = 8;
+
+// dst[o][i] = src[o][index[i]], V bytes a chunk: a CTA takes a stretch of one
+// row, eight chunks in flight a thread.
+template <class V>
+__global__ void __launch_bounds__(kCopyThreads)
+    state_reorder_kernel(const V *src, V *dst, const int32_t *index, int32_t n_src, int32_t n_dst, int64_t chunks,
+                         int64_t tiles) {
+    const int64_t row = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int64_t o = row / n_dst;
+    const int from = index[row % n_dst];
+    if ((unsigned)from >= (unsigned)n_src) return;
+    const V *s = src + (o * n_src + from) * chunks;
+    V *d = dst + row * chunks;
+    const int64_t x0 = tile * kCopyThreads * kInFlight + threadIdx.x;
+    V v[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u)
+        if (x0 + u * kCopyThreads < chunks) v[u] = s[x0 + u * kCopyThreads];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u)
+        if (x0 + u * kCopyThreads < chunks) d[x0 + u * kCopyThreads] = v[u];
+}
+
+template <class V>
+cudaError_t launch_reorder(const void *src, void *dst, const int32_t *index, int64_t outer, int32_t n_src, int32_t n_dst,
+                           int64_t row_bytes, cudaStream_t stream) {
+    const int64_t chunks = row_bytes / sizeof(V), tiles = (chunks + kCopyThreads * kInFlight - 1) / (kCopyThreads * kInFlight);
+    if (tiles > INT32_MAX || outer * n_dst > INT32_MAX / tiles) return cudaErrorInvalidValue;
+    state_reorder_kernel<V><<<(unsigned)(outer * n_dst * tiles), kCopyThreads, 0, stream>>>(
+        static_cast<const V *>(src), static_cast<V *>(dst), index, n_src, n_dst, chunks, tiles);
+    count_launch();
+    return cudaGetLastError();
+}
+
+bool bad(const void *p, uintptr_t align) { return !p || ((uintptr_t)p & (align - 1)); }
+
+bool beam_shape_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out) {
+    if (groups <= 0 || beams <= 0 || beams > kMaxBeams || vocab <= 0 || vocab > (1 << 30) || n_out <= 0 || n_out > kMaxOut)
+        return false;
+    return (int64_t)groups * beams * ((vocab + kChunk - 1) / kChunk) <= INT32_MAX;
+}
+
+template <class T>
+cudaError_t launch_beam(const BeamArgs &a, cudaStream_t stream) {
+    beam_part_kernel<T><<<(unsigned)(a.groups * a.beams * a.chunks), kThreads, 0, stream>>>(a);
+    count_launch();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)a.groups);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, beam_join_kernel, a);
+    count_launch();
+    return e;
+}
+
+}  // namespace
+}  // namespace kvp
+
+using namespace kvp;
+
+extern "C" {
+
+size_t kvp_beam_workspace_size(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out) {
+    if (!beam_shape_ok(groups, beams, vocab, n_out)) return 0;
+    const size_t parts = (size_t)groups * beams * ((vocab + kChunk - 1) / kChunk);
+    return parts * (sizeof(PartHead) + (size_t)n_out * 8);
+}
+
+int kvp_beam_select(const void *logits, int32_t logits_type, int64_t row_stride, const float *scores,
+                    const uint8_t *finished, int32_t pad_token, int32_t groups, int32_t beams, int32_t vocab,
+                    int32_t n_out, float *out_scores, int32_t *out_rows, int32_t *out_tokens, void *workspace,
+                    size_t ws_bytes, void *stream) {
+    if (!beam_shape_ok(groups, beams, vocab, n_out) || row_stride < 0 || logits_type < KVP_F32 || logits_type > KVP_F16)
+        return KVP_ERR_INVALID;
+    const int size = logits_type == KVP_F32 ? 4 : 2;
+    if (bad(logits, size) || bad(scores, 4) || bad(out_scores, 4) || bad(out_rows, 4) || bad(out_tokens, 4) ||
+        bad(workspace, 16) || ws_bytes < kvp_beam_workspace_size(groups, beams, vocab, n_out))
+        return KVP_ERR_INVALID;
+    if (!stream && stream_capturing(nullptr)) return KVP_ERR_STATE;
+    BeamArgs a{};
+    a.logits = logits;
+    a.row_stride = row_stride;
+    a.scores = scores;
+    a.finished = finished;
+    a.pad = pad_token; a.groups = groups; a.beams = beams; a.vocab = vocab; a.n = n_out;
+    a.chunks = (vocab + kChunk - 1) / kChunk;
+    a.vec = ((uintptr_t)logits & 15) == 0 && row_stride * size % 16 == 0;
+    a.out_scores = out_scores; a.out_rows = out_rows; a.out_tokens = out_tokens;
+    const size_t parts = (size_t)groups * beams * a.chunks;
+    a.heads = static_cast<PartHead *>(workspace);
+    a.cand = reinterpret_cast<float *>(a.heads + parts);
+    a.cand_at = reinterpret_cast<int32_t *>(a.cand + parts * n_out);
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = logits_type == KVP_F32    ? launch_beam<float>(a, st)
+                          : logits_type == KVP_BF16 ? launch_beam<__nv_bfloat16>(a, st)
+                                                    : launch_beam<__half>(a, st);
+    return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+int kvp_state_reorder(const void *src, void *dst, const int32_t *index, int64_t outer, int32_t n_src, int32_t n_dst,
+                      int64_t row_bytes, void *stream) {
+    if (outer < 0 || n_src < 0 || n_dst < 0 || row_bytes < 0) return KVP_ERR_INVALID;
+    if (outer == 0 || n_dst == 0 || row_bytes == 0) return KVP_OK;
+    if (n_src == 0) return KVP_OK;              // no index is inside
+    if (!src || !dst || bad(index, 4) || outer > INT64_MAX / std::max(n_src, n_dst) / row_bytes) return KVP_ERR_INVALID;
+    const uintptr_t s = (uintptr_t)src, d = (uintptr_t)dst;
+    if (s < d + (uint64_t)outer * n_dst * row_bytes && d < s + (uint64_t)outer * n_src * row_bytes) return KVP_ERR_INVALID;
+    if (!stream && stream_capturing(nullptr)) return KVP_ERR_STATE;
+    const uintptr_t all = s | d | (uintptr_t)row_bytes;
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (all % 16 == 0)
+        e = launch_reorder<uint4>(src, dst, index, outer, n_src, n_dst, row_bytes, st);
+    else if (all % 4 == 0)
+        e = launch_reorder<uint32_t>(src, dst, index, outer, n_src, n_dst, row_bytes, st);
+    else
+        e = launch_reorder<unsigned char>(src, dst, index, outer, n_src, n_dst, row_bytes, st);
+    return e == cudaSuccess ? KVP_OK : e == cudaErrorInvalidValue ? KVP_ERR_INVALID : KVP_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "kv4_quant.cuh"
 #include "kvp_internal.h"
 
 namespace kvp {
@@ -38,20 +39,6 @@ struct Kv4WriteArgs {
     int32_t cow[3 * NC];            // (source block, copy block, used slots)
     int32_t slots[NS];              // block * bs + slot per token
 };
-
-__device__ __forceinline__ float bf16_bits_to_float(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-
-// e = smallest integer with m <= 7 * 2^e for m > 0, clamped to [-127, 127]:
-// m in [2^E, 2^(E+1)) needs e = E - 2 when m <= 1.75 * 2^E, else E - 1 (both
-// sides exact in fp32).
-__device__ __forceinline__ int row_exponent(float m) {
-    if (!(m > 0.f)) return -127;
-    int E;
-    const float f = frexpf(m, &E);   // m = f * 2^E, f in [0.5, 1)
-    E -= 1;                          // m in [2^E, 2^(E+1))
-    const int e = (f * 2.f <= 1.75f) ? E - 2 : E - 1;
-    return max(-127, min(127, e));
-}
 
 // One warp per (layer, head, unit): a copy-on-write triple's rows, or one
 // appended token's row (quantised).
@@ -91,24 +78,8 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ 
         // lane owns values 2*lane, 2*lane+1 (d 64) or 4*lane .. 4*lane+3 (d 128)
         const int vpl = a.d / 32;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t amax = 0;
-        for (int j = 0; j < vpl; ++j) {
-            x[j] = bf16_bits_to_float(src[lane * vpl + j]);
-            amax = max(amax, __float_as_uint(fabsf(x[j])));
-        }
-        amax = __reduce_max_sync(0xffffffffu, amax);   // |x| bit patterns order like the values
-        const int e = row_exponent(__uint_as_float(amax));
-        uint32_t packed = 0;
-        for (int j = 0; j < vpl; ++j) {
-            const float c = fminf(7.f, fmaxf(-7.f, rintf(ldexpf(x[j], -e))));
-            packed |= ((uint32_t)(int)c & 0xFu) << (4 * j);
-        }
-        if (vpl == 2) {
-            codes[row * rowb + lane] = (uint8_t)packed;
-        } else {
-            reinterpret_cast<uint16_t *>(codes + row * rowb)[lane] = (uint16_t)packed;
-        }
-        if (lane == 0) exps[row] = (int8_t)e;
+        for (int j = 0; j < vpl; ++j) x[j] = bf16_bits_to_float(src[lane * vpl + j]);
+        store_row4(x, vpl, codes + row * rowb, exps + row, lane);
     }
 }
 

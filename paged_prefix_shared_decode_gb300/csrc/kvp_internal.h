@@ -320,6 +320,29 @@ struct EvictLaunch {
 cudaError_t launch_evict(const EvictLaunch &a, int max_len, bool copies, bool packs, const unsigned char *image,
                          size_t bytes, size_t tables_at, cudaStream_t stream);
 
+// Append with the rotation of K and Q by position (rope_kernels.cu).
+constexpr int kMaxRot = 256;
+struct RopeSeq {            // one sequence's new tokens, in the order of k, v and q
+    int32_t ntok, pos0;     // how many, and the first one's slot in the sequence
+    const int32_t *blocks;  // host: its table from block pos0 / bs on
+};
+struct RopeAppend {
+    void *k_pool, *v_pool, *k_exp, *v_exp;   // (k_exp: a pool of 4-bit pages)
+    const void *k, *v, *q;
+    void *q_out;
+    const int32_t *positions;   // device, or null: the slots
+    int32_t L, NB, Hkv, Hq, bs, d;
+    int32_t ntok;               // tokens in k / v / q
+    int32_t rot, adjacent;
+    float scale;
+    uint64_t freq[kMaxRot / 2]; // turns per position, modulo 1, times 2^64
+    const RopeSeq *seqs;
+    int32_t nseq;
+    const int32_t *cow;         // host: (src, dst, used) triples
+    int32_t ncow;
+};
+cudaError_t launch_rope_append(const RopeAppend &r, cudaStream_t stream);
+
 // A descriptor that the attention entry points accept.
 bool attn_desc_ok(const kvp_attn_desc *d);
 // Whether `stream` is being captured into a graph: calls that upload a plan

@@ -1,0 +1,430 @@
+// Which pages of a paged sequence a query should read (sm_103a): bounds of
+// each page's keys, a score of each page from them, and the selection.
+//
+//   bounds   lo_i = min, hi_i = max over the page's keys of dim i;
+//   score    scale * sum over the group's query heads and the dims of
+//            max(q_i lo_i, q_i hi_i)
+//          = scale * ((sum_h min(q_h, 0)) . lo + (sum_h max(q_h, 0)) . hi),
+//            as lo <= hi: one dot product of length 2 d a page, whatever the
+//            group's size;
+//   select   the sinks, the last pages, and the best of the others.
+//
+// All three take tables and lengths from device memory, so a captured call
+// follows them as they change.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/kvp.h"
+#include "kvp_internal.h"
+#include "query_rows.cuh"
+
+namespace kvp {
+namespace {
+
+// ------------------------------------------------------------------ bounds
+
+constexpr int kBoundWarps = 4;
+
+struct BoundsArgs {
+    const uint4 *k;         // 16-byte chunks
+    uint4 *bounds;
+    const int32_t *tables, *lens;
+    int32_t S, MB, L, Hkv, NB, bs, n_new, pages;
+};
+
+template <bool MAX>
+__device__ __forceinline__ uint32_t pick2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&a), y = *reinterpret_cast<const __nv_bfloat162 *>(&b);
+    const __nv_bfloat162 r = MAX ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <bool MAX>
+__device__ __forceinline__ uint4 pick(uint4 a, uint4 b) {
+    return make_uint4(pick2<MAX>(a.x, b.x), pick2<MAX>(a.y, b.y), pick2<MAX>(a.z, b.z), pick2<MAX>(a.w, b.w));
+}
+template <bool MAX>
+__device__ __forceinline__ uint4 pick_across(uint4 a, int step) {
+    uint4 b;
+    b.x = __shfl_xor_sync(0xffffffffu, a.x, step);
+    b.y = __shfl_xor_sync(0xffffffffu, a.y, step);
+    b.z = __shfl_xor_sync(0xffffffffu, a.z, step);
+    b.w = __shfl_xor_sync(0xffffffffu, a.w, step);
+    return pick<MAX>(a, b);
+}
+
+// A warp per (page, kv head, layer): its rows are one contiguous run, read 512
+// bytes an instruction, 16 bytes a lane, each lane keeping its 8 dims.
+template <int D>
+__global__ void __launch_bounds__(32 * kBoundWarps) page_bounds_kernel(const BoundsArgs a) {
+    constexpr int CH = D / 8, RPI = 32 / CH;     // chunks per row, rows per instruction
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = blockIdx.y;
+    const int64_t unit = (int64_t)blockIdx.x * kBoundWarps + warp;      // page-major over (layer, kv head)
+    const int LH = a.L * a.Hkv;
+    const int jj = (int)(unit / LH), lh = (int)(unit % LH);
+    if (jj >= a.pages) return;
+    const int n = (int)min((int64_t)max(a.lens[s], 0), (int64_t)a.MB * a.bs);
+    const int j = max(0, n - a.n_new) / a.bs + jj;
+    if ((int64_t)j * a.bs >= n) return;
+    const int blk = a.tables[(int64_t)s * a.MB + j];
+    if ((unsigned)blk >= (unsigned)a.NB) return;
+    const int l = lh / a.Hkv, h = lh % a.Hkv;
+    const int64_t page = ((int64_t)l * a.NB + blk) * a.Hkv + h;
+    const int rows = min(a.bs, n - j * a.bs);
+    const uint4 *src = a.k + page * a.bs * CH + lane;
+    const int r0 = lane / CH;
+    uint4 lo = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);    // +inf
+    uint4 hi = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+    constexpr int U = 8;
+    for (int r = r0; r < rows; r += RPI * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            // a row past the end: the first one again
+            const int q = r + u * RPI;
+            v[u] = src[(int64_t)((q < rows ? q : r) - r0) * CH];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            lo = pick<false>(lo, v[u]);
+            hi = pick<true>(hi, v[u]);
+        }
+    }
+#pragma unroll
+    for (int step = 16; step >= CH; step >>= 1) {
+        lo = pick_across<false>(lo, step);
+        hi = pick_across<true>(hi, step);
+    }
+    if (lane < CH) {
+        a.bounds[page * 2 * CH + lane] = lo;
+        a.bounds[(page * 2 + 1) * CH + lane] = hi;
+    }
+}
+
+// ------------------------------------------------------------------ scores
+
+constexpr int kScoreWarps = 4;
+constexpr int kScoreSteps = 2;      // groups of 16 pages per warp
+constexpr int kScorePages = 16 * kScoreWarps * kScoreSteps;
+
+struct ScoreArgs {
+    QueryRows rows;
+    const __nv_bfloat16 *q;
+    const uint4 *bounds;
+    float *scores;
+    int64_t stride;
+    int32_t L, Hq, Hkv, G, NB, chunks;
+    float scale;
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// x as the sum of three bf16 numbers (24 bits, all of an fp32's); what is not
+// finite stands whole in the first
+__device__ __forceinline__ void split3(float x, __nv_bfloat16 &a, __nv_bfloat16 &b, __nv_bfloat16 &c) {
+    a = __float2bfloat16_rn(x);
+    float r = x - __bfloat162float(a);
+    if (!isfinite(r)) r = 0.f;
+    b = __float2bfloat16_rn(r);
+    c = __float2bfloat16_rn(r - __bfloat162float(b));
+}
+
+// A warp scores 16 pages at a time for up to QT query rows of one sequence:
+// pages are the rows of mma.sync's A operand, read straight from global memory
+// (the contraction may run over the dims in any order, so a lane's operand is
+// 16 contiguous bytes of its page, four lanes to 64), and the queries' summed
+// parts the columns of B.  Each fp32 part is three bf16 numbers, so that the
+// products carry all of its bits; the three are columns of their own, added up
+// at the end.  QT = 1 has its three columns in one B tile, QT = 8 in three.
+template <int D, int QT>
+__global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const ScoreArgs a) {
+    constexpr int K = 2 * D, C = K / 32;      // 32-value chunks of a page's bounds
+    constexpr int ROW = K + 32;               // shared-memory row: two rows never meet in a bank
+    constexpr int NT = QT == 1 ? 1 : 3;
+    __shared__ __align__(16) __nv_bfloat16 s_part[3 * QT][ROW];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lh = blockIdx.y, l = lh / a.Hkv, h = lh % a.Hkv;
+    // which query rows, which pages
+    int r0, nr, seq;
+    const int chunk = (int)(blockIdx.x % a.chunks);
+    if (!a.rows.tile<QT>(blockIdx.x / a.chunks, r0, nr, seq)) return;
+    const int last = a.rows.pages(seq, r0 + nr - 1);       // pages that the last row sees
+    const int p_begin = chunk * kScorePages;
+    if (p_begin >= last) return;
+    for (int i = threadIdx.x; i < QT * D; i += blockDim.x) {
+        const int r = i / D, e = i % D;
+        float neg = 0.f, pos = 0.f;
+        if (r < nr) {
+            const __nv_bfloat16 *q = a.q + (((int64_t)l * a.rows.T + r0 + r) * a.Hq + h * a.G) * D + e;
+            for (int x = 0; x < a.G; ++x) {
+                const float v = __bfloat162float(q[(int64_t)x * D]);
+                // (a NaN goes into both)
+                neg += v > 0.f ? 0.f : v;
+                pos += v < 0.f ? 0.f : v;
+            }
+        }
+        split3(neg, s_part[r][e], s_part[QT + r][e], s_part[2 * QT + r][e]);
+        split3(pos, s_part[r][D + e], s_part[QT + r][D + e], s_part[2 * QT + r][D + e]);
+    }
+    __syncthreads();
+    const int32_t *table = a.rows.tables + (int64_t)seq * a.rows.MB;
+    uint4 b1[QT == 1 ? C : 1];
+    if constexpr (QT == 1) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            b1[c] = g < 3 ? *reinterpret_cast<const uint4 *>(&s_part[g < 3 ? g : 0][32 * c + 8 * t]) : make_uint4(0, 0, 0, 0);
+    }
+    for (int step = 0; step < kScoreSteps; ++step) {
+        const int p0 = p_begin + (step * kScoreWarps + warp) * 16;
+        if (p0 >= last) return;
+        const int pa = p0 + g, pb = pa + 8;
+        const int ba = pa < last ? table[pa] : -1, bb = pb < last ? table[pb] : -1;
+        const bool oka = (unsigned)ba < (unsigned)a.NB, okb = (unsigned)bb < (unsigned)a.NB;
+        const uint4 *xa = a.bounds + (((int64_t)l * a.NB + (oka ? ba : 0)) * a.Hkv + h) * (K / 8) + t;
+        const uint4 *xb = a.bounds + (((int64_t)l * a.NB + (okb ? bb : 0)) * a.Hkv + h) * (K / 8) + t;
+        uint4 va[C], vb[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            va[c] = oka ? xa[4 * c] : make_uint4(0, 0, 0, 0);
+            vb[c] = okb ? xb[4 * c] : make_uint4(0, 0, 0, 0);
+        }
+        float acc[NT][4] = {};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                uint4 b;
+                if constexpr (QT == 1)
+                    b = b1[c];
+                else
+                    b = *reinterpret_cast<const uint4 *>(&s_part[n * QT + g][32 * c + 8 * t]);
+                mma(acc[n], va[c].x, vb[c].x, va[c].y, vb[c].y, b.x, b.y);
+                mma(acc[n], va[c].z, vb[c].z, va[c].w, vb[c].w, b.z, b.w);
+            }
+        }
+        if constexpr (QT == 1) {
+            // columns 0, 1 are lane t = 0's, column 2 lane t = 1's
+            const float la = __shfl_down_sync(0xffffffffu, acc[0][0], 1), lb = __shfl_down_sync(0xffffffffu, acc[0][2], 1);
+            if (t == 0) {
+                float *out = a.scores + (((int64_t)l * a.rows.T + r0) * a.Hkv + h) * a.stride;
+                if (pa < last) out[pa] = oka ? (acc[0][0] + (acc[0][1] + la)) * a.scale : -INFINITY;
+                if (pb < last) out[pb] = okb ? (acc[0][2] + (acc[0][3] + lb)) * a.scale : -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {       // query columns 2 t, 2 t + 1
+                const int r = 2 * t + e;
+                if (r >= nr) continue;
+                const int seen = a.rows.pages(seq, r0 + r);
+                float *out = a.scores + (((int64_t)l * a.rows.T + r0 + r) * a.Hkv + h) * a.stride;
+                if (pa < seen) out[pa] = oka ? (acc[0][e] + (acc[1][e] + acc[2][e])) * a.scale : -INFINITY;
+                if (pb < seen) out[pb] = okb ? (acc[0][2 + e] + (acc[1][2 + e] + acc[2][2 + e])) * a.scale : -INFINITY;
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------- selection
+
+constexpr int kSelThreads = 256;
+
+struct SelectArgs {
+    QueryRows rows;
+    const float *scores;
+    int64_t stride;
+    int32_t *selected;
+    int32_t Hkv, budget, sink, recent;
+};
+
+// Scores as unsigned keys of the same order: NaN above everything, -0 as 0.
+__device__ __forceinline__ uint32_t score_key(float x) {
+    if (x != x) return 0xfffffffeu;
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+constexpr uint32_t kStays = 0xffffffffu;    // sinks and the last pages: above every score
+
+// A CTA per (layer, query row, kv head): the budget-th largest key by a radix
+// select, 8 bits a pass, then the pages in order.
+__global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SelectArgs a) {
+    __shared__ int s_bin[256];
+    __shared__ int s_up[kSelThreads / 32], s_eq[kSelThreads / 32];
+    __shared__ int s_digit, s_left;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t row = blockIdx.x;
+    const int r = (int)(row / a.Hkv % a.rows.T);
+    const int seq = a.rows.sequence(r);
+    if (seq < 0) return;
+    const int n = a.rows.pages(seq, r);
+    const float *score = a.scores + row * a.stride;
+    int32_t *out = a.selected + row * a.budget;
+    if (n <= a.budget) {
+        for (int j = tid; j < a.budget; j += kSelThreads) out[j] = j < n ? j : -1;
+        return;
+    }
+    const int lo = a.sink, hi = n - a.recent;
+    auto key_at = [&](int j) { return j < lo || j >= hi ? kStays : score_key(score[j]); };
+    uint32_t prefix = 0;
+    int left = a.budget;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        s_bin[tid] = 0;
+        __syncthreads();
+        for (int j = tid; j < n; j += kSelThreads) {
+            const uint32_t key = key_at(j);
+            if (shift == 24 || ((key ^ prefix) >> (shift + 8)) == 0) atomicAdd(&s_bin[(key >> shift) & 255], 1);
+        }
+        __syncthreads();
+        if (tid == 0) {
+            int d = 255, m = left;
+            while (s_bin[d] < m) m -= s_bin[d--];
+            s_digit = d;
+            s_left = m;
+        }
+        __syncthreads();
+        prefix |= (uint32_t)s_digit << shift;
+        left = s_left;
+        __syncthreads();
+    }
+    // keys above `prefix` and the first `left` of those equal to it, in order
+    int base = 0, eq_base = 0;
+    for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+        const int j = j0 + tid;
+        const uint32_t key = j < n ? key_at(j) : 0u;
+        const bool up = j < n && key > prefix, eq = j < n && key == prefix;
+        const uint32_t mu = __ballot_sync(0xffffffffu, up), me = __ballot_sync(0xffffffffu, eq);
+        if (lane == 0) {
+            s_up[warp] = __popc(mu);
+            s_eq[warp] = __popc(me);
+        }
+        __syncthreads();
+        int bu = base, be = eq_base;
+        for (int w = 0; w < kSelThreads / 32; ++w) {
+            if (w < warp) {
+                bu += s_up[w];
+                be += s_eq[w];
+            }
+            base += s_up[w];
+            eq_base += s_eq[w];
+        }
+        const uint32_t below = (1u << lane) - 1u;
+        const int eq_before = be + __popc(me & below);
+        if (up || (eq && eq_before < left)) out[bu + __popc(mu & below) + min(eq_before, left)] = j;
+        __syncthreads();
+    }
+}
+
+bool bad(const void *p, uintptr_t align) { return !p || ((uintptr_t)p & (align - 1)); }
+
+// What the batch's arguments have to satisfy in every call.
+bool batch_ok(const kvp_attn_desc *d, const int32_t *tables, const int32_t *lens, int32_t S, int32_t MB) {
+    return attn_desc_ok(d) && d->kv_format == KVP_KV_BF16 && (int64_t)d->num_layers * d->num_kv_heads <= 65535 &&
+           S > 0 && MB > 0 && (int64_t)MB * d->block_size <= INT32_MAX / 2 && !bad(tables, 4) && !bad(lens, 4);
+}
+
+}  // namespace
+}  // namespace kvp
+
+using namespace kvp;
+
+extern "C" {
+
+int kvp_page_bounds(const void *k_pool, const int32_t *block_tables, const int32_t *seq_lens, int32_t num_seqs,
+                    int32_t max_blocks, int32_t n_new, const kvp_attn_desc *desc, void *bounds, void *stream) {
+    if (!batch_ok(desc, block_tables, seq_lens, num_seqs, max_blocks) || bad(k_pool, 16) || bad(bounds, 16) || n_new < 0 ||
+        num_seqs > 65535)
+        return KVP_ERR_INVALID;
+    if (!stream && stream_capturing(nullptr)) return KVP_ERR_STATE;
+    if (n_new == 0) return KVP_OK;
+    BoundsArgs a{};
+    a.k = static_cast<const uint4 *>(k_pool);
+    a.bounds = static_cast<uint4 *>(bounds);
+    a.tables = block_tables;
+    a.lens = seq_lens;
+    a.S = num_seqs; a.MB = max_blocks; a.L = desc->num_layers; a.Hkv = desc->num_kv_heads;
+    a.NB = desc->num_blocks; a.bs = desc->block_size; a.n_new = n_new;
+    a.pages = (int32_t)std::min<int64_t>(max_blocks, ((int64_t)n_new + a.bs - 2) / a.bs + 1);
+    const int64_t grid = ((int64_t)a.pages * a.L * a.Hkv + kBoundWarps - 1) / kBoundWarps;
+    if (grid > INT32_MAX) return KVP_ERR_INVALID;
+    const dim3 g((unsigned)grid, (unsigned)num_seqs);
+    if (desc->head_dim == 64)
+        page_bounds_kernel<64><<<g, 32 * kBoundWarps, 0, (cudaStream_t)stream>>>(a);
+    else
+        page_bounds_kernel<128><<<g, 32 * kBoundWarps, 0, (cudaStream_t)stream>>>(a);
+    count_launch();
+    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+int kvp_page_scores(const void *q, const int32_t *q_start, int32_t num_q, const void *bounds,
+                    const int32_t *block_tables, const int32_t *seq_lens, int32_t num_seqs, int32_t max_blocks,
+                    const kvp_attn_desc *desc, float *scores, int64_t score_stride, void *stream) {
+    if (!batch_ok(desc, block_tables, seq_lens, num_seqs, max_blocks) || bad(bounds, 16) || score_stride < max_blocks ||
+        num_q < 0 || ((uintptr_t)q_start & 3) || (!q_start && num_q != num_seqs))
+        return KVP_ERR_INVALID;
+    if (num_q == 0) return KVP_OK;
+    if (bad(q, 16) || bad(scores, 4)) return KVP_ERR_INVALID;
+    if (!stream && stream_capturing(nullptr)) return KVP_ERR_STATE;
+    ScoreArgs a{};
+    a.rows = QueryRows{q_start, block_tables, seq_lens, num_seqs, num_q, max_blocks, desc->block_size};
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.bounds = static_cast<const uint4 *>(bounds);
+    a.scores = scores;
+    a.stride = score_stride;
+    a.L = desc->num_layers; a.Hq = desc->num_q_heads; a.Hkv = desc->num_kv_heads; a.G = a.Hq / a.Hkv;
+    a.NB = desc->num_blocks;
+    a.scale = desc->scale > 0.f ? desc->scale : 1.f / sqrtf((float)desc->head_dim);
+    a.chunks = (max_blocks + kScorePages - 1) / kScorePages;
+    const int64_t tiles = q_start ? QueryRows::tiles(num_q, num_seqs, 8) : num_q;
+    if (tiles * a.chunks > INT32_MAX) return KVP_ERR_INVALID;
+    const dim3 g((unsigned)(tiles * a.chunks), (unsigned)(a.L * a.Hkv));
+    cudaStream_t st = (cudaStream_t)stream;
+    const int threads = 32 * kScoreWarps;
+    if (desc->head_dim == 64) {
+        if (q_start)
+            page_score_kernel<64, 8><<<g, threads, 0, st>>>(a);
+        else
+            page_score_kernel<64, 1><<<g, threads, 0, st>>>(a);
+    } else {
+        if (q_start)
+            page_score_kernel<128, 8><<<g, threads, 0, st>>>(a);
+        else
+            page_score_kernel<128, 1><<<g, threads, 0, st>>>(a);
+    }
+    count_launch();
+    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+int kvp_page_select(const float *scores, int64_t score_stride, const int32_t *q_start, int32_t num_q,
+                    const int32_t *seq_lens, int32_t num_seqs, int32_t max_blocks, const kvp_attn_desc *desc,
+                    int32_t budget, int32_t n_sink, int32_t n_recent, int32_t *selected, void *stream) {
+    if (!batch_ok(desc, seq_lens, seq_lens, num_seqs, max_blocks) || score_stride < max_blocks || num_q < 0 ||
+        ((uintptr_t)q_start & 3) || (!q_start && num_q != num_seqs) || budget <= 0 || n_sink < 0 || n_recent < 0 ||
+        (int64_t)n_sink + n_recent > budget)
+        return KVP_ERR_INVALID;
+    if (num_q == 0) return KVP_OK;
+    if (bad(scores, 4) || bad(selected, 4)) return KVP_ERR_INVALID;
+    const int64_t grid = (int64_t)desc->num_layers * num_q * desc->num_kv_heads;
+    if (grid > INT32_MAX) return KVP_ERR_INVALID;
+    if (!stream && stream_capturing(nullptr)) return KVP_ERR_STATE;
+    SelectArgs a{};
+    a.rows = QueryRows{q_start, nullptr, seq_lens, num_seqs, num_q, max_blocks, desc->block_size};
+    a.scores = scores;
+    a.stride = score_stride;
+    a.selected = selected;
+    a.Hkv = desc->num_kv_heads; a.budget = budget; a.sink = n_sink; a.recent = n_recent;
+    page_select_kernel<<<(unsigned)grid, kSelThreads, 0, (cudaStream_t)stream>>>(a);
+    count_launch();
+    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -558,6 +558,94 @@ int seq_append_batch(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32
     return issue_write(p, k, v, total, stream);
 }
 
+int seq_append_rope(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32_t *ntoks, const void *k, const void *v,
+                    const kvp_rope_desc *rope, const int32_t *positions, const void *q, void *q_out,
+                    int32_t num_q_heads, void *stream) try {
+    int64_t total = 0;
+    int rc = kvp::append_batch_check(p, nseq, seqs, ntoks, &total);
+    if (rc != KVP_OK && rc != KVP_ERR_OOM) return rc;
+    const kvp_pool_desc &d = p->desc;
+    kvp::RopeAppend r{};
+    if (!rope || rope->rot_dim < 2 || rope->rot_dim % 2 || rope->rot_dim > std::min(d.head_dim, kvp::kMaxRot))
+        return KVP_ERR_INVALID;
+    if (!std::isfinite(rope->scale) || (!rope->freqs && !(std::isfinite(rope->base) && rope->base > 0)))
+        return KVP_ERR_INVALID;
+    const int32_t half = rope->rot_dim / 2;
+    for (int32_t i = 0; i < half; ++i) {
+        const double f = rope->freqs ? rope->freqs[i] : std::pow(rope->base, -(double)i / half);
+        if (!std::isfinite(f)) return KVP_ERR_INVALID;
+        // turns per position modulo 1, in units of 2^-64 (the conversion of
+        // 1 - 2^-54, the largest fraction a double has, stays below 2^64)
+        const double turns = f / 6.283185307179586476925, part = turns - std::floor(turns);
+        r.freq[i] = part < 1.0 ? (uint64_t)std::ldexp(part, 64) : 0;
+    }
+    if ((q == nullptr) != (q_out == nullptr) || (q && (num_q_heads <= 0 || num_q_heads > 65536)))
+        return KVP_ERR_INVALID;
+    const int64_t units = ((int64_t)d.num_kv_heads * 2 + (q ? num_q_heads : 0)) * (d.head_dim / 2 + 8);
+    if (units > INT32_MAX / 8 || d.num_layers > 2048) return KVP_ERR_INVALID;
+    if (total > 0) {
+        if (!k || !v || !aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out)) return KVP_ERR_INVALID;
+        if ((uintptr_t)positions & 3) return KVP_ERR_INVALID;
+        const int64_t bytes = (int64_t)d.num_layers * total * num_q_heads * d.head_dim * 2;
+        const char *a = static_cast<const char *>(q), *b = static_cast<const char *>(q_out);
+        if (q && a != b && a < b + bytes && b < a + bytes) return KVP_ERR_INVALID;
+    }
+    if (rc) return rc;
+    if (total == 0) return KVP_OK;
+    // the bookkeeping is done once: a replay would write the same slots again
+    if (kvp::stream_capturing((cudaStream_t)stream)) return KVP_ERR_STATE;
+    std::vector<kvp::RopeSeq> runs(nseq);
+    for (int32_t i = 0; i < nseq; ++i) runs[i] = {ntoks[i], p->lens[seqs[i]], nullptr};
+    int32_t ntok = 0;
+    rc = kvp::append_batch_commit_lists(p, nseq, seqs, ntoks, p->slots, p->cow, &ntok);
+    if (rc) return rc;
+    for (int32_t i = 0; i < nseq; ++i)
+        if (ntoks[i] > 0) runs[i].blocks = p->tables[seqs[i]].data() + runs[i].pos0 / d.block_size;
+    r.k_pool = p->k; r.v_pool = p->v; r.k_exp = p->k_exp; r.v_exp = p->v_exp;
+    r.k = k; r.v = v; r.q = q; r.q_out = q_out;
+    r.positions = positions;
+    r.L = d.num_layers; r.NB = d.num_blocks; r.Hkv = d.num_kv_heads; r.Hq = num_q_heads;
+    r.bs = d.block_size; r.d = d.head_dim;
+    r.ntok = ntok;
+    r.rot = rope->rot_dim;
+    r.adjacent = rope->interleaved != 0;
+    r.scale = rope->scale == 0.f ? 1.f : rope->scale;
+    r.seqs = runs.data(); r.nseq = nseq;
+    r.cow = p->cow.data(); r.ncow = (int32_t)(p->cow.size() / 3);
+    return kvp::launch_rope_append(r, (cudaStream_t)stream) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+} catch (const std::bad_alloc &) {
+    return KVP_ERR_OOM;
+}
+
+int seq_reorder(kvp_pool *p, const int32_t *dst, const int32_t *src, int32_t n) try {
+    if (!p || n < 0 || (n > 0 && (!dst || !src))) return KVP_ERR_INVALID;
+    std::vector<uint8_t> seen(p->desc.max_seqs, 0);
+    for (int32_t i = 0; i < n; ++i) {
+        if (!is_live(p, dst[i]) || !is_live(p, src[i]) || seen[dst[i]]) return KVP_ERR_INVALID;
+        seen[dst[i]] = 1;
+    }
+    // the new tables first: a src may be some dst too
+    std::vector<std::vector<int32_t>> tables(n);
+    std::vector<int32_t> lens(n);
+    for (int32_t i = 0; i < n; ++i) {
+        if (dst[i] == src[i]) continue;
+        tables[i] = p->tables[src[i]];
+        lens[i] = p->lens[src[i]];
+    }
+    for (int32_t i = 0; i < n; ++i)
+        for (int32_t b : tables[i]) p->ref[b] += 1;
+    for (int32_t i = n - 1; i >= 0; --i) {
+        if (dst[i] == src[i]) continue;
+        auto &old = p->tables[dst[i]];
+        for (size_t j = old.size(); j-- > 0;) kvp::pool_drop_block(p, old[j]);
+        old.swap(tables[i]);
+        p->lens[dst[i]] = lens[i];
+    }
+    return KVP_OK;
+} catch (const std::bad_alloc &) {
+    return KVP_ERR_OOM;
+}
+
 int seq_block_table(const kvp_pool *p, int32_t seq, int32_t *host_out, int32_t cap,
                     int32_t *nblocks_out) {
     if (!is_live(p, seq)) return KVP_ERR_INVALID;

@@ -1,0 +1,384 @@
+// Append with the rotation of K and Q by position (sm_103a): new keys into
+// their pages rotated, new values as they are, queries rotated beside them,
+// and the copy-on-write copies of shared last pages, in one launch.
+//
+// Pair (x, y) at position p becomes (x cos a - y sin a, y cos a + x sin a),
+// a = p * freq.  In turns, a / 2 pi = p * f with only f modulo 1 of account,
+// as p is a whole number: f is held as 64-bit fixed point, p * f wraps modulo
+// 2^64, and its top 32 bits are the angle to 2^-33 of a turn at any position
+// (fp32 p * freq loses 2^-24 p of it).  The rotation runs in fp32, the result
+// is rounded to bf16 once.
+//
+// One CTA takes a few tokens of a layer.  Its threads work out the tokens'
+// cos and sin once (every head of K and Q uses them) while their first loads
+// are in flight.  A unit of work is 2 x W values of a head: W pairs, or a
+// plain copy of V or of the dims behind rot_dim; W = 8 makes each a 16-byte
+// access, W = 1 serves rot_dim that are no multiple of 16.  Bound by HBM for
+// prompts (4 bytes per value moved), by latency for decode steps.
+//
+// The host describes tokens by runs (a sequence's consecutive slots) and
+// their blocks, in the kernel's parameters: 4 bytes per page instead of per
+// token, so a prompt of 65536 tokens on 16-token pages is one launch.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "kv4_quant.cuh"
+#include "kvp_internal.h"
+
+namespace kvp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;          // units in flight per thread
+constexpr int kMaxTok = 4;         // tokens per CTA
+constexpr int kTokMax = 1 << 19;   // tokens per launch
+
+struct Run {
+    int32_t tok0;    // first token of the run in this launch
+    int32_t pos0;    // its slot in the sequence
+    int32_t blk;     // where the run's blocks start (block of pos0 first)
+};
+
+template <int NR, int NB_, int NC>
+struct RopeArgs {
+    void *k_pool, *v_pool;
+    int8_t *k_exp, *v_exp;
+    const __nv_bfloat16 *k, *v, *q;
+    __nv_bfloat16 *q_out;
+    const int32_t *positions;
+    int32_t L, NB, Hkv, Hq, bs, d;
+    int32_t ntok_total, tok_begin, ntok, per_cta;
+    int32_t rot, adjacent;
+    int32_t nrun, ncow;
+    float scale;
+    uint64_t freq[kMaxRot / 2];
+    Run run[NR];
+    int32_t blk[NB_];
+    int32_t cow[3 * NC];
+};
+// Decode batches pass a small parameter block, prompts a full one.
+using SmallArgs = RopeArgs<64, 128, 64>;
+using LargeArgs = RopeArgs<512, 4096, 512>;
+static_assert(sizeof(LargeArgs) <= 32764, "kernel parameters");
+
+// Where this CTA's tokens go, and their angles.
+struct Tokens {
+    int64_t row[kMaxTok];      // (block * Hkv) * bs + slot: the row of kv head 0 in layer 0
+    float2 turn[kMaxTok][kMaxRot / 2];   // scale * (cos, sin)
+};
+
+template <class Args>
+__device__ __forceinline__ int32_t place_token(const Args &a, int t, int64_t &row) {
+    int lo = 0, hi = a.nrun - 1;       // the run that holds token t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.run[mid].tok0 <= t) lo = mid; else hi = mid - 1;
+    }
+    const int32_t pos0 = a.run[lo].pos0, pos = pos0 + (t - a.run[lo].tok0);
+    const int32_t b = a.blk[a.run[lo].blk + pos / a.bs - pos0 / a.bs];
+    row = (int64_t)b * a.Hkv * a.bs + pos % a.bs;
+    return pos;
+}
+
+template <class Args>
+__device__ __forceinline__ void fill_tokens(const Args &a, Tokens &s, int t0, int nt) {
+    const int half = a.rot / 2;
+    for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
+        const int t = i / half, p = i % half;
+        int64_t row;
+        int32_t pos = place_token(a, t0 + t, row);
+        if (p == 0) s.row[t] = row;
+        if (a.positions) pos = a.positions[a.tok_begin + t0 + t];
+        const uint64_t turns = a.freq[p] * (uint64_t)(int64_t)pos;
+        float sn, cs;
+        // half turns in [-1, 1)
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn, &cs);
+        s.turn[t][p] = make_float2(cs * a.scale, sn * a.scale);
+    }
+}
+
+__device__ __forceinline__ void rotate(float &x, float &y, float2 w) {
+    const float u = __fmaf_rn(x, w.x, -__fmul_rn(y, w.y));
+    y = __fmaf_rn(y, w.x, __fmul_rn(x, w.y));
+    x = u;
+}
+
+template <int W> struct Vec;
+template <> struct Vec<8> { using type = uint4; };
+template <> struct Vec<1> { using type = unsigned short; };
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// W pairs in two vectors: (x_i, y_i) across them, or adjacent in each.
+__device__ __forceinline__ void turn_vec(uint4 &x, uint4 &y, const float2 *w, bool adjacent) {
+    uint32_t *xs = &x.x, *ys = &y.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a0 = lo_f(xs[i]), a1 = hi_f(xs[i]), b0 = lo_f(ys[i]), b1 = hi_f(ys[i]);
+        if (adjacent) {
+            rotate(a0, a1, w[i]);
+            rotate(b0, b1, w[4 + i]);
+        } else {
+            rotate(a0, b0, w[2 * i]);
+            rotate(a1, b1, w[2 * i + 1]);
+        }
+        xs[i] = pack2(a0, a1);
+        ys[i] = pack2(b0, b1);
+    }
+}
+__device__ __forceinline__ void turn_vec(unsigned short &x, unsigned short &y, const float2 *w, bool) {
+    float a = bf16_bits_to_float(x), b = bf16_bits_to_float(y);
+    rotate(a, b, w[0]);
+    x = __bfloat16_as_ushort(__float2bfloat16_rn(a));
+    y = __bfloat16_as_ushort(__float2bfloat16_rn(b));
+}
+
+// Copy-on-write: CTA x of ncow * L copies the used slots of one triple in one
+// layer, K and V.  Rows of `bytes` bytes, 16 at a time where they are whole.
+template <class Args>
+__device__ __forceinline__ void copy_cow(const Args &a, int x) {
+    const int i = x % a.ncow, l = x / a.ncow;
+    const int src = a.cow[3 * i], dst = a.cow[3 * i + 1], used = a.cow[3 * i + 2];
+    const int ch = a.d / 8;                        // 16-byte chunks per row
+    const int64_t run = (int64_t)used * ch, tile = (int64_t)a.bs * ch;
+    for (int64_t y = threadIdx.x; y < 2 * a.Hkv * run; y += blockDim.x) {
+        const int64_t h = y / (2 * run), r = y % (2 * run);
+        uint4 *pool = static_cast<uint4 *>(r < run ? a.k_pool : a.v_pool);
+        const int64_t c = r < run ? r : r - run;
+        const int64_t head = (int64_t)l * a.NB * a.Hkv + h;
+        pool[(head + (int64_t)dst * a.Hkv) * tile + c] = pool[(head + (int64_t)src * a.Hkv) * tile + c];
+    }
+}
+
+template <int W, class Args>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ Args a) {
+    using V = typename Vec<W>::type;
+    __shared__ Tokens s;
+    const int cow_ctas = a.ncow * a.L;
+    if ((int)blockIdx.x < cow_ctas) {
+        copy_cow(a, blockIdx.x);
+        return;
+    }
+    const int groups = (a.ntok + a.per_cta - 1) / a.per_cta;
+    const int x0 = blockIdx.x - cow_ctas;
+    const int l = x0 / groups, t0 = (x0 % groups) * a.per_cta;
+    const int nt = min(a.per_cta, a.ntok - t0);
+    // units of a token: heads of K, then of Q, each its pairs and then the
+    // dims behind them; then the heads of V
+    const int R = a.rot / 2 / W, U = R + (a.d - a.rot + 2 * W - 1) / (2 * W);
+    const int nrot = (a.Hkv + a.Hq) * U, UV = (a.d / 8 + 1) / 2, per_tok = nrot + a.Hkv * UV;
+    const int total = nt * per_tok;
+    const int64_t tok = a.tok_begin + t0;
+    const int64_t layer = (int64_t)l * a.NB * a.Hkv * a.bs;
+    bool ready = false;
+    for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < total; i0 += kThreads * kBatch) {
+        V x[kBatch], y[kBatch];
+        uint4 vx[kBatch], vy[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kThreads;
+            if (i >= total) break;
+            const int t = i / per_tok, r = i % per_tok;
+            if (r < nrot) {
+                const int h = r / U, u = r % U;
+                const int ea = u >= R ? a.rot + (u - R) * 2 * W : a.adjacent ? 2 * u * W : u * W;
+                const int eb = u >= R || a.adjacent ? ea + W : ea + a.rot / 2;
+                const __nv_bfloat16 *p = h < a.Hkv ? a.k + ((l * (int64_t)a.ntok_total + tok + t) * a.Hkv + h) * a.d
+                                                   : a.q + ((l * (int64_t)a.ntok_total + tok + t) * a.Hq + h - a.Hkv) * a.d;
+                x[b] = *reinterpret_cast<const V *>(p + ea);
+                if (eb < a.d) y[b] = *reinterpret_cast<const V *>(p + eb);
+            } else {
+                const int h = (r - nrot) / UV, u = (r - nrot) % UV;
+                const uint4 *p = reinterpret_cast<const uint4 *>(
+                    a.v + ((l * (int64_t)a.ntok_total + tok + t) * a.Hkv + h) * a.d) + 2 * u;
+                vx[b] = p[0];
+                if (16 * u + 8 < a.d) vy[b] = p[1];
+            }
+        }
+        if (!ready) {
+            fill_tokens(a, s, t0, nt);
+            __syncthreads();
+            ready = true;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kThreads;
+            if (i >= total) break;
+            const int t = i / per_tok, r = i % per_tok;
+            if (r < nrot) {
+                const int h = r / U, u = r % U;
+                const int ea = u >= R ? a.rot + (u - R) * 2 * W : a.adjacent ? 2 * u * W : u * W;
+                const int eb = u >= R || a.adjacent ? ea + W : ea + a.rot / 2;
+                __nv_bfloat16 *p = h < a.Hkv ? static_cast<__nv_bfloat16 *>(a.k_pool) +
+                                                   (layer + s.row[t] + (int64_t)h * a.bs) * a.d
+                                             : a.q_out + ((l * (int64_t)a.ntok_total + tok + t) * a.Hq + h - a.Hkv) * a.d;
+                if (u < R) turn_vec(x[b], y[b], s.turn[t] + u * W, a.adjacent);
+                *reinterpret_cast<V *>(p + ea) = x[b];
+                if (eb < a.d) *reinterpret_cast<V *>(p + eb) = y[b];
+            } else {
+                const int h = (r - nrot) / UV, u = (r - nrot) % UV;
+                uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.v_pool) +
+                                                     (layer + s.row[t] + (int64_t)h * a.bs) * a.d) + 2 * u;
+                p[0] = vx[b];
+                if (16 * u + 8 < a.d) p[1] = vy[b];
+            }
+        }
+    }
+}
+
+// 4-bit pages: a CTA per (layer, token), a warp per row.  A row is rotated in
+// shared memory and rounded to bf16 (the keys that a bf16 pool would hold),
+// then quantised as seq_append does.
+template <class Args>
+__global__ void __launch_bounds__(kThreads) rope_append4_kernel(const __grid_constant__ Args a) {
+    __shared__ Tokens s;
+    __shared__ float s_row[kThreads / 32][128];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, vpl = a.d / 32;
+    const int cow_ctas = a.ncow * a.L;
+    if ((int)blockIdx.x < cow_ctas) {
+        const int i = blockIdx.x % a.ncow, l = blockIdx.x / a.ncow;
+        const int src = a.cow[3 * i], dst = a.cow[3 * i + 1], used = a.cow[3 * i + 2];
+        const int ch = a.d / 32;       // 16-byte chunks of codes per row
+        const int64_t tile = (int64_t)a.bs * ch;
+        for (int64_t y = threadIdx.x; y < 2LL * a.Hkv * used * (ch + 1); y += blockDim.x) {
+            const int64_t h = y / (2 * used * (ch + 1)), r = y % (2 * used * (ch + 1));
+            const bool is_v = r >= used * (ch + 1);
+            const int64_t c = is_v ? r - used * (ch + 1) : r;
+            const int64_t from = (int64_t)(l * (int64_t)a.NB + src) * a.Hkv + h, to = (l * (int64_t)a.NB + dst) * a.Hkv + h;
+            if (c < used * ch) {
+                uint4 *pool = static_cast<uint4 *>(is_v ? a.v_pool : a.k_pool);
+                pool[to * tile + c] = pool[from * tile + c];
+            } else {
+                int8_t *pool = is_v ? a.v_exp : a.k_exp;
+                pool[to * a.bs + c - used * ch] = pool[from * a.bs + c - used * ch];
+            }
+        }
+        return;
+    }
+    const int x0 = blockIdx.x - cow_ctas;
+    const int l = x0 / a.ntok, t = x0 % a.ntok;
+    const int64_t tok = l * (int64_t)a.ntok_total + a.tok_begin + t;
+    fill_tokens(a, s, t, 1);
+    __syncthreads();
+    const int half = a.rot / 2;
+    for (int r = warp; r < 2 * a.Hkv + a.Hq; r += kThreads / 32) {
+        const int h = r < a.Hkv ? r : r < 2 * a.Hkv ? r - a.Hkv : r - 2 * a.Hkv;
+        const bool is_v = r >= a.Hkv && r < 2 * a.Hkv, is_q = r >= 2 * a.Hkv;
+        const __nv_bfloat16 *src = (is_q ? a.q + (tok * a.Hq + h) * a.d : (is_v ? a.v : a.k) + (tok * a.Hkv + h) * a.d);
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < vpl; ++j) {
+            x[j] = __bfloat162float(src[lane * vpl + j]);
+            s_row[warp][lane * vpl + j] = x[j];
+        }
+        __syncwarp();
+        if (!is_v) {
+            for (int j = 0; j < vpl; ++j) {
+                const int e = lane * vpl + j;
+                if (e >= a.rot) continue;
+                const int p = a.adjacent ? e / 2 : e % half;
+                float u = s_row[warp][a.adjacent ? 2 * p : p], w = s_row[warp][a.adjacent ? 2 * p + 1 : p + half];
+                rotate(u, w, s.turn[0][p]);
+                const bool second = a.adjacent ? e & 1 : e >= half;
+                x[j] = __bfloat162float(__float2bfloat16_rn(second ? w : u));
+            }
+        }
+        if (is_q) {
+            for (int j = 0; j < vpl; ++j) a.q_out[(tok * a.Hq + h) * a.d + lane * vpl + j] = __float2bfloat16_rn(x[j]);
+        } else {
+            const int64_t row = (int64_t)l * a.NB * a.Hkv * a.bs + s.row[0] + (int64_t)h * a.bs;
+            store_row4(x, vpl, static_cast<uint8_t *>(is_v ? a.v_pool : a.k_pool) + row * (a.d / 2),
+                       (is_v ? a.v_exp : a.k_exp) + row, lane);
+        }
+        __syncwarp();
+    }
+}
+
+// One launch over tokens [tok, tok + ntok) given as runs and blocks.
+template <class Args>
+cudaError_t launch_part(const RopeAppend &r, const Run *run, int nrun, const int32_t *blk, int nblk, int cow0,
+                        int ncow, int tok, int ntok, cudaStream_t stream) {
+    Args a;   // on the stack: parameters are copied at launch
+    a.k_pool = r.k_pool; a.v_pool = r.v_pool;
+    a.k_exp = static_cast<int8_t *>(r.k_exp); a.v_exp = static_cast<int8_t *>(r.v_exp);
+    a.k = static_cast<const __nv_bfloat16 *>(r.k); a.v = static_cast<const __nv_bfloat16 *>(r.v);
+    a.q = static_cast<const __nv_bfloat16 *>(r.q); a.q_out = static_cast<__nv_bfloat16 *>(r.q_out);
+    a.positions = r.positions;
+    a.L = r.L; a.NB = r.NB; a.Hkv = r.Hkv; a.Hq = r.q ? r.Hq : 0; a.bs = r.bs; a.d = r.d;
+    a.ntok_total = r.ntok; a.tok_begin = tok; a.ntok = ntok;
+    a.rot = r.rot; a.adjacent = r.adjacent;
+    a.nrun = nrun; a.ncow = ncow;
+    a.scale = r.scale;
+    std::memcpy(a.freq, r.freq, sizeof a.freq);
+    std::memcpy(a.run, run, sizeof(Run) * nrun);
+    std::memcpy(a.blk, blk, sizeof(int32_t) * nblk);
+    std::memcpy(a.cow, r.cow + 3 * cow0, sizeof(int32_t) * 3 * ncow);
+    a.per_cta = 1;
+    if (r.k_exp) {
+        rope_append4_kernel<Args><<<(unsigned)((ncow + ntok) * r.L), kThreads, 0, stream>>>(a);
+    } else {
+        // several tokens to a CTA once one each would be many per SM
+        while (a.per_cta < kMaxTok && (int64_t)ntok * r.L > 16LL * a.per_cta * device_sm_count()) a.per_cta *= 2;
+        const unsigned grid = (unsigned)((ncow + (ntok + a.per_cta - 1) / a.per_cta) * r.L);
+        if (r.rot % 16 == 0)
+            rope_append_kernel<8, Args><<<grid, kThreads, 0, stream>>>(a);
+        else
+            rope_append_kernel<1, Args><<<grid, kThreads, 0, stream>>>(a);
+    }
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeAppend &r, cudaStream_t stream) {
+    constexpr int NR = 512, NBk = 4096, NC = 512;
+    Run run[NR];
+    int32_t blk[NBk];
+    int nrun = 0, nblk = 0, tok = 0, ntok = 0, cow = 0;
+    // what is gathered, as a launch
+    auto flush = [&]() -> cudaError_t {
+        const int ncow = std::min(NC, r.ncow - cow);
+        if (ntok == 0 && ncow == 0) return cudaSuccess;
+        const bool small = nrun <= 64 && nblk <= 128 && ncow <= 64;
+        const cudaError_t e = small ? launch_part<SmallArgs>(r, run, nrun, blk, nblk, cow, ncow, tok, ntok, stream)
+                                    : launch_part<LargeArgs>(r, run, nrun, blk, nblk, cow, ncow, tok, ntok, stream);
+        cow += ncow;
+        tok += ntok;
+        nrun = nblk = ntok = 0;
+        return e;
+    };
+    for (int i = 0; i < r.nseq; ++i) {
+        int32_t left = r.seqs[i].ntok, pos = r.seqs[i].pos0;
+        const int32_t *b = r.seqs[i].blocks;
+        while (left > 0) {
+            if (nrun == NR || nblk == NBk || ntok == kTokMax) {
+                const cudaError_t e = flush();
+                if (e != cudaSuccess) return e;
+            }
+            const int32_t off = pos % r.bs;
+            const int64_t room = (int64_t)(NBk - nblk) * r.bs - off;
+            const int32_t take = (int32_t)std::min<int64_t>(std::min<int64_t>(left, kTokMax - ntok), room);
+            run[nrun++] = Run{ntok, pos, nblk};
+            const int32_t nb = (int32_t)(((int64_t)off + take + r.bs - 1) / r.bs);
+            for (int32_t j = 0; j < nb; ++j) blk[nblk++] = b[j];
+            ntok += take;
+            left -= take;
+            pos += take;
+            b += ((int64_t)off + take) / r.bs;
+        }
+    }
+    cudaError_t e = flush();
+    while (e == cudaSuccess && cow < r.ncow) e = flush();   // copies beyond a launch's share
+    return e;
+}
+
+}  // namespace kvp
