@@ -8,12 +8,13 @@
 // read once into registers; its maximum, its sum of exponentials and its n
 // best logits go to the workspace.  Within a row scores order like logits, so
 // a row's n best scores are among its chunks' n best logits.  The n best of a
-// chunk: the n-th largest of the threads' own maxima is a lower bound that
-// few more than n logits reach; those are ranked against one another.  (More
-// reach it where many are equal, or the large ones lie in few threads: then
-// one after the other is taken.)
+// chunk: each warp sorts its lanes' maxima, and the smallest of the warps'
+// ceil(n / 8)-th is a bound that at least n logits reach and few more do;
+// those are ranked against one another.  (More reach it where many are equal,
+// or the large ones lie in few threads: then one after the other is taken.)
 // beam_join_kernel: a CTA per request joins the sums (in 64 bits), scores the
-// candidates and ranks them the same way.
+// candidates and ranks them the same way, as 64-bit whole numbers of the same
+// order (comparisons of doubles run on the FP64 pipe: 47 us instead of 8).
 // Bound by HBM for large batches (every logit read once), by latency for one
 // request.
 #include <cuda_bf16.h>
@@ -38,10 +39,9 @@ constexpr int kMaxOut = 128, kMaxBeams = 128;
 constexpr int kCap = 1024;                     // candidates ranked at once
 
 // A chunk's part of its row.
-struct PartHead {
-    float top;         // largest logit; +inf or NaN where the row is not to be used
-    int32_t count;     // candidates (descending)
+struct alignas(16) PartHead {
     double sum;        // of exp(logit - top)
+    float top;         // largest logit; +inf where the row is not to be used
 };
 
 struct BeamArgs {
@@ -54,9 +54,25 @@ struct BeamArgs {
     float *out_scores;
     int32_t *out_rows, *out_tokens;
     PartHead *heads;              // [rows][chunks]
-    float *cand;                  // [rows][chunks][n]
+    float *cand;                  // [rows][chunks][n], descending, then -inf
     int32_t *cand_at;
 };
+
+__device__ __forceinline__ bool bigger(float x, float y) { return x > y; }
+__device__ __forceinline__ bool bigger(uint64_t x, uint64_t y) { return x > y; }
+// A warp's values in descending order.
+template <class T>
+__device__ __forceinline__ T sort_warp(T x, int lane) {
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j; j >>= 1) {
+            const T y = __shfl_xor_sync(0xffffffffu, x, j);
+            const bool large = ((lane & j) == 0) == ((lane & k) == 0);     // this lane takes the larger
+            x = bigger(y, x) == large ? y : x;
+        }
+    return x;
+}
 
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -78,16 +94,16 @@ __device__ __forceinline__ double sum_block(double x, double *s, int warp, int l
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) beam_part_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) beam_part_kernel(const BeamArgs a) {
     __shared__ double s_sum[kWarps];
-    __shared__ float s_max[kThreads];
+    __shared__ float s_max[kWarps], s_bound[kWarps];
     __shared__ float s_c[kCap];
     __shared__ int s_at[kCap];
-    __shared__ float s_bound;
     __shared__ int s_count, s_best[kWarps];
     __shared__ float s_bestv[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");     // the join, which waits for all of this
     if (a.finished && a.finished[row]) return;
     const int x0 = chunk * kChunk, len = min(kChunk, a.vocab - x0);
     const T *src = static_cast<const T *>(a.logits) + row * a.row_stride + x0;
@@ -122,30 +138,29 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(const BeamArgs a) {
         nan |= v[k] != v[k];
     }
     if (nan) top = INFINITY;             // as +inf does: the row has no log-sum-exp
-    s_max[tid] = top;
+    top = sort_warp(top, lane);
+    if (lane == 0) s_max[warp] = top;
+    if (lane == (a.n + kWarps - 1) / kWarps - 1) s_bound[warp] = top;
     if (tid == 0) s_count = 0;
     __syncthreads();
-    // rank of this thread's maximum among all of them
-    int rank = 0;
-    float all = -INFINITY;
-    for (int i = 0; i < kThreads; ++i) {
-        const float y = s_max[i];
-        rank += y > top || (y == top && i < tid);
-        all = fmaxf(all, y);
+    float all = s_max[0], bound = s_bound[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+        all = fmaxf(all, s_max[w]);
+        bound = fminf(bound, s_bound[w]);
     }
-    if (rank == min(a.n, kThreads) - 1) s_bound = top;
     PartHead *head = a.heads + (int64_t)row * a.chunks + chunk;
     float *cand = a.cand + ((int64_t)row * a.chunks + chunk) * a.n;
     int32_t *cand_at = a.cand_at + ((int64_t)row * a.chunks + chunk) * a.n;
     if (!(all < INFINITY) || all == -INFINITY) {       // nothing here, or nothing in the row
-        if (tid == 0) *head = PartHead{all, 0, 0.0};
+        if (tid == 0) *head = PartHead{0.0, all};
+        if (tid < a.n) cand[tid] = -INFINITY;
         return;
     }
     float part = 0.f;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) part += expf(v[k] - all);
-    const double sum = sum_block((double)part, s_sum, warp, lane);     // (its barrier: s_bound is there)
-    const float bound = s_bound;
+    const double sum = sum_block((double)part, s_sum, warp, lane);
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
         if (v[k] >= bound && v[k] > -INFINITY) {
@@ -168,7 +183,8 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(const BeamArgs a) {
                 cand_at[r] = x0 + at;
             }
         }
-        if (tid == 0) *head = PartHead{all, min(found, a.n), sum};
+        if (tid >= found && tid < a.n) cand[tid] = -INFINITY;
+        if (tid == 0) *head = PartHead{sum, all};
         return;
     }
     // one after the other: the largest logit behind the last one taken
@@ -215,17 +231,25 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(const BeamArgs a) {
             cand_at[r] = x0 + at;
         }
     }
-    if (tid == 0) *head = PartHead{all, a.n, sum};     // (more than kCap >= n of them)
+    if (tid == 0) *head = PartHead{sum, all};
 }
 
-// A candidate's place in the order: score, then row, then logit, then token.
+// A candidate; its score as a whole number of the same order.
 struct Entry {
-    double score;
+    uint64_t key;
     float logit;
     int32_t beam, at;
 };
+__device__ __forceinline__ uint64_t score_key(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
+    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_score(uint64_t k) {
+    return __longlong_as_double((long long)(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
+}
+// The order: score, then row, then logit, then token.
 __device__ __forceinline__ bool before(const Entry &x, const Entry &y) {
-    if (x.score != y.score) return x.score > y.score;
+    if (x.key != y.key) return x.key > y.key;
     if (x.beam != y.beam) return x.beam < y.beam;
     if (x.logit != y.logit) return x.logit > y.logit;
     return x.at < y.at;
@@ -234,7 +258,7 @@ __device__ __forceinline__ bool before(const Entry &x, const Entry &y) {
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     __shared__ double s_add[kMaxBeams];     // score - log-sum-exp; -inf: no candidates
     __shared__ Entry s_e[kCap];
-    __shared__ double s_max[kThreads], s_bound;
+    __shared__ uint64_t s_bound[kWarps];
     __shared__ int s_count;
     __shared__ Entry s_best[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -249,12 +273,13 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
                 add = (double)cum;
             } else {
                 const PartHead *h = a.heads + (int64_t)row * a.chunks;
-                float top = -INFINITY;
-                for (int c = lane; c < a.chunks; c += 32) top = fmaxf(top, h[c].top);
+                const float mine = lane < a.chunks ? h[lane].top : -INFINITY;
+                float top = mine;
+                for (int c = lane + 32; c < a.chunks; c += 32) top = fmaxf(top, h[c].top);
 #pragma unroll
                 for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                double sum = 0;
                 if (top < INFINITY && top > -INFINITY) {
+                    double sum = 0;
                     for (int c = lane; c < a.chunks; c += 32)
                         if (h[c].top > -INFINITY) sum += h[c].sum * exp((double)h[c].top - (double)top);
 #pragma unroll
@@ -267,39 +292,40 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     }
     if (tid == 0) s_count = 0;
     __syncthreads();
-    // candidate i: (beam, chunk, place); finished beams have one, in chunk 0
-    const int64_t per_beam = (int64_t)a.chunks * a.n, total = per_beam * a.beams;
-    auto entry = [&](int64_t i, Entry &e) -> bool {
-        const int b = (int)(i / per_beam), row = g * a.beams + b;
+    // candidate i: place i % per_beam of beam i / per_beam; a finished beam's
+    // one is its first
+    const int per_beam = a.chunks * a.n, total = per_beam * a.beams;
+    const float *cand = a.cand + (int64_t)g * total;
+    const int32_t *cand_at = a.cand_at + (int64_t)g * total;
+    auto entry = [&](int i, Entry &e) -> bool {
+        const int b = i / per_beam;
         const double add = s_add[b];
         if (add == -INFINITY) return false;
-        const int64_t in = i % per_beam;
-        if (a.finished && a.finished[row]) {
-            if (in) return false;
-            e = Entry{add, 0.f, b, a.pad};
-            return true;
-        }
-        if ((int)(in % a.n) >= a.heads[(int64_t)row * a.chunks + in / a.n].count) return false;
-        const int64_t at = row * per_beam + in;
-        e.logit = a.cand[at];
-        e.score = add + (double)e.logit;
         e.beam = b;
-        e.at = a.cand_at[at];
-        return true;
+        if (a.finished && a.finished[g * a.beams + b]) {
+            e.key = score_key(add);
+            e.logit = 0.f;
+            e.at = a.pad;
+            return i == b * per_beam;
+        }
+        e.logit = cand[i];
+        e.key = score_key(add + (double)e.logit);
+        e.at = i;                    // (its token: cand_at[i])
+        return e.logit > -INFINITY;
     };
-    double top = -INFINITY;
+    uint64_t top = 0;
     Entry e;
-    for (int64_t i = tid; i < total; i += kThreads)
-        if (entry(i, e)) top = fmax(top, e.score);
-    s_max[tid] = top;
+    for (int i = tid; i < total; i += kThreads)
+        if (entry(i, e)) top = max(top, e.key);
+    top = sort_warp(top, lane);
+    if (lane == (a.n + kWarps - 1) / kWarps - 1) s_bound[warp] = top;
     __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < kThreads; ++i) rank += s_max[i] > top || (s_max[i] == top && i < tid);
-    if (rank == a.n - 1) s_bound = top;
-    __syncthreads();
-    const double bound = s_bound;
-    for (int64_t i = tid; i < total; i += kThreads)
-        if (entry(i, e) && e.score >= bound) {
+    uint64_t bound = s_bound[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) bound = min(bound, s_bound[w]);
+    // (within a beam, candidates of one logit are in the order of their tokens)
+    for (int i = tid; i < total; i += kThreads)
+        if (entry(i, e) && e.key >= bound) {
             const int k = atomicAdd(&s_count, 1);
             if (k < kCap) s_e[k] = e;
         }
@@ -308,9 +334,9 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     float *os = a.out_scores + (int64_t)g * a.n;
     int32_t *orow = a.out_rows + (int64_t)g * a.n, *ot = a.out_tokens + (int64_t)g * a.n;
     auto put = [&](int r, const Entry &x) {
-        os[r] = (float)x.score;
+        os[r] = (float)key_score(x.key);
         orow[r] = g * a.beams + x.beam;
-        ot[r] = x.at;
+        ot[r] = a.finished && a.finished[g * a.beams + x.beam] ? a.pad : cand_at[x.at];
     };
     if (found <= kCap) {
         for (int i = tid; i < found; i += kThreads) {
@@ -326,15 +352,15 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
         return;
     }
     // one after the other, each the best behind the last one
-    Entry last{INFINITY, INFINITY, -1, -1};
+    Entry last{~0ull, INFINITY, -1, -1};
     for (int r = 0; r < a.n; ++r) {
-        Entry best{-INFINITY, -INFINITY, INT_MAX, INT_MAX};
-        for (int64_t i = tid; i < total; i += kThreads)
+        Entry best{0, -INFINITY, INT_MAX, INT_MAX};
+        for (int i = tid; i < total; i += kThreads)
             if (entry(i, e) && before(last, e) && before(e, best)) best = e;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             Entry y;
-            y.score = __shfl_xor_sync(0xffffffffu, best.score, o);
+            y.key = __shfl_xor_sync(0xffffffffu, best.key, o);
             y.logit = __shfl_xor_sync(0xffffffffu, best.logit, o);
             y.beam = __shfl_xor_sync(0xffffffffu, best.beam, o);
             y.at = __shfl_xor_sync(0xffffffffu, best.at, o);
@@ -393,7 +419,8 @@ bool bad(const void *p, uintptr_t align) { return !p || ((uintptr_t)p & (align -
 bool beam_shape_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out) {
     if (groups <= 0 || beams <= 0 || beams > kMaxBeams || vocab <= 0 || vocab > (1 << 30) || n_out <= 0 || n_out > kMaxOut)
         return false;
-    return (int64_t)groups * beams * ((vocab + kChunk - 1) / kChunk) <= INT32_MAX;
+    const int64_t chunks = (vocab + kChunk - 1) / kChunk;
+    return groups * beams * chunks <= INT32_MAX && beams * chunks * n_out <= INT32_MAX / 2;
 }
 
 template <class T>

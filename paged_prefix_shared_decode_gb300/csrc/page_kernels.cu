@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Scor
 // --------------------------------------------------------------- selection
 
 constexpr int kSelThreads = 256;
+constexpr int kSelCap = 1024;        // keys above the bound that are held as a list
 
 struct SelectArgs {
     QueryRows rows;
@@ -255,9 +256,202 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 }
 constexpr uint32_t kStays = 0xffffffffu;    // sinks and the last pages: above every score
 
-// A CTA per (layer, query row, kv head): the budget-th largest key by a radix
-// select, 8 bits a pass, then the pages in order.
-__global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SelectArgs a) {
+// The larger of two lanes' keys to the lower lane, down to a descending warp.
+__device__ __forceinline__ uint32_t sort_warp(uint32_t x, int lane) {
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j; j >>= 1) {
+            const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+            const bool up = ((lane & j) == 0) == ((lane & k) == 0);     // this lane takes the larger
+            x = up ? max(x, y) : min(x, y);
+        }
+    return x;
+}
+
+// A CTA per (layer, query row, kv head) of at most W * 32 * E pages, their keys
+// in registers (page W * 32 e + thread).
+//   1. A bound that at least `budget` keys reach, from the threads' maxima:
+//      each warp's ceil(budget / W)-th largest maximum, the smallest of those.
+//   2. The keys that reach it, few more than `budget`, go on a list, and one
+//      warp finds the budget-th largest of them bit by bit (by all warps over
+//      all keys where the list does not hold them).
+//   3. Keys above it, and those equal to it, as two bit maps by page; counts
+//      up to a word give every chosen page its place.
+template <int W, int E>
+__global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kernel(const SelectArgs a) {
+    constexpr int N = 32 * W * E, WORDS = W * E, PER = (WORDS + 32 * W - 1) / (32 * W);
+    __shared__ uint32_t s_key[kSelCap];
+    __shared__ uint16_t s_at[kSelCap];
+    __shared__ uint32_t s_up[WORDS], s_eq[WORDS];
+    __shared__ uint32_t s_warp[W];
+    __shared__ uint32_t s_cut;
+    __shared__ int s_count, s_above;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t row = blockIdx.x;
+    const int r = (int)(row / a.Hkv % a.rows.T);
+    const int seq = a.rows.sequence(r);
+    if (seq < 0) return;
+    const int n = a.rows.pages(seq, r);
+    const float *score = a.scores + row * a.stride;
+    int32_t *out = a.selected + row * a.budget;
+    if (n <= a.budget) {
+        for (int j = tid; j < a.budget; j += 32 * W) out[j] = j < n ? j : -1;
+        return;
+    }
+    uint32_t key[E];
+    {
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j = e * 32 * W + tid;
+            x[e] = j < n ? __ldcs(score + j) : 0.f;
+        }
+        const int lo = a.sink, hi = n - a.recent;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j = e * 32 * W + tid;
+            key[e] = j >= n ? 0u : j < lo || j >= hi ? kStays : score_key(x[e]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (tid + i * 32 * W < WORDS) s_up[tid + i * 32 * W] = s_eq[tid + i * 32 * W] = 0;
+    if (tid == 0) s_count = 0;
+    uint32_t bound = 0, top = 0;
+    const bool few = a.budget <= 32 * W;
+    if (few) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = max(top, key[e]);
+        top = sort_warp(top, lane);
+        if (lane == (a.budget + W - 1) / W - 1) s_warp[warp] = top;
+    }
+    __syncthreads();
+    if (few) {
+        bound = s_warp[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) bound = min(bound, s_warp[w]);
+    }
+    bound = max(bound, 1u);          // (0: past the end)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (key[e] >= bound) {
+            const int i = atomicAdd(&s_count, 1);
+            if (i < kSelCap) {
+                s_key[i] = key[e];
+                s_at[i] = (uint16_t)(e * 32 * W + tid);
+            }
+        }
+    __syncthreads();
+    const int m = s_count;
+    const bool listed = m <= kSelCap;
+    uint32_t cut = bound;            // the budget-th largest key, from its bits down
+    int above = 0;                   // keys larger than it
+    if (listed) {
+        if (warp == 0) {
+            // the bits that bound and every key share need no test
+            uint32_t differ = 0;
+            for (int i = lane; i < m; i += 32) differ |= s_key[i] ^ bound;
+            differ = __reduce_or_sync(0xffffffffu, differ);
+            const int bits = differ ? 32 - __clz(differ) : 0;
+            cut = bits == 32 ? 0u : bound >> bits << bits;
+            uint32_t x[8];           // the first 256 keys; more are read from shared memory
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = i * 32 + lane < m ? s_key[i * 32 + lane] : 0u;
+            auto count = [&](uint32_t t) {       // keys of at least t
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c += x[i] >= t;
+                for (int i = 256 + lane; i < m; i += 32) c += s_key[i] >= t;
+                return (int)__reduce_add_sync(0xffffffffu, c);
+            };
+            for (int b = bits - 1; b >= 0; --b)
+                if (count(cut | 1u << b) >= a.budget) cut |= 1u << b;
+            above = cut == kStays ? 0 : count(cut + 1);
+            if (lane == 0) {
+                s_cut = cut;
+                s_above = above;
+            }
+        }
+        __syncthreads();
+        cut = s_cut;
+        above = s_above;
+        for (int i = tid; i < m; i += 32 * W) {
+            const uint32_t k = s_key[i];
+            const int at = s_at[i];
+            if (k > cut) atomicOr(&s_up[at >> 5], 1u << (at & 31));
+            if (k == cut) atomicOr(&s_eq[at >> 5], 1u << (at & 31));
+        }
+    } else {
+        auto count = [&](uint32_t t, bool equal) {
+            int c = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) c += key[e] > t || (equal && key[e] == t);
+            c = __reduce_add_sync(0xffffffffu, c);
+            __syncthreads();
+            if (lane == 0) s_warp[warp] = c;
+            __syncthreads();
+            int sum = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) sum += s_warp[w];
+            return sum;
+        };
+        cut = 0;
+        for (int b = 31; b >= 0; --b)
+            if (count(cut | 1u << b, true) >= a.budget) cut |= 1u << b;
+        above = count(cut, false);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const uint32_t up = __ballot_sync(0xffffffffu, key[e] > cut), eq = __ballot_sync(0xffffffffu, key[e] == cut);
+            if (lane == 0) {
+                s_up[e * W + warp] = up;
+                s_eq[e * W + warp] = eq;
+            }
+        }
+    }
+    __syncthreads();
+    // places: words in page order, PER to a thread; counts of both maps in the
+    // halves of one word (N <= 32768)
+    static_assert(N <= 32768, "two 16-bit counts");
+    uint32_t up[PER], eq[PER], mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int w = tid * PER + i;
+        up[i] = w < WORDS ? s_up[w] : 0u;
+        eq[i] = w < WORDS ? s_eq[w] : 0u;
+        mine += __popc(up[i]) + (__popc(eq[i]) << 16);
+    }
+    uint32_t before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) s_warp[warp] = before;
+    __syncthreads();
+    before -= mine;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        if (w < warp) before += s_warp[w];
+    int n_up = before & 0xffff, n_eq = before >> 16;
+    const int left = a.budget - above;          // of the equal ones, the first
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        uint32_t any = up[i] | eq[i];
+        while (any) {
+            const int b = __ffs(any) - 1;
+            any &= any - 1;
+            if (up[i] >> b & 1)
+                out[n_up++ + min(n_eq, left)] = (tid * PER + i) * 32 + b;
+            else if (n_eq++ < left)
+                out[n_up + n_eq - 1] = (tid * PER + i) * 32 + b;
+        }
+    }
+}
+
+// Longer rows: the budget-th largest key by a radix select over the row in
+// global memory, 8 bits a pass, then the pages in order.
+__global__ void __launch_bounds__(kSelThreads) page_select_long_kernel(const SelectArgs a) {
     __shared__ int s_bin[256];
     __shared__ int s_up[kSelThreads / 32], s_eq[kSelThreads / 32];
     __shared__ int s_digit, s_left;
@@ -422,7 +616,24 @@ int kvp_page_select(const float *scores, int64_t score_stride, const int32_t *q_
     a.stride = score_stride;
     a.selected = selected;
     a.Hkv = desc->num_kv_heads; a.budget = budget; a.sink = n_sink; a.recent = n_recent;
-    page_select_kernel<<<(unsigned)grid, kSelThreads, 0, (cudaStream_t)stream>>>(a);
+    // the smallest kernel whose registers hold the longest row that the tables
+    // allow; 1024 threads for rows that 256 do not hold
+    const unsigned ctas = (unsigned)grid;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (max_blocks <= 256)
+        page_select_kernel<4, 2><<<ctas, 128, 0, st>>>(a);
+    else if (max_blocks <= 1024)
+        page_select_kernel<4, 8><<<ctas, 128, 0, st>>>(a);
+    else if (max_blocks <= 2048)
+        page_select_kernel<8, 8><<<ctas, 256, 0, st>>>(a);
+    else if (max_blocks <= 4096)
+        page_select_kernel<8, 16><<<ctas, 256, 0, st>>>(a);
+    else if (max_blocks <= 8192)
+        page_select_kernel<8, 32><<<ctas, 256, 0, st>>>(a);
+    else if (max_blocks <= 32768)
+        page_select_kernel<32, 32><<<ctas, 1024, 0, st>>>(a);
+    else
+        page_select_long_kernel<<<ctas, kSelThreads, 0, st>>>(a);
     count_launch();
     return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }

@@ -581,8 +581,9 @@ int seq_append_rope(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32_
     }
     if ((q == nullptr) != (q_out == nullptr) || (q && (num_q_heads <= 0 || num_q_heads > 65536)))
         return KVP_ERR_INVALID;
-    const int64_t units = ((int64_t)d.num_kv_heads * 2 + (q ? num_q_heads : 0)) * (d.head_dim / 2 + 8);
-    if (units > INT32_MAX / 8 || d.num_layers > 2048) return KVP_ERR_INVALID;
+    // (the kernels count a token's 2-value units in 32 bits, times those of a head)
+    const int64_t units = ((int64_t)d.num_kv_heads * 2 + (q ? num_q_heads : 0)) * (d.head_dim / 2);
+    if (units > (INT64_C(1) << 32) / d.head_dim || d.num_layers > 2048) return KVP_ERR_INVALID;
     if (total > 0) {
         if (!k || !v || !aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out)) return KVP_ERR_INVALID;
         if ((uintptr_t)positions & 3) return KVP_ERR_INVALID;

@@ -33,7 +33,8 @@ namespace kvp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;          // units in flight per thread
+constexpr int kBatch = 2;          // units in flight per thread (4: 119 registers, half the warps)
+constexpr int kCopies = 4;         // 16-byte copies in flight per thread
 constexpr int kMaxTok = 4;         // tokens per CTA
 constexpr int kTokMax = 1 << 19;   // tokens per launch
 
@@ -54,6 +55,7 @@ struct RopeArgs {
     int32_t ntok_total, tok_begin, ntok, per_cta;
     int32_t rot, adjacent;
     int32_t nrun, ncow;
+    uint32_t div_unit, div_token;      // 2^32 / units of a head and of a token, rounded up
     float scale;
     uint64_t freq[kMaxRot / 2];
     Run run[NR];
@@ -143,24 +145,42 @@ __device__ __forceinline__ void turn_vec(unsigned short &x, unsigned short &y, c
 }
 
 // Copy-on-write: CTA x of ncow * L copies the used slots of one triple in one
-// layer, K and V.  Rows of `bytes` bytes, 16 at a time where they are whole.
+// layer, K and V, one contiguous run per head.
 template <class Args>
 __device__ __forceinline__ void copy_cow(const Args &a, int x) {
     const int i = x % a.ncow, l = x / a.ncow;
     const int src = a.cow[3 * i], dst = a.cow[3 * i + 1], used = a.cow[3 * i + 2];
-    const int ch = a.d / 8;                        // 16-byte chunks per row
-    const int64_t run = (int64_t)used * ch, tile = (int64_t)a.bs * ch;
-    for (int64_t y = threadIdx.x; y < 2 * a.Hkv * run; y += blockDim.x) {
-        const int64_t h = y / (2 * run), r = y % (2 * run);
-        uint4 *pool = static_cast<uint4 *>(r < run ? a.k_pool : a.v_pool);
-        const int64_t c = r < run ? r : r - run;
-        const int64_t head = (int64_t)l * a.NB * a.Hkv + h;
-        pool[(head + (int64_t)dst * a.Hkv) * tile + c] = pool[(head + (int64_t)src * a.Hkv) * tile + c];
+    const int64_t run = (int64_t)used * (a.d / 8), tile = (int64_t)a.bs * (a.d / 8);     // 16-byte chunks
+    const int64_t step = (int64_t)(dst - src) * a.Hkv * tile, head = ((int64_t)l * a.NB + src) * a.Hkv;
+    uint4 *kp = static_cast<uint4 *>(a.k_pool), *vp = static_cast<uint4 *>(a.v_pool);
+    if (run * a.Hkv * 2 <= INT32_MAX) {
+        // (a divisor per thread and batch: the loads are what takes time)
+        const int total = (int)run * a.Hkv * 2, r = (int)run;
+        for (int y0 = threadIdx.x; y0 < total; y0 += kThreads * kCopies) {
+            uint4 v[kCopies];
+            uint4 *p[kCopies];
+#pragma unroll
+            for (int u = 0; u < kCopies; ++u) {
+                const int y = y0 + u * kThreads, z = y >> 1, h = z / r;
+                p[u] = (y & 1 ? vp : kp) + (head + h) * tile + (z - h * r);
+                if (y < total) v[u] = *p[u];
+            }
+#pragma unroll
+            for (int u = 0; u < kCopies; ++u)
+                if (y0 + u * kThreads < total) p[u][step] = v[u];
+        }
+    } else {
+        for (int h = 0; h < a.Hkv; ++h)
+            for (int64_t c = threadIdx.x; c < run; c += kThreads) {
+                const int64_t at = (head + h) * tile + c;
+                kp[at + step] = kp[at];
+                vp[at + step] = vp[at];
+            }
     }
 }
 
 template <int W, class Args>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const __grid_constant__ Args a) {
     using V = typename Vec<W>::type;
     __shared__ Tokens s;
     const int cow_ctas = a.ncow * a.L;
@@ -172,37 +192,30 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
     const int x0 = blockIdx.x - cow_ctas;
     const int l = x0 / groups, t0 = (x0 % groups) * a.per_cta;
     const int nt = min(a.per_cta, a.ntok - t0);
-    // units of a token: heads of K, then of Q, each its pairs and then the
-    // dims behind them; then the heads of V
-    const int R = a.rot / 2 / W, U = R + (a.d - a.rot + 2 * W - 1) / (2 * W);
-    const int nrot = (a.Hkv + a.Hq) * U, UV = (a.d / 8 + 1) / 2, per_tok = nrot + a.Hkv * UV;
+    // units of a token: heads of K, of Q, of V; a head's U units, of which the
+    // first R of K and Q are pairs (in halves: W values of each half), the
+    // others 2 W values in a row
+    const int R = a.rot / 2 / W, U = (a.d + 2 * W - 1) / (2 * W), per_tok = (2 * a.Hkv + a.Hq) * U;
     const int total = nt * per_tok;
-    const int64_t tok = a.tok_begin + t0;
+    const int64_t tok = l * (int64_t)a.ntok_total + a.tok_begin + t0;
     const int64_t layer = (int64_t)l * a.NB * a.Hkv * a.bs;
     bool ready = false;
     for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < total; i0 += kThreads * kBatch) {
         V x[kBatch], y[kBatch];
-        uint4 vx[kBatch], vy[kBatch];
+        int tt[kBatch], hh[kBatch], uu[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * kThreads;
-            if (i >= total) break;
-            const int t = i / per_tok, r = i % per_tok;
-            if (r < nrot) {
-                const int h = r / U, u = r % U;
-                const int ea = u >= R ? a.rot + (u - R) * 2 * W : a.adjacent ? 2 * u * W : u * W;
-                const int eb = u >= R || a.adjacent ? ea + W : ea + a.rot / 2;
-                const __nv_bfloat16 *p = h < a.Hkv ? a.k + ((l * (int64_t)a.ntok_total + tok + t) * a.Hkv + h) * a.d
-                                                   : a.q + ((l * (int64_t)a.ntok_total + tok + t) * a.Hq + h - a.Hkv) * a.d;
-                x[b] = *reinterpret_cast<const V *>(p + ea);
-                if (eb < a.d) y[b] = *reinterpret_cast<const V *>(p + eb);
-            } else {
-                const int h = (r - nrot) / UV, u = (r - nrot) % UV;
-                const uint4 *p = reinterpret_cast<const uint4 *>(
-                    a.v + ((l * (int64_t)a.ntok_total + tok + t) * a.Hkv + h) * a.d) + 2 * u;
-                vx[b] = p[0];
-                if (16 * u + 8 < a.d) vy[b] = p[1];
-            }
+            const int i = min(i0 + b * kThreads, total - 1);      // (past the end: the last unit again, not stored)
+            const int t = a.per_cta == 1 ? 0 : (int)__umulhi(i, a.div_token), r = i - t * per_tok;
+            const int h = U == 1 ? r : (int)__umulhi(r, a.div_unit), u = r - h * U;
+            const __nv_bfloat16 *p = h < a.Hkv          ? a.k + ((tok + t) * a.Hkv + h) * a.d
+                                     : h < a.Hkv + a.Hq ? a.q + ((tok + t) * a.Hq + h - a.Hkv) * a.d
+                                                        : a.v + ((tok + t) * a.Hkv + h - a.Hkv - a.Hq) * a.d;
+            const bool halves = u < R && h < a.Hkv + a.Hq && !a.adjacent;
+            const int ea = halves ? u * W : 2 * u * W, eb = halves ? ea + a.rot / 2 : ea + W;
+            x[b] = *reinterpret_cast<const V *>(p + ea);
+            if (eb < a.d) y[b] = *reinterpret_cast<const V *>(p + eb);
+            tt[b] = t; hh[b] = h; uu[b] = u;
         }
         if (!ready) {
             fill_tokens(a, s, t0, nt);
@@ -211,26 +224,18 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * kThreads;
-            if (i >= total) break;
-            const int t = i / per_tok, r = i % per_tok;
-            if (r < nrot) {
-                const int h = r / U, u = r % U;
-                const int ea = u >= R ? a.rot + (u - R) * 2 * W : a.adjacent ? 2 * u * W : u * W;
-                const int eb = u >= R || a.adjacent ? ea + W : ea + a.rot / 2;
-                __nv_bfloat16 *p = h < a.Hkv ? static_cast<__nv_bfloat16 *>(a.k_pool) +
-                                                   (layer + s.row[t] + (int64_t)h * a.bs) * a.d
-                                             : a.q_out + ((l * (int64_t)a.ntok_total + tok + t) * a.Hq + h - a.Hkv) * a.d;
-                if (u < R) turn_vec(x[b], y[b], s.turn[t] + u * W, a.adjacent);
-                *reinterpret_cast<V *>(p + ea) = x[b];
-                if (eb < a.d) *reinterpret_cast<V *>(p + eb) = y[b];
-            } else {
-                const int h = (r - nrot) / UV, u = (r - nrot) % UV;
-                uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.v_pool) +
-                                                     (layer + s.row[t] + (int64_t)h * a.bs) * a.d) + 2 * u;
-                p[0] = vx[b];
-                if (16 * u + 8 < a.d) p[1] = vy[b];
-            }
+            if (i0 + b * kThreads >= total) break;
+            const int t = tt[b], h = hh[b], u = uu[b];
+            const bool is_v = h >= a.Hkv + a.Hq, turned = u < R && !is_v, halves = turned && !a.adjacent;
+            const int ea = halves ? u * W : 2 * u * W, eb = halves ? ea + a.rot / 2 : ea + W;
+            const int64_t row = layer + s.row[t];
+            __nv_bfloat16 *p = h < a.Hkv ? static_cast<__nv_bfloat16 *>(a.k_pool) + (row + (int64_t)h * a.bs) * a.d
+                               : !is_v   ? a.q_out + ((tok + t) * a.Hq + h - a.Hkv) * a.d
+                                         : static_cast<__nv_bfloat16 *>(a.v_pool) +
+                                               (row + (int64_t)(h - a.Hkv - a.Hq) * a.bs) * a.d;
+            if (turned) turn_vec(x[b], y[b], s.turn[t] + u * W, a.adjacent);
+            *reinterpret_cast<V *>(p + ea) = x[b];
+            if (eb < a.d) *reinterpret_cast<V *>(p + eb) = y[b];
         }
     }
 }
@@ -326,7 +331,14 @@ cudaError_t launch_part(const RopeAppend &r, const Run *run, int nrun, const int
         rope_append4_kernel<Args><<<(unsigned)((ncow + ntok) * r.L), kThreads, 0, stream>>>(a);
     } else {
         // several tokens to a CTA once one each would be many per SM
-        while (a.per_cta < kMaxTok && (int64_t)ntok * r.L > 16LL * a.per_cta * device_sm_count()) a.per_cta *= 2;
+        const int W = r.rot % 16 == 0 ? 8 : 1, U = (r.d + 2 * W - 1) / (2 * W);
+        const int64_t per_tok = (2LL * r.Hkv + a.Hq) * U;
+        // x / n as the high word of x * ceil(2^32 / n): exact while x * n < 2^32
+        auto magic = [](int64_t n) { return (uint32_t)(((1LL << 32) + n - 1) / n); };
+        a.div_unit = U > 1 ? magic(U) : 0;
+        a.div_token = magic(per_tok);
+        while (a.per_cta < kMaxTok && (int64_t)ntok * r.L > 16LL * a.per_cta * device_sm_count() && per_tok < 16384)
+            a.per_cta *= 2;
         const unsigned grid = (unsigned)((ncow + (ntok + a.per_cta - 1) / a.per_cta) * r.L);
         if (r.rot % 16 == 0)
             rope_append_kernel<8, Args><<<grid, kThreads, 0, stream>>>(a);
