@@ -12,9 +12,13 @@
 // ceil(n / 8)-th is a bound that at least n logits reach and few more do;
 // those are ranked against one another.  (More reach it where many are equal,
 // or the large ones lie in few threads: then one after the other is taken.)
-// beam_join_kernel: a CTA per request joins the sums (in 64 bits), scores the
-// candidates and ranks them the same way, as 64-bit whole numbers of the same
-// order (comparisons of doubles run on the FP64 pipe: 47 us instead of 8).
+// beam_join_kernel: a CTA per request joins the sums, scores the candidates and
+// ranks them the same way.
+// What decides between beams has to be finer than fp32, and the FP64 pipe is
+// slow here (a join that compared doubles took 47 us, one that added and took
+// exponentials in them 15): sums and scores are pairs of fp32 numbers, value
+// and rest (48 bits, by error-free sums), compared as 64-bit whole numbers of
+// the same order.
 // Bound by HBM for large batches (every logit read once), by latency for one
 // request.
 #include <cuda_bf16.h>
@@ -22,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -40,8 +45,9 @@ constexpr int kCap = 1024;                     // candidates ranked at once
 
 // A chunk's part of its row.
 struct alignas(16) PartHead {
-    double sum;        // of exp(logit - top)
+    float sum, rest;   // of exp(logit - top)
     float top;         // largest logit; +inf where the row is not to be used
+    float pad;
 };
 
 struct BeamArgs {
@@ -51,6 +57,8 @@ struct BeamArgs {
     const uint8_t *finished;
     int32_t pad, groups, beams, vocab, n, chunks;
     int32_t vec;                  // rows may be read 16 bytes at a time
+    int32_t early;                // the join may start beside the parts' CTAs
+    uint32_t div;                 // 2^32 / (chunks * n), rounded up; 0: too large for that
     float *out_scores;
     int32_t *out_rows, *out_tokens;
     PartHead *heads;              // [rows][chunks]
@@ -83,19 +91,22 @@ template <class T> constexpr int kVec = 16 / sizeof(T);
 template <class T>
 __device__ __forceinline__ int place(int tid, int k) { return (k / kVec<T>) * kVec<T> * kThreads + tid * kVec<T> + k % kVec<T>; }
 
-__device__ __forceinline__ double sum_block(double x, double *s, int warp, int lane) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) s[warp] = x;
-    __syncthreads();
-    double r = 0;
-    for (int w = 0; w < kWarps; ++w) r += s[w];
-    return r;
+__device__ __forceinline__ float exp2_sfu(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+// (x, xr) += (y, yr): the error of the fp32 sum goes into the rest.
+__device__ __forceinline__ void add2(float &x, float &xr, float y, float yr) {
+    const float s = __fadd_rn(x, y), b = __fsub_rn(s, x);
+    const float e = __fadd_rn(__fadd_rn(__fsub_rn(x, __fsub_rn(s, b)), __fsub_rn(y, b)), __fadd_rn(xr, yr));
+    x = __fadd_rn(s, e);
+    xr = __fsub_rn(e, __fsub_rn(x, s));
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads, 3) beam_part_kernel(const BeamArgs a) {
-    __shared__ double s_sum[kWarps];
+__global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a) {
+    __shared__ float2 s_sum[kWarps];
     __shared__ float s_max[kWarps], s_bound[kWarps];
     __shared__ float s_c[kCap];
     __shared__ int s_at[kCap];
@@ -103,25 +114,31 @@ __global__ void __launch_bounds__(kThreads, 3) beam_part_kernel(const BeamArgs a
     __shared__ float s_bestv[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");     // the join, which waits for all of this
+    if (a.early) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (a.finished && a.finished[row]) return;
     const int x0 = chunk * kChunk, len = min(kChunk, a.vocab - x0);
     const T *src = static_cast<const T *>(a.logits) + row * a.row_stride + x0;
     float v[kPer];
     if (a.vec) {
         uint4 raw[kPer / kVec<T>];
+        const bool full = len == kChunk;
 #pragma unroll
         for (int i = 0; i < kPer / kVec<T>; ++i) {
             const int at = place<T>(tid, i * kVec<T>);
-            if (at + kVec<T> <= len) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + at));
+            if (full || at + kVec<T> <= len) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + at));
         }
 #pragma unroll
         for (int i = 0; i < kPer / kVec<T>; ++i) {
-            const int at = place<T>(tid, i * kVec<T>);
             const T *e = reinterpret_cast<const T *>(&raw[i]);
 #pragma unroll
-            for (int k = 0; k < kVec<T>; ++k)
-                v[i * kVec<T> + k] = at + kVec<T> <= len ? as_float(e[k]) : at + k < len ? as_float(src[at + k]) : -INFINITY;
+            for (int k = 0; k < kVec<T>; ++k) v[i * kVec<T> + k] = as_float(e[k]);
+        }
+        if (!full) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int at = place<T>(tid, k);
+                if (at / kVec<T> * kVec<T> + kVec<T> > len) v[k] = at < len ? as_float(src[at]) : -INFINITY;
+            }
         }
     } else {
 #pragma unroll
@@ -130,14 +147,21 @@ __global__ void __launch_bounds__(kThreads, 3) beam_part_kernel(const BeamArgs a
             v[k] = at < len ? as_float(src[at]) : -INFINITY;
         }
     }
-    float top = -INFINITY;
-    bool nan = false;
+    constexpr int GROUP = 8;             // maxima of 8 logits: most reach no candidate
+    float part_top[kPer / GROUP], top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        top = fmaxf(top, v[k]);
-        nan |= v[k] != v[k];
+    for (int i = 0; i < kPer / GROUP; ++i) {
+        part_top[i] = v[i * GROUP];
+#pragma unroll
+        for (int k = 1; k < GROUP; ++k) part_top[i] = fmaxf(part_top[i], v[i * GROUP + k]);
+        top = fmaxf(top, part_top[i]);
     }
-    if (nan) top = INFINITY;             // as +inf does: the row has no log-sum-exp
+    if (top == -INFINITY) {              // (a thread of NaNs alone; others show in its sum)
+        bool nan = false;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) nan |= v[k] != v[k];
+        if (nan) top = INFINITY;         // as +inf does: the row has no log-sum-exp
+    }
     top = sort_warp(top, lane);
     if (lane == 0) s_max[warp] = top;
     if (lane == (a.n + kWarps - 1) / kWarps - 1) s_bound[warp] = top;
@@ -149,28 +173,43 @@ __global__ void __launch_bounds__(kThreads, 3) beam_part_kernel(const BeamArgs a
         all = fmaxf(all, s_max[w]);
         bound = fminf(bound, s_bound[w]);
     }
+    bound = fmaxf(bound, -FLT_MAX);      // -inf is no candidate
     PartHead *head = a.heads + (int64_t)row * a.chunks + chunk;
     float *cand = a.cand + ((int64_t)row * a.chunks + chunk) * a.n;
     int32_t *cand_at = a.cand_at + ((int64_t)row * a.chunks + chunk) * a.n;
     if (!(all < INFINITY) || all == -INFINITY) {       // nothing here, or nothing in the row
-        if (tid == 0) *head = PartHead{0.0, all};
+        if (tid == 0) *head = PartHead{0.f, 0.f, all, 0.f};
         if (tid < a.n) cand[tid] = -INFINITY;
         return;
     }
-    float part = 0.f;
+    // 2^((v - all) log2 e): the difference is exact or nearly so, its product
+    // is off by 2^-24 of itself and the power by 2^-22, both ways alike (expf's
+    // two-part product: 10 instructions a logit instead of 4)
+    float part = 0.f, rest = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) part += expf(v[k] - all);
-    const double sum = sum_block((double)part, s_sum, warp, lane);
+    for (int k = 0; k < kPer; ++k) part += exp2_sfu((v[k] - all) * 1.4426950408889634f);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-        if (v[k] >= bound && v[k] > -INFINITY) {
-            const int i = atomicAdd(&s_count, 1);
-            if (i < kCap) {
-                s_c[i] = v[k];
-                s_at[i] = place<T>(tid, k);
+    for (int o = 16; o; o >>= 1)
+        add2(part, rest, __shfl_xor_sync(0xffffffffu, part, o), __shfl_xor_sync(0xffffffffu, rest, o));
+    if (lane == 0) s_sum[warp] = make_float2(part, rest);
+#pragma unroll
+    for (int i = 0; i < kPer / GROUP; ++i) {
+        if (!(part_top[i] >= bound)) continue;
+#pragma unroll
+        for (int k = i * GROUP; k < (i + 1) * GROUP; ++k)
+            if (v[k] >= bound) {
+                const int j = atomicAdd(&s_count, 1);
+                if (j < kCap) {
+                    s_c[j] = v[k];
+                    s_at[j] = place<T>(tid, k);
+                }
             }
-        }
+    }
     __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kWarps; ++w) add2(part, rest, s_sum[w].x, s_sum[w].y);
+        *head = PartHead{part, rest, part == part ? all : INFINITY, 0.f};
+    }
     const int found = s_count;
     if (found <= kCap) {
         for (int i = tid; i < found; i += kThreads) {
@@ -184,7 +223,6 @@ __global__ void __launch_bounds__(kThreads, 3) beam_part_kernel(const BeamArgs a
             }
         }
         if (tid >= found && tid < a.n) cand[tid] = -INFINITY;
-        if (tid == 0) *head = PartHead{sum, all};
         return;
     }
     // one after the other: the largest logit behind the last one taken
@@ -231,21 +269,21 @@ __global__ void __launch_bounds__(kThreads, 3) beam_part_kernel(const BeamArgs a
             cand_at[r] = x0 + at;
         }
     }
-    if (tid == 0) *head = PartHead{sum, all};
 }
 
-// A candidate; its score as a whole number of the same order.
+// A candidate; its score (value and rest) as a whole number of the same order.
 struct Entry {
     uint64_t key;
     float logit;
     int32_t beam, at;
 };
-__device__ __forceinline__ uint64_t score_key(double x) {
-    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
-    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ double key_score(uint64_t k) {
-    return __longlong_as_double((long long)(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t k = (uint32_t)(key >> 32);
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 // The order: score, then row, then logit, then token.
 __device__ __forceinline__ bool before(const Entry &x, const Entry &y) {
@@ -255,94 +293,148 @@ __device__ __forceinline__ bool before(const Entry &x, const Entry &y) {
     return x.at < y.at;
 }
 
+constexpr int kHeld = 8;       // candidates a thread keeps in registers
+
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
-    __shared__ double s_add[kMaxBeams];     // score - log-sum-exp; -inf: no candidates
-    __shared__ Entry s_e[kCap];
+    __shared__ float2 s_add[kMaxBeams];     // score - log-sum-exp; -inf: no candidates
+    __shared__ uint8_t s_done[kMaxBeams];
+    __shared__ uint64_t s_key[kCap];
+    __shared__ float s_logit[kCap];
+    __shared__ int s_at[kCap];
+    __shared__ uint8_t s_beam[kCap];
     __shared__ uint64_t s_bound[kWarps];
     __shared__ int s_count;
     __shared__ Entry s_best[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = blockIdx.x;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int per_beam = a.chunks * a.n, total = per_beam * a.beams;
+    const float *cand = a.cand + (int64_t)g * total;
+    const int32_t *cand_at = a.cand_at + (int64_t)g * total;
+    float held[kHeld];
+    int held_at[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        const int i = tid + k * kThreads;
+        held[k] = i < total ? cand[i] : -INFINITY;
+        held_at[k] = i < total ? cand_at[i] : 0;
+    }
     for (int b = warp; b < a.beams; b += kWarps) {
         const int row = g * a.beams + b;
         const float cum = a.scores[row];
-        double add = -INFINITY;
+        const bool done = a.finished && a.finished[row];
+        float2 add = make_float2(-INFINITY, 0.f);
         if (isfinite(cum)) {
-            if (a.finished && a.finished[row]) {
-                add = (double)cum;
+            if (done) {
+                add.x = cum;
             } else {
                 const PartHead *h = a.heads + (int64_t)row * a.chunks;
-                const float mine = lane < a.chunks ? h[lane].top : -INFINITY;
-                float top = mine;
+                const PartHead mine = lane < a.chunks ? h[lane] : PartHead{0.f, 0.f, -INFINITY, 0.f};
+                float top = mine.top;
                 for (int c = lane + 32; c < a.chunks; c += 32) top = fmaxf(top, h[c].top);
 #pragma unroll
                 for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 if (top < INFINITY && top > -INFINITY) {
-                    double sum = 0;
-                    for (int c = lane; c < a.chunks; c += 32)
-                        if (h[c].top > -INFINITY) sum += h[c].sum * exp((double)h[c].top - (double)top);
+                    float sum = 0.f, rest = 0.f;
+                    for (int c = lane; c < a.chunks; c += 32) {
+                        const PartHead x = c == lane ? mine : h[c];
+                        const float w = expf(x.top - top);
+                        const float y = __fmul_rn(x.sum, w);
+                        add2(sum, rest, y, __fmaf_rn(x.sum, w, -y) + x.rest * w);
+                    }
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    add = (double)cum - ((double)top + log(sum));
+                    for (int o = 16; o; o >>= 1)
+                        add2(sum, rest, __shfl_xor_sync(0xffffffffu, sum, o), __shfl_xor_sync(0xffffffffu, rest, o));
+                    // log(sum) = k log 2 + log(m), m in [0.75, 1.5): log(m) is
+                    // small, and its fp32 rounding with it
+                    int k;
+                    float m = frexpf(sum, &k);          // [0.5, 1)
+                    if (m < 0.75f) {
+                        m *= 2.f;
+                        --k;
+                    }
+                    const double z = (double)cum - (double)top - k * 0.693147180559945309417 -
+                                     ((double)logf(m) + (double)(rest / sum));
+                    add.x = (float)z;
+                    add.y = (float)(z - (double)add.x);
                 }
             }
         }
-        if (lane == 0) s_add[b] = add;
+        if (lane == 0) {
+            s_add[b] = isfinite(add.x) ? add : make_float2(-INFINITY, 0.f);
+            s_done[b] = done;
+        }
     }
     if (tid == 0) s_count = 0;
     __syncthreads();
     // candidate i: place i % per_beam of beam i / per_beam; a finished beam's
     // one is its first
-    const int per_beam = a.chunks * a.n, total = per_beam * a.beams;
-    const float *cand = a.cand + (int64_t)g * total;
-    const int32_t *cand_at = a.cand_at + (int64_t)g * total;
-    auto entry = [&](int i, Entry &e) -> bool {
-        const int b = i / per_beam;
-        const double add = s_add[b];
-        if (add == -INFINITY) return false;
-        e.beam = b;
-        if (a.finished && a.finished[g * a.beams + b]) {
-            e.key = score_key(add);
-            e.logit = 0.f;
-            e.at = a.pad;
-            return i == b * per_beam;
+    auto beam_of = [&](int i) { return a.div ? (int)__umulhi(i, a.div) : i / per_beam; };
+    auto key_of = [&](int i, float logit) -> uint64_t {      // 0: none
+        const int b = beam_of(i);
+        float2 add = s_add[b];
+        if (s_done[b]) {
+            if (i != b * per_beam) return 0;
+        } else {
+            if (!(logit > -INFINITY)) return 0;
+            add2(add.x, add.y, logit, 0.f);
         }
-        e.logit = cand[i];
-        e.key = score_key(add + (double)e.logit);
-        e.at = i;                    // (its token: cand_at[i])
-        return e.logit > -INFINITY;
+        // (a beam without candidates, or a score below fp32's range)
+        if (!(add.x > -INFINITY)) return 0;
+        return (uint64_t)order_key(add.x) << 32 | order_key(add.y);
     };
-    uint64_t top = 0;
-    Entry e;
-    for (int i = tid; i < total; i += kThreads)
-        if (entry(i, e)) top = max(top, e.key);
+    uint64_t key[kHeld], top = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        const int i = tid + k * kThreads;
+        key[k] = i < total ? key_of(i, held[k]) : 0;
+        top = max(top, key[k]);
+    }
+#pragma unroll 1
+    for (int i = tid + kHeld * kThreads; i < total; i += kThreads) top = max(top, key_of(i, cand[i]));
     top = sort_warp(top, lane);
     if (lane == (a.n + kWarps - 1) / kWarps - 1) s_bound[warp] = top;
     __syncthreads();
     uint64_t bound = s_bound[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) bound = min(bound, s_bound[w]);
-    // (within a beam, candidates of one logit are in the order of their tokens)
-    for (int i = tid; i < total; i += kThreads)
-        if (entry(i, e) && e.key >= bound) {
-            const int k = atomicAdd(&s_count, 1);
-            if (k < kCap) s_e[k] = e;
+    bound = max(bound, (uint64_t)1);
+    auto collect = [&](int i, uint64_t x, float logit, int at) {
+        const int k = atomicAdd(&s_count, 1);
+        if (k < kCap) {
+            const int b = beam_of(i);
+            s_key[k] = x;
+            s_logit[k] = s_done[b] ? 0.f : logit;
+            s_at[k] = s_done[b] ? a.pad : at;
+            s_beam[k] = (uint8_t)b;
         }
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+        if (key[k] >= bound) collect(tid + k * kThreads, key[k], held[k], held_at[k]);
+#pragma unroll 1
+    for (int i = tid + kHeld * kThreads; i < total; i += kThreads) {
+        const uint64_t x = key_of(i, cand[i]);
+        if (x >= bound) collect(i, x, cand[i], cand_at[i]);
+    }
     __syncthreads();
     const int found = s_count;
     float *os = a.out_scores + (int64_t)g * a.n;
     int32_t *orow = a.out_rows + (int64_t)g * a.n, *ot = a.out_tokens + (int64_t)g * a.n;
     auto put = [&](int r, const Entry &x) {
-        os[r] = (float)key_score(x.key);
+        os[r] = key_value(x.key);
         orow[r] = g * a.beams + x.beam;
-        ot[r] = a.finished && a.finished[g * a.beams + x.beam] ? a.pad : cand_at[x.at];
+        ot[r] = x.at;
     };
     if (found <= kCap) {
         for (int i = tid; i < found; i += kThreads) {
-            const Entry x = s_e[i];
+            const Entry x{s_key[i], s_logit[i], s_beam[i], s_at[i]};
             int r = 0;
-            for (int j = 0; j < found; ++j) r += before(s_e[j], x);
+            for (int j = 0; j < found; ++j) {
+                const uint64_t k = s_key[j];
+                r += k > x.key;
+                if (k == x.key) r += before(Entry{k, s_logit[j], s_beam[j], s_at[j]}, x);
+            }
             if (r < a.n) put(r, x);
         }
         for (int r = found + tid; r < a.n; r += kThreads) {
@@ -355,8 +447,13 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     Entry last{~0ull, INFINITY, -1, -1};
     for (int r = 0; r < a.n; ++r) {
         Entry best{0, -INFINITY, INT_MAX, INT_MAX};
-        for (int i = tid; i < total; i += kThreads)
-            if (entry(i, e) && before(last, e) && before(e, best)) best = e;
+#pragma unroll 1
+        for (int i = tid; i < total; i += kThreads) {
+            const float x = cand[i];
+            const int b = beam_of(i);
+            const Entry e{key_of(i, x), s_done[b] ? 0.f : x, b, s_done[b] ? a.pad : cand_at[i]};
+            if (e.key && before(last, e) && before(e, best)) best = e;
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             Entry y;
@@ -389,6 +486,7 @@ __global__ void __launch_bounds__(kCopyThreads)
                          int64_t tiles) {
     const int64_t row = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int64_t o = row / n_dst;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int from = index[row % n_dst];
     if ((unsigned)from >= (unsigned)n_src) return;
     const V *s = src + (o * n_src + from) * chunks;
@@ -403,15 +501,30 @@ __global__ void __launch_bounds__(kCopyThreads)
         if (x0 + u * kCopyThreads < chunks) d[x0 + u * kCopyThreads] = v[u];
 }
 
+// A kernel that starts (and then waits) as the one before it ends.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    count_launch();
+    return e;
+}
+
 template <class V>
 cudaError_t launch_reorder(const void *src, void *dst, const int32_t *index, int64_t outer, int32_t n_src, int32_t n_dst,
                            int64_t row_bytes, cudaStream_t stream) {
     const int64_t chunks = row_bytes / sizeof(V), tiles = (chunks + kCopyThreads * kInFlight - 1) / (kCopyThreads * kInFlight);
     if (tiles > INT32_MAX || outer * n_dst > INT32_MAX / tiles) return cudaErrorInvalidValue;
-    state_reorder_kernel<V><<<(unsigned)(outer * n_dst * tiles), kCopyThreads, 0, stream>>>(
-        static_cast<const V *>(src), static_cast<V *>(dst), index, n_src, n_dst, chunks, tiles);
-    count_launch();
-    return cudaGetLastError();
+    return launch_behind(state_reorder_kernel<V>, outer * n_dst * tiles, kCopyThreads, stream, static_cast<const V *>(src),
+                         static_cast<V *>(dst), index, n_src, n_dst, chunks, tiles);
 }
 
 bool bad(const void *p, uintptr_t align) { return !p || ((uintptr_t)p & (align - 1)); }
@@ -424,23 +537,19 @@ bool beam_shape_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out) 
 }
 
 template <class T>
-cudaError_t launch_beam(const BeamArgs &a, cudaStream_t stream) {
+cudaError_t launch_beam(BeamArgs a, cudaStream_t stream) {
+    // (several waves: the joins' CTAs would only take the parts' places, 113
+    // instead of 73 us for 4096 of them)
+    a.early = a.groups * a.beams * a.chunks <= 2 * device_sm_count();
+    const int64_t per_beam = (int64_t)a.chunks * a.n;
+    a.div = per_beam > 1 && per_beam * per_beam * a.beams < (INT64_C(1) << 32)
+                ? (uint32_t)(((INT64_C(1) << 32) + per_beam - 1) / per_beam)
+                : 0;
     beam_part_kernel<T><<<(unsigned)(a.groups * a.beams * a.chunks), kThreads, 0, stream>>>(a);
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)a.groups);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, beam_join_kernel, a);
-    count_launch();
-    return e;
+    return launch_behind(beam_join_kernel, a.groups, kThreads, stream, a);
 }
 
 }  // namespace

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Scor
 // --------------------------------------------------------------- selection
 
 constexpr int kSelThreads = 256;
-constexpr int kSelCap = 1024;        // keys above the bound that are held as a list
+constexpr int kSelCap = 128;         // keys above the bound that a warp lists
 
 struct SelectArgs {
     QueryRows rows;
@@ -248,9 +248,9 @@ struct SelectArgs {
     int32_t Hkv, budget, sink, recent;
 };
 
-// Scores as unsigned keys of the same order: NaN above everything, -0 as 0.
+// Scores as unsigned keys of the same order: NaN above everything (a sum that
+// is NaN is the one positive NaN 0x7fffffff), -0 as 0.
 __device__ __forceinline__ uint32_t score_key(float x) {
-    if (x != x) return 0xfffffffeu;
     const uint32_t b = __float_as_uint(x + 0.f);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
@@ -269,105 +269,120 @@ __device__ __forceinline__ uint32_t sort_warp(uint32_t x, int lane) {
     return x;
 }
 
-// A CTA per (layer, query row, kv head) of at most W * 32 * E pages, their keys
-// in registers (page W * 32 e + thread).
-//   1. A bound that at least `budget` keys reach, from the threads' maxima:
-//      each warp's ceil(budget / W)-th largest maximum, the smallest of those.
-//   2. The keys that reach it, few more than `budget`, go on a list, and one
-//      warp finds the budget-th largest of them bit by bit (by all warps over
-//      all keys where the list does not hold them).
+// A CTA per (layer, query row, kv head) of at most W * 32 * E pages: k = budget
+// - sinks - last pages of those in between are to be found, whose keys are in
+// registers (page sink + W * 32 e + thread; steps past the end are as low as
+// -inf and behind every page of that score).
+//   1. A bound that at least k keys reach, from the threads' maxima: each
+//      warp's ceil(k / W)-th largest maximum, the smallest of those.
+//   2. The keys that reach it, few more than k, go on the warps' lists, and
+//      one warp finds the k-th largest of them bit by bit (all warps over all
+//      keys where the lists do not hold them).
 //   3. Keys above it, and those equal to it, as two bit maps by page; counts
 //      up to a word give every chosen page its place.
 template <int W, int E>
 __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kernel(const SelectArgs a) {
-    constexpr int N = 32 * W * E, WORDS = W * E, PER = (WORDS + 32 * W - 1) / (32 * W);
-    __shared__ uint32_t s_key[kSelCap];
-    __shared__ uint16_t s_at[kSelCap];
+    constexpr int WORDS = W * E, PER = (WORDS + 32 * W - 1) / (32 * W), STEP = 32 * W;
+    __shared__ uint32_t s_key[W][kSelCap];
+    __shared__ uint16_t s_at[W][kSelCap];
     __shared__ uint32_t s_up[WORDS], s_eq[WORDS];
-    __shared__ uint32_t s_warp[W];
+    __shared__ uint32_t s_warp[W], s_hits[W];
     __shared__ uint32_t s_cut;
-    __shared__ int s_count, s_above;
+    __shared__ int s_above;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x;
     const int r = (int)(row / a.Hkv % a.rows.T);
     const int seq = a.rows.sequence(r);
     if (seq < 0) return;
     const int n = a.rows.pages(seq, r);
-    const float *score = a.scores + row * a.stride;
+    const int lo = a.sink, len = n - a.recent - lo, k = a.budget - a.sink - a.recent;
+    const float *score = a.scores + row * a.stride + lo;
     int32_t *out = a.selected + row * a.budget;
     if (n <= a.budget) {
-        for (int j = tid; j < a.budget; j += 32 * W) out[j] = j < n ? j : -1;
+        for (int j = tid; j < a.budget; j += STEP) out[j] = j < n ? j : -1;
         return;
     }
     uint32_t key[E];
     {
         float x[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int j = e * 32 * W + tid;
-            x[e] = j < n ? __ldcs(score + j) : 0.f;
-        }
-        const int lo = a.sink, hi = n - a.recent;
+        for (int e = 0; e < E; ++e) x[e] = e * STEP + tid < len ? __ldcs(score + e * STEP + tid) : -INFINITY;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int j = e * 32 * W + tid;
-            key[e] = j >= n ? 0u : j < lo || j >= hi ? kStays : score_key(x[e]);
-        }
+        for (int e = 0; e < E; ++e) key[e] = score_key(x[e]);
     }
+    for (int j = tid; j < lo; j += STEP) out[j] = j;
+    for (int j = tid; j < a.recent; j += STEP) out[a.budget - a.recent + j] = n - a.recent + j;
+    if (k == 0) return;
+    out += lo;
+    uint32_t top = key[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) top = max(top, key[e]);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        if (tid + i * 32 * W < WORDS) s_up[tid + i * 32 * W] = s_eq[tid + i * 32 * W] = 0;
-    if (tid == 0) s_count = 0;
-    uint32_t bound = 0, top = 0;
-    const bool few = a.budget <= 32 * W;
+        if (tid + i * STEP < WORDS) s_up[tid + i * STEP] = s_eq[tid + i * STEP] = 0;
+    const bool few = k <= STEP;
     if (few) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) top = max(top, key[e]);
         top = sort_warp(top, lane);
-        if (lane == (a.budget + W - 1) / W - 1) s_warp[warp] = top;
+        if (lane == (k + W - 1) / W - 1) s_warp[warp] = top;
     }
     __syncthreads();
+    uint32_t bound = 0;
     if (few) {
         bound = s_warp[0];
 #pragma unroll
         for (int w = 1; w < W; ++w) bound = min(bound, s_warp[w]);
     }
-    bound = max(bound, 1u);          // (0: past the end)
+    int hits = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (key[e] >= bound) {
-            const int i = atomicAdd(&s_count, 1);
-            if (i < kSelCap) {
-                s_key[i] = key[e];
-                s_at[i] = (uint16_t)(e * 32 * W + tid);
-            }
+    for (int e = 0; e < E; ++e) {
+        const uint32_t any = __ballot_sync(0xffffffffu, key[e] >= bound);
+        if (any == 0) continue;
+        const int at = hits + __popc(any & ((1u << lane) - 1u));
+        if (key[e] >= bound && at < kSelCap) {
+            s_key[warp][at] = key[e];
+            s_at[warp][at] = (uint16_t)(e * STEP + tid);
         }
+        hits += __popc(any);
+    }
+    if (lane == 0) s_hits[warp] = hits;
     __syncthreads();
-    const int m = s_count;
-    const bool listed = m <= kSelCap;
-    uint32_t cut = bound;            // the budget-th largest key, from its bits down
+    int most = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) most = max(most, (int)s_hits[w]);
+    uint32_t cut = 0;                // the k-th largest key
     int above = 0;                   // keys larger than it
-    if (listed) {
+    if (most <= kSelCap) {
         if (warp == 0) {
-            // the bits that bound and every key share need no test
+            constexpr int H = W <= 8 ? 2 : 1;        // 32 * H keys of each list in registers
+            uint32_t x[W * H];
             uint32_t differ = 0;
-            for (int i = lane; i < m; i += 32) differ |= s_key[i] ^ bound;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const int at = 32 * i + lane;
+                    x[w * H + i] = at < (int)s_hits[w] ? s_key[w][at] : 0u;
+                    if (at < (int)s_hits[w]) differ |= x[w * H + i] ^ bound;
+                }
+            if (most > 32 * H)
+                for (int w = 0; w < W; ++w)
+                    for (int at = 32 * H + lane; at < (int)s_hits[w]; at += 32) differ |= s_key[w][at] ^ bound;
+            auto count = [&](uint32_t t) {           // keys of at least t
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < W * H; ++i) c += x[i] >= t;
+                if (most > 32 * H)
+                    for (int w = 0; w < W; ++w)
+                        for (int at = 32 * H + lane; at < (int)s_hits[w]; at += 32) c += s_key[w][at] >= t;
+                return (int)__reduce_add_sync(0xffffffffu, c);
+            };
+            // the bits that the bound and every key share need no test
             differ = __reduce_or_sync(0xffffffffu, differ);
             const int bits = differ ? 32 - __clz(differ) : 0;
             cut = bits == 32 ? 0u : bound >> bits << bits;
-            uint32_t x[8];           // the first 256 keys; more are read from shared memory
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = i * 32 + lane < m ? s_key[i * 32 + lane] : 0u;
-            auto count = [&](uint32_t t) {       // keys of at least t
-                int c = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) c += x[i] >= t;
-                for (int i = 256 + lane; i < m; i += 32) c += s_key[i] >= t;
-                return (int)__reduce_add_sync(0xffffffffu, c);
-            };
             for (int b = bits - 1; b >= 0; --b)
-                if (count(cut | 1u << b) >= a.budget) cut |= 1u << b;
-            above = cut == kStays ? 0 : count(cut + 1);
+                if (count(cut | 1u << b) >= k) cut |= 1u << b;
+            above = cut == 0xffffffffu ? 0 : count(cut + 1);
             if (lane == 0) {
                 s_cut = cut;
                 s_above = above;
@@ -376,17 +391,17 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
         __syncthreads();
         cut = s_cut;
         above = s_above;
-        for (int i = tid; i < m; i += 32 * W) {
-            const uint32_t k = s_key[i];
-            const int at = s_at[i];
-            if (k > cut) atomicOr(&s_up[at >> 5], 1u << (at & 31));
-            if (k == cut) atomicOr(&s_eq[at >> 5], 1u << (at & 31));
+        for (int i = lane; i < hits; i += 32) {
+            const uint32_t x = s_key[warp][i];
+            const int at = s_at[warp][i];
+            if (x > cut) atomicOr(&s_up[at >> 5], 1u << (at & 31));
+            if (x == cut) atomicOr(&s_eq[at >> 5], 1u << (at & 31));
         }
     } else {
-        auto count = [&](uint32_t t, bool equal) {
+        auto count = [&](uint32_t t) {               // keys of at least t
             int c = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) c += key[e] > t || (equal && key[e] == t);
+            for (int e = 0; e < E; ++e) c += key[e] >= t;
             c = __reduce_add_sync(0xffffffffu, c);
             __syncthreads();
             if (lane == 0) s_warp[warp] = c;
@@ -396,10 +411,9 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
             for (int w = 0; w < W; ++w) sum += s_warp[w];
             return sum;
         };
-        cut = 0;
         for (int b = 31; b >= 0; --b)
-            if (count(cut | 1u << b, true) >= a.budget) cut |= 1u << b;
-        above = count(cut, false);
+            if (count(cut | 1u << b) >= k) cut |= 1u << b;
+        above = cut == 0xffffffffu ? 0 : count(cut + 1);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const uint32_t up = __ballot_sync(0xffffffffu, key[e] > cut), eq = __ballot_sync(0xffffffffu, key[e] == cut);
@@ -411,8 +425,8 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
     }
     __syncthreads();
     // places: words in page order, PER to a thread; counts of both maps in the
-    // halves of one word (N <= 32768)
-    static_assert(N <= 32768, "two 16-bit counts");
+    // halves of one word
+    static_assert(STEP * E <= 32768, "two 16-bit counts");
     uint32_t up[PER], eq[PER], mine = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -434,17 +448,17 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
     for (int w = 0; w < W; ++w)
         if (w < warp) before += s_warp[w];
     int n_up = before & 0xffff, n_eq = before >> 16;
-    const int left = a.budget - above;          // of the equal ones, the first
+    const int left = k - above;                 // of the equal ones, the first
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         uint32_t any = up[i] | eq[i];
         while (any) {
             const int b = __ffs(any) - 1;
             any &= any - 1;
-            if (up[i] >> b & 1)
-                out[n_up++ + min(n_eq, left)] = (tid * PER + i) * 32 + b;
-            else if (n_eq++ < left)
-                out[n_up + n_eq - 1] = (tid * PER + i) * 32 + b;
+            const bool is_up = up[i] >> b & 1;
+            if (is_up || n_eq < left) out[n_up + min(n_eq, left)] = lo + (tid * PER + i) * 32 + b;
+            n_up += is_up;
+            n_eq += !is_up;
         }
     }
 }
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_long_kernel(const Sel
         return;
     }
     const int lo = a.sink, hi = n - a.recent;
-    auto key_at = [&](int j) { return j < lo || j >= hi ? kStays : score_key(score[j]); };
+    auto key_at = [&](int j) { return j < lo || j >= hi ? kStays : min(score_key(score[j]), kStays - 1); };
     uint32_t prefix = 0;
     int left = a.budget;
     for (int shift = 24; shift >= 0; shift -= 8) {
