@@ -751,9 +751,9 @@ int kvp_page_select(const float *scores, int64_t score_stride, const int32_t *q_
  * query does not see or whose table entry is outside [0, NB), are passed
  * over; their order does not matter, and a page named twice counts twice.  A
  * row without keys gives out 0 and lse -inf.  q, out: bf16 [L][num_q][Hq][d];
- * lse: fp32 [L][num_q][Hq] or NULL.  A NaN among the keys and values that a
- * row sees shows in its results (they should be finite); other slots do not
- * matter, whatever they hold.  Sums and
+ * lse: fp32 [L][num_q][Hq] or NULL.  Keys and values that a row sees should be
+ * finite: a NaN among them shows in its results, an infinite value as an
+ * infinity or a NaN.  Other slots do not matter, whatever they hold.  Sums and
  * weights are held in 32 bits (a weight meets V as two bf16 parts), and
  * repeated calls give equal bits.
  */

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Scor
     // which query rows, which pages
     int r0, nr, seq;
     const int chunk = (int)(blockIdx.x % a.chunks);
-    if (!a.rows.tile<QT>(blockIdx.x / a.chunks, r0, nr, seq)) return;
+    if (!a.rows.tile(QT, blockIdx.x / a.chunks, r0, nr, seq)) return;
     const int last = a.rows.pages(seq, r0 + nr - 1);       // pages that the last row sees
     const int p_begin = chunk * kScorePages;
     if (p_begin >= last) return;

@@ -37,12 +37,11 @@ struct QueryRows {
         const int p = position(s, r);
         return p < 0 ? 0 : p / bs + 1;
     }
-    // Tile x of at most QT consecutive rows of one sequence: tiles start anew
+    // Tile x of at most qt consecutive rows of one sequence: tiles start anew
     // at every sequence's first row.  The tiles of sequence s begin at index
-    // start[s] / QT + s, so at most T / QT + S of them have rows.
-    template <int QT>
-    __device__ __forceinline__ bool tile(int x, int &r0, int &nr, int &s) const {
-        if (QT == 1 || !start) {
+    // start[s] / qt + s, so at most T / qt + S of them have rows.
+    __device__ __forceinline__ bool tile(int qt, int x, int &r0, int &nr, int &s) const {
+        if (qt == 1 || !start) {
             r0 = x;
             nr = 1;
             s = sequence(x);
@@ -51,12 +50,12 @@ struct QueryRows {
         int lo = 0, hi = S - 1;       // the last s whose tiles begin at or before x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (start[mid] / QT + mid <= x) lo = mid; else hi = mid - 1;
+            if (start[mid] / qt + mid <= x) lo = mid; else hi = mid - 1;
         }
         s = lo;
-        r0 = start[s] + (x - (start[s] / QT + s)) * QT;
+        r0 = start[s] + (x - (start[s] / qt + s)) * qt;
         const int end = min(start[s + 1], T);
-        nr = min(QT, end - r0);
+        nr = min(qt, end - r0);
         return r0 >= 0 && nr > 0;
     }
     static int64_t tiles(int64_t rows, int64_t seqs, int qt) { return rows / qt + seqs; }

@@ -248,9 +248,11 @@ def check_sparse(b, sel, scale=None, lse=True):
     # a score of magnitude 8 in fp32 and the exponential's argument are off by
     # at most 2^-18 or so, which doubles in a normalised weight: 2^-12 of sum p
     # |v| leaves room
-    # (a NaN that a row sees shows everywhere in it)
-    assert np.array_equal(np.isnan(got), np.isnan(want))
-    ok = ~np.isnan(want)
+    # (a NaN that a row sees shows in it.  An infinite value meets the weight's
+    # two parts one by one: the second is 0 or of either sign, 0 * inf is NaN and
+    # inf - inf too, so that the result is an infinity or a NaN)
+    assert np.array_equal(np.isfinite(got), np.isfinite(want)) and np.isnan(got)[np.isnan(want)].all()
+    ok = np.isfinite(want)
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * mag)[ok].all()
     if lse:
         g = ls.double().cpu().numpy()
@@ -408,3 +410,75 @@ def test_wrong_tensors_are_refused():
                 dict(l=torch.empty(1, 2, 4, device="cuda"))):
         with pytest.raises(ValueError):
             call(**bad)
+
+
+CHUNKS = [((8, 2), 64, 16, [300, 350], [280, 260]), ((8, 2), 128, 32, [1000, 9], [306, 3]),
+          ((8, 1), 128, 16, [700], [650]), ((16, 4), 64, 16, [90, 400], [90, 88]), ((4, 4), 64, 16, [2000], [640]),
+          ((6, 2), 128, 16, [500], [480]), ((5, 1), 64, 64, [950], [930]), ((16, 8), 128, 16, [340, 60, 200], [300, 1, 77])]
+
+
+def like_neighbours(b, budget, seed=1):
+    """Every 13 rows choose from one set of pages, with the newest and a few of
+    their own; ascending as kvp_page_select leaves them."""
+    g = np.random.default_rng(seed)
+    sel = np.full((b.L, b.T, b.Hkv, budget), -1, np.int32)
+    for l, h in np.ndindex(b.L, b.Hkv):
+        for t in range(b.T):
+            n = b.seen(t)
+            if t % 13 == 0 or b.rows[t][0] != b.rows[t - 1][0]:
+                common = g.permutation(n)[:budget]
+            pick = np.unique(np.concatenate([common, [n - 1], g.integers(0, n, 3)]))
+            pick = g.permutation(pick)[:min(budget, n)]
+            sel[l, t, h, :len(pick)] = np.sort(pick)
+    return sel
+
+
+@pytest.mark.parametrize("heads,d,bs,lens,q_lens", CHUNKS)
+def test_chunks(heads, d, bs, lens, q_lens):
+    b = Batch(lens, q_lens, heads, d, bs, L=2, seed=20)
+    x = check_sparse(b, like_neighbours(b, 9))
+    y = check_sparse(b, like_neighbours(b, 9))
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    check_sparse(b, some_pages(b, 7))           # no order, nothing in common, entries of -1
+
+
+@pytest.mark.parametrize("heads,d,bs,lens,q_lens", CHUNKS[:3])
+def test_chunks_with_a_page_twice(heads, d, bs, lens, q_lens):
+    b = Batch(lens, q_lens, heads, d, bs, L=2, seed=21)
+    sel = like_neighbours(b, 9)
+    sel[:, 5, 0, 3] = sel[:, 5, 0, 2]
+    sel[1, 40] = 0                              # nine times
+    sel[0, 50] = -1                             # none at all
+    sel[0, 51, 0] = [-3, 2 ** 31 - 1, -2 ** 31, 5000, 20000, -1, 16384, 1 << 24, 0]
+    check_sparse(b, sel)
+
+
+def test_chunks_with_values_that_some_rows_do_not_see():
+    b = Batch([400], [380], (8, 2), 64, 16, L=2, seed=22, poison=False)
+    sel = like_neighbours(b, 6)
+    for l in range(2):
+        sel[l, 100:200, 0] = np.array([0, 1, 2, 3, 4, -1])
+        sel[l, 120, 0] = [0, 1, 2, 3, 5, -1]    # one row alone names page 5, which holds a NaN
+        sel[l, 150:153, 0, 4] = -1
+    b.v[:, int(b.tables[0, 5]), 0, 3, 7] = math.nan
+    b.k[:, int(b.tables[0, 4]), 0, 1, 1] = math.nan
+    b.v[0, int(b.tables[0, 4]), 0, 2] = math.inf
+    sel[:, 300:, 0] = np.array([0, 1, 2, 3, 19, 20])
+    b.v[:, int(b.tables[0, 20]), 0, 5] = -math.inf      # token 325: seen from row 305 on
+    check_sparse(b, sel)
+
+
+def test_chunks_of_padded_rows_and_short_sequences():
+    # more queries than tokens: the first rows have no position
+    b = Batch([400, 10], [300, 40], (8, 2), 64, 16, L=2, seed=23)
+    q = torch.cat([b.q, b.q[:, :9]], 1).contiguous()
+    sel = np.zeros((2, 349, 2, 3), np.int32)
+    sel[..., 1], sel[..., 2] = 2, -1
+    out = torch.full_like(q, 5.0)
+    lse = torch.full((2, 349, 8), 5.0, device="cuda")
+    kvp.paged_sparse_attention(q, b.start, b.k, b.v, b.t, b.n, torch.from_numpy(sel).cuda(), b.desc, out, lse)
+    assert bool((out[:, 340:] == 5.0).all()) and bool((lse[:, 340:] == 5.0).all())
+    assert bool((out[:, 300:330] == 0).all()) and bool((lse[:, 300:330] == -math.inf).all())
+    want, wl, mag = sparse_want(b, sel[:, :340])
+    got = out[:, :340].double().cpu().numpy()
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * mag).all()
