@@ -33,6 +33,7 @@
 
 #include "../../include/kvp.h"
 #include "kvp_internal.h"
+#include "launch.cuh"
 
 namespace kvp {
 namespace {
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
     __shared__ float s_bestv[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
+    griddep_wait();
     if (a.early) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (a.finished && a.finished[row]) return;
     const int x0 = chunk * kChunk, len = min(kChunk, a.vocab - x0);
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     __shared__ Entry s_best[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = blockIdx.x;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    griddep_wait();
     const int per_beam = a.chunks * a.n, total = per_beam * a.beams;
     const float *cand = a.cand + (int64_t)g * total;
     const int32_t *cand_at = a.cand_at + (int64_t)g * total;
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kCopyThreads)
                          int64_t tiles) {
     const int64_t row = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int64_t o = row / n_dst;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    griddep_wait();
     const int from = index[row % n_dst];
     if ((unsigned)from >= (unsigned)n_src) return;
     const V *s = src + (o * n_src + from) * chunks;
@@ -501,29 +503,12 @@ __global__ void __launch_bounds__(kCopyThreads)
         if (x0 + u * kCopyThreads < chunks) d[x0 + u * kCopyThreads] = v[u];
 }
 
-// A kernel that starts (and then waits) as the one before it ends.
-template <class... P, class... A>
-cudaError_t launch_behind(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-    count_launch();
-    return e;
-}
-
 template <class V>
 cudaError_t launch_reorder(const void *src, void *dst, const int32_t *index, int64_t outer, int32_t n_src, int32_t n_dst,
                            int64_t row_bytes, cudaStream_t stream) {
     const int64_t chunks = row_bytes / sizeof(V), tiles = (chunks + kCopyThreads * kInFlight - 1) / (kCopyThreads * kInFlight);
     if (tiles > INT32_MAX || outer * n_dst > INT32_MAX / tiles) return cudaErrorInvalidValue;
-    return launch_behind(state_reorder_kernel<V>, outer * n_dst * tiles, kCopyThreads, stream, static_cast<const V *>(src),
+    return launch_behind(state_reorder_kernel<V>, dim3((unsigned)(outer * n_dst * tiles)), kCopyThreads, 0, 1, stream, static_cast<const V *>(src),
                          static_cast<V *>(dst), index, n_src, n_dst, chunks, tiles);
 }
 
@@ -545,11 +530,10 @@ cudaError_t launch_beam(BeamArgs a, cudaStream_t stream) {
     a.div = per_beam > 1 && per_beam * per_beam * a.beams < (INT64_C(1) << 32)
                 ? (uint32_t)(((INT64_C(1) << 32) + per_beam - 1) / per_beam)
                 : 0;
-    beam_part_kernel<T><<<(unsigned)(a.groups * a.beams * a.chunks), kThreads, 0, stream>>>(a);
-    count_launch();
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_behind(beam_part_kernel<T>, dim3((unsigned)(a.groups * a.beams * a.chunks)), kThreads, 0, 1, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_behind(beam_join_kernel, a.groups, kThreads, stream, a);
+    return launch_behind(beam_join_kernel, dim3((unsigned)a.groups), kThreads, 0, 1, stream, a);
 }
 
 }  // namespace

@@ -18,9 +18,11 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/kvp.h"
 #include "kvp_internal.h"
+#include "launch.cuh"
 #include "query_rows.cuh"
 
 namespace kvp {
@@ -62,6 +64,7 @@ __device__ __forceinline__ uint4 pick_across(uint4 a, int step) {
 template <int D>
 __global__ void __launch_bounds__(32 * kBoundWarps) page_bounds_kernel(const BoundsArgs a) {
     constexpr int CH = D / 8, RPI = 32 / CH;     // chunks per row, rows per instruction
+    griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = blockIdx.y;
     const int64_t unit = (int64_t)blockIdx.x * kBoundWarps + warp;      // page-major over (layer, kv head)
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(32 * kBoundWarps) page_bounds_kernel(const Bou
 // ------------------------------------------------------------------ scores
 
 constexpr int kScoreWarps = 4;
-constexpr int kScoreSteps = 2;      // groups of 16 pages per warp
+constexpr int kScoreSteps = 4;      // groups of 16 pages per warp
 constexpr int kScorePages = 16 * kScoreWarps * kScoreSteps;
 
 struct ScoreArgs {
@@ -155,6 +158,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Scor
     __shared__ __align__(16) __nv_bfloat16 s_part[3 * QT][ROW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int lh = blockIdx.y, l = lh / a.Hkv, h = lh % a.Hkv;
+    griddep_wait();
     // which query rows, which pages
     int r0, nr, seq;
     const int chunk = (int)(blockIdx.x % a.chunks);
@@ -162,43 +166,70 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Scor
     const int last = a.rows.pages(seq, r0 + nr - 1);       // pages that the last row sees
     const int p_begin = chunk * kScorePages;
     if (p_begin >= last) return;
-    for (int i = threadIdx.x; i < QT * D; i += blockDim.x) {
-        const int r = i / D, e = i % D;
-        float neg = 0.f, pos = 0.f;
+    // the warp's first pages and their bounds while the queries come in
+    const int32_t *table = a.rows.tables + (int64_t)seq * a.rows.MB;
+    int ba, bb;              // blocks of pages p0 + g and p0 + g + 8
+    auto find = [&](int p0) {
+        ba = p0 + g < last ? table[p0 + g] : -1;
+        bb = p0 + g + 8 < last ? table[p0 + g + 8] : -1;
+    };
+    int p0 = p_begin + warp * 16;
+    find(p0);
+    uint4 va[C], vb[C];
+    auto fetch = [&]() {
+        const bool oka = (unsigned)ba < (unsigned)a.NB, okb = (unsigned)bb < (unsigned)a.NB;
+        const uint4 *xa = a.bounds + (((int64_t)l * a.NB + (oka ? ba : 0)) * a.Hkv + h) * (K / 8) + t;
+        const uint4 *xb = a.bounds + (((int64_t)l * a.NB + (okb ? bb : 0)) * a.Hkv + h) * (K / 8) + t;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            va[c] = oka ? __ldg(xa + 4 * c) : make_uint4(0, 0, 0, 0);
+            vb[c] = okb ? __ldg(xb + 4 * c) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    fetch();
+    // E dims of a row per thread: one, so that all threads have work, or eight
+    constexpr int E = QT == 1 ? 1 : 8, U = 4;         // heads in flight
+    using Dims = typename std::conditional<QT == 1, unsigned short, uint4>::type;
+    for (int i = threadIdx.x; i < QT * D / E; i += blockDim.x) {
+        const int r = i / (D / E), e0 = i % (D / E) * E;
+        float neg[E] = {}, pos[E] = {};
         if (r < nr) {
-            const __nv_bfloat16 *q = a.q + (((int64_t)l * a.rows.T + r0 + r) * a.Hq + h * a.G) * D + e;
-            for (int x = 0; x < a.G; ++x) {
-                const float v = __bfloat162float(q[(int64_t)x * D]);
-                // (a NaN goes into both)
-                neg += v > 0.f ? 0.f : v;
-                pos += v < 0.f ? 0.f : v;
+            const __nv_bfloat16 *q = a.q + (((int64_t)l * a.rows.T + r0 + r) * a.Hq + h * a.G) * D + e0;
+            for (int x = 0; x < a.G; x += U) {
+                Dims v[U];
+#pragma unroll
+                for (int y = 0; y < U; ++y)
+                    v[y] = x + y < a.G ? *reinterpret_cast<const Dims *>(q + (int64_t)(x + y) * D) : Dims();
+#pragma unroll
+                for (int y = 0; y < U; ++y)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float f = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(&v[y])[e]);
+                        neg[e] += f > 0.f ? 0.f : f;      // (a NaN goes into both)
+                        pos[e] += f < 0.f ? 0.f : f;
+                    }
             }
         }
-        split3(neg, s_part[r][e], s_part[QT + r][e], s_part[2 * QT + r][e]);
-        split3(pos, s_part[r][D + e], s_part[QT + r][D + e], s_part[2 * QT + r][D + e]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            split3(neg[e], s_part[r][e0 + e], s_part[QT + r][e0 + e], s_part[2 * QT + r][e0 + e]);
+            split3(pos[e], s_part[r][D + e0 + e], s_part[QT + r][D + e0 + e], s_part[2 * QT + r][D + e0 + e]);
+        }
     }
     __syncthreads();
-    const int32_t *table = a.rows.tables + (int64_t)seq * a.rows.MB;
     uint4 b1[QT == 1 ? C : 1];
     if constexpr (QT == 1) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
             b1[c] = g < 3 ? *reinterpret_cast<const uint4 *>(&s_part[g < 3 ? g : 0][32 * c + 8 * t]) : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll 1
     for (int step = 0; step < kScoreSteps; ++step) {
-        const int p0 = p_begin + (step * kScoreWarps + warp) * 16;
         if (p0 >= last) return;
         const int pa = p0 + g, pb = pa + 8;
-        const int ba = pa < last ? table[pa] : -1, bb = pb < last ? table[pb] : -1;
         const bool oka = (unsigned)ba < (unsigned)a.NB, okb = (unsigned)bb < (unsigned)a.NB;
-        const uint4 *xa = a.bounds + (((int64_t)l * a.NB + (oka ? ba : 0)) * a.Hkv + h) * (K / 8) + t;
-        const uint4 *xb = a.bounds + (((int64_t)l * a.NB + (okb ? bb : 0)) * a.Hkv + h) * (K / 8) + t;
-        uint4 va[C], vb[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            va[c] = oka ? xa[4 * c] : make_uint4(0, 0, 0, 0);
-            vb[c] = okb ? xb[4 * c] : make_uint4(0, 0, 0, 0);
-        }
+        p0 += 16 * kScoreWarps;
+        if (step + 1 < kScoreSteps) find(p0);
         float acc[NT][4] = {};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -232,6 +263,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Scor
                 if (pb < seen) out[pb] = okb ? (acc[0][2 + e] + (acc[1][2 + e] + acc[2][2 + e])) * a.scale : -INFINITY;
             }
         }
+        if (step + 1 < kScoreSteps) fetch();
     }
 }
 
@@ -291,6 +323,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
     __shared__ int s_above;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x;
+    griddep_wait();
     const int r = (int)(row / a.Hkv % a.rows.T);
     const int seq = a.rows.sequence(r);
     if (seq < 0) return;
@@ -471,6 +504,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_long_kernel(const Sel
     __shared__ int s_digit, s_left;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x;
+    griddep_wait();
     const int r = (int)(row / a.Hkv % a.rows.T);
     const int seq = a.rows.sequence(r);
     if (seq < 0) return;
@@ -565,12 +599,12 @@ int kvp_page_bounds(const void *k_pool, const int32_t *block_tables, const int32
     const int64_t grid = ((int64_t)a.pages * a.L * a.Hkv + kBoundWarps - 1) / kBoundWarps;
     if (grid > INT32_MAX) return KVP_ERR_INVALID;
     const dim3 g((unsigned)grid, (unsigned)num_seqs);
+    cudaError_t e;
     if (desc->head_dim == 64)
-        page_bounds_kernel<64><<<g, 32 * kBoundWarps, 0, (cudaStream_t)stream>>>(a);
+        e = launch_behind(page_bounds_kernel<64>, g, 32 * kBoundWarps, 0, 1, (cudaStream_t)stream, a);
     else
-        page_bounds_kernel<128><<<g, 32 * kBoundWarps, 0, (cudaStream_t)stream>>>(a);
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+        e = launch_behind(page_bounds_kernel<128>, g, 32 * kBoundWarps, 0, 1, (cudaStream_t)stream, a);
+    return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 int kvp_page_scores(const void *q, const int32_t *q_start, int32_t num_q, const void *bounds,
@@ -597,19 +631,19 @@ int kvp_page_scores(const void *q, const int32_t *q_start, int32_t num_q, const 
     const dim3 g((unsigned)(tiles * a.chunks), (unsigned)(a.L * a.Hkv));
     cudaStream_t st = (cudaStream_t)stream;
     const int threads = 32 * kScoreWarps;
+    cudaError_t e;
     if (desc->head_dim == 64) {
         if (q_start)
-            page_score_kernel<64, 8><<<g, threads, 0, st>>>(a);
+            e = launch_behind(page_score_kernel<64, 8>, g, threads, 0, 1, st, a);
         else
-            page_score_kernel<64, 1><<<g, threads, 0, st>>>(a);
+            e = launch_behind(page_score_kernel<64, 1>, g, threads, 0, 1, st, a);
     } else {
         if (q_start)
-            page_score_kernel<128, 8><<<g, threads, 0, st>>>(a);
+            e = launch_behind(page_score_kernel<128, 8>, g, threads, 0, 1, st, a);
         else
-            page_score_kernel<128, 1><<<g, threads, 0, st>>>(a);
+            e = launch_behind(page_score_kernel<128, 1>, g, threads, 0, 1, st, a);
     }
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+    return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 int kvp_page_select(const float *scores, int64_t score_stride, const int32_t *q_start, int32_t num_q,
@@ -632,24 +666,24 @@ int kvp_page_select(const float *scores, int64_t score_stride, const int32_t *q_
     a.Hkv = desc->num_kv_heads; a.budget = budget; a.sink = n_sink; a.recent = n_recent;
     // the smallest kernel whose registers hold the longest row that the tables
     // allow; 1024 threads for rows that 256 do not hold
-    const unsigned ctas = (unsigned)grid;
+    const dim3 ctas((unsigned)grid);
+    cudaError_t e;
     cudaStream_t st = (cudaStream_t)stream;
     if (max_blocks <= 256)
-        page_select_kernel<4, 2><<<ctas, 128, 0, st>>>(a);
+        e = launch_behind(page_select_kernel<4, 2>, ctas, 128, 0, 1, st, a);
     else if (max_blocks <= 1024)
-        page_select_kernel<4, 8><<<ctas, 128, 0, st>>>(a);
+        e = launch_behind(page_select_kernel<4, 8>, ctas, 128, 0, 1, st, a);
     else if (max_blocks <= 2048)
-        page_select_kernel<8, 8><<<ctas, 256, 0, st>>>(a);
+        e = launch_behind(page_select_kernel<8, 8>, ctas, 256, 0, 1, st, a);
     else if (max_blocks <= 4096)
-        page_select_kernel<8, 16><<<ctas, 256, 0, st>>>(a);
+        e = launch_behind(page_select_kernel<8, 16>, ctas, 256, 0, 1, st, a);
     else if (max_blocks <= 8192)
-        page_select_kernel<8, 32><<<ctas, 256, 0, st>>>(a);
+        e = launch_behind(page_select_kernel<8, 32>, ctas, 256, 0, 1, st, a);
     else if (max_blocks <= 32768)
-        page_select_kernel<32, 32><<<ctas, 1024, 0, st>>>(a);
+        e = launch_behind(page_select_kernel<32, 32>, ctas, 1024, 0, 1, st, a);
     else
-        page_select_long_kernel<<<ctas, kSelThreads, 0, st>>>(a);
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+        e = launch_behind(page_select_long_kernel, ctas, kSelThreads, 0, 1, st, a);
+    return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 }  // extern "C"

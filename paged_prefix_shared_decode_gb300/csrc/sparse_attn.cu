@@ -27,6 +27,7 @@
 
 #include "../../include/kvp.h"
 #include "kvp_internal.h"
+#include "launch.cuh"
 #include "query_rows.cuh"
 
 namespace kvp {
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) sparse_attn_kern
     Partial<D, NT> *part = reinterpret_cast<Partial<D, NT> *>(smem);
     __shared__ int32_t s_page[kList], s_blk[kList];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    griddep_wait();
     const int rank = blockIdx.x % a.ctas;
     int64_t unit = blockIdx.x / a.ctas;
     const int slice = (int)(unit % a.parts);
@@ -389,6 +391,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) sparse_tile_kernel(const Spars
     int32_t *s_page = s_blk + kTileList;                                 // page << 8 | rows
     __shared__ int s_scan[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    griddep_wait();
     const int h = blockIdx.y % a.Hkv, l = blockIdx.y / a.Hkv;
     int r0, nr, seq;
     if (!a.rows.tile(a.qt, blockIdx.x, r0, nr, seq)) return;
@@ -546,28 +549,15 @@ cudaError_t launch_sparse(SparseArgs a, cudaStream_t stream) {
     while (a.ctas < kMaxCtas && units * a.ctas * 2 <= 2LL * device_sm_count() && tiles >= 2LL * kWarps * a.ctas * 2)
         a.ctas *= 2;
     if (units * a.ctas > INT32_MAX) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(units * a.ctas));
-    cfg.blockDim = dim3(32 * kWarps);
-    cfg.dynamicSmemBytes = sizeof(Partial<D, NT>) * kWarps;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, sparse_attn_kernel<D, NT>, a);
-    count_launch();
-    return e;
+    return launch_behind(sparse_attn_kernel<D, NT>, dim3((unsigned)(units * a.ctas)), 32 * kWarps,
+                         sizeof(Partial<D, NT>) * kWarps, a.ctas, stream, a);
 }
 
 template <int D, int NT>
 cudaError_t launch_tile(const SparseArgs &a, int64_t tiles, cudaStream_t stream) {
     const size_t bytes = std::max<size_t>(sizeof(Partial<D, NT>) * kWarps, kTileBytes);
-    sparse_tile_kernel<D, NT><<<dim3((unsigned)tiles, (unsigned)(a.L * a.Hkv)), 32 * kWarps, bytes, stream>>>(a);
-    count_launch();
-    return cudaGetLastError();
+    return launch_behind(sparse_tile_kernel<D, NT>, dim3((unsigned)tiles, (unsigned)(a.L * a.Hkv)), 32 * kWarps, bytes, 1,
+                         stream, a);
 }
 
 template <int D>
