@@ -10,6 +10,7 @@ is missing.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -619,7 +620,7 @@ def _batch_i32(name, a, n):
 def _torch():
     """torch and the current device (0 before CUDA is in use: no tensor is on it)."""
     import torch
-    return torch, torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    return torch, torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
 def _pool_shape(d: AttnDesc):
@@ -764,32 +765,62 @@ def rope_desc(rot_dim: int, base: float = 10000.0, freqs=None, interleaved: bool
     return d
 
 
+def _i32s(a):
+    """A host int32 array of a list or array, its address and length."""
+    if type(a) is list:
+        a = array.array("i", a)
+        at, n = a.buffer_info()
+        return a, at, n
+    a = np.ascontiguousarray(a, dtype=np.int32)
+    if a.ndim != 1:
+        raise ValueError(f"expected one dimension, got shape {a.shape}")
+    return a, a.ctypes.data, len(a)
+
+
+def _here(stream):
+    """torch, the current device (0 before CUDA is in use: no tensor is on it)
+    and the stream's handle."""
+    torch, dev = _torch()
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch, dev, raw(dev) if raw else _stream(None)
+    return torch, dev, stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def seq_append_rope(pool, seqs, ntoks, k, v, rope: RopeDesc, positions=None, q=None, q_out=None, stream=None):
     """seq_append_batch with k rotated into the pages, and q [L][T][Hq][d]
     into q_out (q itself or apart).  k, v [L][T][Hkv][d] bf16, T = sum of
     ntoks; positions: device int32 [T], or None (the cache's)."""
-    s, sp = _host_i32(seqs)
-    n, np_ = _batch_i32("ntoks", ntoks, len(s))
-    torch, dev = _torch()
-    layers, heads = kvp_pool_shape(pool)
-    T, bf16 = sum(n.tolist()), torch.bfloat16
-    hq = 0
-    if k is not None and not isinstance(k, int):
+    s, sp, ns = _i32s(seqs)
+    n, np_, nn = _i32s(ntoks)
+    if nn != ns:
+        raise ValueError(f"ntoks: expected {ns} entries, got {nn}")
+    torch, dev, st = _here(stream)
+    bf16, T, hq = torch.bfloat16, sum(n.tolist()), 0
+    if T:
+        layers, heads = kvp_pool_shape(pool)
         d = k.shape[-1]
-        k, v = (_arg(nm, x, bf16, (layers, T, heads, d), dev) for nm, x in (("k", k), ("v", v)))
+        shape = (layers, T, heads, d)
+        k, v = _arg("k", k, bf16, shape, dev), _arg("v", v, bf16, shape, dev)
         if q is not None:
             hq = q.shape[-2]
-            q, q_out = (_arg(nm, x, bf16, (layers, T, hq, d), dev) for nm, x in (("q", q), ("q_out", q_out)))
-    _check(load().seq_append_rope(pool, len(s), sp, np_, k, v, ctypes.byref(rope),
-                                  _arg("positions", positions, torch.int32, (T,), dev), q, q_out, hq,
-                                  _stream(stream)), "seq_append_rope")
+            shape = (layers, T, hq, d)
+            q, q_out = _arg("q", q, bf16, shape, dev), _arg("q_out", q_out, bf16, shape, dev)
+        if positions is not None:
+            positions = _arg("positions", positions, torch.int32, (T,), dev)
+    else:
+        k = v = q = q_out = positions = None
+    _check(load().seq_append_rope(pool, ns, sp, np_, k, v, ctypes.byref(rope), positions, q, q_out, hq, st),
+           "seq_append_rope")
 
 
 def seq_reorder(pool, dst, src):
     """Sequence dst[i] becomes a fork of what sequence src[i] was."""
-    d, dp = _host_i32(dst)
-    s, sp = _batch_i32("src", src, len(d))
-    _check(load().seq_reorder(pool, dp, sp, len(d)), "seq_reorder")
+    d, dp, nd = _i32s(dst)
+    s, sp, ns = _i32s(src)
+    if nd != ns:
+        raise ValueError(f"src: expected {nd} entries, got {ns}")
+    _check(load().seq_reorder(pool, dp, sp, nd), "seq_reorder")
 
 
 def _batch(desc, block_tables, seq_lens, q_start, torch, dev):
@@ -800,18 +831,18 @@ def _batch(desc, block_tables, seq_lens, q_start, torch, dev):
         mb = block_tables.shape[-1]
         block_tables = _arg("block_tables", block_tables, i32, (S, mb), dev)
     return (S, mb, block_tables, _arg("seq_lens", seq_lens, i32, (S,), dev),
-            _arg("q_start", q_start, i32, (S + 1,), dev))
+            None if q_start is None else _arg("q_start", q_start, i32, (S + 1,), dev))
 
 
 def kvp_page_bounds(k_pool, block_tables, seq_lens, n_new: int, desc: AttnDesc, bounds, stream=None):
     """Smallest and largest key per dim of the pages that hold one of the last
     n_new tokens of a sequence, into bounds [L][NB][Hkv][2][d] bf16.
     block_tables [S][MB], seq_lens [S]: device int32."""
-    torch, dev = _torch()
+    torch, dev, st = _here(stream)
     S, mb, tp, lp, _ = _batch(desc, block_tables, seq_lens, None, torch, dev)
     bf16, shape = torch.bfloat16, (desc.num_layers, desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim)
     _check(load().kvp_page_bounds(_arg("k_pool", k_pool, bf16, _pool_shape(desc), dev), tp, lp, S, mb, n_new,
-                                  ctypes.byref(desc), _arg("bounds", bounds, bf16, shape, dev), _stream(stream)),
+                                  ctypes.byref(desc), _arg("bounds", bounds, bf16, shape, dev), st),
            "kvp_page_bounds")
 
 
@@ -819,7 +850,7 @@ def kvp_page_scores(q, q_start, bounds, block_tables, seq_lens, desc: AttnDesc, 
     """Scores [L][T][Hkv][stride] fp32 of the pages that each query row of q
     [L][T][Hq][d] sees; q_start: device int32 [S + 1], or None (one row a
     sequence)."""
-    torch, dev = _torch()
+    torch, dev, st = _here(stream)
     S, mb, tp, lp, sp = _batch(desc, block_tables, seq_lens, q_start, torch, dev)
     L, T, heads, d = desc.num_layers, q.shape[1], desc.num_kv_heads, desc.head_dim
     stride = scores.shape[-1]
@@ -827,7 +858,7 @@ def kvp_page_scores(q, q_start, bounds, block_tables, seq_lens, desc: AttnDesc, 
                                   _arg("bounds", bounds, torch.bfloat16, (L, desc.num_blocks, heads, 2, d), dev), tp,
                                   lp, S, mb, ctypes.byref(desc),
                                   _arg("scores", scores, torch.float32, (L, T, heads, stride), dev), stride,
-                                  _stream(stream)), "kvp_page_scores")
+                                  st), "kvp_page_scores")
 
 
 def kvp_page_select(scores, q_start, seq_lens, desc: AttnDesc, n_sink: int, n_recent: int, selected, max_blocks=None,
@@ -835,21 +866,21 @@ def kvp_page_select(scores, q_start, seq_lens, desc: AttnDesc, n_sink: int, n_re
     """The best selected.shape[-1] pages of each row of scores
     [L][T][Hkv][stride] into selected [L][T][Hkv][budget] int32, ascending;
     max_blocks (None: as long as the scores' rows): the tables' width."""
-    torch, dev = _torch()
+    torch, dev, st = _here(stream)
     S, _, _, lp, sp = _batch(desc, None, seq_lens, q_start, torch, dev)
     L, T, heads = desc.num_layers, scores.shape[1], desc.num_kv_heads
     stride, budget = scores.shape[-1], selected.shape[-1]
     _check(load().kvp_page_select(_arg("scores", scores, torch.float32, (L, T, heads, stride), dev), stride, sp, T, lp,
                                   S, stride if max_blocks is None else max_blocks, ctypes.byref(desc), budget, n_sink,
                                   n_recent, _arg("selected", selected, torch.int32, (L, T, heads, budget), dev),
-                                  _stream(stream)), "kvp_page_select")
+                                  st), "kvp_page_select")
 
 
 def paged_sparse_attention(q, q_start, k_pool, v_pool, block_tables, seq_lens, selected, desc: AttnDesc, out, lse,
                            stream=None):
     """Attention of each query row over its selected [L][T][Hkv][budget]
     pages; out like q [L][T][Hq][d] bf16, lse [L][T][Hq] fp32 or None."""
-    torch, dev = _torch()
+    torch, dev, st = _here(stream)
     S, mb, tp, lp, sp = _batch(desc, block_tables, seq_lens, q_start, torch, dev)
     T, budget, bf16 = q.shape[1], selected.shape[-1], torch.bfloat16
     rows = (desc.num_layers, T, desc.num_q_heads)
@@ -859,7 +890,7 @@ def paged_sparse_attention(q, q_start, k_pool, v_pool, block_tables, seq_lens, s
                                          _arg("selected", selected, torch.int32,
                                               (desc.num_layers, T, desc.num_kv_heads, budget), dev), budget,
                                          ctypes.byref(desc), _arg("out", out, bf16, wide, dev),
-                                         _arg("lse", lse, torch.float32, rows, dev), _stream(stream)),
+                                         _arg("lse", lse, torch.float32, rows, dev), st),
            "paged_sparse_attention")
 
 
@@ -876,7 +907,7 @@ def kvp_beam_select(logits, scores, finished, pad_token: int, out_scores, out_ro
     bf16 or fp16 (last dimension contiguous, rows evenly spaced), scores [G][B]
     fp32, finished [G][B] bool or uint8 (or None); out_scores fp32, out_rows
     and out_tokens int32 [G][n]."""
-    torch, dev = _torch()
+    torch, dev, st = _here(stream)
     G, B, V = logits.shape
     types = {torch.float32: KVP_F32, torch.bfloat16: KVP_BF16, torch.float16: KVP_F16}
     if logits.dtype not in types or logits.get_device() != dev:
@@ -895,13 +926,13 @@ def kvp_beam_select(logits, scores, finished, pad_token: int, out_scores, out_ro
                                   _arg("out_scores", out_scores, torch.float32, (G, n), dev),
                                   _arg("out_rows", out_rows, i32, (G, n), dev),
                                   _arg("out_tokens", out_tokens, i32, (G, n), dev), _dev(workspace),
-                                  _ws_bytes(workspace, ws_bytes), _stream(stream)), "kvp_beam_select")
+                                  _ws_bytes(workspace, ws_bytes), st), "kvp_beam_select")
 
 
 def kvp_state_reorder(src, dst, index, dim: int = 0, stream=None):
     """dst row i = src row index[i] along dimension `dim` (the ones before it
     are outer); index: device int32, as many as dst has rows, in any shape."""
-    torch, dev = _torch()
+    torch, dev, st = _here(stream)
     outer, inner = src.shape[:dim], src.shape[dim + 1:]
     n_src, n_dst = src.shape[dim], dst.shape[dim]
     if index.numel() != n_dst:
@@ -910,7 +941,7 @@ def kvp_state_reorder(src, dst, index, dim: int = 0, stream=None):
     _check(load().kvp_state_reorder(_arg("src", src, src.dtype, src.shape, dev),
                                     _arg("dst", dst, src.dtype, (*outer, n_dst, *inner), dev),
                                     _arg("index", index, torch.int32, index.shape, dev), math.prod(outer), n_src, n_dst,
-                                    math.prod(inner) * size, _stream(stream)), "kvp_state_reorder")
+                                    math.prod(inner) * size, st), "kvp_state_reorder")
 
 
 def kvp_device_error(workspace, stream=None) -> int:

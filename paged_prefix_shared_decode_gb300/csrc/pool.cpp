@@ -21,7 +21,6 @@
 #include <cstring>
 #include <new>
 #include <set>
-#include <unordered_map>
 #include <vector>
 
 #include "../../include/kvp.h"
@@ -43,6 +42,20 @@ struct kvp_pool {
     int64_t cow_count = 0;
     // scratch reused by appends and exports
     std::vector<int32_t> slots, cow, stage;
+    // which sequences and blocks a batch has met: marks of the current batch
+    // (an ordered set and a map cost 8 us for 64 sequences, these under 1)
+    std::vector<uint32_t> seq_mark, block_mark;
+    std::vector<int32_t> block_drops;
+    uint32_t mark = 0;
+
+    uint32_t new_mark() {
+        if (++mark == 0) {               // wrapped: old marks could be met again
+            std::fill(seq_mark.begin(), seq_mark.end(), 0u);
+            std::fill(block_mark.begin(), block_mark.end(), 0u);
+            mark = 1;
+        }
+        return mark;
+    }
 };
 
 namespace {
@@ -71,10 +84,10 @@ struct Need {
     int64_t fresh;
 };
 
-// Blocks an append of ntok tokens to s would take, given refcount drops
-// `dec` already implied by earlier appends of the same batch.
-Need blocks_needed(const kvp_pool *p, int32_t s, int32_t ntok,
-                   const std::unordered_map<int32_t, int32_t> *dec) {
+// Blocks an append of ntok tokens to s would take, given the refcount drops
+// already implied by earlier appends of the same batch (batch: its mark, 0: a
+// single append).
+Need blocks_needed(const kvp_pool *p, int32_t s, int32_t ntok, uint32_t batch) {
     const int32_t bs = p->desc.block_size;
     const auto &t = p->tables[s];
     const int64_t n = p->lens[s];
@@ -82,10 +95,7 @@ Need blocks_needed(const kvp_pool *p, int32_t s, int32_t ntok,
     if (ntok > 0 && n % bs != 0) {
         int32_t last = t.back();
         int32_t rc = p->ref[last];
-        if (dec) {
-            auto it = dec->find(last);
-            if (it != dec->end()) rc -= it->second;
-        }
+        if (batch && p->block_mark[last] == batch) rc -= p->block_drops[last];
         need.cow = rc > 1 ? 1 : 0;
     }
     need.fresh = (n + ntok + bs - 1) / bs - (int64_t)t.size();
@@ -118,10 +128,9 @@ void commit_append(kvp_pool *p, int32_t s, int32_t ntok, std::vector<int32_t> &s
     p->lens[s] = n + ntok;
 }
 
-int check_append(const kvp_pool *p, int32_t s, int32_t ntok,
-                 const std::unordered_map<int32_t, int32_t> *dec, Need *out) {
+int check_append(const kvp_pool *p, int32_t s, int32_t ntok, uint32_t batch, Need *out) {
     if (!is_live(p, s) || ntok < 0) return KVP_ERR_INVALID;
-    Need nd = blocks_needed(p, s, ntok, dec);
+    Need nd = blocks_needed(p, s, ntok, batch);
     if ((int64_t)p->tables[s].size() + nd.fresh > p->desc.max_blocks_per_seq) return KVP_ERR_INVALID;
     if ((int64_t)p->lens[s] + ntok > (int64_t)INT32_MAX / 2) return KVP_ERR_INVALID;
     *out = nd;
@@ -202,6 +211,9 @@ kvp_pool *new_pool(const kvp_pool_desc &d) {
     p->tables.resize(d.max_seqs);
     p->lens.assign(d.max_seqs, 0);
     p->live.assign(d.max_seqs, 0);
+    p->seq_mark.assign(d.max_seqs, 0);
+    p->block_mark.assign(d.num_blocks, 0);
+    p->block_drops.assign(d.num_blocks, 0);
     for (int32_t i = 0; i < d.max_seqs; ++i) p->free_ids.insert(i);
     return p;
 }
@@ -519,7 +531,7 @@ int seq_free(kvp_pool *p, int32_t seq) {
 int seq_reserve(kvp_pool *p, int32_t seq, int32_t ntok, int32_t *slots_out, int32_t *cow_out) {
     if (!p) return KVP_ERR_INVALID;
     Need nd{};
-    int rc = check_append(p, seq, ntok, nullptr, &nd);
+    int rc = check_append(p, seq, ntok, 0, &nd);
     if (rc) return rc;
     if (nd.cow + nd.fresh > (int64_t)p->free_.size()) return KVP_ERR_OOM;
     p->slots.clear();
@@ -541,7 +553,7 @@ int seq_append(kvp_pool *p, int32_t seq, const void *k, const void *v, int32_t n
     if (!p->k) return KVP_ERR_STATE;
     if (ntok > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return KVP_ERR_INVALID;
     Need nd{};
-    int rc = check_append(p, seq, ntok, nullptr, &nd);
+    int rc = check_append(p, seq, ntok, 0, &nd);
     if (rc) return rc;
     if (nd.cow + nd.fresh > (int64_t)p->free_.size()) return KVP_ERR_OOM;
     p->slots.clear();
@@ -571,13 +583,14 @@ int seq_append_rope(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32_
     if (!std::isfinite(rope->scale) || (!rope->freqs && !(std::isfinite(rope->base) && rope->base > 0)))
         return KVP_ERR_INVALID;
     const int32_t half = rope->rot_dim / 2;
+    const double log2_base = rope->freqs ? 0.0 : std::log2(rope->base);
     for (int32_t i = 0; i < half; ++i) {
-        const double f = rope->freqs ? rope->freqs[i] : std::pow(rope->base, -(double)i / half);
+        const double f = rope->freqs ? rope->freqs[i] : std::exp2(-(double)i / half * log2_base);
         if (!std::isfinite(f)) return KVP_ERR_INVALID;
-        // turns per position modulo 1, in units of 2^-64 (the conversion of
-        // 1 - 2^-54, the largest fraction a double has, stays below 2^64)
+        // turns per position modulo 1, in units of 2^-64 (a whole power of two:
+        // exact, and below 2^64 as the fraction is below 1)
         const double turns = f / 6.283185307179586476925, part = turns - std::floor(turns);
-        r.freq[i] = part < 1.0 ? (uint64_t)std::ldexp(part, 64) : 0;
+        r.freq[i] = part < 1.0 ? (uint64_t)(part * 18446744073709551616.0) : 0;
     }
     if ((q == nullptr) != (q_out == nullptr) || (q && (num_q_heads <= 0 || num_q_heads > 65536)))
         return KVP_ERR_INVALID;
@@ -620,27 +633,46 @@ int seq_append_rope(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32_
 
 int seq_reorder(kvp_pool *p, const int32_t *dst, const int32_t *src, int32_t n) try {
     if (!p || n < 0 || (n > 0 && (!dst || !src))) return KVP_ERR_INVALID;
-    std::vector<uint8_t> seen(p->desc.max_seqs, 0);
+    const uint32_t batch = p->new_mark();
     for (int32_t i = 0; i < n; ++i) {
-        if (!is_live(p, dst[i]) || !is_live(p, src[i]) || seen[dst[i]]) return KVP_ERR_INVALID;
-        seen[dst[i]] = 1;
+        if (!is_live(p, dst[i]) || !is_live(p, src[i]) || p->seq_mark[dst[i]] == batch) return KVP_ERR_INVALID;
+        p->seq_mark[dst[i]] = batch;
     }
-    // the new tables first: a src may be some dst too
-    std::vector<std::vector<int32_t>> tables(n);
-    std::vector<int32_t> lens(n);
+    // What a sequence and its new source have in common (a beam and its parent
+    // most of their tables) stays held as it is; the rest of every source is
+    // taken first, then the rest of every old table released, last to first.
+    // A source that is a destination too is copied while it is whole.
+    struct Move {
+        size_t keep;
+        int32_t len;
+        std::vector<int32_t> copy;
+    };
+    std::vector<Move> moves(n);
     for (int32_t i = 0; i < n; ++i) {
-        if (dst[i] == src[i]) continue;
-        tables[i] = p->tables[src[i]];
-        lens[i] = p->lens[src[i]];
+        const auto &from = p->tables[src[i]];
+        auto &to = p->tables[dst[i]];
+        Move &m = moves[i];
+        m.len = p->lens[src[i]];
+        m.keep = std::mismatch(to.begin(), to.begin() + std::min(to.size(), from.size()), from.begin()).first - to.begin();
+        if (p->seq_mark[src[i]] == batch) m.copy.assign(from.begin() + m.keep, from.end());
+        if (to.capacity() < from.size()) to.reserve(from.size());
     }
-    for (int32_t i = 0; i < n; ++i)
-        for (int32_t b : tables[i]) p->ref[b] += 1;
+    for (int32_t i = 0; i < n; ++i) {
+        const auto &from = p->tables[src[i]];
+        for (size_t j = moves[i].keep; j < from.size(); ++j) p->ref[from[j]] += 1;
+    }
     for (int32_t i = n - 1; i >= 0; --i) {
-        if (dst[i] == src[i]) continue;
-        auto &old = p->tables[dst[i]];
-        for (size_t j = old.size(); j-- > 0;) kvp::pool_drop_block(p, old[j]);
-        old.swap(tables[i]);
-        p->lens[dst[i]] = lens[i];
+        const Move &m = moves[i];
+        auto &to = p->tables[dst[i]];
+        for (size_t j = to.size(); j-- > m.keep;) kvp::pool_drop_block(p, to[j]);
+        to.resize(m.keep);
+        if (p->seq_mark[src[i]] == batch) {
+            to.insert(to.end(), m.copy.begin(), m.copy.end());
+        } else {
+            const auto &from = p->tables[src[i]];
+            to.insert(to.end(), from.begin() + m.keep, from.end());
+        }
+        p->lens[dst[i]] = m.len;
     }
     return KVP_OK;
 } catch (const std::bad_alloc &) {
@@ -761,15 +793,20 @@ int append_batch_check(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int
     if (total_out) *total_out = 0;
     if (!p || nseq < 0 || (nseq > 0 && (!seqs || !ntoks))) return KVP_ERR_INVALID;
     if (!p->k) return KVP_ERR_STATE;
-    std::unordered_map<int32_t, int32_t> dec;
-    std::set<int32_t> seen;
+    const uint32_t batch = p->new_mark();
     int64_t need = 0, total = 0;
     for (int32_t i = 0; i < nseq; ++i) {
-        if (!seen.insert(seqs[i]).second) return KVP_ERR_INVALID;
         Need nd{};
-        int rc = check_append(p, seqs[i], ntoks[i], &dec, &nd);
+        int rc = check_append(p, seqs[i], ntoks[i], batch, &nd);
         if (rc) return rc;
-        if (nd.cow) dec[p->tables[seqs[i]].back()] += 1;
+        if (p->seq_mark[seqs[i]] == batch) return KVP_ERR_INVALID;
+        p->seq_mark[seqs[i]] = batch;
+        if (nd.cow) {
+            const int32_t last = p->tables[seqs[i]].back();
+            if (p->block_mark[last] != batch) p->block_drops[last] = 0;
+            p->block_mark[last] = batch;
+            p->block_drops[last] += 1;
+        }
         need += nd.cow + nd.fresh;
         total += ntoks[i];
     }
