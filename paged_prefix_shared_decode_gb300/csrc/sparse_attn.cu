@@ -24,6 +24,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/kvp.h"
 #include "kvp_internal.h"
@@ -100,6 +101,22 @@ struct Partial {
     float m[8 * NT], l[8 * NT];
 };
 
+// Where a row's 16-byte chunk lies in shared memory: the four lanes of two
+// neighbouring rows (K), and of four even or odd ones (V), meet in no bank.
+__device__ __forceinline__ int swizzle(int row, int chunk) { return chunk ^ (row & 6) ^ (row & 1) << 2; }
+
+// 16 bytes into shared memory, or zeros.
+__device__ __forceinline__ void copy16(const uint4 *to, const void *from, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "r"(real ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
 // A warp's state: columns 8 n + 2 t + e of a lane are (query, head) pairs.
 template <int D, int NT>
 struct Warp {
@@ -117,10 +134,9 @@ struct Warp {
         }
     }
 
-    // 16 tokens at k and v (rows of D), of which the first `valid` are read;
-    // column (n, e) sees those up to last(n, e).
-    template <class Last>
-    __device__ __forceinline__ void step(const __nv_bfloat16 *k, const __nv_bfloat16 *v, int valid, int lane, Last last) {
+    // 16 tokens at k and v (rows of D), of which the first `valid` are read and
+    // seen by every column.
+    __device__ __forceinline__ void step(const __nv_bfloat16 *k, const __nv_bfloat16 *v, int valid, int lane) {
         constexpr int KC = D / 32, VC = D / 64;
         const int g = lane >> 2, t = lane & 3;
         uint4 kv[2][KC], vv[4][VC];
@@ -138,21 +154,35 @@ struct Warp {
             }
         float s[NT][4] = {};
 #pragma unroll
-        for (int c = 0; c < KC; ++c)
+        for (int c = 0; c < KC; ++c) scores(s, kv[0][c], kv[1][c], c);
+        uint32_t p_hi[NT][2], p_lo[NT][2];
+        weigh(s, lane, valid, p_hi, p_lo);
+        values(vv, p_hi, p_lo);
+    }
+
+    // S^T += K Q^T over chunk c of the dims: rows g and g + 8 are tokens.
+    __device__ __forceinline__ void scores(float (&s)[NT][4], const uint4 &ka, const uint4 &kb, int c) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma(s[n], kv[0][c].x, kv[1][c].x, kv[0][c].y, kv[1][c].y, q[n][c].x, q[n][c].y);
-                mma(s[n], kv[0][c].z, kv[1][c].z, kv[0][c].w, kv[1][c].w, q[n][c].z, q[n][c].w);
-            }
-        // s[n][0..1]: token g, columns 2 t, 2 t + 1; s[n][2..3]: token g + 8
+        for (int n = 0; n < NT; ++n) {
+            mma(s[n], ka.x, kb.x, ka.y, kb.y, q[n][c].x, q[n][c].y);
+            mma(s[n], ka.z, kb.z, ka.w, kb.w, q[n][c].z, q[n][c].w);
+        }
+    }
+
+    // Scores (s[n][0..1]: token g, columns 2 t, 2 t + 1; s[n][2..3]: token g + 8)
+    // to weights as B operands.
+    __device__ __forceinline__ void weigh(float (&s)[NT][4], int lane, int valid, uint32_t (&p_hi)[NT][2],
+                                          uint32_t (&p_lo)[NT][2]) {
+        const int g = lane >> 2;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = g + 8 * (e >> 1) < valid ? s[n][e] * scale_log2 : -INFINITY;
         bool raise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[n][e] = g + 8 * (e >> 1) <= last(n, e & 1) ? s[n][e] * scale_log2 : -INFINITY;
-                raise |= !(s[n][e] <= m[n][e & 1] + 8.f);    // (a NaN too)
-            }
+            for (int e = 0; e < 4; ++e) raise |= !(s[n][e] <= m[n][e & 1] + 8.f);    // (a NaN too)
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -172,27 +202,32 @@ struct Warp {
                     }
                 }
         }
-        uint32_t p_hi[NT][2], p_lo[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            // (2^(-inf - 0) = 0 for a column that has seen nothing yet)
+            const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float x[2], y[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float z = s[n][2 * e + i];
-                    x[i] = z == -INFINITY ? 0.f : exp2_sfu(z - m[n][i]);
-                    l[n][i] += x[i];
-                    y[i] = x[i] - __bfloat162float(__float2bfloat16_rn(x[i]));
-                }
-                const __nv_bfloat162 hi = __floats2bfloat162_rn(x[0], x[1]), lo = __floats2bfloat162_rn(y[0], y[1]);
-                p_hi[n][e] = transpose8(*reinterpret_cast<const uint32_t *>(&hi));
+                const float x0 = exp2_sfu(s[n][2 * e] - m0), x1 = exp2_sfu(s[n][2 * e + 1] - m1);
+                l[n][0] += x0;
+                l[n][1] += x1;
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(x0, x1);
+                const uint32_t h = *reinterpret_cast<const uint32_t *>(&hi);
+                const __nv_bfloat162 lo =
+                    __floats2bfloat162_rn(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xffff0000u));
+                p_hi[n][e] = transpose8(h);
                 p_lo[n][e] = transpose8(*reinterpret_cast<const uint32_t *>(&lo));
             }
+        }
+    }
+
+    // O^T += V^T P^T.  Rows g and g + 8 of V^T tile j are dims 8 g + j and 64 +
+    // 8 g + j (head dim 64: 8 g + j and 8 g + 4 + j).
+    __device__ __forceinline__ void values(const uint4 (&vv)[4][D / 64], const uint32_t (&p_hi)[NT][2],
+                                           const uint32_t (&p_lo)[NT][2]) {
+        constexpr int VC = D / 64;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-            // rows g and g + 8 of V^T tile j: dims 8 g + j and 64 + 8 g + j
-            // (head dim 64: 8 g + j and 8 g + 4 + j)
             const int c1 = VC - 1, j1 = VC == 2 ? j : j + 4;
             const uint32_t sel0 = j & 1 ? 0x7632 : 0x5410, sel1 = j1 & 1 ? 0x7632 : 0x5410;
             const uint32_t a0 = __byte_perm(word(vv[0][0], j >> 1), word(vv[1][0], j >> 1), sel0);
@@ -305,7 +340,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) sparse_attn_kern
             if (blk < 0 || first > pos) continue;
             const int valid = min(16, pos - first + 1);
             const int64_t at = (((head + (int64_t)blk * a.Hkv) << a.bs_log2) + 16 * sub) * D;
-            w.step(a.k + at, a.v + at, valid, lane, [&](int, int) { return valid - 1; });
+            w.step(a.k + at, a.v + at, valid, lane);
         }
     }
     w.leave(part[warp], lane);
@@ -369,9 +404,141 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) sparse_attn_kern
 }
 
 
-constexpr int kTilePages = 16384;    // pages of a sequence that a tile's map covers
-constexpr int kTileList = 1024;      // pages listed at a time
-constexpr int kTileBytes = kTilePages + kTileList * 8;
+// A warp's state for 16 (query, head) rows: rows g and g + 8 of a lane.  With
+// that many the queries are the 16 rows and K the columns of S = Q K^T, whose
+// fragments are those of P in O += P V, and K's operand is two registers of
+// one load in a row (as rows, tokens g and g + 8 interleave: a quarter of the
+// kernel's instructions were moves).
+template <int D>
+struct Rows16 {
+    uint32_t q[D / 16][4];
+    float o[D / 8][4];              // tile 8 c + j: dims 64 c + 8 (2 t) + j and 64 c + 8 (2 t + 1) + j
+    float m[2], l[2];
+    float scale_log2;
+
+    __device__ __forceinline__ void clear() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    }
+    // 8 dims of rows g and g + 8, from 32 c + 8 t on
+    __device__ __forceinline__ void load_q(int c, uint4 a, uint4 b) {
+        q[2 * c][0] = a.x; q[2 * c][1] = b.x; q[2 * c][2] = a.y; q[2 * c][3] = b.y;
+        q[2 * c + 1][0] = a.z; q[2 * c + 1][1] = b.z; q[2 * c + 1][2] = a.w; q[2 * c + 1][3] = b.w;
+    }
+
+    // 16 tokens in shared memory: K, then V, rows of D with their 16-byte
+    // chunks at swizzle(row, chunk).  Row g + 8 e sees those up to last[e].
+    __device__ __forceinline__ void step(const uint4 *kv, int lane, bool full, const int (&last)[2]) {
+        constexpr int CH = D / 8, VC = D / 64;
+        const int g = lane >> 2, t = lane & 3;
+        float s[2][4] = {};
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const int at = g * CH + swizzle(g, 4 * c + t);           // (tokens g and g + 8 alike)
+            const uint4 k0 = kv[at], k1 = kv[at + 8 * CH];
+            mma(s[0], q[2 * c][0], q[2 * c][1], q[2 * c][2], q[2 * c][3], k0.x, k0.y);
+            mma(s[1], q[2 * c][0], q[2 * c][1], q[2 * c][2], q[2 * c][3], k1.x, k1.y);
+            mma(s[0], q[2 * c + 1][0], q[2 * c + 1][1], q[2 * c + 1][2], q[2 * c + 1][3], k0.z, k0.w);
+            mma(s[1], q[2 * c + 1][0], q[2 * c + 1][1], q[2 * c + 1][2], q[2 * c + 1][3], k1.z, k1.w);
+        }
+        // s[n][0..1]: row g, tokens 8 n + 2 t, + 1; s[n][2..3]: row g + 8
+        if (!full) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (8 * n + 2 * t + (i & 1) > last[i >> 1]) s[n][i] = -INFINITY;
+        }
+        // the reference is in units of unscaled scores: 2^((s - m) scale)
+        bool raise = false;
+        const float slack = 8.f / scale_log2;
+        float top[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+            raise |= top[e] > m[e] + slack;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = top[e];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                x = fmaxf(x, m[e]);
+                const float f = m[e] == -INFINITY ? 0.f : exp2_sfu((m[e] - x) * scale_log2);
+                m[e] = x;
+                l[e] *= f;
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    o[j][2 * e] *= f;
+                    o[j][2 * e + 1] *= f;
+                }
+            }
+        }
+        uint32_t p_hi[4], p_lo[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // (2^-inf = 0 for a row that has seen nothing yet)
+            const float shift = m[e] == -INFINITY ? 0.f : -m[e] * scale_log2;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float x0 = exp2_sfu(fmaf(s[n][2 * e], scale_log2, shift));
+                const float x1 = exp2_sfu(fmaf(s[n][2 * e + 1], scale_log2, shift));
+                l[e] += x0 + x1;
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(x0, x1);
+                const uint32_t h = *reinterpret_cast<const uint32_t *>(&hi);
+                const __nv_bfloat162 lo =
+                    __floats2bfloat162_rn(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xffff0000u));
+                p_hi[2 * n + e] = h;
+                p_lo[2 * n + e] = *reinterpret_cast<const uint32_t *>(&lo);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < VC; ++c) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
+                v[i] = kv[(16 + tok) * CH + swizzle(tok, 8 * c + g)];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t pick = j & 1 ? 0x7632 : 0x5410;
+                const uint32_t b0 = __byte_perm(word(v[0], j >> 1), word(v[1], j >> 1), pick);
+                const uint32_t b1 = __byte_perm(word(v[2], j >> 1), word(v[3], j >> 1), pick);
+                mma(o[8 * c + j], p_hi[0], p_hi[1], p_hi[2], p_hi[3], b0, b1);
+                mma(o[8 * c + j], p_lo[0], p_lo[1], p_lo[2], p_lo[3], b0, b1);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void leave(Partial<D, 2> &part, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = g + 8 * e;
+            float x = l[e];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            if (t == 0) {
+                part.m[r] = m[e] * scale_log2;
+                part.l[r] = x;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                part.o[r][64 * (j / 8) + 16 * t + j % 8] = o[j][2 * e];
+                part.o[r][64 * (j / 8) + 16 * t + 8 + j % 8] = o[j][2 * e + 1];
+            }
+        }
+    }
+};
+
+constexpr int kTilePages = 4096;     // pages of a sequence that a tile's map covers
+constexpr int kTileList = 256;       // pages listed at a time
+constexpr int kTileStages = 2;       // 16-token steps in a warp's ring
+constexpr int kTileMap = kTilePages + kTileList * 8;
 
 // Several consecutive query rows of a sequence (as many as fill 16 columns with
 // their groups' heads): neighbours choose much the same pages, so a page is
@@ -381,14 +548,20 @@ constexpr int kTileBytes = kTilePages + kTileList * 8;
 // A value that is not finite in a page that only some of the rows see would
 // reach the others as 0 * inf; then (and when a row names a page twice) the
 // rows are done one after the other instead, each by its own list.
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, 2) sparse_tile_kernel(const SparseArgs a) {
+//
+// Each warp takes its own 16-token steps through its own ring in shared memory
+// (cp.async two steps ahead): straight from global memory, as single rows do
+// it, the two CTAs' 8 warps that 230 registers leave waited for every load.
+template <int D>
+__global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const SparseArgs a) {
     constexpr int THREADS = 32 * kWarps;
     extern __shared__ __align__(16) unsigned char smem[];
-    Partial<D, NT> *part = reinterpret_cast<Partial<D, NT> *>(smem);     // after the pages are done
     uint32_t *s_rows = reinterpret_cast<uint32_t *>(smem);               // a byte per page
     int32_t *s_blk = reinterpret_cast<int32_t *>(smem + kTilePages);
     int32_t *s_page = s_blk + kTileList;                                 // page << 8 | rows
+    constexpr int CH = D / 8, STEP = 32 * CH;                            // 16-byte chunks of a row, of a step
+    uint4 *s_ring = reinterpret_cast<uint4 *>(smem + kTileMap);
+    Partial<D, 2> *part = reinterpret_cast<Partial<D, 2> *>(s_ring);   // after the pages are done
     __shared__ int s_scan[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     griddep_wait();
@@ -401,21 +574,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) sparse_tile_kernel(const Spars
     const int64_t lr0 = (int64_t)l * a.rows.T + r0;
     auto q_row = [&](int c) { return (lr0 + c / a.G) * a.Hq + h * a.G + c % a.G; };   // row of q, out, lse
 
-    Warp<D, NT> w;
+    Rows16<D> w;
     w.scale_log2 = a.scale_log2;
+    int row[2];                                          // query row of rows g and g + 8; 31: none
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int c = 8 * n + g;
-        const __nv_bfloat16 *q = a.q + (c < cols ? q_row(c) : 0) * D + 8 * t;
+    for (int e = 0; e < 2; ++e) row[e] = g + 8 * e < cols ? (g + 8 * e) / a.G : 31;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) w.q[n][i] = c < cols ? load16(q + 32 * i) : make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < D / 32; ++c) {
+        uint4 x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            x[e] = g + 8 * e < cols ? load16(a.q + q_row(g + 8 * e) * D + 32 * c + 8 * t) : make_uint4(0, 0, 0, 0);
+        w.load_q(c, x[0], x[1]);
     }
     w.clear();
-    int row[NT][2];                                      // row of each of the lane's columns; 31: none
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) row[n][e] = 8 * n + 2 * t + e < cols ? (8 * n + 2 * t + e) / a.G : 31;
 
     const int sub_log2 = a.bs_log2 - 4;
     const int64_t head = (int64_t)l * a.NB * a.Hkv + h;
@@ -426,19 +598,63 @@ __global__ void __launch_bounds__(32 * kWarps, 2) sparse_tile_kernel(const Spars
         const int page = sel[q * sel_row + i];
         return page >= 0 && pos0 + q >= 0 && page <= (pos0 + q) >> a.bs_log2 ? page : -1;
     };
+    uint4 *ring = s_ring + warp * kTileStages * STEP;
     auto attend = [&](int n_list) {
         const int tiles = n_list << sub_log2;
+        // the tokens of step x that the last of the rows naming its page sees
+        auto look = [&](int x, int &blk, int &first, int &rows) {
+            const int i = x >> sub_log2;
+            blk = s_blk[i];
+            rows = s_page[i] & 255;
+            first = ((s_page[i] >> 8) << a.bs_log2) + 16 * (x & ((1 << sub_log2) - 1));
+            return blk < 0 ? 0 : min(16, pos0 + (31 - __clz(rows | 1)) - first + 1);
+        };
+        auto fetch = [&](int x, int stage) {
+            int blk, first, rows;
+            const int valid = x < tiles ? look(x, blk, first, rows) : 0;
+            if (valid > 0) {
+                const int64_t at = (((head + (int64_t)blk * a.Hkv) << a.bs_log2) + (first & ((1 << a.bs_log2) - 1))) * D;
+                const uint4 *k = reinterpret_cast<const uint4 *>(a.k + at), *v = reinterpret_cast<const uint4 *>(a.v + at);
+                // token RPI i + lane / CH, chunk lane % CH, i = 0, 1, ...: of the
+                // swizzle's terms one is the lane's and one the step's
+                constexpr int RPI = 32 / CH;
+                const int tok = lane / CH, c = lane % CH ^ (tok & 6) ^ (tok & 1) << 2;
+                uint4 *to = ring + stage * STEP + tok * CH;
+                if (valid == 16) {
+#pragma unroll
+                    for (int i = 0; i < 16 / RPI; ++i) {
+                        copy16(to + RPI * i * CH + (c ^ (RPI * i & 6)), k + lane + 32 * i, true);
+                        copy16(to + (16 + RPI * i) * CH + (c ^ (RPI * i & 6)), v + lane + 32 * i, true);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16 / RPI; ++i) {
+                        const bool real = tok + RPI * i < valid;
+                        copy16(to + RPI * i * CH + (c ^ (RPI * i & 6)), k + (real ? lane + 32 * i : 0), real);
+                        copy16(to + (16 + RPI * i) * CH + (c ^ (RPI * i & 6)), v + (real ? lane + 32 * i : 0), real);
+                    }
+                }
+            }
+            copies_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kTileStages - 1; ++i) fetch(warp + i * kWarps, i);
+        int stage = 0;
         for (int x = warp; x < tiles; x += kWarps) {
-            const int i = x >> sub_log2, sub = x & ((1 << sub_log2) - 1);
-            const int blk = s_blk[i], page = s_page[i] >> 8, rows = s_page[i] & 255;
-            const int first = (page << a.bs_log2) + 16 * sub;
-            // the tokens that the last of the rows naming the page sees
-            const int valid = min(16, pos0 + (31 - __clz(rows | 1)) - first + 1);
-            if (blk < 0 || valid <= 0) continue;
-            const int64_t at = (((head + (int64_t)blk * a.Hkv) << a.bs_log2) + 16 * sub) * D;
-            w.step(a.k + at, a.v + at, valid, lane,
-                   [&](int n, int e) { return rows >> row[n][e] & 1 ? pos0 + row[n][e] - first : -1; });
+            fetch(x + (kTileStages - 1) * kWarps, stage == 0 ? kTileStages - 1 : stage - 1);
+            copies_wait<kTileStages - 1>();
+            __syncwarp();
+            int blk, first, rows;
+            if (look(x, blk, first, rows) > 0) {
+                const bool full = rows == (1 << nr) - 1 && first + 15 <= pos0;
+                const int last[2] = {rows >> row[0] & 1 ? pos0 + row[0] - first : -1,
+                                     rows >> row[1] & 1 ? pos0 + row[1] - first : -1};
+                w.step(ring + stage * STEP, lane, full, last);
+            }
+            __syncwarp();          // before the stage is filled again
+            stage = stage == kTileStages - 1 ? 0 : stage + 1;
         }
+        copies_wait<0>();
     };
     auto block_of = [&](int page) {
         const int blk = table[page];
@@ -458,16 +674,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) sparse_tile_kernel(const Spars
     if (!single) {
         const uint8_t *rows_of = reinterpret_cast<const uint8_t *>(s_rows);
         for (int p0 = 0; p0 < seen; p0 += kTileList) {
-            // pages that some row names, in order: eight in a row per thread
+            // pages that some row names, in order: a few in a row per thread
             constexpr int PER = kTileList / THREADS;
             const int p = p0 + tid * PER;
             int mine = 0;
-            uint32_t two[PER / 4];
 #pragma unroll
-            for (int i = 0; i < PER / 4; ++i) {
-                two[i] = p + 4 * i < seen ? s_rows[(p >> 2) + i] : 0u;
-                mine += __popc(__vcmpne4(two[i], 0u)) >> 3;
-            }
+            for (int i = 0; i < PER; ++i) mine += p + i < seen && rows_of[p + i];
             int before = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -493,15 +705,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) sparse_tile_kernel(const Spars
             attend(all);
             __syncthreads();
         }
-        bool bad = false;
+        bool bad = !isfinite(w.l[0]) || !isfinite(w.l[1]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                bad |= !isfinite(w.l[n][e & 1]);
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) bad |= !isfinite(w.o[n][j][e]);
-            }
+            for (int i = 0; i < 4; ++i) bad |= !isfinite(w.o[j][i]);
         single = __syncthreads_or(bad);
     }
     // the sums of columns c0 .. c1 - 1 joined and written (part takes the
@@ -553,10 +761,20 @@ cudaError_t launch_sparse(SparseArgs a, cudaStream_t stream) {
                          sizeof(Partial<D, NT>) * kWarps, a.ctas, stream, a);
 }
 
-template <int D, int NT>
+template <int D>
 cudaError_t launch_tile(const SparseArgs &a, int64_t tiles, cudaStream_t stream) {
-    const size_t bytes = std::max<size_t>(sizeof(Partial<D, NT>) * kWarps, kTileBytes);
-    return launch_behind(sparse_tile_kernel<D, NT>, dim3((unsigned)tiles, (unsigned)(a.L * a.Hkv)), 32 * kWarps, bytes, 1,
+    constexpr size_t ring = (size_t)kWarps * kTileStages * 64 * D, parts = sizeof(Partial<D, 2>) * kWarps;
+    constexpr size_t bytes = kTileMap + (ring > parts ? ring : parts);
+    static std::once_flag once[kMaxDevices];
+    static bool ok[kMaxDevices];
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [dev] {
+        ok[dev] = cudaFuncSetAttribute(sparse_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)bytes) == cudaSuccess;
+    });
+    if (!ok[dev]) return cudaErrorInvalidDevice;
+    return launch_behind(sparse_tile_kernel<D>, dim3((unsigned)tiles, (unsigned)(a.L * a.Hkv)), 32 * kWarps, bytes, 1,
                          stream, a);
 }
 
@@ -568,8 +786,7 @@ cudaError_t launch_for(SparseArgs a, cudaStream_t stream) {
     a.qt = std::min(8, 16 / a.G);
     if (a.rows.start && a.qt > 1 && a.rows.MB <= kTilePages && a.L * a.Hkv <= 65535 &&
         (int64_t)(a.rows.T / a.qt) * a.L * a.Hkv >= 2LL * device_sm_count())
-        return a.qt * a.G <= 8 ? launch_tile<D, 1>(a, QueryRows::tiles(a.rows.T, a.rows.S, a.qt), stream)
-                               : launch_tile<D, 2>(a, QueryRows::tiles(a.rows.T, a.rows.S, a.qt), stream);
+        return launch_tile<D>(a, QueryRows::tiles(a.rows.T, a.rows.S, a.qt), stream);
     return a.G <= 8 ? launch_sparse<D, 1>(a, stream) : launch_sparse<D, 2>(a, stream);
 }
 
