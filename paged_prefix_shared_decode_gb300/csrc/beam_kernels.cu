@@ -8,9 +8,9 @@
 // read once into registers; its maximum, its sum of exponentials and its n
 // best logits go to the workspace.  Within a row scores order like logits, so
 // a row's n best scores are among its chunks' n best logits.  The n best of a
-// chunk: each warp sorts its lanes' maxima, and the smallest of the warps'
-// ceil(n / 8)-th is a bound that at least n logits reach and few more do;
-// those are ranked against one another.  (More reach it where many are equal,
+// chunk: each warp sorts its lanes' maxima; all eight warps' ceil(n / 8)-th, and
+// four warps' ceil(n / 4)-th, are bounds that at least n logits reach, and few
+// more do (about 30 for n = 16); those are ranked against one another.  (More reach it where many are equal,
 // or the large ones lie in few threads: then one after the other is taken.)
 // beam_join_kernel: a CTA per request joins the sums, scores the candidates and
 // ranks them the same way.
@@ -67,6 +67,35 @@ struct BeamArgs {
     int32_t *cand_at;
 };
 
+// An fp32 number as a whole number of the same order (-0 as 0), and back from
+// the upper half of a 64-bit one.
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t k = (uint32_t)(key >> 32);
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+// The fourth largest of eight.
+__device__ __forceinline__ float fourth_of_8(float4 a, float4 b) {
+    auto order = [](float &x, float &y) {
+        const float t = fmaxf(x, y);
+        y = fminf(x, y);
+        x = t;
+    };
+    auto sort4 = [&](float4 &v) {
+        order(v.x, v.y);
+        order(v.z, v.w);
+        order(v.x, v.z);
+        order(v.y, v.w);
+        order(v.y, v.z);
+    };
+    sort4(a);
+    sort4(b);
+    return fmaxf(fmaxf(fmaxf(a.w, b.w), fminf(a.y, b.y)), fmaxf(fminf(a.x, b.z), fminf(a.z, b.x)));
+}
+
 __device__ __forceinline__ bool bigger(float x, float y) { return x > y; }
 __device__ __forceinline__ bool bigger(uint64_t x, uint64_t y) { return x > y; }
 // A warp's values in descending order.
@@ -108,9 +137,8 @@ __device__ __forceinline__ void add2(float &x, float &xr, float y, float yr) {
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a) {
     __shared__ float2 s_sum[kWarps];
-    __shared__ float s_max[kWarps], s_bound[kWarps];
-    __shared__ float s_c[kCap];
-    __shared__ int s_at[kCap];
+    __shared__ __align__(16) float s_max[kWarps], s_eighth[kWarps], s_fourth[kWarps];
+    __shared__ uint64_t s_key[kCap];
     __shared__ int s_count, s_best[kWarps];
     __shared__ float s_bestv[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -149,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
             v[k] = at < len ? as_float(src[at]) : -INFINITY;
         }
     }
-    constexpr int GROUP = 8;             // maxima of 8 logits: most reach no candidate
+    constexpr int GROUP = 4;             // maxima of 4 logits: most reach no candidate
     float part_top[kPer / GROUP], top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kPer / GROUP; ++i) {
@@ -166,15 +194,18 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
     }
     top = sort_warp(top, lane);
     if (lane == 0) s_max[warp] = top;
-    if (lane == (a.n + kWarps - 1) / kWarps - 1) s_bound[warp] = top;
+    if (lane == (a.n + 7) / 8 - 1) s_eighth[warp] = top;
+    if (lane == (a.n + 3) / 4 - 1) s_fourth[warp] = top;
     if (tid == 0) s_count = 0;
     __syncthreads();
-    float all = s_max[0], bound = s_bound[0];
+    static_assert(kWarps == 8, "eight warps");
+    float all = s_max[0], bound = s_eighth[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
         all = fmaxf(all, s_max[w]);
-        bound = fminf(bound, s_bound[w]);
+        bound = fminf(bound, s_eighth[w]);
     }
+    bound = fmaxf(bound, fourth_of_8(*reinterpret_cast<const float4 *>(s_fourth), *reinterpret_cast<const float4 *>(s_fourth + 4)));
     bound = fmaxf(bound, -FLT_MAX);      // -inf is no candidate
     PartHead *head = a.heads + (int64_t)row * a.chunks + chunk;
     float *cand = a.cand + ((int64_t)row * a.chunks + chunk) * a.n;
@@ -184,12 +215,21 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
         if (tid < a.n) cand[tid] = -INFINITY;
         return;
     }
-    // 2^((v - all) log2 e): the difference is exact or nearly so, its product
-    // is off by 2^-24 of itself and the power by 2^-22, both ways alike (expf's
-    // two-part product: 10 instructions a logit instead of 4)
+    // 2^(v log2 e - c), c = all log2 e rounded: one rounding of each exponent
+    // (2^-24 of it) and the power's 2^-22, both ways alike; c's own rounding,
+    // known exactly, is one factor of the sum.  (expf: 10 instructions a logit
+    // instead of 3)
+    constexpr float kLog2e = 1.4426950408889634f;
+    const bool near = fabsf(all) < 256.f;     // (c's rounding is below 2^-15)
+    const float c = __fmul_rn(all, kLog2e);
     float part = 0.f, rest = 0.f;
+    if (near) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) part += exp2_sfu((v[k] - all) * 1.4426950408889634f);
+        for (int k = 0; k < kPer; ++k) part += exp2_sfu(__fmaf_rn(v[k], kLog2e, -c));
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) part += exp2_sfu((v[k] - all) * kLog2e);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         add2(part, rest, __shfl_xor_sync(0xffffffffu, part, o), __shfl_xor_sync(0xffffffffu, rest, o));
@@ -201,27 +241,28 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
         for (int k = i * GROUP; k < (i + 1) * GROUP; ++k)
             if (v[k] >= bound) {
                 const int j = atomicAdd(&s_count, 1);
-                if (j < kCap) {
-                    s_c[j] = v[k];
-                    s_at[j] = place<T>(tid, k);
-                }
+                // (larger first, then the lower token)
+                if (j < kCap) s_key[j] = (uint64_t)order_key(v[k]) << 32 | (uint32_t)~place<T>(tid, k);
             }
     }
     __syncthreads();
     if (tid == 0) {
         for (int w = 1; w < kWarps; ++w) add2(part, rest, s_sum[w].x, s_sum[w].y);
+        // times 2^(c - all log2 e) = 1 - d log 2 and terms below 2^-30
+        const float d = near ? __fmaf_rn(all, kLog2e, -c) * 0.69314718f : 0.f;
+        add2(part, rest, -d * part, 0.f);
         *head = PartHead{part, rest, part == part ? all : INFINITY, 0.f};
     }
     const int found = s_count;
     if (found <= kCap) {
         for (int i = tid; i < found; i += kThreads) {
-            const float x = s_c[i];
-            const int at = s_at[i];
+            const uint64_t x = s_key[i];
             int r = 0;
-            for (int j = 0; j < found; ++j) r += s_c[j] > x || (s_c[j] == x && s_at[j] < at);
+#pragma unroll 4
+            for (int j = 0; j < found; ++j) r += s_key[j] > x;
             if (r < a.n) {
-                cand[r] = x;
-                cand_at[r] = x0 + at;
+                cand[r] = key_value(x);
+                cand_at[r] = x0 + (int)~(uint32_t)x;
             }
         }
         if (tid >= found && tid < a.n) cand[tid] = -INFINITY;
@@ -279,14 +320,6 @@ struct Entry {
     float logit;
     int32_t beam, at;
 };
-__device__ __forceinline__ uint32_t order_key(float x) {
-    const uint32_t b = __float_as_uint(x + 0.f);
-    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint64_t key) {
-    const uint32_t k = (uint32_t)(key >> 32);
-    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-}
 // The order: score, then row, then logit, then token.
 __device__ __forceinline__ bool before(const Entry &x, const Entry &y) {
     if (x.key != y.key) return x.key > y.key;
