@@ -28,13 +28,14 @@
 
 #include "kv4_quant.cuh"
 #include "kvp_internal.h"
+#include "launch.cuh"
 
 namespace kvp {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 2;          // units in flight per thread (4: 119 registers, half the warps)
-constexpr int kCopies = 4;         // 16-byte copies in flight per thread
+constexpr int kCopies = 8;         // 16-byte copies in flight per thread
 constexpr int kMaxTok = 4;         // tokens per CTA
 constexpr int kTokMax = 1 << 19;   // tokens per launch
 
@@ -153,21 +154,21 @@ __device__ __forceinline__ void copy_cow(const Args &a, int x) {
     const int64_t run = (int64_t)used * (a.d / 8), tile = (int64_t)a.bs * (a.d / 8);     // 16-byte chunks
     const int64_t step = (int64_t)(dst - src) * a.Hkv * tile, head = ((int64_t)l * a.NB + src) * a.Hkv;
     uint4 *kp = static_cast<uint4 *>(a.k_pool), *vp = static_cast<uint4 *>(a.v_pool);
-    if (run * a.Hkv * 2 <= INT32_MAX) {
+    if (tile * a.Hkv * 2 <= INT32_MAX) {
         // (a divisor per thread and batch: the loads are what takes time)
         const int total = (int)run * a.Hkv * 2, r = (int)run;
         for (int y0 = threadIdx.x; y0 < total; y0 += kThreads * kCopies) {
             uint4 v[kCopies];
-            uint4 *p[kCopies];
+            int at[kCopies];             // chunk behind the source block's first
 #pragma unroll
             for (int u = 0; u < kCopies; ++u) {
-                const int y = y0 + u * kThreads, z = y >> 1, h = z / r;
-                p[u] = (y & 1 ? vp : kp) + (head + h) * tile + (z - h * r);
-                if (y < total) v[u] = *p[u];
+                const int z = (y0 + u * kThreads) >> 1, h = z / r;
+                at[u] = h * (int)tile + (z - h * r);
+                if (y0 + u * kThreads < total) v[u] = (y0 & 1 ? vp : kp)[head * tile + at[u]];
             }
 #pragma unroll
             for (int u = 0; u < kCopies; ++u)
-                if (y0 + u * kThreads < total) p[u][step] = v[u];
+                if (y0 + u * kThreads < total) (y0 & 1 ? vp : kp)[head * tile + at[u] + step] = v[u];
         }
     } else {
         for (int h = 0; h < a.Hkv; ++h)
@@ -183,6 +184,7 @@ template <int W, class Args>
 __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const __grid_constant__ Args a) {
     using V = typename Vec<W>::type;
     __shared__ Tokens s;
+    griddep_wait();
     const int cow_ctas = a.ncow * a.L;
     if ((int)blockIdx.x < cow_ctas) {
         copy_cow(a, blockIdx.x);
@@ -247,6 +249,7 @@ template <class Args>
 __global__ void __launch_bounds__(kThreads) rope_append4_kernel(const __grid_constant__ Args a) {
     __shared__ Tokens s;
     __shared__ float s_row[kThreads / 32][128];
+    griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, vpl = a.d / 32;
     const int cow_ctas = a.ncow * a.L;
     if ((int)blockIdx.x < cow_ctas) {
@@ -328,7 +331,7 @@ cudaError_t launch_part(const RopeAppend &r, const Run *run, int nrun, const int
     std::memcpy(a.cow, r.cow + 3 * cow0, sizeof(int32_t) * 3 * ncow);
     a.per_cta = 1;
     if (r.k_exp) {
-        rope_append4_kernel<Args><<<(unsigned)((ncow + ntok) * r.L), kThreads, 0, stream>>>(a);
+        return launch_behind(rope_append4_kernel<Args>, dim3((unsigned)((ncow + ntok) * r.L)), kThreads, 0, 1, stream, a);
     } else {
         // several tokens to a CTA once one each would be many per SM
         const int W = r.rot % 16 == 0 ? 8 : 1, U = (r.d + 2 * W - 1) / (2 * W);
@@ -340,13 +343,9 @@ cudaError_t launch_part(const RopeAppend &r, const Run *run, int nrun, const int
         while (a.per_cta < kMaxTok && (int64_t)ntok * r.L > 16LL * a.per_cta * device_sm_count() && per_tok < 16384)
             a.per_cta *= 2;
         const unsigned grid = (unsigned)((ncow + (ntok + a.per_cta - 1) / a.per_cta) * r.L);
-        if (r.rot % 16 == 0)
-            rope_append_kernel<8, Args><<<grid, kThreads, 0, stream>>>(a);
-        else
-            rope_append_kernel<1, Args><<<grid, kThreads, 0, stream>>>(a);
+        return launch_behind(W == 8 ? rope_append_kernel<8, Args> : rope_append_kernel<1, Args>, dim3(grid), kThreads, 0, 1,
+                             stream, a);
     }
-    count_launch();
-    return cudaGetLastError();
 }
 
 }  // namespace
