@@ -48,6 +48,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # KVP_LIB_PATH points the binding at another build of the same C ABI.
 lib_path = os.environ.get("KVP_LIB_PATH") or os.path.join(_HERE, "libkvp.so")
 _lib = None
+_tc = None     # torch, once a call has needed it
 
 
 class KvpError(RuntimeError):
@@ -341,9 +342,10 @@ def kvp_cow_count(pool) -> int:
 
 def kvp_pool_shape(pool):
     """The pool's layers and kv heads."""
-    layers, heads = _I32(), _I32()
-    _check(load().kvp_pool_shape(pool, ctypes.byref(layers), ctypes.byref(heads)), "kvp_pool_shape")
-    return layers.value, heads.value
+    out = (_I32 * 2)()
+    at = ctypes.addressof(out)
+    _check(load().kvp_pool_shape(pool, at, at + 4), "kvp_pool_shape")
+    return out[0], out[1]
 
 
 def kvp_gather_tables(pool, seqs, width: int):
@@ -767,6 +769,10 @@ def rope_desc(rot_dim: int, base: float = 10000.0, freqs=None, interleaved: bool
 
 def _i32s(a):
     """A host int32 array of a list or array, its address and length."""
+    if isinstance(a, np.ndarray) and a.size <= 256:
+        if a.ndim != 1:
+            raise ValueError(f"expected one dimension, got shape {a.shape}")
+        a = a.tolist()      # (a numpy array's address alone takes 1 us to get)
     if type(a) is list:
         a = array.array("i", a)
         at, n = a.buffer_info()
@@ -780,11 +786,14 @@ def _i32s(a):
 def _here(stream):
     """torch, the current device (0 before CUDA is in use: no tensor is on it)
     and the stream's handle."""
-    torch, dev = _torch()
+    global _tc
+    if _tc is None:
+        import torch as _tc
+    dev = _tc._C._cuda_getDevice() if _tc.cuda.is_initialized() else 0
     if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return torch, dev, raw(dev) if raw else _stream(None)
-    return torch, dev, stream if isinstance(stream, int) else stream.cuda_stream
+        raw = getattr(_tc._C, "_cuda_getCurrentRawStream", None)
+        return _tc, dev, raw(dev) if raw else _stream(None)
+    return _tc, dev, stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def seq_append_rope(pool, seqs, ntoks, k, v, rope: RopeDesc, positions=None, q=None, q_out=None, stream=None):
