@@ -301,6 +301,25 @@ __device__ __forceinline__ uint32_t sort_warp(uint32_t x, int lane) {
     return x;
 }
 
+// The k-th largest key, of which all but the lowest `bits` bits are in `cut`,
+// from the number of keys >= t; above: how many are larger.  It ends early at a
+// t that exactly k keys reach (after about half of the bits where keys do not
+// repeat): those are then all above `cut`, and none of the equal ones is due.
+template <class Count>
+__device__ __forceinline__ void find_cut(int bits, int k, uint32_t &cut, int &above, Count count) {
+    for (int b = bits - 1; b >= 0; --b) {
+        const uint32_t t = cut | 1u << b;
+        const int c = count(t);
+        if (c == k) {
+            cut = t - 1;
+            above = k;
+            return;
+        }
+        if (c > k) cut = t;
+    }
+    above = cut == 0xffffffffu ? 0 : count(cut + 1);
+}
+
 // A CTA per (layer, query row, kv head) of at most W * 32 * E pages: k = budget
 // - sinks - last pages of those in between are to be found, whose keys are in
 // registers (page sink + W * 32 e + thread; steps past the end are as low as
@@ -413,9 +432,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
             differ = __reduce_or_sync(0xffffffffu, differ);
             const int bits = differ ? 32 - __clz(differ) : 0;
             cut = bits == 32 ? 0u : bound >> bits << bits;
-            for (int b = bits - 1; b >= 0; --b)
-                if (count(cut | 1u << b) >= k) cut |= 1u << b;
-            above = cut == 0xffffffffu ? 0 : count(cut + 1);
+            find_cut(bits, k, cut, above, count);
             if (lane == 0) {
                 s_cut = cut;
                 s_above = above;
@@ -444,9 +461,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
             for (int w = 0; w < W; ++w) sum += s_warp[w];
             return sum;
         };
-        for (int b = 31; b >= 0; --b)
-            if (count(cut | 1u << b) >= k) cut |= 1u << b;
-        above = cut == 0xffffffffu ? 0 : count(cut + 1);
+        find_cut(32, k, cut, above, count);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const uint32_t up = __ballot_sync(0xffffffffu, key[e] > cut), eq = __ballot_sync(0xffffffffu, key[e] == cut);
