@@ -152,20 +152,25 @@ struct Warp {
                 const int tok = 2 * t + (e & 1) + 8 * (e >> 1);
                 vv[e][c] = tok < valid ? load16(v + tok * D + 64 * c + 8 * g) : make_uint4(0, 0, 0, 0);
             }
-        float s[NT][4] = {};
+        float s[NT][4] = {}, s2[NT][4] = {};
 #pragma unroll
-        for (int c = 0; c < KC; ++c) scores(s, kv[0][c], kv[1][c], c);
+        for (int c = 0; c < KC; ++c) scores(s, s2, kv[0][c], kv[1][c], c);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
         uint32_t p_hi[NT][2], p_lo[NT][2];
         weigh(s, lane, valid, p_hi, p_lo);
         values(vv, p_hi, p_lo);
     }
 
-    // S^T += K Q^T over chunk c of the dims: rows g and g + 8 are tokens.
-    __device__ __forceinline__ void scores(float (&s)[NT][4], const uint4 &ka, const uint4 &kb, int c) {
+    // S^T += K Q^T over chunk c of the dims, in two sums (one chain of products
+    // waits for every result): rows g and g + 8 are tokens.
+    __device__ __forceinline__ void scores(float (&s)[NT][4], float (&s2)[NT][4], const uint4 &ka, const uint4 &kb, int c) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             mma(s[n], ka.x, kb.x, ka.y, kb.y, q[n][c].x, q[n][c].y);
-            mma(s[n], ka.z, kb.z, ka.w, kb.w, q[n][c].z, q[n][c].w);
+            mma(s2[n], ka.z, kb.z, ka.w, kb.w, q[n][c].z, q[n][c].w);
         }
     }
 
@@ -225,20 +230,27 @@ struct Warp {
     // 8 g + j (head dim 64: 8 g + j and 8 g + 4 + j).
     __device__ __forceinline__ void values(const uint4 (&vv)[4][D / 64], const uint32_t (&p_hi)[NT][2],
                                            const uint32_t (&p_lo)[NT][2]) {
-        constexpr int VC = D / 64;
+        constexpr int VC = D / 64, J = 4;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            const int c1 = VC - 1, j1 = VC == 2 ? j : j + 4;
-            const uint32_t sel0 = j & 1 ? 0x7632 : 0x5410, sel1 = j1 & 1 ? 0x7632 : 0x5410;
-            const uint32_t a0 = __byte_perm(word(vv[0][0], j >> 1), word(vv[1][0], j >> 1), sel0);
-            const uint32_t a1 = __byte_perm(word(vv[0][c1], j1 >> 1), word(vv[1][c1], j1 >> 1), sel1);
-            const uint32_t a2 = __byte_perm(word(vv[2][0], j >> 1), word(vv[3][0], j >> 1), sel0);
-            const uint32_t a3 = __byte_perm(word(vv[2][c1], j1 >> 1), word(vv[3][c1], j1 >> 1), sel1);
+        for (int j0 = 0; j0 < D / 16; j0 += J) {
+            uint32_t a[J][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma(o[n][j], a0, a1, a2, a3, p_hi[n][0], p_hi[n][1]);
-                mma(o[n][j], a0, a1, a2, a3, p_lo[n][0], p_lo[n][1]);
+            for (int i = 0; i < J; ++i) {
+                const int j = j0 + i, c1 = VC - 1, j1 = VC == 2 ? j : j + 4;
+                const uint32_t sel0 = j & 1 ? 0x7632 : 0x5410, sel1 = j1 & 1 ? 0x7632 : 0x5410;
+                a[i][0] = __byte_perm(word(vv[0][0], j >> 1), word(vv[1][0], j >> 1), sel0);
+                a[i][1] = __byte_perm(word(vv[0][c1], j1 >> 1), word(vv[1][c1], j1 >> 1), sel1);
+                a[i][2] = __byte_perm(word(vv[2][0], j >> 1), word(vv[3][0], j >> 1), sel0);
+                a[i][3] = __byte_perm(word(vv[2][c1], j1 >> 1), word(vv[3][c1], j1 >> 1), sel1);
             }
+#pragma unroll
+            for (int i = 0; i < J; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma(o[n][j0 + i], a[i][0], a[i][1], a[i][2], a[i][3], p_hi[n][0], p_hi[n][1]);
+#pragma unroll
+            for (int i = 0; i < J; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma(o[n][j0 + i], a[i][0], a[i][1], a[i][2], a[i][3], p_lo[n][0], p_lo[n][1]);
         }
     }
 
@@ -433,15 +445,22 @@ struct Rows16 {
     __device__ __forceinline__ void step(const uint4 *kv, int lane, bool full, const int (&last)[2]) {
         constexpr int CH = D / 8, VC = D / 64;
         const int g = lane >> 2, t = lane & 3;
-        float s[2][4] = {};
+        // (two chains of products for each tile of tokens: one after the other
+        // they wait for one another's results)
+        float s[2][4] = {}, s2[2][4] = {};
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             const int at = g * CH + swizzle(g, 4 * c + t);           // (tokens g and g + 8 alike)
             const uint4 k0 = kv[at], k1 = kv[at + 8 * CH];
             mma(s[0], q[2 * c][0], q[2 * c][1], q[2 * c][2], q[2 * c][3], k0.x, k0.y);
             mma(s[1], q[2 * c][0], q[2 * c][1], q[2 * c][2], q[2 * c][3], k1.x, k1.y);
-            mma(s[0], q[2 * c + 1][0], q[2 * c + 1][1], q[2 * c + 1][2], q[2 * c + 1][3], k0.z, k0.w);
-            mma(s[1], q[2 * c + 1][0], q[2 * c + 1][1], q[2 * c + 1][2], q[2 * c + 1][3], k1.z, k1.w);
+            mma(s2[0], q[2 * c + 1][0], q[2 * c + 1][1], q[2 * c + 1][2], q[2 * c + 1][3], k0.z, k0.w);
+            mma(s2[1], q[2 * c + 1][0], q[2 * c + 1][1], q[2 * c + 1][2], q[2 * c + 1][3], k1.z, k1.w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[0][i] += s2[0][i];
+            s[1][i] += s2[1][i];
         }
         // s[n][0..1]: row g, tokens 8 n + 2 t, + 1; s[n][2..3]: row g + 8
         if (!full) {
@@ -503,14 +522,17 @@ struct Rows16 {
                 const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
                 v[i] = kv[(16 + tok) * CH + swizzle(tok, 8 * c + g)];
             }
+            uint32_t b[8][2];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t pick = j & 1 ? 0x7632 : 0x5410;
-                const uint32_t b0 = __byte_perm(word(v[0], j >> 1), word(v[1], j >> 1), pick);
-                const uint32_t b1 = __byte_perm(word(v[2], j >> 1), word(v[3], j >> 1), pick);
-                mma(o[8 * c + j], p_hi[0], p_hi[1], p_hi[2], p_hi[3], b0, b1);
-                mma(o[8 * c + j], p_lo[0], p_lo[1], p_lo[2], p_lo[3], b0, b1);
+                b[j][0] = __byte_perm(word(v[0], j >> 1), word(v[1], j >> 1), pick);
+                b[j][1] = __byte_perm(word(v[2], j >> 1), word(v[3], j >> 1), pick);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mma(o[8 * c + j], p_hi[0], p_hi[1], p_hi[2], p_hi[3], b[j][0], b[j][1]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mma(o[8 * c + j], p_lo[0], p_lo[1], p_lo[2], p_lo[3], b[j][0], b[j][1]);
         }
     }
 
@@ -563,6 +585,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
     uint4 *s_ring = reinterpret_cast<uint4 *>(smem + kTileMap);
     Partial<D, 2> *part = reinterpret_cast<Partial<D, 2> *>(s_ring);   // after the pages are done
     __shared__ int s_scan[kWarps];
+    __shared__ float s_share[kWarps][16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     griddep_wait();
     const int h = blockIdx.y % a.Hkv, l = blockIdx.y / a.Hkv;
@@ -664,12 +687,15 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
     for (int i = tid; i < (seen + 15) / 16; i += THREADS) reinterpret_cast<uint4 *>(s_rows)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     bool twice = false;
-    for (int64_t x = tid; x < (int64_t)nr * a.budget; x += THREADS) {
-        const int q = (int)(x / a.budget), page = page_of(q, (int)(x % a.budget));
-        if (page < 0) continue;
-        const uint32_t bit = 1u << ((page & 3) * 8 + q);
-        twice |= (atomicOr(&s_rows[page >> 2], bit) & bit) != 0;
-    }
+    // (a row's entries by a quarter of the threads or more, so that no thread
+    // divides by the budget)
+    for (int q = warp; q < nr; q += kWarps)
+        for (int i = lane; i < a.budget; i += 32) {
+            const int page = page_of(q, i);
+            if (page < 0) continue;
+            const uint32_t bit = 1u << ((page & 3) * 8 + q);
+            twice |= (atomicOr(&s_rows[page >> 2], bit) & bit) != 0;
+        }
     bool single = __syncthreads_or(twice);
     if (!single) {
         const uint8_t *rows_of = reinterpret_cast<const uint8_t *>(s_rows);
@@ -718,11 +744,45 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
         __syncthreads();
         w.leave(part[warp], lane);
         __syncthreads();
-        for (int x = c0 * D + tid; x < c1 * D; x += THREADS) {
-            const int c = x / D, e = x % D;
-            float sum, z, top;
-            join_warps(part, c, e, sum, z, top);
-            put(a, q_row(c) * D + e, e == 0 ? q_row(c) : -1, sum, z, top);
+        // what each warp counts for in a row's sum, then 8 dims at a time
+        if (tid < 16) {
+            float top = part[0].m[tid], z = 0.f;
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) top = fmaxf(top, part[i].m[tid]);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float f = share(part[i].m[tid], part[i].l[tid], top);
+                z += f * part[i].l[tid];
+                s_share[i][tid] = f;
+            }
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) s_share[i][tid] = z == 0.f ? 0.f : s_share[i][tid] / z;
+            if (tid >= c0 && tid < c1 && a.lse)
+                a.lse[q_row(tid)] = z == 0.f ? -INFINITY : (top + log2f(z)) * 0.69314718055994531f;
+        }
+        __syncthreads();
+        for (int x = c0 * CH + tid; x < c1 * CH; x += THREADS) {
+            const int c = x / CH, e = x % CH * 8;
+            float sum[8] = {};
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float f = s_share[i][c];
+                const float4 u = *reinterpret_cast<const float4 *>(&part[i].o[c][e]);
+                const float4 v = *reinterpret_cast<const float4 *>(&part[i].o[c][e + 4]);
+                // (a warp that saw no key counts for nothing, whatever it holds)
+                if (f != 0.f) {
+                    sum[0] += f * u.x; sum[1] += f * u.y; sum[2] += f * u.z; sum[3] += f * u.w;
+                    sum[4] += f * v.x; sum[5] += f * v.y; sum[6] += f * v.z; sum[7] += f * v.w;
+                }
+            }
+            uint4 out;
+            uint32_t *o = &out.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(sum[2 * i], sum[2 * i + 1]);
+                o[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(a.out + q_row(c) * D + e) = out;
         }
     };
     if (!single) {
