@@ -559,33 +559,40 @@ struct Rows16 {
 
 constexpr int kTilePages = 4096;     // pages of a sequence that a tile's map covers
 constexpr int kTileList = 256;       // pages listed at a time
-constexpr int kTileStages = 2;       // 16-token steps in a warp's ring
-constexpr int kTileMap = kTilePages + kTileList * 8;
+constexpr int kTileSteps = 8;        // 16-token steps in a CTA's rings
+constexpr int kTileMap = kTilePages + kTileList * 16;
 
-// Several consecutive query rows of a sequence (as many as fill 16 columns with
-// their groups' heads): neighbours choose much the same pages, so a page is
-// read once for all the rows that named it.  Which rows name a page is a byte
-// per page in shared memory, and the pages are taken in ascending order.
+// Several consecutive query rows of a sequence (as many as fill 16 MT rows with
+// their groups' heads, at most 8): neighbours choose much the same pages, so a
+// page is read once for all the rows that named it.  Which rows name a page is
+// a byte per page in shared memory, and the pages are taken in ascending order.
+// Bound by what L2 delivers, 10 to 11 TB/s: 53 pages of the 128 that four rows
+// of 32 pages name, 59 of eight's 256 (rows that share most of their choice).
 //
 // A value that is not finite in a page that only some of the rows see would
 // reach the others as 0 * inf; then (and when a row names a page twice) the
 // rows are done one after the other instead, each by its own list.
 //
-// Each warp takes its own 16-token steps through its own ring in shared memory
-// (cp.async two steps ahead): straight from global memory, as single rows do
-// it, the two CTAs' 8 warps that 230 registers leave waited for every load.
-template <int D>
+// MT warps, with 16 rows each, go through the same 16-token steps, which they
+// copy (cp.async) into a ring in shared memory some steps ahead; 4 / MT rings
+// of a CTA share the list.  (Straight from global memory, as single rows do it,
+// the 8 warps of two CTAs that 230 registers leave waited for every load.)
+struct alignas(16) Page {
+    int64_t at;          // where its rows of K and V start
+    int32_t first;       // position of its first token
+    int32_t count_rows;  // tokens that the last of the rows naming it sees << 8 | those rows
+};
+template <int D, int MT>
 __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const SparseArgs a) {
-    constexpr int THREADS = 32 * kWarps;
+    constexpr int THREADS = 32 * kWarps, SPLITS = kWarps / MT, STAGES = kTileSteps / SPLITS;
     extern __shared__ __align__(16) unsigned char smem[];
     uint32_t *s_rows = reinterpret_cast<uint32_t *>(smem);               // a byte per page
-    int32_t *s_blk = reinterpret_cast<int32_t *>(smem + kTilePages);
-    int32_t *s_page = s_blk + kTileList;                                 // page << 8 | rows
+    Page *s_list = reinterpret_cast<Page *>(smem + kTilePages);
     constexpr int CH = D / 8, STEP = 32 * CH;                            // 16-byte chunks of a row, of a step
     uint4 *s_ring = reinterpret_cast<uint4 *>(smem + kTileMap);
     Partial<D, 2> *part = reinterpret_cast<Partial<D, 2> *>(s_ring);   // after the pages are done
     __shared__ int s_scan[kWarps];
-    __shared__ float s_share[kWarps][16];
+    __shared__ float s_share[SPLITS][16 * MT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     griddep_wait();
     const int h = blockIdx.y % a.Hkv, l = blockIdx.y / a.Hkv;
@@ -597,20 +604,24 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
     const int64_t lr0 = (int64_t)l * a.rows.T + r0;
     auto q_row = [&](int c) { return (lr0 + c / a.G) * a.Hq + h * a.G + c % a.G; };   // row of q, out, lse
 
+    const int mt = warp % MT, split = warp / MT, col0 = 16 * mt;         // this warp's rows and steps
     Rows16<D> w;
     w.scale_log2 = a.scale_log2;
     int row[2];                                          // query row of rows g and g + 8; 31: none
 #pragma unroll
-    for (int e = 0; e < 2; ++e) row[e] = g + 8 * e < cols ? (g + 8 * e) / a.G : 31;
+    for (int e = 0; e < 2; ++e) row[e] = col0 + g + 8 * e < cols ? (col0 + g + 8 * e) / a.G : 31;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
         uint4 x[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            x[e] = g + 8 * e < cols ? load16(a.q + q_row(g + 8 * e) * D + 32 * c + 8 * t) : make_uint4(0, 0, 0, 0);
+            x[e] = row[e] < 31 ? load16(a.q + q_row(col0 + g + 8 * e) * D + 32 * c + 8 * t) : make_uint4(0, 0, 0, 0);
         w.load_q(c, x[0], x[1]);
     }
     w.clear();
+    // its query rows, as bits (none: a tile with fewer rows than it has room for)
+    const int q_lo = col0 / a.G, q_hi = min(col0 + 15, cols - 1) / a.G;
+    const int own = col0 < cols ? (2 << q_hi) - (1 << q_lo) : 0;
 
     const int sub_log2 = a.bs_log2 - 4;
     const int64_t head = (int64_t)l * a.NB * a.Hkv + h;
@@ -621,67 +632,77 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
         const int page = sel[q * sel_row + i];
         return page >= 0 && pos0 + q >= 0 && page <= (pos0 + q) >> a.bs_log2 ? page : -1;
     };
-    uint4 *ring = s_ring + warp * kTileStages * STEP;
+    uint4 *ring = s_ring + split * STAGES * STEP;
+    // the warps of a ring, of which each has waited for its own copies
+    auto meet = [&] {
+        if constexpr (MT == 1)
+            __syncwarp();
+        else if (split == 0)
+            asm volatile("bar.sync 1, %0;\n" ::"n"(32 * MT) : "memory");
+        else
+            asm volatile("bar.sync 2, %0;\n" ::"n"(32 * MT) : "memory");
+    };
     auto attend = [&](int n_list) {
         const int tiles = n_list << sub_log2;
-        // the tokens of step x that the last of the rows naming its page sees
-        auto look = [&](int x, int &blk, int &first, int &rows) {
-            const int i = x >> sub_log2;
-            blk = s_blk[i];
-            rows = s_page[i] & 255;
-            first = ((s_page[i] >> 8) << a.bs_log2) + 16 * (x & ((1 << sub_log2) - 1));
-            return blk < 0 ? 0 : min(16, pos0 + (31 - __clz(rows | 1)) - first + 1);
-        };
+        const int sub_mask = (1 << sub_log2) - 1;
         auto fetch = [&](int x, int stage) {
-            int blk, first, rows;
-            const int valid = x < tiles ? look(x, blk, first, rows) : 0;
+            if (x >= tiles) {
+                copies_commit();
+                return;
+            }
+            const Page p = s_list[x >> sub_log2];
+            const int sub = 16 * (x & sub_mask), valid = min(16, (p.count_rows >> 8) - sub);
             if (valid > 0) {
-                const int64_t at = (((head + (int64_t)blk * a.Hkv) << a.bs_log2) + (first & ((1 << a.bs_log2) - 1))) * D;
-                const uint4 *k = reinterpret_cast<const uint4 *>(a.k + at), *v = reinterpret_cast<const uint4 *>(a.v + at);
+                const uint4 *k = reinterpret_cast<const uint4 *>(a.k + p.at + sub * D);
+                const uint4 *v = reinterpret_cast<const uint4 *>(a.v + p.at + sub * D);
                 // token RPI i + lane / CH, chunk lane % CH, i = 0, 1, ...: of the
                 // swizzle's terms one is the lane's and one the step's
                 constexpr int RPI = 32 / CH;
                 const int tok = lane / CH, c = lane % CH ^ (tok & 6) ^ (tok & 1) << 2;
                 uint4 *to = ring + stage * STEP + tok * CH;
-                if (valid == 16) {
+                auto rows16 = [&](const uint4 *from, uint4 *to) {
+                    if (valid == 16) {
 #pragma unroll
-                    for (int i = 0; i < 16 / RPI; ++i) {
-                        copy16(to + RPI * i * CH + (c ^ (RPI * i & 6)), k + lane + 32 * i, true);
-                        copy16(to + (16 + RPI * i) * CH + (c ^ (RPI * i & 6)), v + lane + 32 * i, true);
-                    }
-                } else {
+                        for (int i = 0; i < 16 / RPI; ++i)
+                            copy16(to + RPI * i * CH + (c ^ (RPI * i & 6)), from + lane + 32 * i, true);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 16 / RPI; ++i) {
-                        const bool real = tok + RPI * i < valid;
-                        copy16(to + RPI * i * CH + (c ^ (RPI * i & 6)), k + (real ? lane + 32 * i : 0), real);
-                        copy16(to + (16 + RPI * i) * CH + (c ^ (RPI * i & 6)), v + (real ? lane + 32 * i : 0), real);
+                        for (int i = 0; i < 16 / RPI; ++i) {
+                            const bool real = tok + RPI * i < valid;
+                            copy16(to + RPI * i * CH + (c ^ (RPI * i & 6)), from + (real ? lane + 32 * i : 0), real);
+                        }
                     }
-                }
+                };
+                if (MT == 1 || mt == 0) rows16(k, to);
+                if (MT == 1 || mt == 1) rows16(v, to + 16 * CH);
             }
             copies_commit();
         };
 #pragma unroll
-        for (int i = 0; i < kTileStages - 1; ++i) fetch(warp + i * kWarps, i);
+        for (int i = 0; i < STAGES - 1; ++i) fetch(split + i * SPLITS, i);
         int stage = 0;
-        for (int x = warp; x < tiles; x += kWarps) {
-            fetch(x + (kTileStages - 1) * kWarps, stage == 0 ? kTileStages - 1 : stage - 1);
-            copies_wait<kTileStages - 1>();
-            __syncwarp();
-            int blk, first, rows;
-            if (look(x, blk, first, rows) > 0) {
-                const bool full = rows == (1 << nr) - 1 && first + 15 <= pos0;
-                const int last[2] = {rows >> row[0] & 1 ? pos0 + row[0] - first : -1,
-                                     rows >> row[1] & 1 ? pos0 + row[1] - first : -1};
-                w.step(ring + stage * STEP, lane, full, last);
+        for (int x = split; x < tiles; x += SPLITS) {
+            copies_wait<STAGES - 2>();
+            meet();                // the step is there, and the one before it done with
+            fetch(x + (STAGES - 1) * SPLITS, stage == 0 ? STAGES - 1 : stage - 1);
+            const Page p = s_list[x >> sub_log2];
+            const int sub = 16 * (x & sub_mask), rows = p.count_rows & 255, mine = rows & own;
+            if (mine && (p.count_rows >> 8) > sub) {
+                // how far behind the step's first token row 0 is
+                const int ahead = pos0 - p.first - sub;
+                const int last[2] = {mine >> row[0] & 1 ? ahead + row[0] : -1, mine >> row[1] & 1 ? ahead + row[1] : -1};
+                w.step(ring + stage * STEP, lane, mine == own && ahead + q_lo >= 15, last);
             }
-            __syncwarp();          // before the stage is filled again
-            stage = stage == kTileStages - 1 ? 0 : stage + 1;
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
         }
         copies_wait<0>();
+        meet();
     };
-    auto block_of = [&](int page) {
-        const int blk = table[page];
-        return (unsigned)blk < (unsigned)a.NB ? blk : -1;
+    auto entry = [&](int page, int rows) {
+        const int blk = table[page], first = page << a.bs_log2;
+        // (an entry without a block is passed over)
+        const int count = (unsigned)blk < (unsigned)a.NB ? min(1 << a.bs_log2, pos0 + 31 - __clz(rows) - first + 1) : 0;
+        return Page{((head + (int64_t)max(blk, 0) * a.Hkv) << a.bs_log2) * D, first, max(count, 0) << 8 | rows};
     };
 
     for (int i = tid; i < (seen + 15) / 16; i += THREADS) reinterpret_cast<uint4 *>(s_rows)[i] = make_uint4(0, 0, 0, 0);
@@ -723,10 +744,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
             }
             if (mine)
                 for (int i = 0; i < PER; ++i)
-                    if (p + i < seen && rows_of[p + i]) {
-                        s_page[before] = (p + i) << 8 | rows_of[p + i];
-                        s_blk[before++] = block_of(p + i);
-                    }
+                    if (p + i < seen && rows_of[p + i]) s_list[before++] = entry(p + i, rows_of[p + i]);
             __syncthreads();
             attend(all);
             __syncthreads();
@@ -745,18 +763,19 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
         w.leave(part[warp], lane);
         __syncthreads();
         // what each warp counts for in a row's sum, then 8 dims at a time
-        if (tid < 16) {
-            float top = part[0].m[tid], z = 0.f;
+        if (tid < 16 * MT) {
+            const Partial<D, 2> *p = part + tid / 16;          // part[split * MT + mt]
+            const int c = tid % 16;
+            float top = -INFINITY, z = 0.f, f[SPLITS];
 #pragma unroll
-            for (int i = 1; i < kWarps; ++i) top = fmaxf(top, part[i].m[tid]);
+            for (int i = 0; i < SPLITS; ++i) top = fmaxf(top, p[i * MT].m[c]);
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                const float f = share(part[i].m[tid], part[i].l[tid], top);
-                z += f * part[i].l[tid];
-                s_share[i][tid] = f;
+            for (int i = 0; i < SPLITS; ++i) {
+                f[i] = share(p[i * MT].m[c], p[i * MT].l[c], top);
+                z += f[i] * p[i * MT].l[c];
             }
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) s_share[i][tid] = z == 0.f ? 0.f : s_share[i][tid] / z;
+            for (int i = 0; i < SPLITS; ++i) s_share[i][tid] = z == 0.f ? 0.f : f[i] / z;
             if (tid >= c0 && tid < c1 && a.lse)
                 a.lse[q_row(tid)] = z == 0.f ? -INFINITY : (top + log2f(z)) * 0.69314718055994531f;
         }
@@ -765,10 +784,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
             const int c = x / CH, e = x % CH * 8;
             float sum[8] = {};
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
+            for (int i = 0; i < SPLITS; ++i) {
                 const float f = s_share[i][c];
-                const float4 u = *reinterpret_cast<const float4 *>(&part[i].o[c][e]);
-                const float4 v = *reinterpret_cast<const float4 *>(&part[i].o[c][e + 4]);
+                const float *p = &part[i * MT + c / 16].o[c % 16][e];
+                const float4 u = *reinterpret_cast<const float4 *>(p), v = *reinterpret_cast<const float4 *>(p + 4);
                 // (a warp that saw no key counts for nothing, whatever it holds)
                 if (f != 0.f) {
                     sum[0] += f * u.x; sum[1] += f * u.y; sum[2] += f * u.z; sum[3] += f * u.w;
@@ -796,8 +815,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
             __syncthreads();
             for (int i = tid; i < n; i += THREADS) {
                 const int page = page_of(q, i0 + i);
-                s_page[i] = page < 0 ? 0 : page << 8 | 1 << q;
-                s_blk[i] = page < 0 ? -1 : block_of(page);
+                s_list[i] = page < 0 ? Page{0, 0, 0} : entry(page, 1 << q);
             }
             __syncthreads();
             attend(n);
@@ -821,32 +839,35 @@ cudaError_t launch_sparse(SparseArgs a, cudaStream_t stream) {
                          sizeof(Partial<D, NT>) * kWarps, a.ctas, stream, a);
 }
 
-template <int D>
-cudaError_t launch_tile(const SparseArgs &a, int64_t tiles, cudaStream_t stream) {
-    constexpr size_t ring = (size_t)kWarps * kTileStages * 64 * D, parts = sizeof(Partial<D, 2>) * kWarps;
+template <int D, int MT>
+cudaError_t launch_tile(const SparseArgs &a, cudaStream_t stream) {
+    constexpr size_t ring = (size_t)kTileSteps * 64 * D, parts = sizeof(Partial<D, 2>) * kWarps;
     constexpr size_t bytes = kTileMap + (ring > parts ? ring : parts);
     static std::once_flag once[kMaxDevices];
     static bool ok[kMaxDevices];
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(sparse_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        ok[dev] = cudaFuncSetAttribute(sparse_tile_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)bytes) == cudaSuccess;
     });
     if (!ok[dev]) return cudaErrorInvalidDevice;
-    return launch_behind(sparse_tile_kernel<D>, dim3((unsigned)tiles, (unsigned)(a.L * a.Hkv)), 32 * kWarps, bytes, 1,
-                         stream, a);
+    const dim3 grid((unsigned)QueryRows::tiles(a.rows.T, a.rows.S, a.qt), (unsigned)(a.L * a.Hkv));
+    return launch_behind(sparse_tile_kernel<D, MT>, grid, 32 * kWarps, bytes, 1, stream, a);
 }
 
 template <int D>
 cudaError_t launch_for(SparseArgs a, cudaStream_t stream) {
-    // rows of a chunk by tiles, where a tile holds two or more of them and
-    // there is a CTA for every place on the GPU (two per SM); single rows
-    // spread over clusters otherwise
-    a.qt = std::min(8, 16 / a.G);
-    if (a.rows.start && a.qt > 1 && a.rows.MB <= kTilePages && a.L * a.Hkv <= 65535 &&
-        (int64_t)(a.rows.T / a.qt) * a.L * a.Hkv >= 2LL * device_sm_count())
-        return launch_tile<D>(a, QueryRows::tiles(a.rows.T, a.rows.S, a.qt), stream);
+    // rows of a chunk by tiles of 32 (query, head) rows where that gives a CTA
+    // for two places of every SM, by tiles of 16 where those do; single rows,
+    // spread over clusters when they are few, otherwise
+    if (a.rows.start && a.rows.MB <= kTilePages && a.L * a.Hkv <= 65535) {
+        auto many = [&](int qt) { return (int64_t)(a.rows.T / qt) * a.L * a.Hkv >= 2LL * device_sm_count(); };
+        a.qt = std::min(8, 32 / a.G);
+        if (a.qt > 1 && a.qt * a.G > 16 && many(a.qt)) return launch_tile<D, 2>(a, stream);
+        a.qt = std::min(8, 16 / a.G);
+        if (a.qt > 1 && many(a.qt)) return launch_tile<D, 1>(a, stream);
+    }
     return a.G <= 8 ? launch_sparse<D, 1>(a, stream) : launch_sparse<D, 2>(a, stream);
 }
 

@@ -482,3 +482,35 @@ def test_chunks_of_padded_rows_and_short_sequences():
     want, wl, mag = sparse_want(b, sel[:, :340])
     got = out[:, :340].double().cpu().numpy()
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * mag).all()
+
+
+# shapes whose tiles hold more than 16 (query, head) rows
+WIDE = [((32, 8), 128, 32, [1000, 77, 600], [333, 1, 316]), ((16, 4), 64, 16, [400], [330]),
+        ((24, 2), 128, 16, [300], [170]), ((16, 2), 64, 64, [2000, 90], [290, 60]), ((10, 2), 128, 16, [520], [470])]
+
+
+@pytest.mark.parametrize("heads,d,bs,lens,q_lens", WIDE)
+def test_wide_chunks(heads, d, bs, lens, q_lens):
+    b = Batch(lens, q_lens, heads, d, bs, L=2, seed=24)
+    sel = like_neighbours(b, 9)
+    x = check_sparse(b, sel)
+    y = check_sparse(b, sel)
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    check_sparse(b, some_pages(b, 7))
+
+
+@pytest.mark.parametrize("heads,d,bs,lens,q_lens", WIDE)
+def test_wide_chunks_with_repeated_and_unseen(heads, d, bs, lens, q_lens):
+    b = Batch(lens, q_lens, heads, d, bs, L=2, seed=25)
+    sel = like_neighbours(b, 9)
+    sel[:, 5, 0, 3] = sel[:, 5, 0, 2]
+    sel[1, 40] = 0
+    sel[0, 50] = -1
+    sel[0, 51, 0] = [-3, 2 ** 31 - 1, -2 ** 31, 5000, 20000, -1, 4096, 1 << 24, 0]
+    # a page that one row of its tile names holds a NaN and an infinite value
+    sel[:, 64:96, 1] = -1
+    sel[:, 64:96, 1, 0] = 0
+    sel[:, 70, 1, 1] = 1
+    b.v[:, int(b.tables[0, 1]), 1, 2, 3] = math.nan
+    b.v[:, int(b.tables[0, 1]), 1, 4] = math.inf
+    check_sparse(b, sel)
