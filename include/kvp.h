@@ -668,10 +668,11 @@ typedef struct {
  * caches, whose slots are no positions; draft trees, whose nodes share
  * depths), or NULL: the slots that the tokens take in their sequences.
  * Semantics, copy-on-write and errors of seq_append_batch, all or nothing;
- * KVP_ERR_INVALID also for a rotation outside the above.  One kernel for
- * appends of up to 512 sequences and 4096 pages, no workspace.  A batch whose
- * ntoks are all 0 does nothing.  After KVP_ERR_CUDA from a launch the
- * bookkeeping stands.
+ * KVP_ERR_INVALID also for a rotation outside the above, KVP_ERR_STATE also
+ * while `stream` is being captured (a replay would write the same slots again).
+ * One kernel for appends of up to 512 sequences, 512 copied blocks and 4096
+ * pages; no workspace.  A batch whose ntoks are all 0 does nothing.  After
+ * KVP_ERR_CUDA from a launch the bookkeeping stands.
  */
 int seq_append_rope(kvp_pool *pool, int32_t nseq, const int32_t *seqs, const int32_t *ntoks, const void *k,
                     const void *v, const kvp_rope_desc *rope, const int32_t *positions, const void *q, void *q_out,
@@ -699,7 +700,10 @@ int seq_reorder(kvp_pool *pool, const int32_t *dst, const int32_t *src, int32_t 
  * padded batch) are left as they are.  A query at position p sees the tokens
  * up to p, in the pages 0 .. p / bs of its sequence; page j is table entry j.
  * A length above max_blocks * bs counts as that.  desc as for
- * paged_decode_attention (bf16 pages; use_sharing is not used).
+ * paged_decode_attention (bf16 pages; use_sharing is not used), layers * kv
+ * heads at most 65535.  These calls, kvp_beam_select and kvp_state_reorder
+ * return KVP_ERR_STATE on the legacy default stream while a stream that
+ * synchronises with it is being captured.
  *
  * kvp_page_bounds: for every layer, kv head and page that holds one of the
  * last n_new tokens of a sequence (n_new >= its length: every page), the
@@ -710,7 +714,7 @@ int seq_reorder(kvp_pool *pool, const int32_t *dst, const int32_t *src, int32_t 
  * seq_accept_draft, seq_evict.  NaN keys give NaN bounds.  A page listed
  * with different lengths (a shared page that one sequence was cut back in)
  * must be refreshed by the longer one's call last.  Table entries outside
- * [0, NB) are passed over.
+ * [0, NB) are passed over.  At most 65535 sequences a call.
  */
 int kvp_page_bounds(const void *k_pool, const int32_t *block_tables, const int32_t *seq_lens, int32_t num_seqs,
                     int32_t max_blocks, int32_t n_new, const kvp_attn_desc *desc, void *bounds, void *stream);
@@ -776,8 +780,10 @@ int paged_sparse_attention(const void *q, const int32_t *q_start, int32_t num_q,
  * nothing above -inf, gives no continuation, nor does a logit of -inf (a
  * masked token).  out_scores fp32, out_rows (r) and out_tokens (x) int32, all
  * [groups][n_out]; where there are fewer than n_out continuations: -inf, -1
- * and -1.  1 <= beams <= 128, 1 <= n_out <= 128.  Log-sum-exps and the
- * comparison are in 64 bits (exponentials in 32), the results rounded to fp32.
+ * and -1.  1 <= beams <= 128, 1 <= n_out <= 128.  Exponentials are fp32; sums
+ * of them and the scores that are compared are pairs of fp32 numbers (48
+ * bits), the results rounded to fp32.  A score below fp32's range counts as
+ * none.
  * workspace: 16-byte aligned, ws_bytes >= kvp_beam_workspace_size() (0 on
  * invalid input), its content does not matter; one call at a time.  May be
  * captured into a graph.

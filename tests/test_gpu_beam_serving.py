@@ -152,3 +152,47 @@ def test_beam_search_loop():
         kvp.seq_free(pool, s)
     assert kvp.kvp_free_block_count(pool) == NB
     kvp.kv_pool_destroy(pool)
+
+
+def test_default_stream_beside_a_capture_is_refused():
+    """The legacy default stream cannot be used while a stream that synchronises with it is captured: every call says
+    so before anything changes, and the capture goes on."""
+    import ctypes
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    kp, vp, bounds = torch.zeros(1, 8, 1, bs, d, **bf16), torch.zeros(1, 8, 1, bs, d, **bf16), torch.zeros(1, 8, 1, 2, d, **bf16)
+    pool = kvp.kv_pool_create(kvp.PoolDesc(1, 8, bs, 1, d, 2, 8, 0), kp, vp)
+    a = kvp.seq_alloc(pool)
+    desc = kvp.AttnDesc(1, 2, 1, d, bs, 8, 0.0, 0)
+    q, out = torch.zeros(1, 1, 2, d, **bf16), torch.zeros(1, 1, 2, d, **bf16)
+    new = torch.zeros(1, 3, 1, d, **bf16)
+    t, n = torch.zeros(1, 8, dtype=torch.int32, device="cuda"), torch.full((1,), 40, dtype=torch.int32, device="cuda")
+    sc, sel = torch.zeros(1, 1, 1, 8, device="cuda"), torch.zeros(1, 1, 1, 2, dtype=torch.int32, device="cuda")
+    x, cum = torch.zeros(1, 2, 100, device="cuda"), torch.zeros(1, 2, device="cuda")
+    best, row, tok = torch.zeros(1, 2, device="cuda"), *(torch.zeros(1, 2, dtype=torch.int32, device="cuda") for _ in range(2))
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    src, dst = torch.zeros(2, 8, device="cuda"), torch.ones(2, 8, device="cuda")
+    torch.cuda.synchronize()
+    cu = ctypes.CDLL("libcuda.so.1")
+    s, g = ctypes.c_void_p(), ctypes.c_void_p()
+    assert cu.cuStreamCreate(ctypes.byref(s), 0) == 0
+    assert cu.cuStreamBeginCapture_v2(s, 1) == 0         # a capture of this thread's
+    codes = []
+    for call in (lambda: kvp.seq_append_rope(pool, [a], [3], new, new, kvp.rope_desc(d), stream=0),
+                 lambda: kvp.kvp_page_bounds(kp, t, n, 1, desc, bounds, stream=0),
+                 lambda: kvp.kvp_page_scores(q, None, bounds, t, n, desc, sc, stream=0),
+                 lambda: kvp.kvp_page_select(sc, None, n, desc, 0, 1, sel, stream=0),
+                 lambda: kvp.paged_sparse_attention(q, None, kp, vp, t, n, sel, desc, out, None, stream=0),
+                 lambda: kvp.kvp_beam_select(x, cum, None, 0, best, row, tok, ws, stream=0),
+                 lambda: kvp.kvp_state_reorder(src, dst, row.view(-1), stream=0)):
+        try:
+            call()
+            codes.append(0)
+        except kvp.KvpError as e:
+            codes.append(e.code)
+    ended = cu.cuStreamEndCapture(s, ctypes.byref(g))
+    cu.cuStreamDestroy_v2(s)
+    assert codes == [kvp.KVP_ERR_STATE] * 7 and ended == 0
+    assert kvp.seq_len(pool, a) == 0 and kvp.kvp_free_block_count(pool) == 8
+    torch.cuda.synchronize()
+    assert float(dst.sum()) == 16
+    kvp.kv_pool_destroy(pool)
