@@ -286,6 +286,9 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     const uint32_t b = __float_as_uint(x + 0.f);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float key_score(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
 constexpr uint32_t kStays = 0xffffffffu;    // sinks and the last pages: above every score
 
 // The larger of two lanes' keys to the lower lane, down to a descending warp.
@@ -321,18 +324,21 @@ __device__ __forceinline__ void find_cut(int bits, int k, uint32_t &cut, int &ab
 }
 
 // A CTA per (layer, query row, kv head) of at most W * 32 * E pages: k = budget
-// - sinks - last pages of those in between are to be found, whose keys are in
-// registers (page sink + W * 32 e + thread; steps past the end are as low as
-// -inf and behind every page of that score).
-//   1. A bound that at least k keys reach, from the threads' maxima: each
+// - sinks - last pages of those in between are to be found.  Page sink + W * 32
+// e + thread is the thread's e-th.
+//   1. The scores, rounded to bf16 and packed in pairs (rounding keeps the
+//      order, if not strictly), which is what most of them are looked at as:
+//      half of the registers and of the instructions.
+//   2. A bound that at least k of them reach, from the threads' maxima: each
 //      warp's ceil(k / W)-th largest maximum, the smallest of those.
-//   2. The keys that reach it, few more than k, go on the warps' lists, and
-//      one warp finds the k-th largest of them bit by bit (all warps over all
-//      keys where the lists do not hold them).
-//   3. Keys above it, and those equal to it, as two bit maps by page; counts
+//   3. The pages that reach it (a NaN always does), few more than k, go on the
+//      warps' lists with their scores as they are, and one warp finds the k-th
+//      largest of those.  Where the lists do not hold them (many equal scores,
+//      k above W * 32), all warps look through all keys instead.
+//   4. Keys above it, and those equal to it, as two bit maps by page; counts
 //      up to a word give every chosen page its place.
 template <int W, int E>
-__global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(32 * W, W <= 8 ? 48 / W : 1) page_select_kernel(const SelectArgs a) {
     constexpr int WORDS = W * E, PER = (WORDS + 32 * W - 1) / (32 * W), STEP = 32 * W;
     __shared__ uint32_t s_key[W][kSelCap];
     __shared__ uint16_t s_at[W][kSelCap];
@@ -354,49 +360,67 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
         for (int j = tid; j < a.budget; j += STEP) out[j] = j < n ? j : -1;
         return;
     }
-    uint32_t key[E];
+    // pair i: pages 2 i (low half) and 2 i + 1 of the thread
+    __nv_bfloat162 pair[E / 2];
     {
         float x[E];
+        if (len == STEP * E) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = e * STEP + tid < len ? __ldcs(score + e * STEP + tid) : -INFINITY;
+            for (int e = 0; e < E; ++e) x[e] = __ldg(score + e * STEP + tid);
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) key[e] = score_key(x[e]);
+            for (int e = 0; e < E; ++e) x[e] = e * STEP + tid < len ? __ldg(score + e * STEP + tid) : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) pair[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     }
     for (int j = tid; j < lo; j += STEP) out[j] = j;
     for (int j = tid; j < a.recent; j += STEP) out[a.budget - a.recent + j] = n - a.recent + j;
     if (k == 0) return;
     out += lo;
-    uint32_t top = key[0];
-#pragma unroll
-    for (int e = 1; e < E; ++e) top = max(top, key[e]);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         if (tid + i * STEP < WORDS) s_up[tid + i * STEP] = s_eq[tid + i * STEP] = 0;
     const bool few = k <= STEP;
+    uint32_t bound = 0;
     if (few) {
-        top = sort_warp(top, lane);
+        __nv_bfloat162 most = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) most = __hmax2(most, pair[i]);      // (a NaN is not taken)
+        const uint32_t top = sort_warp(score_key(fmaxf(__low2float(most), __high2float(most))), lane);
         if (lane == (k + W - 1) / W - 1) s_warp[warp] = top;
     }
     __syncthreads();
-    uint32_t bound = 0;
+    uint32_t mine = 0;               // the thread's pages that reach the bound, even ones in the low half
     if (few) {
         bound = s_warp[0];
 #pragma unroll
         for (int w = 1; w < W; ++w) bound = min(bound, s_warp[w]);
-    }
-    int hits = 0;
+        const __nv_bfloat162 least = __float2bfloat162_rn(key_score(bound));
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const uint32_t any = __ballot_sync(0xffffffffu, key[e] >= bound);
-        if (any == 0) continue;
-        const int at = hits + __popc(any & ((1u << lane) - 1u));
-        if (key[e] >= bound && at < kSelCap) {
-            s_key[warp][at] = key[e];
-            s_at[warp][at] = (uint16_t)(e * STEP + tid);
-        }
-        hits += __popc(any);
+        for (int i = 0; i < E / 2; ++i) mine |= __hgeu2_mask(pair[i], least) & (0x10001u << i);
+        const int have = max(0, min(E, (len - tid + STEP - 1) / STEP));
+        mine &= ((1u << (have + 1) / 2) - 1u) | ((1u << have / 2) - 1u) << 16;
     }
-    if (lane == 0) s_hits[warp] = hits;
+    int at = __popc(mine);
+    int hits = at;                   // up to this lane, then all of the warp's
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, hits, o);
+        if (lane >= o) hits += y;
+    }
+    at = hits - at;
+    hits = __shfl_sync(0xffffffffu, hits, 31);
+    while (mine) {
+        const int b = __ffs(mine) - 1;
+        mine &= mine - 1;
+        if (at < kSelCap) s_at[warp][at] = (uint16_t)((2 * (b & 15) + (b >> 4)) * STEP + tid);
+        ++at;
+    }
+    __syncwarp();
+    if (hits <= kSelCap)
+        for (int i = lane; i < hits; i += 32) s_key[warp][i] = score_key(score[s_at[warp][i]]);
+    if (lane == 0) s_hits[warp] = few ? hits : kSelCap + 1;
     __syncthreads();
     int most = 0;
 #pragma unroll
@@ -407,31 +431,38 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
         if (warp == 0) {
             constexpr int H = W <= 8 ? 2 : 1;        // 32 * H keys of each list in registers
             uint32_t x[W * H];
-            uint32_t differ = 0;
+            uint32_t any = 0, all = 0xffffffffu;
 #pragma unroll
             for (int w = 0; w < W; ++w)
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    const int at = 32 * i + lane;
-                    x[w * H + i] = at < (int)s_hits[w] ? s_key[w][at] : 0u;
-                    if (at < (int)s_hits[w]) differ |= x[w * H + i] ^ bound;
+                    const int j = 32 * i + lane;
+                    x[w * H + i] = j < (int)s_hits[w] ? s_key[w][j] : 0u;
+                    if (j < (int)s_hits[w]) {
+                        any |= x[w * H + i];
+                        all &= x[w * H + i];
+                    }
                 }
             if (most > 32 * H)
                 for (int w = 0; w < W; ++w)
-                    for (int at = 32 * H + lane; at < (int)s_hits[w]; at += 32) differ |= s_key[w][at] ^ bound;
+                    for (int j = 32 * H + lane; j < (int)s_hits[w]; j += 32) {
+                        any |= s_key[w][j];
+                        all &= s_key[w][j];
+                    }
             auto count = [&](uint32_t t) {           // keys of at least t
                 int c = 0;
 #pragma unroll
                 for (int i = 0; i < W * H; ++i) c += x[i] >= t;
                 if (most > 32 * H)
                     for (int w = 0; w < W; ++w)
-                        for (int at = 32 * H + lane; at < (int)s_hits[w]; at += 32) c += s_key[w][at] >= t;
+                        for (int j = 32 * H + lane; j < (int)s_hits[w]; j += 32) c += s_key[w][j] >= t;
                 return (int)__reduce_add_sync(0xffffffffu, c);
             };
-            // the bits that the bound and every key share need no test
-            differ = __reduce_or_sync(0xffffffffu, differ);
-            const int bits = differ ? 32 - __clz(differ) : 0;
-            cut = bits == 32 ? 0u : bound >> bits << bits;
+            // the leading bits that all keys share need no test
+            any = __reduce_or_sync(0xffffffffu, any);
+            all = __reduce_and_sync(0xffffffffu, all);
+            const int bits = any != all ? 32 - __clz(any ^ all) : 0;
+            cut = bits == 32 ? 0u : all >> bits << bits;
             find_cut(bits, k, cut, above, count);
             if (lane == 0) {
                 s_cut = cut;
@@ -443,11 +474,15 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
         above = s_above;
         for (int i = lane; i < hits; i += 32) {
             const uint32_t x = s_key[warp][i];
-            const int at = s_at[warp][i];
-            if (x > cut) atomicOr(&s_up[at >> 5], 1u << (at & 31));
-            if (x == cut) atomicOr(&s_eq[at >> 5], 1u << (at & 31));
+            const int j = s_at[warp][i];
+            if (x > cut) atomicOr(&s_up[j >> 5], 1u << (j & 31));
+            if (x == cut) atomicOr(&s_eq[j >> 5], 1u << (j & 31));
         }
     } else {
+        // (steps past the end are as low as -inf, and behind every page of that score)
+        uint32_t key[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) key[e] = score_key(e * STEP + tid < len ? score[e * STEP + tid] : -INFINITY);
         auto count = [&](uint32_t t) {               // keys of at least t
             int c = 0;
 #pragma unroll
@@ -475,15 +510,15 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
     // places: words in page order, PER to a thread; counts of both maps in the
     // halves of one word
     static_assert(STEP * E <= 32768, "two 16-bit counts");
-    uint32_t up[PER], eq[PER], mine = 0;
+    uint32_t up[PER], eq[PER], here = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int w = tid * PER + i;
         up[i] = w < WORDS ? s_up[w] : 0u;
         eq[i] = w < WORDS ? s_eq[w] : 0u;
-        mine += __popc(up[i]) + (__popc(eq[i]) << 16);
+        here += __popc(up[i]) + (__popc(eq[i]) << 16);
     }
-    uint32_t before = mine;
+    uint32_t before = here;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
@@ -491,7 +526,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 32 / W : 1) page_select_kerne
     }
     if (lane == 31) s_warp[warp] = before;
     __syncthreads();
-    before -= mine;
+    before -= here;
 #pragma unroll
     for (int w = 0; w < W; ++w)
         if (w < warp) before += s_warp[w];
