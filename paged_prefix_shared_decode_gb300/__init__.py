@@ -918,23 +918,25 @@ def kvp_beam_select(logits, scores, finished, pad_token: int, out_scores, out_ro
     and out_tokens int32 [G][n]."""
     torch, dev, st = _here(stream)
     G, B, V = logits.shape
-    types = {torch.float32: KVP_F32, torch.bfloat16: KVP_BF16, torch.float16: KVP_F16}
-    if logits.dtype not in types or logits.get_device() != dev:
+    kind = {torch.float32: KVP_F32, torch.bfloat16: KVP_BF16, torch.float16: KVP_F16}.get(logits.dtype)
+    if kind is None or logits.get_device() != dev:
         raise ValueError(f"logits: expected float32, bfloat16 or float16 on cuda:{dev}, got {logits.dtype} on "
                          f"{logits.device}")
-    row = logits.stride(1) if B > 1 else logits.stride(0) if G > 1 else V
-    if (V > 1 and logits.stride(2) != 1) or (G > 1 and logits.stride(0) != B * row):
+    group, row, step = logits.stride()
+    if B == 1:
+        row = group if G > 1 else V
+    if (V > 1 and step != 1) or (G > 1 and group != B * row):
         raise ValueError(f"logits: expected evenly spaced contiguous rows, got strides {logits.stride()}")
-    if finished is not None and finished.dtype not in (torch.bool, torch.uint8):
-        raise ValueError(f"finished: expected bool or uint8, got {finished.dtype}")
-    n, i32 = out_scores.shape[-1], torch.int32
-    _check(load().kvp_beam_select(logits.data_ptr(), types[logits.dtype], row,
-                                  _arg("scores", scores, torch.float32, (G, B), dev),
-                                  finished if finished is None else
-                                  _arg("finished", finished, finished.dtype, (G, B), dev), pad_token, G, B, V, n,
-                                  _arg("out_scores", out_scores, torch.float32, (G, n), dev),
-                                  _arg("out_rows", out_rows, i32, (G, n), dev),
-                                  _arg("out_tokens", out_tokens, i32, (G, n), dev), _dev(workspace),
+    if finished is not None:
+        if finished.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"finished: expected bool or uint8, got {finished.dtype}")
+        finished = _arg("finished", finished, finished.dtype, (G, B), dev)
+    n = out_scores.shape[-1]
+    i32, f32, shape = torch.int32, torch.float32, (G, n)
+    _check(load().kvp_beam_select(logits.data_ptr(), kind, row, _arg("scores", scores, f32, (G, B), dev), finished,
+                                  pad_token, G, B, V, n, _arg("out_scores", out_scores, f32, shape, dev),
+                                  _arg("out_rows", out_rows, i32, shape, dev),
+                                  _arg("out_tokens", out_tokens, i32, shape, dev), _dev(workspace),
                                   _ws_bytes(workspace, ws_bytes), st), "kvp_beam_select")
 
 
@@ -942,15 +944,16 @@ def kvp_state_reorder(src, dst, index, dim: int = 0, stream=None):
     """dst row i = src row index[i] along dimension `dim` (the ones before it
     are outer); index: device int32, as many as dst has rows, in any shape."""
     torch, dev, st = _here(stream)
-    outer, inner = src.shape[:dim], src.shape[dim + 1:]
-    n_src, n_dst = src.shape[dim], dst.shape[dim]
+    shape, dtype = src.shape, src.dtype
+    n_src, n_dst = shape[dim], dst.shape[dim]
     if index.numel() != n_dst:
         raise ValueError(f"index: expected {n_dst} entries, got {index.numel()}")
-    size = src.element_size()
-    _check(load().kvp_state_reorder(_arg("src", src, src.dtype, src.shape, dev),
-                                    _arg("dst", dst, src.dtype, (*outer, n_dst, *inner), dev),
-                                    _arg("index", index, torch.int32, index.shape, dev), math.prod(outer), n_src, n_dst,
-                                    math.prod(inner) * size, st), "kvp_state_reorder")
+    outer = 1 if dim == 0 else math.prod(shape[:dim])
+    row = math.prod(shape[dim + 1:]) * src.element_size()
+    want = shape if n_src == n_dst else (*shape[:dim], n_dst, *shape[dim + 1:])
+    _check(load().kvp_state_reorder(_arg("src", src, dtype, shape, dev), _arg("dst", dst, dtype, want, dev),
+                                    _arg("index", index, torch.int32, index.shape, dev), outer, n_src, n_dst, row, st),
+           "kvp_state_reorder")
 
 
 def kvp_device_error(workspace, stream=None) -> int:
