@@ -296,8 +296,9 @@ __device__ __forceinline__ void join_warps(const Partial<D, NT> *part, int c, in
 }
 
 // One query row (and up to 8 NT heads of a group) per cluster of CTAs.
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) sparse_attn_kernel(const SparseArgs a) {
+// OCC: CTAs per SM that the registers are cut for.
+template <int D, int NT, int OCC>
+__global__ void __launch_bounds__(32 * kWarps, OCC) sparse_attn_kernel(const SparseArgs a) {
     constexpr int H = 8 * NT;
     extern __shared__ __align__(16) unsigned char smem[];
     Partial<D, NT> *part = reinterpret_cast<Partial<D, NT> *>(smem);
@@ -824,7 +825,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) sparse_tile_kernel(const Spars
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, int OCC>
 cudaError_t launch_sparse(SparseArgs a, cudaStream_t stream) {
     a.parts = (a.G + 8 * NT - 1) / (8 * NT);
     const int64_t units = (int64_t)a.L * a.rows.T * a.Hkv * a.parts;
@@ -835,7 +836,7 @@ cudaError_t launch_sparse(SparseArgs a, cudaStream_t stream) {
     while (a.ctas < kMaxCtas && units * a.ctas * 2 <= 2LL * device_sm_count() && tiles >= 2LL * kWarps * a.ctas * 2)
         a.ctas *= 2;
     if (units * a.ctas > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_behind(sparse_attn_kernel<D, NT>, dim3((unsigned)(units * a.ctas)), 32 * kWarps,
+    return launch_behind(sparse_attn_kernel<D, NT, OCC>, dim3((unsigned)(units * a.ctas)), 32 * kWarps,
                          sizeof(Partial<D, NT>) * kWarps, a.ctas, stream, a);
 }
 
@@ -868,7 +869,12 @@ cudaError_t launch_for(SparseArgs a, cudaStream_t stream) {
         a.qt = std::min(8, 16 / a.G);
         if (a.qt > 1 && many(a.qt)) return launch_tile<D, 1>(a, stream);
     }
-    return a.G <= 8 ? launch_sparse<D, 1>(a, stream) : launch_sparse<D, 2>(a, stream);
+    if (a.G > 8) return launch_sparse<D, 2, 2>(a, stream);
+    // three CTAs per SM have the registers to load faster (256 of 128 pages at
+    // head dim 128: 50 us, with four 64), four come in fewer rounds where three
+    // do not hold all rows (512: 89 us against 112, 1024: 173 against 183)
+    const bool all = (int64_t)a.L * a.rows.T * a.Hkv <= 3LL * device_sm_count();
+    return all ? launch_sparse<D, 1, 3>(a, stream) : launch_sparse<D, 1, 4>(a, stream);
 }
 
 bool bad(const void *p, uintptr_t align) { return !p || ((uintptr_t)p & (align - 1)); }
