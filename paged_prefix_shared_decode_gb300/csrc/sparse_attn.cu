@@ -829,12 +829,13 @@ template <int D, int NT, int OCC>
 cudaError_t launch_sparse(SparseArgs a, cudaStream_t stream) {
     a.parts = (a.G + 8 * NT - 1) / (8 * NT);
     const int64_t units = (int64_t)a.L * a.rows.T * a.Hkv * a.parts;
-    // few rows: several CTAs to each, as long as all of them run at once and
-    // each warp has a tile or two
+    // few rows: several CTAs to each, as long as all of them run at once (three
+    // fit on an SM, four at head dim 64) and each warp has a tile or two.  (24
+    // sequences of 128 pages at head dim 128: two each 38 us, one 46; 32 four
+    // each, which do not fit, 66 against 50.)
     a.ctas = 1;
-    const int64_t tiles = (int64_t)a.budget << (a.bs_log2 - 4);
-    while (a.ctas < kMaxCtas && units * a.ctas * 2 <= 2LL * device_sm_count() && tiles >= 2LL * kWarps * a.ctas * 2)
-        a.ctas *= 2;
+    const int64_t tiles = (int64_t)a.budget << (a.bs_log2 - 4), places = (D == 64 ? 4LL : 3LL) * device_sm_count();
+    while (a.ctas < kMaxCtas && units * a.ctas * 2 <= places && tiles >= 2LL * kWarps * a.ctas * 2) a.ctas *= 2;
     if (units * a.ctas > INT32_MAX) return cudaErrorInvalidValue;
     return launch_behind(sparse_attn_kernel<D, NT, OCC>, dim3((unsigned)(units * a.ctas)), 32 * kWarps,
                          sizeof(Partial<D, NT>) * kWarps, a.ctas, stream, a);
