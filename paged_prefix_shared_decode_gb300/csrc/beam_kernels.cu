@@ -41,6 +41,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kPer = 32;                       // logits per thread
 constexpr int kChunk = kThreads * kPer;
+constexpr int kUneven = kChunk - 8;            // chunk of a row off 16-byte boundaries (8 logits at most in 16 bytes)
 constexpr int kMaxOut = 128, kMaxBeams = 128;
 constexpr int kCap = 1024;                     // candidates ranked at once
 
@@ -57,7 +58,7 @@ struct BeamArgs {
     const float *scores;
     const uint8_t *finished;
     int32_t pad, groups, beams, vocab, n, chunks;
-    int32_t vec;                  // rows may be read 16 bytes at a time
+    int32_t step;                 // logits of a chunk
     int32_t early;                // the join may start beside the parts' CTAs
     uint32_t div;                 // 2^32 / (chunks * n), rounded up; 0: too large for that
     float *out_scores;
@@ -146,35 +147,33 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
     griddep_wait();
     if (a.early) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (a.finished && a.finished[row]) return;
-    const int x0 = chunk * kChunk, len = min(kChunk, a.vocab - x0);
+    // logits x0 .. x0 + len - 1, the thread's k-th at place(tid, k) - shift: rows
+    // may begin anywhere, their 16-byte pieces are read whole all the same, and
+    // only the ends one by one
+    const int x0 = chunk * a.step, len = min(a.step, a.vocab - x0);
     const T *src = static_cast<const T *>(a.logits) + row * a.row_stride + x0;
+    const int shift = (int)((uintptr_t)src % 16 / sizeof(T));
+    const bool full = len == kChunk && shift == 0;
     float v[kPer];
-    if (a.vec) {
+    {
         uint4 raw[kPer / kVec<T>];
-        const bool full = len == kChunk;
 #pragma unroll
         for (int i = 0; i < kPer / kVec<T>; ++i) {
-            const int at = place<T>(tid, i * kVec<T>);
-            if (full || at + kVec<T> <= len) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + at));
+            const int at = place<T>(tid, i * kVec<T>) - shift;
+            if (full || (at >= 0 && at + kVec<T> <= len)) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + at));
         }
 #pragma unroll
         for (int i = 0; i < kPer / kVec<T>; ++i) {
+            const int at = place<T>(tid, i * kVec<T>) - shift;
             const T *e = reinterpret_cast<const T *>(&raw[i]);
+            if (full || (at >= 0 && at + kVec<T> <= len)) {
 #pragma unroll
-            for (int k = 0; k < kVec<T>; ++k) v[i * kVec<T> + k] = as_float(e[k]);
-        }
-        if (!full) {
+                for (int k = 0; k < kVec<T>; ++k) v[i * kVec<T> + k] = as_float(e[k]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int at = place<T>(tid, k);
-                if (at / kVec<T> * kVec<T> + kVec<T> > len) v[k] = at < len ? as_float(src[at]) : -INFINITY;
+                for (int k = 0; k < kVec<T>; ++k)
+                    v[i * kVec<T> + k] = (unsigned)(at + k) < (unsigned)len ? as_float(src[at + k]) : -INFINITY;
             }
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int at = place<T>(tid, k);
-            v[k] = at < len ? as_float(src[at]) : -INFINITY;
         }
     }
     constexpr int GROUP = 4;             // maxima of 4 logits: most reach no candidate
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
             if (v[k] >= bound) {
                 const int j = atomicAdd(&s_count, 1);
                 // (larger first, then the lower token)
-                if (j < kCap) s_key[j] = (uint64_t)order_key(v[k]) << 32 | (uint32_t)~place<T>(tid, k);
+                if (j < kCap) s_key[j] = (uint64_t)order_key(v[k]) << 32 | (uint32_t)~(place<T>(tid, k) - shift);
             }
     }
     __syncthreads();
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
         int at = INT_MAX;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int p = place<T>(tid, k);
+            const int p = place<T>(tid, k) - shift;
             const bool open = v[k] < last || (v[k] == last && p > last_at);
             if (open && (v[k] > best || (v[k] == best && p < at)) && v[k] > -INFINITY) {
                 best = v[k];
@@ -550,7 +549,7 @@ bool bad(const void *p, uintptr_t align) { return !p || ((uintptr_t)p & (align -
 bool beam_shape_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out) {
     if (groups <= 0 || beams <= 0 || beams > kMaxBeams || vocab <= 0 || vocab > (1 << 30) || n_out <= 0 || n_out > kMaxOut)
         return false;
-    const int64_t chunks = (vocab + kChunk - 1) / kChunk;
+    const int64_t chunks = (vocab + kUneven - 1) / kUneven;
     return groups * beams * chunks <= INT32_MAX && beams * chunks * n_out <= INT32_MAX / 2;
 }
 
@@ -578,7 +577,7 @@ extern "C" {
 
 size_t kvp_beam_workspace_size(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out) {
     if (!beam_shape_ok(groups, beams, vocab, n_out)) return 0;
-    const size_t parts = (size_t)groups * beams * ((vocab + kChunk - 1) / kChunk);
+    const size_t parts = (size_t)groups * beams * ((vocab + kUneven - 1) / kUneven);
     return parts * (sizeof(PartHead) + (size_t)n_out * 8);
 }
 
@@ -599,8 +598,10 @@ int kvp_beam_select(const void *logits, int32_t logits_type, int64_t row_stride,
     a.scores = scores;
     a.finished = finished;
     a.pad = pad_token; a.groups = groups; a.beams = beams; a.vocab = vocab; a.n = n_out;
-    a.chunks = (vocab + kChunk - 1) / kChunk;
-    a.vec = ((uintptr_t)logits & 15) == 0 && row_stride * size % 16 == 0;
+    // (rows off 16-byte boundaries: the pieces of a chunk reach over its ends)
+    const bool even = ((uintptr_t)logits & 15) == 0 && row_stride * size % 16 == 0;
+    a.step = even ? kChunk : kUneven;
+    a.chunks = (vocab + a.step - 1) / a.step;
     a.out_scores = out_scores; a.out_rows = out_rows; a.out_tokens = out_tokens;
     const size_t parts = (size_t)groups * beams * a.chunks;
     a.heads = static_cast<PartHead *>(workspace);
