@@ -60,7 +60,7 @@ struct BeamArgs {
     int32_t pad, groups, beams, vocab, n, chunks;
     int32_t step;                 // logits of a chunk
     int32_t early;                // the join may start beside the parts' CTAs
-    uint32_t div;                 // 2^32 / (chunks * n), rounded up; 0: too large for that
+    uint32_t div;                 // 2^32 / (chunks * beams), rounded up; 0: too large for that
     float *out_scores;
     int32_t *out_rows, *out_tokens;
     PartHead *heads;              // [rows][chunks]
@@ -79,22 +79,28 @@ __device__ __forceinline__ float key_value(uint64_t key) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 // The fourth largest of eight.
-__device__ __forceinline__ float fourth_of_8(float4 a, float4 b) {
-    auto order = [](float &x, float &y) {
-        const float t = fmaxf(x, y);
-        y = fminf(x, y);
+template <class T>
+__device__ __forceinline__ T fourth_of_8(const T *from) {
+    T a[4], b[4];
+    auto least = [](T x, T y) { return x < y ? x : y; };
+    auto most = [](T x, T y) { return x < y ? y : x; };
+    auto order = [&](T &x, T &y) {
+        const T t = most(x, y);
+        y = least(x, y);
         x = t;
     };
-    auto sort4 = [&](float4 &v) {
-        order(v.x, v.y);
-        order(v.z, v.w);
-        order(v.x, v.z);
-        order(v.y, v.w);
-        order(v.y, v.z);
+    auto sort4 = [&](T (&v)[4], const T *from) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = from[i];
+        order(v[0], v[1]);
+        order(v[2], v[3]);
+        order(v[0], v[2]);
+        order(v[1], v[3]);
+        order(v[1], v[2]);
     };
-    sort4(a);
-    sort4(b);
-    return fmaxf(fmaxf(fmaxf(a.w, b.w), fminf(a.y, b.y)), fmaxf(fminf(a.x, b.z), fminf(a.z, b.x)));
+    sort4(a, from);
+    sort4(b, from + 4);
+    return most(most(most(a[3], b[3]), least(a[1], b[1])), most(least(a[0], b[2]), least(a[2], b[0])));
 }
 
 __device__ __forceinline__ bool bigger(float x, float y) { return x > y; }
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
         all = fmaxf(all, s_max[w]);
         bound = fminf(bound, s_eighth[w]);
     }
-    bound = fmaxf(bound, fourth_of_8(*reinterpret_cast<const float4 *>(s_fourth), *reinterpret_cast<const float4 *>(s_fourth + 4)));
+    bound = fmaxf(bound, fourth_of_8(s_fourth));
     bound = fmaxf(bound, -FLT_MAX);      // -inf is no candidate
     PartHead *head = a.heads + (int64_t)row * a.chunks + chunk;
     float *cand = a.cand + ((int64_t)row * a.chunks + chunk) * a.n;
@@ -313,18 +319,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_part_kernel(const BeamArgs a
     }
 }
 
-// A candidate; its score (value and rest) as a whole number of the same order.
-struct Entry {
-    uint64_t key;
-    float logit;
-    int32_t beam, at;
+// A candidate's place in the order: its score (value and rest) as a whole number
+// of the same order, 0 for none; then the lower row, the higher logit, the lower
+// token.
+struct Place {
+    uint64_t score, tie;
 };
-// The order: score, then row, then logit, then token.
-__device__ __forceinline__ bool before(const Entry &x, const Entry &y) {
-    if (x.key != y.key) return x.key > y.key;
-    if (x.beam != y.beam) return x.beam < y.beam;
-    if (x.logit != y.logit) return x.logit > y.logit;
-    return x.at < y.at;
+__device__ __forceinline__ bool before(const Place &x, const Place &y) {
+    return x.score > y.score || (x.score == y.score && x.tie > y.tie);
 }
 
 constexpr int kHeld = 8;       // candidates a thread keeps in registers
@@ -332,26 +334,33 @@ constexpr int kHeld = 8;       // candidates a thread keeps in registers
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     __shared__ float2 s_add[kMaxBeams];     // score - log-sum-exp; -inf: no candidates
     __shared__ uint8_t s_done[kMaxBeams];
-    __shared__ uint64_t s_key[kCap];
-    __shared__ float s_logit[kCap];
-    __shared__ int s_at[kCap];
-    __shared__ uint8_t s_beam[kCap];
-    __shared__ uint64_t s_bound[kWarps];
+    __shared__ Place s_place[kCap];
+    __shared__ int s_token[kCap];
+    __shared__ uint64_t s_rank[4][kWarps];  // each warp's ceil(n / 8)-th, n / 4, n / 2 and n-th largest maximum
     __shared__ int s_count;
-    __shared__ Entry s_best[kWarps];
+    __shared__ Place s_best[kWarps];
+    __shared__ int s_best_token[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = blockIdx.x;
     griddep_wait();
-    const int per_beam = a.chunks * a.n, total = per_beam * a.beams;
+    const int lists = a.chunks * a.beams, per_beam = a.chunks * a.n, total = lists * a.n;
     const float *cand = a.cand + (int64_t)g * total;
     const int32_t *cand_at = a.cand_at + (int64_t)g * total;
+    // candidate x in the order in which threads take them: the best of every
+    // chunk first, then all second ones, and so on, so that the first few are
+    // most of what is looked for; where it lies
+    auto lies = [&](int x) {
+        const int rank = a.div ? (int)__umulhi(x, a.div) : x / lists;
+        return (x - rank * lists) * a.n + rank;
+    };
     float held[kHeld];
-    int held_at[kHeld];
+    int held_at[kHeld], held_in[kHeld];
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
-        const int i = tid + k * kThreads;
-        held[k] = i < total ? cand[i] : -INFINITY;
-        held_at[k] = i < total ? cand_at[i] : 0;
+        const int x = tid + k * kThreads;
+        held_in[k] = x < total ? lies(x) : 0;
+        held[k] = x < total ? cand[held_in[k]] : -INFINITY;
+        held_at[k] = x < total ? cand_at[held_in[k]] : 0;
     }
     for (int b = warp; b < a.beams; b += kWarps) {
         const int row = g * a.beams + b;
@@ -399,77 +408,85 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
             s_done[b] = done;
         }
     }
+    if (tid < 4 * kWarps) s_rank[tid / kWarps][tid % kWarps] = 0;
     if (tid == 0) s_count = 0;
     __syncthreads();
-    // candidate i: place i % per_beam of beam i / per_beam; a finished beam's
-    // one is its first
-    auto beam_of = [&](int i) { return a.div ? (int)__umulhi(i, a.div) : i / per_beam; };
-    auto key_of = [&](int i, float logit) -> uint64_t {      // 0: none
-        const int b = beam_of(i);
+    // the place of the candidate that lies at i; a finished beam's one is its
+    // first
+    auto place_of = [&](int i, float logit) -> Place {
+        const int b = i / per_beam;
         float2 add = s_add[b];
         if (s_done[b]) {
-            if (i != b * per_beam) return 0;
+            if (i != b * per_beam) return Place{0, 0};
+            logit = 0.f;
         } else {
-            if (!(logit > -INFINITY)) return 0;
+            if (!(logit > -INFINITY)) return Place{0, 0};
             add2(add.x, add.y, logit, 0.f);
         }
         // (a beam without candidates, or a score below fp32's range)
-        if (!(add.x > -INFINITY)) return 0;
-        return (uint64_t)order_key(add.x) << 32 | order_key(add.y);
+        if (!(add.x > -INFINITY)) return Place{0, 0};
+        // (of equal logits of a beam, the one that lies first has the lower
+        // token; per_beam is below 2^25)
+        return Place{(uint64_t)order_key(add.x) << 32 | order_key(add.y),
+                     (uint64_t)(kMaxBeams - 1 - b) << 57 | (uint64_t)order_key(logit) << 25 | (0x1ffffff - (i - b * per_beam))};
     };
-    uint64_t key[kHeld], top = 0;
+    Place place[kHeld];
+    uint64_t top = 0;
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
-        const int i = tid + k * kThreads;
-        key[k] = i < total ? key_of(i, held[k]) : 0;
-        top = max(top, key[k]);
+        place[k] = tid + k * kThreads < total ? place_of(held_in[k], held[k]) : Place{0, 0};
+        top = max(top, place[k].score);
     }
-#pragma unroll 1
-    for (int i = tid + kHeld * kThreads; i < total; i += kThreads) top = max(top, key_of(i, cand[i]));
+    // (the chunks' best ones are among those held)
     top = sort_warp(top, lane);
-    if (lane == (a.n + kWarps - 1) / kWarps - 1) s_bound[warp] = top;
-    __syncthreads();
-    uint64_t bound = s_bound[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) bound = min(bound, s_bound[w]);
-    bound = max(bound, (uint64_t)1);
-    auto collect = [&](int i, uint64_t x, float logit, int at) {
+    for (int i = 0; i < 4; ++i)
+        if (lane == (a.n + (8 >> i) - 1) / (8 >> i) - 1) s_rank[i][warp] = top;
+    __syncthreads();
+    // a score that 8, 4, 2 or 1 of the warps reach with an eighth, a fourth, ...
+    // of n maxima each: the largest of those bounds
+    uint64_t bound = s_rank[0][0], first = 0, second = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        bound = min(bound, s_rank[0][w]);
+        second = max(second, min(first, s_rank[2][w]));
+        first = max(first, s_rank[2][w]);
+    }
+    bound = max(max(bound, fourth_of_8(s_rank[1])), max(second, (uint64_t)1));
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) bound = max(bound, s_rank[3][w]);
+    auto collect = [&](const Place &x, int i, int at) {
         const int k = atomicAdd(&s_count, 1);
         if (k < kCap) {
-            const int b = beam_of(i);
-            s_key[k] = x;
-            s_logit[k] = s_done[b] ? 0.f : logit;
-            s_at[k] = s_done[b] ? a.pad : at;
-            s_beam[k] = (uint8_t)b;
+            s_place[k] = x;
+            s_token[k] = s_done[i / per_beam] ? a.pad : at;
         }
     };
 #pragma unroll
     for (int k = 0; k < kHeld; ++k)
-        if (key[k] >= bound) collect(tid + k * kThreads, key[k], held[k], held_at[k]);
+        if (place[k].score >= bound) collect(place[k], held_in[k], held_at[k]);
 #pragma unroll 1
-    for (int i = tid + kHeld * kThreads; i < total; i += kThreads) {
-        const uint64_t x = key_of(i, cand[i]);
-        if (x >= bound) collect(i, x, cand[i], cand_at[i]);
+    for (int x = tid + kHeld * kThreads; x < total; x += kThreads) {
+        const int i = lies(x);
+        const Place p = place_of(i, cand[i]);
+        if (p.score >= bound) collect(p, i, cand_at[i]);
     }
     __syncthreads();
     const int found = s_count;
     float *os = a.out_scores + (int64_t)g * a.n;
     int32_t *orow = a.out_rows + (int64_t)g * a.n, *ot = a.out_tokens + (int64_t)g * a.n;
-    auto put = [&](int r, const Entry &x) {
-        os[r] = key_value(x.key);
-        orow[r] = g * a.beams + x.beam;
-        ot[r] = x.at;
+    auto put = [&](int r, const Place &x, int token) {
+        os[r] = key_value(x.score);
+        orow[r] = g * a.beams + kMaxBeams - 1 - (int)(x.tie >> 57);
+        ot[r] = token;
     };
     if (found <= kCap) {
         for (int i = tid; i < found; i += kThreads) {
-            const Entry x{s_key[i], s_logit[i], s_beam[i], s_at[i]};
+            const Place x = s_place[i];
             int r = 0;
-            for (int j = 0; j < found; ++j) {
-                const uint64_t k = s_key[j];
-                r += k > x.key;
-                if (k == x.key) r += before(Entry{k, s_logit[j], s_beam[j], s_at[j]}, x);
-            }
-            if (r < a.n) put(r, x);
+#pragma unroll 4
+            for (int j = 0; j < found; ++j) r += before(s_place[j], x);
+            if (r < a.n) put(r, x, s_token[i]);
         }
         for (int r = found + tid; r < a.n; r += kThreads) {
             os[r] = -INFINITY;
@@ -478,33 +495,44 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
         return;
     }
     // one after the other, each the best behind the last one
-    Entry last{~0ull, INFINITY, -1, -1};
+    Place last{~0ull, ~0ull};
     for (int r = 0; r < a.n; ++r) {
-        Entry best{0, -INFINITY, INT_MAX, INT_MAX};
+        Place best{0, 0};
+        int token = -1;
 #pragma unroll 1
         for (int i = tid; i < total; i += kThreads) {
-            const float x = cand[i];
-            const int b = beam_of(i);
-            const Entry e{key_of(i, x), s_done[b] ? 0.f : x, b, s_done[b] ? a.pad : cand_at[i]};
-            if (e.key && before(last, e) && before(e, best)) best = e;
+            const Place p = place_of(i, cand[i]);
+            if (before(last, p) && before(p, best)) {
+                best = p;
+                token = s_done[i / per_beam] ? a.pad : cand_at[i];
+            }
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
-            Entry y;
-            y.key = __shfl_xor_sync(0xffffffffu, best.key, o);
-            y.logit = __shfl_xor_sync(0xffffffffu, best.logit, o);
-            y.beam = __shfl_xor_sync(0xffffffffu, best.beam, o);
-            y.at = __shfl_xor_sync(0xffffffffu, best.at, o);
-            if (before(y, best)) best = y;
+            Place y;
+            y.score = __shfl_xor_sync(0xffffffffu, best.score, o);
+            y.tie = __shfl_xor_sync(0xffffffffu, best.tie, o);
+            const int t = __shfl_xor_sync(0xffffffffu, token, o);
+            if (before(y, best)) {
+                best = y;
+                token = t;
+            }
         }
         __syncthreads();
-        if (lane == 0) s_best[warp] = best;
+        if (lane == 0) {
+            s_best[warp] = best;
+            s_best_token[warp] = token;
+        }
         __syncthreads();
         best = s_best[0];
+        token = s_best_token[0];
         for (int w = 1; w < kWarps; ++w)
-            if (before(s_best[w], best)) best = s_best[w];
+            if (before(s_best[w], best)) {
+                best = s_best[w];
+                token = s_best_token[w];
+            }
         last = best;
-        if (tid == 0) put(r, best);
+        if (tid == 0) put(r, best, token);
     }
 }
 
@@ -558,10 +586,8 @@ cudaError_t launch_beam(BeamArgs a, cudaStream_t stream) {
     // (several waves: the joins' CTAs would only take the parts' places, 113
     // instead of 73 us for 4096 of them)
     a.early = a.groups * a.beams * a.chunks <= 2 * device_sm_count();
-    const int64_t per_beam = (int64_t)a.chunks * a.n;
-    a.div = per_beam > 1 && per_beam * per_beam * a.beams < (INT64_C(1) << 32)
-                ? (uint32_t)(((INT64_C(1) << 32) + per_beam - 1) / per_beam)
-                : 0;
+    const int64_t lists = (int64_t)a.chunks * a.beams;
+    a.div = lists > 1 && lists * lists * a.n < (INT64_C(1) << 32) ? (uint32_t)(((INT64_C(1) << 32) + lists - 1) / lists) : 0;
     const cudaError_t e =
         launch_behind(beam_part_kernel<T>, dim3((unsigned)(a.groups * a.beams * a.chunks)), kThreads, 0, 1, stream, a);
     if (e != cudaSuccess) return e;
