@@ -10,17 +10,22 @@
 // a row's n best scores are among its chunks' n best logits.  The n best of a
 // chunk: each warp sorts its lanes' maxima; all eight warps' ceil(n / 8)-th, and
 // four warps' ceil(n / 4)-th, are bounds that at least n logits reach, and few
-// more do (about 30 for n = 16); those are ranked against one another.  (More reach it where many are equal,
-// or the large ones lie in few threads: then one after the other is taken.)
+// more do (about 30 for n = 16); those are ranked against one another.  (More
+// reach it where many are equal, or the large ones lie in few threads: then one
+// after the other is taken.)
 // beam_join_kernel: a CTA per request joins the sums, scores the candidates and
-// ranks them the same way.
+// ranks them the same way, taking the best of every chunk first.
 // What decides between beams has to be finer than fp32, and the FP64 pipe is
 // slow here (a join that compared doubles took 47 us, one that added and took
 // exponentials in them 15): sums and scores are pairs of fp32 numbers, value
 // and rest (48 bits, by error-free sums), compared as 64-bit whole numbers of
 // the same order.
-// Bound by HBM for large batches (every logit read once), by latency for one
-// request.
+// 32 requests of 8 beams over 131072 fp32 tokens, n = 16 (a fifth of the beams
+// finished): parts 29 us (107 MB, 3.7 TB/s; 668 instructions a warp and chunk at
+// 55% of the issue slots), join 6.  One request of 4 beams over 32000: 8.8 us
+// with the states' gather, the two kernels' latencies.  32 logits a thread and
+// four CTAs per SM were best: 64 logits 63 us, 16 logits 52, a persistent grid
+// that copies the next chunk ahead 69 (of 40 for all three kernels).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -14,7 +14,10 @@
 // are in flight.  A unit of work is 2 x W values of a head: W pairs, or a
 // plain copy of V or of the dims behind rot_dim; W = 8 makes each a 16-byte
 // access, W = 1 serves rot_dim that are no multiple of 16.  Bound by HBM for
-// prompts (4 bytes per value moved), by latency for decode steps.
+// prompts (4 bytes per value moved): 26800 tokens in 2 layers, 48 heads of 128
+// in all, 190 us, 6.9 TB/s of 1.32 GB, the rate of a plain copy.  By latency for
+// decode steps: 64 beams in 8 layers, of which 59 copy their last page, 8.9 us
+// (39 MB), one token in 22 layers 2.8 us.
 //
 // The host describes tokens by runs (a sequence's consecutive slots) and
 // their blocks, in the kernel's parameters: 4 bytes per page instead of per
