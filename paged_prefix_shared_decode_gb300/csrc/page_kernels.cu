@@ -335,12 +335,15 @@ __device__ __forceinline__ void find_cut(int bits, int k, uint32_t &cut, int &ab
 //   1. The scores, rounded to bf16 and packed in pairs (rounding keeps the
 //      order, if not strictly), which is what most of them are looked at as:
 //      half of the registers and of the instructions.
-//   2. A bound that at least k of them reach, from the threads' maxima: each
-//      warp's ceil(k / W)-th largest maximum, the smallest of those.
+//   2. A bound that at least k of them reach, from the threads' maxima (of four
+//      parts each where k is above W * 32): each warp's ceil(k / W)-th largest
+//      maximum, the smallest of those.
 //   3. The pages that reach it (a NaN always does), few more than k, go on the
-//      warps' lists with their scores as they are, and one warp finds the k-th
-//      largest of those.  Where the lists do not hold them (many equal scores,
-//      k above W * 32), all warps look through all keys instead.
+//      warps' lists with their scores as they are, and one warp (short lists: 22
+//      us for 2048 rows, all warps 24) or all of them (k above W * 32: 300 pages
+//      31 us, one warp 55) find the k-th largest of those.  Where the lists do
+//      not hold them (many equal scores, k above W * 70 or so), all warps look
+//      through all keys instead.
 //   4. Keys above it, and those equal to it, as two bit maps by page; counts
 //      up to a word give every chosen page its place.
 template <int W, int E>
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 48 / W : 1) page_select_kerne
     __shared__ uint32_t s_up[WORDS], s_eq[WORDS];
     __shared__ uint32_t s_warp[W], s_hits[W];
     __shared__ uint32_t s_cut;
-    __shared__ int s_above;
+    __shared__ int s_above, s_count[34];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x;
     griddep_wait();
@@ -387,9 +390,33 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 48 / W : 1) page_select_kerne
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         if (tid + i * STEP < WORDS) s_up[tid + i * STEP] = s_eq[tid + i * STEP] = 0;
-    const bool few = k <= STEP;
+    if (tid < 34) s_count[tid] = 0;
+    // maxima to bound it by: the threads', or of four parts of each one's pages
+    constexpr int PARTS = E >= 8 ? 4 : 1;
+    const bool few = k <= STEP * PARTS;
     uint32_t bound = 0;
-    if (few) {
+    if (few && k > STEP) {
+        // the warp's ceil(k / W)-th largest of 32 PARTS, by the 16 bits that a
+        // bf16's key has
+        const int rank = (k + W - 1) / W;
+        uint32_t top[PARTS], at_least = 0;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            __nv_bfloat162 most = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int i = 0; i < E / 2 / PARTS; ++i) most = __hmax2(most, pair[q * (E / 2 / PARTS) + i]);
+            top[q] = score_key(fmaxf(__low2float(most), __high2float(most))) >> 16;
+        }
+#pragma unroll 1
+        for (uint32_t b = 0x8000; b; b >>= 1) {
+            int c = 0;
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) c += __popc(__ballot_sync(0xffffffffu, top[q] >= (at_least | b)));
+            if (c >= rank) at_least |= b;
+        }
+        // (the low half of a negative bf16's key is ones)
+        if (lane == 0) s_warp[warp] = at_least << 16 | (at_least & 0x8000 ? 0u : 0xffffu);
+    } else if (few) {
         __nv_bfloat162 most = __floats2bfloat162_rn(-INFINITY, -INFINITY);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) most = __hmax2(most, pair[i]);      // (a NaN is not taken)
@@ -433,8 +460,25 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 48 / W : 1) page_select_kerne
     for (int w = 0; w < W; ++w) most = max(most, (int)s_hits[w]);
     uint32_t cut = 0;                // the k-th largest key
     int above = 0;                   // keys larger than it
+    int step = 0;                    // (counts of all warps, each with a word of its own)
+    auto total = [&](int c) {
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) atomicAdd(&s_count[step], c);
+        __syncthreads();
+        return s_count[step++];
+    };
     if (most <= kSelCap) {
-        if (warp == 0) {
+        if (k > STEP) {
+            uint32_t held[kSelCap / 32];
+#pragma unroll
+            for (int i = 0; i < kSelCap / 32; ++i) held[i] = 32 * i + lane < hits ? s_key[warp][32 * i + lane] : 0u;
+            find_cut(32, k, cut, above, [&](uint32_t t) {      // keys of at least t
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < kSelCap / 32; ++i) c += held[i] >= t;
+                return total(c);
+            });
+        } else if (warp == 0) {
             constexpr int H = W <= 8 ? 2 : 1;        // 32 * H keys of each list in registers
             uint32_t x[W * H];
             uint32_t any = 0, all = 0xffffffffu;
@@ -475,9 +519,11 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 48 / W : 1) page_select_kerne
                 s_above = above;
             }
         }
-        __syncthreads();
-        cut = s_cut;
-        above = s_above;
+        if (k <= STEP) {
+            __syncthreads();
+            cut = s_cut;
+            above = s_above;
+        }
         for (int i = lane; i < hits; i += 32) {
             const uint32_t x = s_key[warp][i];
             const int j = s_at[warp][i];
@@ -489,20 +535,12 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 48 / W : 1) page_select_kerne
         uint32_t key[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) key[e] = score_key(e * STEP + tid < len ? score[e * STEP + tid] : -INFINITY);
-        auto count = [&](uint32_t t) {               // keys of at least t
+        find_cut(32, k, cut, above, [&](uint32_t t) {
             int c = 0;
 #pragma unroll
             for (int e = 0; e < E; ++e) c += key[e] >= t;
-            c = __reduce_add_sync(0xffffffffu, c);
-            __syncthreads();
-            if (lane == 0) s_warp[warp] = c;
-            __syncthreads();
-            int sum = 0;
-#pragma unroll
-            for (int w = 0; w < W; ++w) sum += s_warp[w];
-            return sum;
-        };
-        find_cut(32, k, cut, above, count);
+            return total(c);
+        });
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const uint32_t up = __ballot_sync(0xffffffffu, key[e] > cut), eq = __ballot_sync(0xffffffffu, key[e] == cut);

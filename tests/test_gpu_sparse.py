@@ -171,7 +171,7 @@ def values(kind, shape, g):
 
 @pytest.mark.parametrize("kind", ["normal", "ties", "equal", "up", "close", "wide", "odd"])
 @pytest.mark.parametrize("budget,sink,recent", [(1, 0, 0), (1, 1, 0), (8, 1, 2), (8, 8, 0), (8, 0, 8), (64, 4, 7),
-                                               (300, 0, 1), (2000, 1, 1)])
+                                               (300, 0, 1), (700, 2, 9), (2000, 1, 1)])
 def test_select(kind, budget, sink, recent):
     lens = [1, 16 * 7, 16 * 9 + 1, 16 * 100, 16 * 513, 16 * 1025, 16 * 4095 + 3, 16 * 9001]
     for q_lens in (None, [1, 3, 0, 2, 1, 1, 1, 2]):
