@@ -10,9 +10,7 @@ is missing.
 """
 from __future__ import annotations
 
-import array
 import ctypes
-import math
 import os
 
 import numpy as np
@@ -48,7 +46,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # KVP_LIB_PATH points the binding at another build of the same C ABI.
 lib_path = os.environ.get("KVP_LIB_PATH") or os.path.join(_HERE, "libkvp.so")
 _lib = None
-_tc = None     # torch, once a call has needed it
+_native_calls = None   # _calls, once a call has needed it
 
 
 class KvpError(RuntimeError):
@@ -342,10 +340,9 @@ def kvp_cow_count(pool) -> int:
 
 def kvp_pool_shape(pool):
     """The pool's layers and kv heads."""
-    out = (_I32 * 2)()
-    at = ctypes.addressof(out)
-    _check(load().kvp_pool_shape(pool, at, at + 4), "kvp_pool_shape")
-    return out[0], out[1]
+    layers, heads = _I32(), _I32()
+    _check(load().kvp_pool_shape(pool, ctypes.byref(layers), ctypes.byref(heads)), "kvp_pool_shape")
+    return layers.value, heads.value
 
 
 def kvp_gather_tables(pool, seqs, width: int):
@@ -622,7 +619,7 @@ def _batch_i32(name, a, n):
 def _torch():
     """torch and the current device (0 before CUDA is in use: no tensor is on it)."""
     import torch
-    return torch, torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+    return torch, torch.cuda.current_device() if torch.cuda.is_initialized() else 0
 
 
 def _pool_shape(d: AttnDesc):
@@ -767,107 +764,51 @@ def rope_desc(rot_dim: int, base: float = 10000.0, freqs=None, interleaved: bool
     return d
 
 
-def _i32s(a):
-    """A host int32 array of a list or array, its address and length."""
-    if isinstance(a, np.ndarray) and a.size <= 256:
-        if a.ndim != 1:
-            raise ValueError(f"expected one dimension, got shape {a.shape}")
-        a = a.tolist()      # (a numpy array's address alone takes 1 us to get)
-    if type(a) is list:
-        a = array.array("i", a)
-        at, n = a.buffer_info()
-        return a, at, n
-    a = np.ascontiguousarray(a, dtype=np.int32)
-    if a.ndim != 1:
-        raise ValueError(f"expected one dimension, got shape {a.shape}")
-    return a, a.ctypes.data, len(a)
-
-
-def _here(stream):
-    """torch, the current device (0 before CUDA is in use: no tensor is on it)
-    and the stream's handle."""
-    global _tc
-    if _tc is None:
-        import torch as _tc
-    dev = _tc._C._cuda_getDevice() if _tc.cuda.is_initialized() else 0
-    if stream is None:
-        raw = getattr(_tc._C, "_cuda_getCurrentRawStream", None)
-        return _tc, dev, raw(dev) if raw else _stream(None)
-    return _tc, dev, stream if isinstance(stream, int) else stream.cuda_stream
+def _native():
+    """The extension module that checks these calls' arguments and makes them,
+    bound to the library that is loaded (raises RuntimeError if not built)."""
+    global _native_calls
+    if _native_calls is None:
+        import torch
+        lib = load()
+        path = os.path.join(_HERE, "_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_calls.so is not built ({path}); run "
+                               "`python -m paged_prefix_shared_decode_gb300.build`")
+        from . import _calls as m     # (after torch, whose libraries it needs)
+        if m.torch_version != torch.__version__:
+            raise RuntimeError(f"_calls.so was built for torch {m.torch_version}, this is {torch.__version__}; run "
+                               "`python -m paged_prefix_shared_decode_gb300.build`")
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: _stream(None))
+        m.bind(KvpError, torch._C._cuda_getDevice, raw, *(ctypes.cast(getattr(lib, n), _P).value for n in m.functions))
+        _native_calls = m
+    return _native_calls
 
 
 def seq_append_rope(pool, seqs, ntoks, k, v, rope: RopeDesc, positions=None, q=None, q_out=None, stream=None):
     """seq_append_batch with k rotated into the pages, and q [L][T][Hq][d]
     into q_out (q itself or apart).  k, v [L][T][Hkv][d] bf16, T = sum of
     ntoks; positions: device int32 [T], or None (the cache's)."""
-    s, sp, ns = _i32s(seqs)
-    n, np_, nn = _i32s(ntoks)
-    if nn != ns:
-        raise ValueError(f"ntoks: expected {ns} entries, got {nn}")
-    torch, dev, st = _here(stream)
-    bf16, T, hq = torch.bfloat16, sum(n.tolist()), 0
-    if T:
-        layers, heads = kvp_pool_shape(pool)
-        d = k.shape[-1]
-        shape = (layers, T, heads, d)
-        k, v = _arg("k", k, bf16, shape, dev), _arg("v", v, bf16, shape, dev)
-        if q is not None:
-            hq = q.shape[-2]
-            shape = (layers, T, hq, d)
-            q, q_out = _arg("q", q, bf16, shape, dev), _arg("q_out", q_out, bf16, shape, dev)
-        if positions is not None:
-            positions = _arg("positions", positions, torch.int32, (T,), dev)
-    else:
-        k = v = q = q_out = positions = None
-    _check(load().seq_append_rope(pool, ns, sp, np_, k, v, ctypes.byref(rope), positions, q, q_out, hq, st),
-           "seq_append_rope")
+    _native().seq_append_rope(pool, seqs, ntoks, k, v, rope, positions, q, q_out, stream)
 
 
 def seq_reorder(pool, dst, src):
     """Sequence dst[i] becomes a fork of what sequence src[i] was."""
-    d, dp, nd = _i32s(dst)
-    s, sp, ns = _i32s(src)
-    if nd != ns:
-        raise ValueError(f"src: expected {nd} entries, got {ns}")
-    _check(load().seq_reorder(pool, dp, sp, nd), "seq_reorder")
-
-
-def _batch(desc, block_tables, seq_lens, q_start, torch, dev):
-    """Addresses and sizes of a batch held on the device."""
-    S = seq_lens.shape[0]
-    i32, mb = torch.int32, None
-    if block_tables is not None:
-        mb = block_tables.shape[-1]
-        block_tables = _arg("block_tables", block_tables, i32, (S, mb), dev)
-    return (S, mb, block_tables, _arg("seq_lens", seq_lens, i32, (S,), dev),
-            None if q_start is None else _arg("q_start", q_start, i32, (S + 1,), dev))
+    _native().seq_reorder(pool, dst, src)
 
 
 def kvp_page_bounds(k_pool, block_tables, seq_lens, n_new: int, desc: AttnDesc, bounds, stream=None):
     """Smallest and largest key per dim of the pages that hold one of the last
     n_new tokens of a sequence, into bounds [L][NB][Hkv][2][d] bf16.
     block_tables [S][MB], seq_lens [S]: device int32."""
-    torch, dev, st = _here(stream)
-    S, mb, tp, lp, _ = _batch(desc, block_tables, seq_lens, None, torch, dev)
-    bf16, shape = torch.bfloat16, (desc.num_layers, desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim)
-    _check(load().kvp_page_bounds(_arg("k_pool", k_pool, bf16, _pool_shape(desc), dev), tp, lp, S, mb, n_new,
-                                  ctypes.byref(desc), _arg("bounds", bounds, bf16, shape, dev), st),
-           "kvp_page_bounds")
+    _native().kvp_page_bounds(k_pool, block_tables, seq_lens, n_new, desc, bounds, stream)
 
 
 def kvp_page_scores(q, q_start, bounds, block_tables, seq_lens, desc: AttnDesc, scores, stream=None):
     """Scores [L][T][Hkv][stride] fp32 of the pages that each query row of q
     [L][T][Hq][d] sees; q_start: device int32 [S + 1], or None (one row a
     sequence)."""
-    torch, dev, st = _here(stream)
-    S, mb, tp, lp, sp = _batch(desc, block_tables, seq_lens, q_start, torch, dev)
-    L, T, heads, d = desc.num_layers, q.shape[1], desc.num_kv_heads, desc.head_dim
-    stride = scores.shape[-1]
-    _check(load().kvp_page_scores(_arg("q", q, torch.bfloat16, (L, T, desc.num_q_heads, d), dev), sp, T,
-                                  _arg("bounds", bounds, torch.bfloat16, (L, desc.num_blocks, heads, 2, d), dev), tp,
-                                  lp, S, mb, ctypes.byref(desc),
-                                  _arg("scores", scores, torch.float32, (L, T, heads, stride), dev), stride,
-                                  st), "kvp_page_scores")
+    _native().kvp_page_scores(q, q_start, bounds, block_tables, seq_lens, desc, scores, stream)
 
 
 def kvp_page_select(scores, q_start, seq_lens, desc: AttnDesc, n_sink: int, n_recent: int, selected, max_blocks=None,
@@ -875,32 +816,15 @@ def kvp_page_select(scores, q_start, seq_lens, desc: AttnDesc, n_sink: int, n_re
     """The best selected.shape[-1] pages of each row of scores
     [L][T][Hkv][stride] into selected [L][T][Hkv][budget] int32, ascending;
     max_blocks (None: as long as the scores' rows): the tables' width."""
-    torch, dev, st = _here(stream)
-    S, _, _, lp, sp = _batch(desc, None, seq_lens, q_start, torch, dev)
-    L, T, heads = desc.num_layers, scores.shape[1], desc.num_kv_heads
-    stride, budget = scores.shape[-1], selected.shape[-1]
-    _check(load().kvp_page_select(_arg("scores", scores, torch.float32, (L, T, heads, stride), dev), stride, sp, T, lp,
-                                  S, stride if max_blocks is None else max_blocks, ctypes.byref(desc), budget, n_sink,
-                                  n_recent, _arg("selected", selected, torch.int32, (L, T, heads, budget), dev),
-                                  st), "kvp_page_select")
+    _native().kvp_page_select(scores, q_start, seq_lens, desc, n_sink, n_recent, selected, max_blocks, stream)
 
 
 def paged_sparse_attention(q, q_start, k_pool, v_pool, block_tables, seq_lens, selected, desc: AttnDesc, out, lse,
                            stream=None):
     """Attention of each query row over its selected [L][T][Hkv][budget]
     pages; out like q [L][T][Hq][d] bf16, lse [L][T][Hq] fp32 or None."""
-    torch, dev, st = _here(stream)
-    S, mb, tp, lp, sp = _batch(desc, block_tables, seq_lens, q_start, torch, dev)
-    T, budget, bf16 = q.shape[1], selected.shape[-1], torch.bfloat16
-    rows = (desc.num_layers, T, desc.num_q_heads)
-    wide, pool = (*rows, desc.head_dim), _pool_shape(desc)
-    _check(load().paged_sparse_attention(_arg("q", q, bf16, wide, dev), sp, T, _arg("k_pool", k_pool, bf16, pool, dev),
-                                         _arg("v_pool", v_pool, bf16, pool, dev), tp, lp, S, mb,
-                                         _arg("selected", selected, torch.int32,
-                                              (desc.num_layers, T, desc.num_kv_heads, budget), dev), budget,
-                                         ctypes.byref(desc), _arg("out", out, bf16, wide, dev),
-                                         _arg("lse", lse, torch.float32, rows, dev), st),
-           "paged_sparse_attention")
+    _native().paged_sparse_attention(q, q_start, k_pool, v_pool, block_tables, seq_lens, selected, desc, out, lse,
+                                     stream)
 
 
 def kvp_beam_workspace_size(groups: int, beams: int, vocab: int, n_out: int) -> int:
@@ -916,44 +840,14 @@ def kvp_beam_select(logits, scores, finished, pad_token: int, out_scores, out_ro
     bf16 or fp16 (last dimension contiguous, rows evenly spaced), scores [G][B]
     fp32, finished [G][B] bool or uint8 (or None); out_scores fp32, out_rows
     and out_tokens int32 [G][n]."""
-    torch, dev, st = _here(stream)
-    G, B, V = logits.shape
-    kind = {torch.float32: KVP_F32, torch.bfloat16: KVP_BF16, torch.float16: KVP_F16}.get(logits.dtype)
-    if kind is None or logits.get_device() != dev:
-        raise ValueError(f"logits: expected float32, bfloat16 or float16 on cuda:{dev}, got {logits.dtype} on "
-                         f"{logits.device}")
-    group, row, step = logits.stride()
-    if B == 1:
-        row = group if G > 1 else V
-    if (V > 1 and step != 1) or (G > 1 and group != B * row):
-        raise ValueError(f"logits: expected evenly spaced contiguous rows, got strides {logits.stride()}")
-    if finished is not None:
-        if finished.dtype not in (torch.bool, torch.uint8):
-            raise ValueError(f"finished: expected bool or uint8, got {finished.dtype}")
-        finished = _arg("finished", finished, finished.dtype, (G, B), dev)
-    n = out_scores.shape[-1]
-    i32, f32, shape = torch.int32, torch.float32, (G, n)
-    _check(load().kvp_beam_select(logits.data_ptr(), kind, row, _arg("scores", scores, f32, (G, B), dev), finished,
-                                  pad_token, G, B, V, n, _arg("out_scores", out_scores, f32, shape, dev),
-                                  _arg("out_rows", out_rows, i32, shape, dev),
-                                  _arg("out_tokens", out_tokens, i32, shape, dev), _dev(workspace),
-                                  _ws_bytes(workspace, ws_bytes), st), "kvp_beam_select")
+    _native().kvp_beam_select(logits, scores, finished, pad_token, out_scores, out_rows, out_tokens, workspace,
+                              ws_bytes, stream)
 
 
 def kvp_state_reorder(src, dst, index, dim: int = 0, stream=None):
     """dst row i = src row index[i] along dimension `dim` (the ones before it
     are outer); index: device int32, as many as dst has rows, in any shape."""
-    torch, dev, st = _here(stream)
-    shape, dtype = src.shape, src.dtype
-    n_src, n_dst = shape[dim], dst.shape[dim]
-    if index.numel() != n_dst:
-        raise ValueError(f"index: expected {n_dst} entries, got {index.numel()}")
-    outer = 1 if dim == 0 else math.prod(shape[:dim])
-    row = math.prod(shape[dim + 1:]) * src.element_size()
-    want = shape if n_src == n_dst else (*shape[:dim], n_dst, *shape[dim + 1:])
-    _check(load().kvp_state_reorder(_arg("src", src, dtype, shape, dev), _arg("dst", dst, dtype, want, dev),
-                                    _arg("index", index, torch.int32, index.shape, dev), outer, n_src, n_dst, row, st),
-           "kvp_state_reorder")
+    _native().kvp_state_reorder(src, dst, index, dim, stream)
 
 
 def kvp_device_error(workspace, stream=None) -> int:

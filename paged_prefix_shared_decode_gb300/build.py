@@ -1,13 +1,18 @@
 """Builds libkvp.so in-tree for sm_103a with nvcc (no cmake, no torch
-extension machinery).  Translation units compile in parallel, then link.
+extension machinery) and _calls.so, the binding's argument checks in C++, with
+g++ against the installed torch's headers.  Translation units compile in
+parallel, then link.
 
     python -m paged_prefix_shared_decode_gb300.build [--force]
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import runpy
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvp.so")
+CALLS = os.path.join(HERE, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 SOURCES = ["pool.cpp", "radix.cpp", "plan.cpp", "attn_kernels.cu", "attn_tc.cu", "kv_kernels.cu", "kv4_kernels.cu", "no_alloc.cu",
@@ -43,6 +49,25 @@ def _stale(target: str, deps: list) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _calls_job(force: bool, headers: list):
+    """The command that compiles _calls.so and where it writes to, or None if
+    the module is up to date (with the sources and with the torch installed)."""
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    version = runpy.run_path(os.path.join(torch, "version.py"))["__version__"]
+    src = os.path.join(CSRC, "py_calls.cpp")
+    stamp = os.path.join(OUT_DIR, "calls_torch_version")
+    built = open(stamp).read() if os.path.exists(stamp) else ""
+    if not force and built == version and not _stale(CALLS, [src] + headers):
+        return None
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    lib = os.path.join(torch, "lib")
+    cmd = [os.environ.get("CXX") or "g++", "-shared", "-O2", "-std=c++17", "-fPIC", src, "-o", tmp,
+           f'-DKVP_TORCH_VERSION="{version}"', "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    return cmd, tmp, stamp, version
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -66,10 +91,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
-        for err in ex.map(run, jobs):
+    calls = _calls_job(force, headers)
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        for err in ex.map(run, ([calls[0]] if calls else []) + jobs):
             if verbose and err:
                 print(err)
+    if calls:
+        _, tmp, stamp, version = calls
+        os.replace(tmp, CALLS)
+        with open(stamp, "w") as f:
+            f.write(version)
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         run([nvcc, "-shared", "-o", tmp] + objs + ARCH + ["-lcudart"])
