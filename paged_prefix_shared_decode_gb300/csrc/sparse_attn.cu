@@ -1,5 +1,6 @@
 // Attention over selected pages of a paged sequence (sm_103a): each query row
-// and kv head with its own list of pages, decode steps and short chunks.
+// and kv head with its own list of pages: decode steps, a few rows each of many
+// sequences, and the calls.  (Chunks of prompts: sparse_tc.cuh.)
 //
 // Two products per 16 tokens of a page and the group's query heads, both with
 // the tokens or dims on mma.sync's 16 rows and up to 8 heads on its columns
@@ -33,6 +34,7 @@
 #include "kvp_internal.h"
 #include "launch.cuh"
 #include "query_rows.cuh"
+#include "tc_ops.cuh"
 
 namespace kvp {
 namespace {
@@ -62,11 +64,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ float exp2_sfu(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16 *p) {
@@ -570,8 +567,9 @@ constexpr int kTileMap = kTilePages + kTileList * 16;
 // their groups' heads, at most 8): neighbours choose much the same pages, so a
 // page is read once for all the rows that named it.  Which rows name a page is
 // a byte per page in shared memory, and the pages are taken in ascending order.
-// Bound by what L2 delivers, 10 to 11 TB/s: 53 pages of the 128 that four rows
-// of 32 pages name, 59 of eight's 256 (rows that share most of their choice).
+// For batches of a few rows each (64 sequences of 2.4 rows on average, 32 pages of
+// 32 tokens, d 128: 86 us; tiles of 128 rows, which suit chunks, 100).  Bound by
+// what L2 delivers, 10 to 11 TB/s.
 //
 // A value that is not finite in a page that only some of the rows see would
 // reach the others as 0 * inf; then (and when a row names a page twice) the
@@ -861,11 +859,32 @@ cudaError_t launch_tile(const SparseArgs &a, cudaStream_t stream) {
     return launch_behind(sparse_tile_kernel<D, MT>, grid, 32 * kWarps, bytes, 1, stream, a);
 }
 
+}  // namespace
+}  // namespace kvp
+
+#include "sparse_tc.cuh"
+
+namespace kvp {
+namespace {
+
 template <int D>
 cudaError_t launch_for(SparseArgs a, cudaStream_t stream) {
-    // rows of a chunk by tiles of 32 (query, head) rows where that gives a CTA
-    // for two places of every SM, by tiles of 16 where those do; single rows,
-    // spread over clusters when they are few, otherwise
+    // chunks by tiles of 128 (query, head) rows on the tensor cores, which cost 12
+    // us before their first page (of 8 kv heads at head dim 128, 53 queries 33 us
+    // where single rows take 29, 105 queries 33 against 62; at head dim 64 with 4
+    // heads 300 queries 29 against 28) and read a page for all their rows whatever
+    // part of a tile these fill (64 sequences of 5.4 rows on average 112 us against
+    // 126, of 2.4 100 against 86)
+    const int64_t units = (int64_t)a.rows.T * a.L * a.Hkv;
+    if (a.rows.start && a.rows.MB <= kTcPages && a.L * a.Hkv <= 65535 && a.G <= kTcRows / 2 &&
+        units * D >= 512LL * device_sm_count() && a.rows.T >= 5LL * a.rows.S &&
+        tc_path_supported(a.L, a.NB, a.Hkv, 1 << a.bs_log2)) {
+        a.qt = std::min(32, kTcRows / a.G);
+        return launch_tc<D>(a, stream);
+    }
+    // a few rows each of many sequences by tiles of 32 (query, head) rows where
+    // that gives a CTA for two places of every SM, by tiles of 16 where those do;
+    // single rows, spread over clusters when they are few, otherwise
     if (a.rows.start && a.rows.MB <= kTilePages && a.L * a.Hkv <= 65535) {
         auto many = [&](int qt) { return (int64_t)(a.rows.T / qt) * a.L * a.Hkv >= 2LL * device_sm_count(); };
         a.qt = std::min(8, 32 / a.G);

@@ -514,3 +514,122 @@ def test_wide_chunks_with_repeated_and_unseen(heads, d, bs, lens, q_lens):
     b.v[:, int(b.tables[0, 1]), 1, 2, 3] = math.nan
     b.v[:, int(b.tables[0, 1]), 1, 4] = math.inf
     check_sparse(b, sel)
+
+
+# tiles of the tensor-core kernel: groups that fill 128 rows and that do not, rows
+# of several tiles, pages from 16 tokens to more than a step's 128, steps that end
+# inside a page, budgets above a warp's lanes
+LARGE = [((64, 1), 128, 16, [900], [640], 9), ((40, 1), 64, 32, [1500, 3000], [700, 640], 5),
+         ((16, 8), 64, 128, [1000, 40, 900], [150, 0, 75], 4), ((8, 8), 128, 256, [2000], [97], 3),
+         ((12, 4), 128, 1024, [1500, 2049], [33, 180], 2), ((32, 8), 64, 16, [1200], [160], 40),
+         ((7, 1), 128, 64, [4000], [641], 6), ((4, 2), 128, 16, [330], [330], 33)]
+
+
+@pytest.mark.parametrize("heads,d,bs,lens,q_lens,budget", LARGE)
+def test_large_tiles(heads, d, bs, lens, q_lens, budget):
+    b = Batch(lens, q_lens, heads, d, bs, seed=30)
+    sel = like_neighbours(b, budget)
+    x = check_sparse(b, sel)
+    y = check_sparse(b, sel)
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    sel = sel[:, :, :, g_perm(budget)]          # no order
+    sel[:, 3:40] = -1                           # a tile's rows without keys, then a whole tile's
+    sel[:, 64:130, 0] = -1
+    check_sparse(b, sel, lse=False)
+
+
+def g_perm(n):
+    return np.random.default_rng(n).permutation(n)
+
+
+@pytest.mark.parametrize("heads,d,bs,lens,q_lens,budget", LARGE)
+def test_large_tiles_with_repeated_and_unseen(heads, d, bs, lens, q_lens, budget):
+    b = Batch(lens, q_lens, heads, d, bs, seed=31)
+    sel = like_neighbours(b, budget)
+    sel[:, 5, 0, -1] = sel[:, 5, 0, 0]          # twice
+    h = b.Hkv - 1
+    sel[:, 32:64, h] = -1
+    sel[:, 32:64, h, 0] = 0
+    sel[:, 40, h, 1] = 1                        # one row of its tile names page 1
+    b.v[:, int(b.tables[0, 1]), h, 2, 3] = math.nan
+    b.k[:, int(b.tables[0, 1]), h, 4, 1] = math.inf
+    check_sparse(b, sel)
+
+
+def test_large_tiles_whose_scores_grow():
+    # every page's scores are above those before it, by far more than the
+    # reference's slack, and fall again: both chains raise theirs and are joined
+    b = Batch([2000], [80], (16, 8), 128, 16, seed=32, poison=False)
+    rise = torch.linspace(-1, 1, 125, device="cuda")
+    rise = torch.where(rise > 0.6, -rise, rise)
+    unit = b.q[:, :, ::2].float().mean(1)                                   # [L][Hkv][d]
+    for j in range(125):
+        blk = int(b.tables[0, j])
+        b.k[:, blk] = (b.k[:, blk].float() * 0.1 + 30 * rise[j] * unit[:, :, None] / unit.norm(dim=-1)[:, :, None, None]).bfloat16()
+    b.q[:] = (b.q.float() * 0.2 + unit.repeat_interleave(2, 1)[:, None] / unit.norm() * 5).bfloat16()
+    sel = np.broadcast_to(np.arange(0, 120, 2, dtype=np.int32), (1, 80, 8, 60)).copy()
+    check_sparse(b, sel)
+
+
+def test_large_tiles_far_in_a_long_table():
+    b = Batch([65000], [100], (8, 8), 128, 16, seed=33)
+    sel = np.broadcast_to(np.array([4062, 0, 2047, 2048, 3999, 1, 4061], np.int32), (1, 100, 8, 7)).copy()
+    check_sparse(b, sel)
+    wide = torch.full((1, 4096), -1, dtype=torch.int32, device="cuda")      # the widest table, and one more
+    wide[:, :b.MB] = b.t
+    for more in (0, 1):
+        b.t = torch.cat([wide, wide[:, :more]], 1).contiguous()
+        check_sparse(b, sel)
+
+
+# a few rows each of many sequences: tiles of 32 and of 16 (query, head) rows
+@pytest.mark.parametrize("heads,d,bs,S", [((16, 4), 128, 16, 120), ((16, 2), 64, 32, 230), ((8, 4), 128, 16, 130),
+                                          ((4, 4), 64, 16, 200)])
+def test_few_rows_of_many_sequences(heads, d, bs, S):
+    g = np.random.default_rng(S)
+    q_lens = g.integers(3, 6, S)
+    b = Batch([int(n) for n in g.integers(5, 180, S)], [int(n) for n in q_lens], heads, d, bs, L=3, seed=34)
+    assert b.T < 5 * S
+    sel = like_neighbours(b, 5)
+    x = check_sparse(b, sel)
+    y = check_sparse(b, sel)
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    sel = some_pages(b, 4)
+    sel[0, 11] = 0                              # a page four times
+    sel[:, 20:30, 1] = -1
+    sel[:, 20:30, 1, 0] = 0
+    sel[:, 23, 1, 1] = 1
+    s = b.rows[23][0]
+    if b.tables[s, 1] >= 0:
+        b.v[:, int(b.tables[s, 1]), 1, 0, 5] = math.nan
+    check_sparse(b, sel)
+
+
+def test_large_tiles_captured_twice_and_on_two_streams():
+    b = Batch([500, 700], [300, 200], (8, 2), 128, 16, seed=35)
+    sel = torch.from_numpy(like_neighbours(b, 6)).cuda()
+    want = torch.empty_like(b.q)
+    kvp.paged_sparse_attention(b.q, b.start, b.k, b.v, b.t, b.n, sel, b.desc, want, None)
+    outs, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        outs.append(torch.zeros_like(b.q))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            for _ in range(3):
+                kvp.paged_sparse_attention(b.q, b.start, b.k, b.v, b.t, b.n, sel, b.desc, outs[-1], None)
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+    b.n -= 17                                   # a graph follows the lengths: their pages' ends, rows without a position
+    b.lens = [n - 17 for n in b.lens]
+    b.rows = [(s, p - 17) for s, p in b.rows]
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    out, _, mag = sparse_want(b, sel.cpu().numpy())
+    got = outs[0].double().cpu().numpy()
+    assert (np.abs(got - out) <= 2.0 ** -8 * np.abs(out) + 2.0 ** -12 * mag).all()
