@@ -16,27 +16,16 @@ struct QueryRows {
     __device__ __forceinline__ int len(int s) const {
         return (int)min((int64_t)max(lens[s], 0), (int64_t)MB * bs);
     }
-    // The last sequence s for which below(s) holds, 0 if it does for none; it
-    // holds up to some sequence.  By whole warps, 32 places at a time: each turn
-    // is a load's latency, and one finds a sequence of 32, two of 1024.
-    template <class Below>
-    __device__ __forceinline__ int last(Below below) const {
-        int lo = 0, n = S;
-        while (n > 1) {
-            const int step = (n + 31) >> 5, at = (threadIdx.x & 31) * step;
-            const uint32_t m = __ballot_sync(0xffffffffu, at < n && below(lo + at));
-            const int k = m ? 31 - __clz(m) : 0;
-            lo += k * step;
-            n = min(step, n - k * step);
-        }
-        return lo;
-    }
-    // The sequence of row r, or -1: a row behind the last sequence's.  (Of empty
-    // sequences and the one behind them the last.)  By whole warps.
+    // The sequence of row r, or -1: a row behind the last sequence's.
     __device__ __forceinline__ int sequence(int r) const {
         if (!start) return r;
         if (r < start[0] || r >= start[S]) return -1;
-        return last([&](int s) { return start[s] <= r; });
+        int lo = 0, hi = S - 1;       // the last s with start[s] <= r (empty sequences lie before it)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (start[mid] <= r) lo = mid; else hi = mid - 1;
+        }
+        return lo;
     }
     // Position of row r of sequence s; negative for a query without a token.
     __device__ __forceinline__ int position(int s, int r) const {
@@ -50,7 +39,7 @@ struct QueryRows {
     }
     // Tile x of at most qt consecutive rows of one sequence: tiles start anew
     // at every sequence's first row.  The tiles of sequence s begin at index
-    // start[s] / qt + s, so at most T / qt + S of them have rows.  By whole warps.
+    // start[s] / qt + s, so at most T / qt + S of them have rows.
     __device__ __forceinline__ bool tile(int qt, int x, int &r0, int &nr, int &s) const {
         if (qt == 1 || !start) {
             r0 = x;
@@ -58,7 +47,12 @@ struct QueryRows {
             s = sequence(x);
             return s >= 0;
         }
-        s = last([&](int i) { return start[i] / qt + i <= x; });
+        int lo = 0, hi = S - 1;       // the last s whose tiles begin at or before x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (start[mid] / qt + mid <= x) lo = mid; else hi = mid - 1;
+        }
+        s = lo;
         r0 = start[s] + (x - (start[s] / qt + s)) * qt;
         const int end = min(start[s + 1], T);
         nr = min(qt, end - r0);
