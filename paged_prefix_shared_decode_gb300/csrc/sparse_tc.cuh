@@ -36,7 +36,7 @@
 // Bound by the chain of a step, 2300 cycles for 128 tokens of which the products
 // are 1536, and by 12 us before a tile's first page and after its last (Q, the
 // lists and the table in sequence, the join).  643 queries over 32 pages of 32
-// tokens, 8 kv heads of four query heads at d 128: 66 us (176 tiles of about 70
+// tokens, 8 kv heads of four query heads at d 128: 65 us (176 tiles of about 70
 // pages on 152 SMs, two rounds; tiles of 32 rows on mma.sync 144 us), 194
 // queries 37 us.  One chain with one MMA issuer and steps of 64 tokens took 78
 // us, a TMA box per 16 tokens with the groups worked out one by one 87, cp.async
@@ -50,7 +50,7 @@ namespace {
 constexpr int kTcThreads = 20 * 32;
 constexpr int kTcRows = 128;         // (query, head) rows of a tile
 constexpr int kTcPages = 4096;       // pages of a sequence that a tile's map covers
-constexpr int kTcStep = 128;          // tokens of a step
+constexpr int kTcStep = 128;         // tokens of a step
 constexpr int kTcGroups = kTcStep / 16;
 constexpr int kTcCols = 512;         // TMEM columns: S / P of two steps, both O
 constexpr int kTcSlots = 8;          // steps whose groups are kept
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_wait();
+    if (warp == 0 && lane < a.rows.S) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(a.rows.lens + lane));
     const int h = blockIdx.y % a.Hkv, l = blockIdx.y / a.Hkv;
     int r0, nr, seq;
     if (!a.rows.tile(a.qt, blockIdx.x, r0, nr, seq)) return;
@@ -246,10 +247,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     // Q, and zeros behind the last row
     const uint32_t q_smem = saddr(smem), k_smem = saddr(smem + C::K_OFF), v_smem = saddr(smem + C::V_OFF);
-    for (int x = tid; x < kTcRows * C::CH; x += kTcThreads) {
-        const int r = x / C::CH, c = x % C::CH;
-        cp_async16(q_smem + (c >> 3) * C::Q_SLAB + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                   a.q + (r < cols ? q_row(r) * D + 8 * c : 0), r < cols ? 16 : 0);
+    {
+        // a thread's rows are a multiple of 8 apart, so that their swizzle is one;
+        // r / G by a product (exact for r < 128)
+        constexpr int EACH = kTcThreads / C::CH;
+        static_assert(EACH % 8 == 0 && kTcThreads % C::CH == 0);
+        const int c = tid % C::CH, first = tid / C::CH, inv = (65535 + a.G) / a.G;
+        const uint32_t to = q_smem + (c >> 3) * C::Q_SLAB + (((c & 7) ^ (first & 7)) << 4);
+        const __nv_bfloat16 *from = a.q + (lr0 * a.Hq + h * a.G) * D + 8 * c;
+        for (int r = first; r < kTcRows; r += EACH) {
+            const int q = r * inv >> 16;
+            cp_async16(to + r * 128, r < cols ? from + (int64_t)(q * (a.Hq - a.G) + r) * D : a.q, r < cols ? 16 : 0);
+        }
     }
     for (int i = tid; i < (seen + 3) / 4; i += kTcThreads) reinterpret_cast<uint4 *>(s_map)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
