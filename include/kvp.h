@@ -754,12 +754,15 @@ int kvp_page_select(const float *scores, int64_t score_stride, const int32_t *q_
  * natural log-sum-exp.  Entries that are negative, or name a page that the
  * query does not see or whose table entry is outside [0, NB), are passed
  * over; their order does not matter, and a page named twice counts twice.  A
- * row without keys gives out 0 and lse -inf.  q, out: bf16 [L][num_q][Hq][d];
- * lse: fp32 [L][num_q][Hq] or NULL.  Keys and values that a row sees should be
- * finite: a NaN among them shows in its results, an infinite value as an
- * infinity or a NaN.  Other slots do not matter, whatever they hold.  Sums and
- * weights are held in 32 bits (a weight meets V as two bf16 parts), and
- * repeated calls give equal bits.
+ * row without keys gives out 0 and lse -inf.  q, out (apart from q): bf16
+ * [L][num_q][Hq][d]; lse: fp32 [L][num_q][Hq] or NULL.  Keys and values that a
+ * row sees should be finite: a NaN among them shows in its results, an infinite
+ * value as an infinity or a NaN.  Other slots do not matter, whatever they hold
+ * (but neighbouring rows of a chunk are done together, and one by one, several
+ * times slower, where one of them names a page twice or a page that one of them
+ * names holds a value that is not finite).  Sums and weights are held in 32 bits
+ * (a weight meets V as two bf16 parts), and repeated calls give equal bits.  A
+ * kernel's wait that runs out, which no input causes, leaves NaN in its rows.
  */
 int paged_sparse_attention(const void *q, const int32_t *q_start, int32_t num_q, const void *k_pool,
                            const void *v_pool, const int32_t *block_tables, const int32_t *seq_lens,
