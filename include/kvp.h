@@ -162,7 +162,10 @@ int seq_append(kvp_pool *pool, int32_t seq, const void *k, const void *v, int32_
 /* Append to several distinct sequences in one launch: ntoks[i] tokens to
  * seqs[i] (host arrays), processed in order with the semantics of seq_append;
  * k, v: device [L][sum ntoks][Hkv][d], sequence-major.  All or nothing: if the
- * pool cannot hold every append, nothing changes and KVP_ERR_OOM returns. */
+ * pool cannot hold every append, nothing changes and KVP_ERR_OOM returns.
+ * (Appends beyond a launch's parameters take several; so does a batch in which
+ * one sequence copies a shared page and another, cut back in that page by
+ * seq_accept_draft, goes on in it: the copies are made first.) */
 int seq_append_batch(kvp_pool *pool, int32_t nseq, const int32_t *seqs, const int32_t *ntoks,
                      const void *k, const void *v, void *stream);
 
@@ -464,7 +467,8 @@ int kvp_decode_step(kvp_pool *pool, const int32_t *seq_ids, int32_t num_seqs, in
  * Both kvp_decode_step and kvp_decode_step_run, when the step's inputs are
  * already on the device or in mapped host memory (KVP_STEP_HOST_MAPPED), the
  * pool holds bf16 pages, the append has at most 64 tokens and 16
- * copy-on-write blocks and the plan at most 24 KB, make steps 1-2 and the
+ * copy-on-write blocks, its copies need not come first (see seq_append_batch)
+ * and the plan has at most 24 KB, make steps 1-2 and the
  * plan upload one kernel: the new K/V go straight into their pool slots (from
  * host memory when mapped; d_k_new / d_v_new are then left unwritten), q to
  * d_q, and the plan, carried in the kernel's parameters, into the workspace;
@@ -475,7 +479,8 @@ int kvp_decode_step(kvp_pool *pool, const int32_t *seq_ids, int32_t num_seqs, in
  * plan that is still waiting for its run is KVP_ERR_INVALID, since its
  * tokens are already in the sequences.  Between plan and run no call may
  * change the planned sequences or free blocks; appends and attention on other
- * sequences may run.  `workspace` belongs to the run until the stream passes
+ * sequences may run (but no append to a sequence that was cut back in a page
+ * which it shared with a planned one: the run still copies that page).  `workspace` belongs to the run until the stream passes
  * its kernels, as for every attention call.  The run takes its device
  * buffers from io as kvp_decode_step does (num_seqs and ntok are the plan's).
  * Errors: the plan call as kvp_decode_step's (KVP_ERR_INVALID, KVP_ERR_OOM;
@@ -671,7 +676,7 @@ typedef struct {
  * KVP_ERR_INVALID also for a rotation outside the above, KVP_ERR_STATE also
  * while `stream` is being captured (a replay would write the same slots again).
  * One kernel for appends of up to 512 sequences, 512 copied blocks and 4096
- * pages; no workspace.  A batch whose ntoks are all 0 does nothing.  After
+ * pages (two where the copies come first, see seq_append_batch); no workspace.  A batch whose ntoks are all 0 does nothing.  After
  * KVP_ERR_CUDA from a launch the bookkeeping stands.
  */
 int seq_append_rope(kvp_pool *pool, int32_t nseq, const int32_t *seqs, const int32_t *ntoks, const void *k,

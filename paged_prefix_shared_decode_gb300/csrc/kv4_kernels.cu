@@ -152,6 +152,13 @@ cudaError_t launch_part4(const Kv4Write &w, int cow_done, int ncow, int tok_done
 cudaError_t launch_kv4_write(const Kv4Write &w, cudaStream_t stream) {
     if (w.ncow == 0 && w.ntok == 0) return cudaSuccess;
     if (w.d != 64 && w.d != 128) return cudaErrorInvalidValue;
+    if (w.copies_first) {
+        Kv4Write copies = w, tokens = w;
+        copies.copies_first = tokens.copies_first = false;
+        copies.ntok = tokens.ncow = 0;
+        const cudaError_t e = launch_kv4_write(copies, stream);
+        return e == cudaSuccess ? launch_kv4_write(tokens, stream) : e;
+    }
     if (w.ntok <= 64 && w.ncow <= 16) return launch_part4<64, 16>(w, 0, w.ncow, 0, w.ntok, stream);
     int cow_done = 0, tok_done = 0;
     while (cow_done < w.ncow || tok_done < w.ntok) {

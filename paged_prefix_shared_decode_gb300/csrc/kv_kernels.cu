@@ -8,7 +8,8 @@
 // [bs][d], those slots are one contiguous run of used*d elements.
 // The scatter writes token i of the append, [L][ntok][Hkv][d], to slot
 // slots[i] = block*bs + slot.  The copies touch slots < used of the copy
-// block and the scatter slots >= used, so both run in the same grid.
+// block and the scatter slots >= used, so both run in the same grid (but for
+// KvWrite's copies_first, whose copies have grids of their own).
 // Every thread moves 16-byte chunks (d is a multiple of 8).
 #include <cuda_runtime.h>
 
@@ -307,7 +308,7 @@ cudaError_t launch_step_write_pb(const KvWrite &w, const void *q_src, void *q_ds
 }
 
 bool step_write_fits(const KvWrite &w, size_t plan_bytes) {
-    return w.ntok <= kSmallSlots && w.ncow <= kSmallCow && plan_bytes <= kStepPlanMax && plan_bytes % 16 == 0 &&
+    return !w.copies_first && w.ntok <= kSmallSlots && w.ncow <= kSmallCow && plan_bytes <= kStepPlanMax && plan_bytes % 16 == 0 &&
            w.d % 8 == 0;
 }
 
@@ -321,6 +322,13 @@ cudaError_t launch_step_write(const KvWrite &w, const void *q_src, void *q_dst, 
 
 cudaError_t launch_kv_write(const KvWrite &w, cudaStream_t stream) {
     if (w.ncow == 0 && w.ntok == 0) return cudaSuccess;
+    if (w.copies_first) {
+        KvWrite copies = w, tokens = w;
+        copies.copies_first = tokens.copies_first = false;
+        copies.ntok = tokens.ncow = 0;
+        const cudaError_t e = launch_kv_write(copies, stream);
+        return e == cudaSuccess ? launch_kv_write(tokens, stream) : e;
+    }
     if (w.ntok <= kSmallSlots && w.ncow <= kSmallCow)
         return launch_part<kSmallSlots, kSmallCow>(w, 0, w.ncow, 0, w.ntok, stream);
     int cow_done = 0, tok_done = 0;

@@ -145,12 +145,14 @@ int append_batch_commit(kvp_pool *p, int32_t nseq, const int32_t *seqs, const in
 // seq_append_batch in two halves: the checks and the bookkeeping, whose
 // token slots and copy-on-write triples go to the caller's lists (the
 // sequences grow at once), then the device write of those lists, with the
-// new tokens' K/V [L][slots.size()][Hkv][d].  No call that frees or
+// new tokens' K/V [L][slots.size()][Hkv][d].  copies_first: the copies have to
+// be made before any token is written (see KvWrite).  No call that frees or
 // reallocates the lists' blocks may come in between.
 int append_batch_commit_lists(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32_t *ntoks,
-                              std::vector<int32_t> &slots, std::vector<int32_t> &cow, int32_t *total_out);
+                              std::vector<int32_t> &slots, std::vector<int32_t> &cow, bool *copies_first,
+                              int32_t *total_out);
 int append_issue_lists(kvp_pool *p, const std::vector<int32_t> &slots, const std::vector<int32_t> &cow,
-                       const void *k, const void *v, void *stream);
+                       bool copies_first, const void *k, const void *v, void *stream);
 
 // A pool's shape and device storage (codes and exponents for 4-bit pages).
 struct PoolView {
@@ -179,7 +181,14 @@ int device_sm_count();
 void count_launch();
 long long launch_count();
 
-// K/V write: copy-on-write copies (src, dst, used slots) then token scatter.
+// Copies and tokens of an append are written side by side: a copy reads slots
+// below `used` of a block that its sequence leaves, and the block's last holder,
+// which may be in the same batch and writes in place, writes at its own end.
+// That lies below `used` where the holder was cut back in the shared block;
+// the copies then go in launches of their own, ahead of the tokens
+// (copies_first).
+//
+// K/V write: copy-on-write copies (src, dst, used slots) and token scatter.
 struct KvWrite {
     void *k_pool;
     void *v_pool;
@@ -190,6 +199,7 @@ struct KvWrite {
     const int32_t *slots;  // host: block*bs + slot per token
     int32_t ncow;
     const int32_t *cow;    // host: (src, dst, used) triples
+    bool copies_first;
 };
 
 cudaError_t launch_kv_write(const KvWrite &w, cudaStream_t stream);
@@ -237,6 +247,7 @@ struct Kv4Write {
     const int32_t *slots;  // host: block*bs + slot per token
     int32_t ncow;
     const int32_t *cow;    // host: (src, dst, used) triples
+    bool copies_first;
 };
 cudaError_t launch_kv4_write(const Kv4Write &w, cudaStream_t stream);
 
@@ -340,6 +351,7 @@ struct RopeAppend {
     int32_t nseq;
     const int32_t *cow;         // host: (src, dst, used) triples
     int32_t ncow;
+    bool copies_first;          // as in KvWrite
 };
 cudaError_t launch_rope_append(const RopeAppend &r, cudaStream_t stream);
 

@@ -908,6 +908,7 @@ std::atomic<long long> g_launches{0};
 struct StagedAppend {
     kvp_pool *pool;
     const std::vector<int32_t> *slots, *cow;
+    bool copies_first;
     const void *k, *v;
 };
 
@@ -932,7 +933,8 @@ int launch_packed(const Packed &pk, const kvp_attn_desc &d, const void *q, const
         cudaMemcpyAsync(ws, pk.image.data(), w.plan_bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess)
         return KVP_ERR_CUDA;
     if (append) {
-        const int rc = append_issue_lists(append->pool, *append->slots, *append->cow, append->k, append->v, stream);
+        const int rc = append_issue_lists(append->pool, *append->slots, *append->cow, append->copies_first, append->k,
+                                          append->v, stream);
         if (rc) return rc;
     }
     unsigned char *base = (unsigned char *)ws;
@@ -1140,6 +1142,7 @@ struct kvp_step_plan {
     int32_t num_seqs = 0, ntok = 0;
     bool ready = false;                // planned and not yet run
     std::vector<int32_t> slots, cow;   // the append's device write
+    bool copies_first = false;
     Packed pk;
 };
 
@@ -1205,9 +1208,10 @@ int plan_step(kvp_step_plan &sp, kvp_pool *pool, const int32_t *seq_ids, int32_t
     sp.ntok = ntok;
     sp.slots.clear();
     sp.cow.clear();
+    sp.copies_first = false;
     if (ntok > 0) {
         int32_t total = 0;
-        const int rc = append_batch_commit_lists(pool, num_seqs, seq_ids, ntoks, sp.slots, sp.cow, &total);
+        const int rc = append_batch_commit_lists(pool, num_seqs, seq_ids, ntoks, sp.slots, sp.cow, &sp.copies_first, &total);
         if (rc) return rc;
     }
     HostPlan &hp = t_plan;
@@ -1230,11 +1234,11 @@ int launch_step(kvp_step_plan &sp, const kvp_step_io *io, void *ws, size_t ws_by
     float *lse = mapped && io->h_lse ? io->h_lse : io->d_lse;
     if (ws_bytes < sp.pk.w.total) {   // the pool already holds the new tokens: write them
         if (!sp.slots.empty() &&
-            append_issue_lists(sp.pool, sp.slots, sp.cow, io->d_k_new, io->d_v_new, st) != KVP_OK)
+            append_issue_lists(sp.pool, sp.slots, sp.cow, sp.copies_first, io->d_k_new, io->d_v_new, st) != KVP_OK)
             return KVP_ERR_CUDA;
         return KVP_ERR_WORKSPACE;
     }
-    const StagedAppend staged{sp.pool, &sp.slots, &sp.cow, io->d_k_new, io->d_v_new};
+    const StagedAppend staged{sp.pool, &sp.slots, &sp.cow, sp.copies_first, io->d_k_new, io->d_v_new};
     int rc = launch_packed(sp.pk, sp.desc, io->d_q, pv.k, pv.v, sp.num_seqs, nullptr, 0, out, lse, ws, ws_bytes,
                            st, pv.kv4 ? pv.k_exp : nullptr, pv.kv4 ? pv.v_exp : nullptr,
                            sp.slots.empty() ? nullptr : &staged);
@@ -1270,6 +1274,7 @@ int launch_fused(kvp_step_plan &sp, const kvp_step_io *io, void *ws, size_t ws_b
     w.slots = sp.slots.data();
     w.ncow = (int32_t)(sp.cow.size() / 3);
     w.cow = sp.cow.data();
+    w.copies_first = sp.copies_first;
     if (!step_write_fits(w, sp.pk.w.plan_bytes)) return KVP_OK;
     *launched = true;
     sp.ready = false;

@@ -42,10 +42,12 @@ struct kvp_pool {
     int64_t cow_count = 0;
     // scratch reused by appends and exports
     std::vector<int32_t> slots, cow, stage;
+    bool copies_first = false;           // of the append staged in slots and cow
     // which sequences and blocks a batch has met: marks of the current batch
-    // (an ordered set and a map cost 8 us for 64 sequences, these under 1)
+    // (an ordered set and a map cost 8 us for 64 sequences, these under 1);
+    // block_note goes with block_mark
     std::vector<uint32_t> seq_mark, block_mark;
-    std::vector<int32_t> block_drops;
+    std::vector<int32_t> block_note;
     uint32_t mark = 0;
 
     uint32_t new_mark() {
@@ -95,7 +97,7 @@ Need blocks_needed(const kvp_pool *p, int32_t s, int32_t ntok, uint32_t batch) {
     if (ntok > 0 && n % bs != 0) {
         int32_t last = t.back();
         int32_t rc = p->ref[last];
-        if (batch && p->block_mark[last] == batch) rc -= p->block_drops[last];
+        if (batch && p->block_mark[last] == batch) rc -= p->block_note[last];
         need.cow = rc > 1 ? 1 : 0;
     }
     need.fresh = (n + ntok + bs - 1) / bs - (int64_t)t.size();
@@ -128,6 +130,33 @@ void commit_append(kvp_pool *p, int32_t s, int32_t ntok, std::vector<int32_t> &s
     p->lens[s] = n + ntok;
 }
 
+// Commits the appends of a checked batch in order.  Whether its copies have to
+// be made before any token is written: a sequence that held a block's last
+// reference writes in place below the slots that an earlier one's copy reads
+// (they shared the block, and the later one was cut back in it).
+bool commit_batch(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32_t *ntoks, std::vector<int32_t> &slots,
+                  std::vector<int32_t> &cow) {
+    const uint32_t batch = p->new_mark();
+    bool first = false;
+    slots.clear();
+    cow.clear();
+    for (int32_t i = 0; i < nseq; ++i) {
+        const int32_t s = seqs[i], used = p->lens[s] % p->desc.block_size;
+        const int32_t last = ntoks[i] > 0 && used > 0 ? p->tables[s].back() : -1;
+        const size_t copies = cow.size();
+        commit_append(p, s, ntoks[i], slots, cow);
+        if (last < 0) continue;
+        const bool met = p->block_mark[last] == batch;
+        if (cow.size() > copies) {       // block_note: the most slots of it that a copy reads
+            p->block_note[last] = met ? std::max(p->block_note[last], used) : used;
+            p->block_mark[last] = batch;
+        } else if (met && used < p->block_note[last]) {
+            first = true;
+        }
+    }
+    return first;
+}
+
 int check_append(const kvp_pool *p, int32_t s, int32_t ntok, uint32_t batch, Need *out) {
     if (!is_live(p, s) || ntok < 0) return KVP_ERR_INVALID;
     Need nd = blocks_needed(p, s, ntok, batch);
@@ -139,8 +168,8 @@ int check_append(const kvp_pool *p, int32_t s, int32_t ntok, uint32_t batch, Nee
 
 // The device write of an append: the copy-on-write triples cow[0..3*ncow)
 // and the token scatter to slots[0..ntok).
-int issue_write_lists(kvp_pool *p, const int32_t *slots, const int32_t *cow, int32_t ncow, const void *k,
-                      const void *v, int32_t ntok, void *stream) {
+int issue_write_lists(kvp_pool *p, const int32_t *slots, const int32_t *cow, int32_t ncow, bool copies_first,
+                      const void *k, const void *v, int32_t ntok, void *stream) {
     if (ntok == 0 && ncow == 0) return KVP_OK;
     if (p->kv4) {
         kvp::Kv4Write w{};
@@ -159,6 +188,7 @@ int issue_write_lists(kvp_pool *p, const int32_t *slots, const int32_t *cow, int
         w.slots = slots;
         w.ncow = ncow;
         w.cow = cow;
+        w.copies_first = copies_first;
         return kvp::launch_kv4_write(w, (cudaStream_t)stream) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
     }
     kvp::KvWrite w{};
@@ -175,13 +205,15 @@ int issue_write_lists(kvp_pool *p, const int32_t *slots, const int32_t *cow, int
     w.slots = slots;
     w.ncow = ncow;
     w.cow = cow;
+    w.copies_first = copies_first;
     cudaError_t e = kvp::launch_kv_write(w, (cudaStream_t)stream);
     return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 // The write of the append staged in the pool.
 int issue_write(kvp_pool *p, const void *k, const void *v, int32_t ntok, void *stream) {
-    return issue_write_lists(p, p->slots.data(), p->cow.data(), (int32_t)(p->cow.size() / 3), k, v, ntok, stream);
+    return issue_write_lists(p, p->slots.data(), p->cow.data(), (int32_t)(p->cow.size() / 3), p->copies_first, k, v, ntok,
+                             stream);
 }
 
 bool aligned16(const void *ptr) { return ((uintptr_t)ptr & 15) == 0; }
@@ -213,7 +245,7 @@ kvp_pool *new_pool(const kvp_pool_desc &d) {
     p->live.assign(d.max_seqs, 0);
     p->seq_mark.assign(d.max_seqs, 0);
     p->block_mark.assign(d.num_blocks, 0);
-    p->block_drops.assign(d.num_blocks, 0);
+    p->block_note.assign(d.num_blocks, 0);
     for (int32_t i = 0; i < d.max_seqs; ++i) p->free_ids.insert(i);
     return p;
 }
@@ -559,6 +591,7 @@ int seq_append(kvp_pool *p, int32_t seq, const void *k, const void *v, int32_t n
     p->slots.clear();
     p->cow.clear();
     commit_append(p, seq, ntok, p->slots, p->cow);
+    p->copies_first = false;
     return issue_write(p, k, v, ntok, stream);
 }
 
@@ -611,7 +644,7 @@ int seq_append_rope(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32_
     std::vector<kvp::RopeSeq> runs(nseq);
     for (int32_t i = 0; i < nseq; ++i) runs[i] = {ntoks[i], p->lens[seqs[i]], nullptr};
     int32_t ntok = 0;
-    rc = kvp::append_batch_commit_lists(p, nseq, seqs, ntoks, p->slots, p->cow, &ntok);
+    rc = kvp::append_batch_commit_lists(p, nseq, seqs, ntoks, p->slots, p->cow, &r.copies_first, &ntok);
     if (rc) return rc;
     for (int32_t i = 0; i < nseq; ++i)
         if (ntoks[i] > 0) runs[i].blocks = p->tables[seqs[i]].data() + runs[i].pos0 / d.block_size;
@@ -803,9 +836,9 @@ int append_batch_check(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int
         p->seq_mark[seqs[i]] = batch;
         if (nd.cow) {
             const int32_t last = p->tables[seqs[i]].back();
-            if (p->block_mark[last] != batch) p->block_drops[last] = 0;
+            if (p->block_mark[last] != batch) p->block_note[last] = 0;
             p->block_mark[last] = batch;
-            p->block_drops[last] += 1;
+            p->block_note[last] += 1;    // references that leave it
         }
         need += nd.cow + nd.fresh;
         total += ntoks[i];
@@ -823,29 +856,26 @@ int append_batch_commit(kvp_pool *p, int32_t nseq, const int32_t *seqs, const in
     if (rc != KVP_OK && rc != KVP_ERR_OOM) return rc;
     if (total > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return KVP_ERR_INVALID;
     if (rc) return rc;
-    p->slots.clear();
-    p->cow.clear();
-    for (int32_t i = 0; i < nseq; ++i) commit_append(p, seqs[i], ntoks[i], p->slots, p->cow);
+    p->copies_first = commit_batch(p, nseq, seqs, ntoks, p->slots, p->cow);
     *total_out = (int32_t)total;
     return KVP_OK;
 }
 
 int append_batch_commit_lists(kvp_pool *p, int32_t nseq, const int32_t *seqs, const int32_t *ntoks,
-                              std::vector<int32_t> &slots, std::vector<int32_t> &cow, int32_t *total_out) {
+                              std::vector<int32_t> &slots, std::vector<int32_t> &cow, bool *copies_first,
+                              int32_t *total_out) {
     int64_t total = 0;
     int rc = append_batch_check(p, nseq, seqs, ntoks, &total);
     if (rc) return rc;
-    slots.clear();
-    cow.clear();
-    for (int32_t i = 0; i < nseq; ++i) commit_append(p, seqs[i], ntoks[i], slots, cow);
+    *copies_first = commit_batch(p, nseq, seqs, ntoks, slots, cow);
     *total_out = (int32_t)total;
     return KVP_OK;
 }
 
 int append_issue_lists(kvp_pool *p, const std::vector<int32_t> &slots, const std::vector<int32_t> &cow,
-                       const void *k, const void *v, void *stream) {
-    return issue_write_lists(p, slots.data(), cow.data(), (int32_t)(cow.size() / 3), k, v, (int32_t)slots.size(),
-                             stream);
+                       bool copies_first, const void *k, const void *v, void *stream) {
+    return issue_write_lists(p, slots.data(), cow.data(), (int32_t)(cow.size() / 3), copies_first, k, v,
+                             (int32_t)slots.size(), stream);
 }
 
 PoolView pool_view(const kvp_pool *p) {

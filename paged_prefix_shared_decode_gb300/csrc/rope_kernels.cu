@@ -354,6 +354,13 @@ cudaError_t launch_part(const RopeAppend &r, const Run *run, int nrun, const int
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeAppend &r, cudaStream_t stream) {
+    if (r.copies_first) {
+        RopeAppend copies = r, tokens = r;
+        copies.copies_first = tokens.copies_first = false;
+        copies.nseq = tokens.ncow = 0;
+        const cudaError_t e = launch_rope_append(copies, stream);
+        return e == cudaSuccess ? launch_rope_append(tokens, stream) : e;
+    }
     constexpr int NR = 512, NBk = 4096, NC = 512;
     Run run[NR];
     int32_t blk[NBk];
