@@ -184,6 +184,7 @@ int block_refcount(const kvp_pool *pool, int32_t block, int32_t *rc_out);
 int kvp_free_block_count(const kvp_pool *pool, int32_t *n_out);
 int kvp_cow_count(const kvp_pool *pool, int64_t *n_out);
 int kvp_pool_shape(const kvp_pool *pool, int32_t *layers_out, int32_t *kv_heads_out);
+int kvp_pool_head_dim(const kvp_pool *pool, int32_t *head_dim_out);
 
 /* Block tables and lengths of n sequences into host arrays h_tables
  * [n][width] (padded with -1) and h_lens [n]. */

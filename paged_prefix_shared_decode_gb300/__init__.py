@@ -19,7 +19,7 @@ __all__ = [
     "KvpError", "PoolDesc", "AttnDesc", "load", "lib_path",
     "kv_pool_create", "kv_pool_create_kv4", "kv_pool_destroy", "seq_alloc", "seq_fork", "seq_free", "seq_append",
     "seq_append_batch", "seq_reserve", "seq_block_table", "seq_len", "block_refcount",
-    "kvp_free_block_count", "kvp_cow_count", "kvp_pool_shape", "kvp_gather_tables", "kvp_export_tables",
+    "kvp_free_block_count", "kvp_cow_count", "kvp_pool_shape", "kvp_pool_head_dim", "kvp_gather_tables", "kvp_export_tables",
     "kvp_decode_workspace_size", "paged_decode_attention", "kvp_verify_workspace_size",
     "tree_verify_attention", "kvp_device_error", "kvp_decode_plan_stats", "kvp_strerror",
     "kvp_set_kernel_events", "kvp_kernel_launches", "paged_decode_attention_noalloc",
@@ -114,6 +114,7 @@ _SIGS = {
     "kvp_free_block_count": ([_P, _I32P], ctypes.c_int),
     "kvp_cow_count": ([_P, ctypes.POINTER(ctypes.c_int64)], ctypes.c_int),
     "kvp_pool_shape": ([_P, _P, _P], ctypes.c_int),
+    "kvp_pool_head_dim": ([_P, _I32P], ctypes.c_int),
     "kvp_gather_tables": ([_P, _P, _I32, _I32, _P, _P], ctypes.c_int),
     "kvp_export_tables": ([_P, _P, _I32, _I32, _P, _P, _P], ctypes.c_int),
     "kvp_decode_workspace_size": ([ctypes.POINTER(AttnDesc), _P, _P, _I32, _I32], ctypes.c_size_t),
@@ -343,6 +344,12 @@ def kvp_pool_shape(pool):
     layers, heads = _I32(), _I32()
     _check(load().kvp_pool_shape(pool, ctypes.byref(layers), ctypes.byref(heads)), "kvp_pool_shape")
     return layers.value, heads.value
+
+
+def kvp_pool_head_dim(pool) -> int:
+    n = _I32()
+    _check(load().kvp_pool_head_dim(pool, ctypes.byref(n)), "kvp_pool_head_dim")
+    return n.value
 
 
 def kvp_gather_tables(pool, seqs, width: int):

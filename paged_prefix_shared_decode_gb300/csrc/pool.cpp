@@ -753,6 +753,12 @@ int kvp_pool_shape(const kvp_pool *p, int32_t *layers_out, int32_t *kv_heads_out
     return KVP_OK;
 }
 
+int kvp_pool_head_dim(const kvp_pool *p, int32_t *head_dim_out) {
+    if (!p || !head_dim_out) return KVP_ERR_INVALID;
+    *head_dim_out = p->desc.head_dim;
+    return KVP_OK;
+}
+
 int kvp_gather_tables(const kvp_pool *p, const int32_t *seqs, int32_t n, int32_t width,
                       int32_t *h_tables, int32_t *h_lens) {
     if (!p || n < 0 || width < 0 || (n > 0 && !seqs)) return KVP_ERR_INVALID;

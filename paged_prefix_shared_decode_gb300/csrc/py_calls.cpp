@@ -32,6 +32,7 @@ struct Lib {                         // (in the order of the module's `functions
     decltype(&::seq_append_rope) append_rope;
     decltype(&::seq_reorder) reorder;
     decltype(&::kvp_pool_shape) pool_shape;
+    decltype(&::kvp_pool_head_dim) pool_head_dim;
     decltype(&::kvp_page_bounds) bounds;
     decltype(&::kvp_page_scores) scores;
     decltype(&::kvp_page_select) select;
@@ -248,9 +249,9 @@ void f_append_rope(PyObject *const *a) {
     void *k = nullptr, *v = nullptr, *q = nullptr, *q_out = nullptr;
     int32_t *positions = nullptr, hq = 0;
     if (T != 0) {
-        int32_t layers = 0, heads = 0;
+        int32_t layers = 0, heads = 0, d = 0;
         run("kvp_pool_shape", [&] { return g_lib.pool_shape(pool, &layers, &heads); });
-        const int64_t d = size_of("k", a[3], -1);
+        run("kvp_pool_head_dim", [&] { return g_lib.pool_head_dim(pool, &d); });
         k = at.arg("k", a[3], at::kBFloat16, {layers, T, heads, d});
         v = at.arg("v", a[4], at::kBFloat16, {layers, T, heads, d});
         positions = static_cast<int32_t *>(at.arg("positions", a[6], at::kInt, {T}));
@@ -461,9 +462,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 PyMODINIT_FUNC PyInit__calls(void) {
     PyObject *m = PyModule_Create(&module);
-    PyObject *f = Py_BuildValue("(sssssssss)", "seq_append_rope", "seq_reorder", "kvp_pool_shape", "kvp_page_bounds",
-                                "kvp_page_scores", "kvp_page_select", "paged_sparse_attention", "kvp_beam_select",
-                                "kvp_state_reorder");
+    PyObject *f = Py_BuildValue("(ssssssssss)", "seq_append_rope", "seq_reorder", "kvp_pool_shape", "kvp_pool_head_dim",
+                                "kvp_page_bounds", "kvp_page_scores", "kvp_page_select", "paged_sparse_attention",
+                                "kvp_beam_select", "kvp_state_reorder");
     if (!m || !f || PyModule_AddObjectRef(m, "functions", f) != 0 ||
         PyModule_AddStringConstant(m, "torch_version", KVP_TORCH_VERSION) != 0)
         Py_CLEAR(m);
