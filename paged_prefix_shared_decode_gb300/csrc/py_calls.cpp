@@ -334,6 +334,19 @@ void f_sparse(PyObject *const *a) {
 
 void f_beam(PyObject *const *a) {
     const Here at(a[9]);
+    // the workspace: a tensor that has what ws_bytes says (None: all of it), or an
+    // address of ws_bytes
+    int64_t bytes = a[8] == Py_None ? -1 : integer("ws_bytes", a[8]);
+    if (a[8] != Py_None && bytes < 0) value_error("ws_bytes: out of range");
+    const at::Tensor *room = THPVariable_Check(a[7]) ? &THPVariable_Unpack(a[7]) : nullptr;
+    if (room) {
+        const int64_t has = (int64_t)room->nbytes();
+        if (bytes > has)
+            value_error("ws_bytes: " + std::to_string(bytes) + ", but the workspace has " + std::to_string(has));
+        if (bytes < 0) bytes = has;
+    } else if (bytes < 0) {
+        value_error("ws_bytes: needed where the workspace is no tensor");
+    }
     const at::Tensor &x = tensor("logits", a[0]);
     const at::ScalarType type = x.scalar_type();
     const int kind = type == at::kFloat ? KVP_F32 : type == at::kBFloat16 ? KVP_BF16 : type == at::kHalf ? KVP_F16 : -1;
@@ -358,22 +371,12 @@ void f_beam(PyObject *const *a) {
     float *best = static_cast<float *>(at.arg("out_scores", a[4], at::kFloat, {G, n}));
     int32_t *rows = static_cast<int32_t *>(at.arg("out_rows", a[5], at::kInt, {G, n}));
     int32_t *tokens = static_cast<int32_t *>(at.arg("out_tokens", a[6], at::kInt, {G, n}));
-    void *ws;
-    size_t bytes;
-    if (THPVariable_Check(a[7])) {
-        const at::Tensor &w = THPVariable_Unpack(a[7]);
-        if (!w.is_cuda() || !w.is_contiguous()) value_error("workspace: expected a contiguous CUDA tensor");
-        ws = w.data_ptr();
-        bytes = a[8] == Py_None ? w.nbytes() : (size_t)integer("ws_bytes", a[8]);
-    } else {
-        ws = address(a[7]);
-        bytes = (size_t)integer("ws_bytes", a[8]);
-    }
+    void *ws = room ? at.arg("workspace", a[7], room->scalar_type(), room->sizes()) : address(a[7]);
     const int32_t pad = integer32("pad_token", a[3]);
     const void *logits = x.data_ptr();
     run("kvp_beam_select", [&] {
         return g_lib.beam(logits, kind, row, cum, finished, pad, (int32_t)G, (int32_t)B, (int32_t)V, (int32_t)n, best, rows,
-                          tokens, ws, bytes, at.stream);
+                          tokens, ws, (size_t)bytes, at.stream);
     });
 }
 
