@@ -583,7 +583,7 @@ bool beam_shape_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out) 
     if (groups <= 0 || beams <= 0 || beams > kMaxBeams || vocab <= 0 || vocab > (1 << 30) || n_out <= 0 || n_out > kMaxOut)
         return false;
     const int64_t chunks = (vocab + kUneven - 1) / kUneven;
-    return groups * beams * chunks <= INT32_MAX && beams * chunks * n_out <= INT32_MAX / 2;
+    return (int64_t)groups * beams * chunks <= INT32_MAX && beams * chunks * n_out <= INT32_MAX / 2;
 }
 
 template <class T>
