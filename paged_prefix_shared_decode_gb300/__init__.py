@@ -11,6 +11,7 @@ is missing.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -799,9 +800,28 @@ def seq_append_rope(pool, seqs, ntoks, k, v, rope: RopeDesc, positions=None, q=N
     _native().seq_append_rope(pool, seqs, ntoks, k, v, rope, positions, q, q_out, stream)
 
 
+def _host_indices(name, x) -> np.ndarray:
+    if getattr(x, "ndim", 1) != 1:
+        raise ValueError(f"{name}: expected one dimension")
+    x = [operator.index(i) for i in x]
+    if x and not (-2 ** 31 <= min(x) and max(x) < 2 ** 31):
+        raise ValueError(f"{name}: out of range")
+    return np.array(x, np.int32)
+
+
 def seq_reorder(pool, dst, src):
-    """Sequence dst[i] becomes a fork of what sequence src[i] was."""
-    _native().seq_reorder(pool, dst, src)
+    """Sequence dst[i] becomes a fork of what sequence src[i] was.  (Needs no
+    torch: without _calls.so it checks its arguments here.)"""
+    try:
+        calls = _native()
+    except (ImportError, RuntimeError):
+        calls = None
+    if calls is not None:
+        return calls.seq_reorder(pool, dst, src)
+    d, s = _host_indices("dst", dst), _host_indices("src", src)
+    if len(d) != len(s):
+        raise ValueError(f"src: expected {len(d)} entries, got {len(s)}")
+    _check(load().seq_reorder(pool, d.ctypes.data, s.ctypes.data, len(d)), "seq_reorder")
 
 
 def kvp_page_bounds(k_pool, block_tables, seq_lens, n_new: int, desc: AttnDesc, bounds, stream=None):

@@ -1,7 +1,9 @@
 """Builds libkvp.so in-tree for sm_103a with nvcc (no cmake, no torch
 extension machinery) and _calls.so, the binding's argument checks in C++, with
 g++ against the installed torch's headers.  Translation units compile in
-parallel, then link.
+parallel, then link.  The library needs neither torch nor Python's headers:
+where _calls.so cannot be built, a warning says why, and the calls that need it
+raise.
 
     python -m paged_prefix_shared_decode_gb300.build [--force]
 """
@@ -13,6 +15,7 @@ import runpy
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,8 +54,12 @@ def _stale(target: str, deps: list) -> bool:
 
 def _calls_job(force: bool, headers: list):
     """The command that compiles _calls.so and where it writes to, or None if
-    the module is up to date (with the sources and with the torch installed)."""
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    the module is up to date (with the sources and with the torch installed).
+    Raises ModuleNotFoundError without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise ModuleNotFoundError("No module named 'torch'")
+    torch = list(spec.submodule_search_locations)[0]
     version = runpy.run_path(os.path.join(torch, "version.py"))["__version__"]
     src = os.path.join(CSRC, "py_calls.cpp")
     stamp = os.path.join(OUT_DIR, "calls_torch_version")
@@ -91,16 +98,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    calls = _calls_job(force, headers)
-    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
-        for err in ex.map(run, ([calls[0]] if calls else []) + jobs):
-            if verbose and err:
-                print(err)
-    if calls:
-        _, tmp, stamp, version = calls
+    def build_calls():
+        job = _calls_job(force, headers)
+        if job is None:
+            return ""
+        cmd, tmp, stamp, version = job
+        try:
+            err = run(cmd)
+        except (OSError, RuntimeError):
+            if os.path.exists(CALLS):
+                os.remove(CALLS)      # (of other sources or another torch)
+            raise
         os.replace(tmp, CALLS)
         with open(stamp, "w") as f:
             f.write(version)
+        return err
+
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        calls = ex.submit(build_calls)
+        for err in ex.map(run, jobs):
+            if verbose and err:
+                print(err)
+    try:
+        err = calls.result()
+        if verbose and err:
+            print(err)
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"_calls.so is not built: {e}")
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         run([nvcc, "-shared", "-o", tmp] + objs + ARCH + ["-lcudart"])
