@@ -789,7 +789,9 @@ int paged_sparse_attention(const void *q, const int32_t *q_start, int32_t num_q,
  * nothing above -inf, gives no continuation, nor does a logit of -inf (a
  * masked token).  out_scores fp32, out_rows (r) and out_tokens (x) int32, all
  * [groups][n_out]; where there are fewer than n_out continuations: -inf, -1
- * and -1.  1 <= beams <= 128, 1 <= n_out <= 128.  Exponentials are fp32; sums
+ * and -1.  out_scores may be scores itself where n_out == beams; otherwise the
+ * results do not overlap scores or finished.  1 <= beams <= 128, 1 <= n_out <=
+ * 128.  Exponentials are fp32; sums
  * of them and the scores that are compared are pairs of fp32 numbers (48
  * bits), the results rounded to fp32.  A score below fp32's range counts as
  * none.

@@ -579,6 +579,11 @@ cudaError_t launch_reorder(const void *src, void *dst, const int32_t *index, int
 
 bool bad(const void *p, uintptr_t align) { return !p || ((uintptr_t)p & (align - 1)); }
 
+bool overlap(const void *x, size_t nx, const void *y, size_t ny) {
+    const uintptr_t a = (uintptr_t)x, b = (uintptr_t)y;
+    return a < b + ny && b < a + nx;
+}
+
 bool beam_shape_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t n_out) {
     if (groups <= 0 || beams <= 0 || beams > kMaxBeams || vocab <= 0 || vocab > (1 << 30) || n_out <= 0 || n_out > kMaxOut)
         return false;
@@ -621,6 +626,15 @@ int kvp_beam_select(const void *logits, int32_t logits_type, int64_t row_stride,
     const int size = logits_type == KVP_F32 ? 4 : 2;
     if (bad(logits, size) || bad(scores, 4) || bad(out_scores, 4) || bad(out_rows, 4) || bad(out_tokens, 4) ||
         bad(workspace, 16) || ws_bytes < kvp_beam_workspace_size(groups, beams, vocab, n_out))
+        return KVP_ERR_INVALID;
+    // a request's results are written while others' scores are still read; its own
+    // are read by then, so that new scores may take the old ones' places
+    const size_t rows = (size_t)groups * beams, results = (size_t)groups * n_out * 4;
+    const bool in_place = out_scores == scores && n_out == beams;
+    if (!in_place && overlap(out_scores, results, scores, rows * 4)) return KVP_ERR_INVALID;
+    if (overlap(out_rows, results, scores, rows * 4) || overlap(out_tokens, results, scores, rows * 4)) return KVP_ERR_INVALID;
+    if (finished && (overlap(out_scores, results, finished, rows) || overlap(out_rows, results, finished, rows) ||
+                     overlap(out_tokens, results, finished, rows)))
         return KVP_ERR_INVALID;
     if (!stream && stream_capturing(nullptr)) return KVP_ERR_STATE;
     BeamArgs a{};

@@ -24,3 +24,16 @@ def test_rows_and_chunks_beyond_32_bits(G, K, V, n):
 def test_the_largest_sizes_have_a_workspace(G, K, V, n):
     # a head of 16 bytes and n candidates of 8 for every row and chunk of 8184
     assert kvp.kvp_beam_workspace_size(G, K, V, n) == G * K * -(-V // 8184) * (16 + 8 * n)
+
+
+def select(scores=A, done=None, K=4, n=4, out=B, rows=B + 4096, tokens=B + 8192, G=3):
+    return kvp.load().kvp_beam_select(A, 0, 100, scores, done, 0, G, K, 100, n, out, rows, tokens, A, 1 << 20, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(scores=B, n=5), dict(scores=B, n=3), dict(scores=B, K=5),      # in place, but not as many as beams
+    dict(scores=B + 4), dict(scores=B + 44), dict(scores=B - 44),       # overlaps without being it
+    dict(scores=B + 4096), dict(scores=B + 8192), dict(scores=B + 4096, rows=B + 4096, out=B + 4096),
+    dict(done=B), dict(done=B + 47), dict(done=B - 11), dict(done=B + 4096), dict(done=B + 8200)])
+def test_results_over_inputs_that_are_still_read(bad):
+    assert select(**bad) == kvp.KVP_ERR_INVALID
