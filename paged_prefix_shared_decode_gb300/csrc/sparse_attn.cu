@@ -42,6 +42,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kList = 512;       // selected pages looked up at a time
 constexpr int kMaxCtas = 8;      // CTAs of a cluster
+// Largest reference m, in powers of two, for 2^(s scale - m) in one fused
+// instruction: m = s scale rounded is off by 2^-24 m, a factor that every weight
+// of the row carries; it stays far from fp32's ends.
+constexpr float kLargestScore = 0x1p28f;
 
 struct SparseArgs {
     QueryRows rows;
@@ -501,7 +505,15 @@ struct Rows16 {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             // (2^-inf = 0 for a row that has seen nothing yet)
-            const float shift = m[e] == -INFINITY ? 0.f : -m[e] * scale_log2;
+            float shift = m[e] == -INFINITY ? 0.f : -m[e] * scale_log2;
+            if (fabsf(shift) > kLargestScore) {      // the difference first
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    s[n][2 * e] -= m[e];
+                    s[n][2 * e + 1] -= m[e];
+                }
+                shift = 0.f;
+            }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const float x0 = exp2_sfu(fmaf(s[n][2 * e], scale_log2, shift));

@@ -29,7 +29,8 @@
 // zeros, whatever the page holds.  A NaN or an infinity in a page that some rows
 // name reaches the others too, as 0 times that, and a row that names a page
 // twice counts it twice: both are found, and such a tile's rows are then done
-// one after the other, each by its own list, in slow_row().
+// one after the other, each by its own list, in slow_row().  So are those of a
+// tile with scores beyond kLargestScore.
 //
 // Every wait is bounded; should one run out, the tile's results are NaN.
 //
@@ -449,7 +450,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int64_t row = r < cols ? q_row(r) : 0;
         if (par == 0 && half == 0 && r < cols && a.lse)
             a.lse[row] = lost ? NAN : z == 0.f ? -INFINITY : (top + log2f(z)) * 0.69314718055994531f;
-        bad = !isfinite(z);
+        bad = !isfinite(z) || (fabsf(m0) > kLargestScore && m0 > -INFINITY) ||
+              (fabsf(m1) > kLargestScore && m1 > -INFINITY);
         for (int c = 32 * par; c < D / 2; c += 64) {
             uint32_t y0[32] = {}, y1[32] = {};
             if (steps > 0) tmem_ld32(o_half + c, y0);
