@@ -475,9 +475,10 @@ struct Rows16 {
                 for (int i = 0; i < 4; ++i)
                     if (8 * n + 2 * t + (i & 1) > last[i >> 1]) s[n][i] = -INFINITY;
         }
-        // the reference is in units of unscaled scores: 2^((s - m) scale)
+        // the reference is in units of unscaled scores: 2^((s - m) scale).  (slack is
+        // finite: the first reference is -inf)
         bool raise = false;
-        const float slack = 8.f / scale_log2;
+        const float slack = fminf(8.f / scale_log2, 1e30f);
         float top[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

@@ -1,5 +1,5 @@
-"""Sparse attention where scores are very large, by single rows, by tiles and on the
-tensor cores."""
+"""Sparse attention where scores are very large, and where the scale is next to
+nothing, by single rows, by tiles and on the tensor cores."""
 import numpy as np
 import pytest
 
@@ -51,3 +51,10 @@ def test_large_scores(how, size, sign):
     f = 0.5 + torch.rand(b.L, b.T, b.Hq, 1, generator=gen, device="cuda")
     b.q[:] = (sign * size * f * u[:, :, :, 0].repeat_interleave(b.Hq // b.Hkv, 2)).bfloat16()
     check(b, like_neighbours(b, 5), 0.125, (b.d / 16 + 1) * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("scale", [1e-30, 1e-37, 1e-38, 1e-39, 1e-42])
+def test_scales_next_to_nothing(how, scale):
+    b = batch(how)
+    check(b, like_neighbours(b, 5), scale, 2.0 ** -22)
