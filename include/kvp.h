@@ -653,9 +653,11 @@ int kvp_draft_verify(const float *target, int64_t target_batch_stride, int64_t t
  *   (x cos a - y sin a, y cos a + x sin a) * scale,   a = p * freq_i,
  * freq_i = freqs[i] (host, radians per position, rot_dim / 2 of them; read
  * during the call) or, with freqs NULL, base ^ (-2 i / rot_dim).  The other
- * dims stay as they are.  scale 0 counts as 1.  Angles are reduced exactly
- * (positions are whole numbers: p * freq / 2 pi modulo 1 in 64-bit fixed
- * point), so far positions lose nothing.
+ * dims stay as they are.  scale 0 counts as 1.  Angles are reduced in 64-bit
+ * fixed point: freq_i / 2 pi modulo 1, a double's quotient, times the whole
+ * number p wraps exactly.  So an angle is off by 2^-33 of a turn and by p times
+ * the quotient's rounding (2^-56 of a turn for a frequency of 1: 2^-33 at
+ * position 2^23, 2^-25 at 2^31), and by what freq_i itself was rounded.
  */
 typedef struct {
     int32_t rot_dim;
@@ -766,9 +768,12 @@ int kvp_page_select(const float *scores, int64_t score_stride, const int32_t *q_
  * value as an infinity or a NaN.  Other slots do not matter, whatever they hold
  * (but neighbouring rows of a chunk are done together, and one by one, several
  * times slower, where one of them names a page twice or a page that one of them
- * names holds a value that is not finite).  Sums and weights are held in 32 bits
- * (a weight meets V as two bf16 parts), and repeated calls give equal bits.  A
- * kernel's wait that runs out, which no input causes, leaves NaN in its rows.
+ * names holds a value that is not finite, or one of their scores is beyond 2^28).
+ * Chunks share their pages' reads in tables of at most 4096 pages; wider ones are
+ * done row by row, some four times slower, however short their sequences.  Softmax
+ * statistics and sums are fp32; a weight meets V as two bf16 numbers, which keep 16
+ * bits of it.  Repeated calls give equal bits.  A kernel's wait that runs out,
+ * which no input causes, leaves NaN in its rows.
  */
 int paged_sparse_attention(const void *q, const int32_t *q_start, int32_t num_q, const void *k_pool,
                            const void *v_pool, const int32_t *block_tables, const int32_t *seq_lens,
@@ -791,10 +796,12 @@ int paged_sparse_attention(const void *q, const int32_t *q_start, int32_t num_q,
  * [groups][n_out]; where there are fewer than n_out continuations: -inf, -1
  * and -1.  out_scores may be scores itself where n_out == beams; otherwise the
  * results do not overlap scores or finished.  1 <= beams <= 128, 1 <= n_out <=
- * 128.  Exponentials are fp32; sums
- * of them and the scores that are compared are pairs of fp32 numbers (48
- * bits), the results rounded to fp32.  A score below fp32's range counts as
- * none.
+ * 128.  Exponentials and sums of 32 of them are fp32, sums of those pairs of fp32
+ * numbers (48 bits): a row's log-sum-exp is within 2^-21.  Scores are compared as
+ * such pairs and rounded to fp32 at the end; they hold 48 bits of the row's largest
+ * logit, too (x in magnitude: 2^-47 x), so that a row masked whole by its type's
+ * lowest value, instead of -inf, scores about 0: give such a row a score of -inf.
+ * A score below fp32's range counts as none.
  * workspace: 16-byte aligned, ws_bytes >= kvp_beam_workspace_size() (0 on
  * invalid input), its content does not matter; one call at a time.  May be
  * captured into a graph.

@@ -17,12 +17,14 @@
 // ranks them the same way, taking the best of every chunk first.
 // What decides between beams has to be finer than fp32, and the FP64 pipe is
 // slow here (a join that compared doubles took 47 us, one that added and took
-// exponentials in them 15): sums and scores are pairs of fp32 numbers, value
-// and rest (48 bits, by error-free sums), compared as 64-bit whole numbers of
-// the same order.
+// exponentials in them 15): scores, and sums beyond a thread's 32 exponentials
+// (which are added in fp32: 2^-22 of the sum, as the exponentials themselves),
+// are pairs of fp32 numbers, value and rest (48 bits, by error-free sums),
+// compared as 64-bit whole numbers of the same order.
 // 32 requests of 8 beams over 131072 fp32 tokens, n = 16 (a fifth of the beams
 // finished): parts 29 us (107 MB, 3.7 TB/s; 668 instructions a warp and chunk at
-// 55% of the issue slots), join 6.  One request of 4 beams over 32000: 8.8 us
+// 55% of the issue slots), join 6; as bf16 or fp16, half the bytes at the same
+// instructions, 34 us in place of 36.  One request of 4 beams over 32000: 8.8 us
 // with the states' gather, the two kernels' latencies.  32 logits a thread and
 // four CTAs per SM were best: 64 logits 63 us, 16 logits 52, a persistent grid
 // that copies the next chunk ahead 69 (of 40 for all three kernels).

@@ -5,9 +5,10 @@
 // Pair (x, y) at position p becomes (x cos a - y sin a, y cos a + x sin a),
 // a = p * freq.  In turns, a / 2 pi = p * f with only f modulo 1 of account,
 // as p is a whole number: f is held as 64-bit fixed point, p * f wraps modulo
-// 2^64, and its top 32 bits are the angle to 2^-33 of a turn at any position
-// (fp32 p * freq loses 2^-24 p of it).  The rotation runs in fp32, the result
-// is rounded to bf16 once.
+// 2^64, and its top 32 bits are the angle to 2^-33 of a turn, beside p times the
+// rounding of f (a double's quotient: 2^-56 of a turn for a frequency of 1, so
+// 2^-33 at position 2^23 and 2^-25 at 2^31; fp32 p * freq loses 2^-24 p of it).
+// The rotation runs in fp32, the result is rounded to bf16 once.
 //
 // One CTA takes a few tokens of a layer.  Its threads work out the tokens'
 // cos and sin once (every head of K and Q uses them) while their first loads
@@ -17,7 +18,9 @@
 // prompts (4 bytes per value moved): 26800 tokens in 2 layers, 48 heads of 128
 // in all, 190 us, 6.9 TB/s of 1.32 GB, the rate of a plain copy.  By latency for
 // decode steps: 64 beams in 8 layers, of which 59 copy their last page, 8.9 us
-// (39 MB), one token in 22 layers 2.8 us.
+// (39 MB), one token in 22 layers 2.8 us.  4-bit pages have a CTA per token and a
+// warp per row with accesses of 2 to 8 bytes: 27700 prompt tokens in 2 layers 910
+// us, 1.3 TB/s; 64 beams in 8 layers 15 us.
 //
 // The host describes tokens by runs (a sequence's consecutive slots) and
 // their blocks, in the kernel's parameters: 4 bytes per page instead of per

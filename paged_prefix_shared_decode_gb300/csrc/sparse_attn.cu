@@ -887,7 +887,9 @@ cudaError_t launch_for(SparseArgs a, cudaStream_t stream) {
     // where single rows take 29, 105 queries 33 against 62; at head dim 64 with 4
     // heads 300 queries 29 against 28) and read a page for all their rows whatever
     // part of a tile these fill (64 sequences of 5.4 rows on average 112 us against
-    // 126, of 2.4 100 against 86)
+    // 126, of 2.4 100 against 86).  Both kinds of tile have a place in shared memory
+    // for each page that the table can name; chunks in wider tables are done by
+    // single rows (643 queries over 32 pages of 32 tokens 275 us in place of 63)
     const int64_t units = (int64_t)a.rows.T * a.L * a.Hkv;
     if (a.rows.start && a.rows.MB <= kTcPages && a.L * a.Hkv <= 65535 && a.G <= kTcRows / 2 &&
         units * D >= 512LL * device_sm_count() && a.rows.T >= 5LL * a.rows.S &&
