@@ -481,8 +481,9 @@ int kvp_decode_step(kvp_pool *pool, const int32_t *seq_ids, int32_t num_seqs, in
  * tokens are already in the sequences.  Between plan and run no call may
  * change the planned sequences or free blocks; appends and attention on other
  * sequences may run (but no append to a sequence that was cut back in a page
- * which it shared with a planned one: the run still copies that page).  `workspace` belongs to the run until the stream passes
- * its kernels, as for every attention call.  The run takes its device
+ * which it shared with a planned one: the run still copies that page).
+ * `workspace` belongs to the run until the stream passes its kernels, as for
+ * every attention call.  The run takes its device
  * buffers from io as kvp_decode_step does (num_seqs and ntok are the plan's).
  * Errors: the plan call as kvp_decode_step's (KVP_ERR_INVALID, KVP_ERR_OOM;
  * nothing changed); the run returns KVP_ERR_INVALID for a plan that is not
@@ -679,8 +680,9 @@ typedef struct {
  * KVP_ERR_INVALID also for a rotation outside the above, KVP_ERR_STATE also
  * while `stream` is being captured (a replay would write the same slots again).
  * One kernel for appends of up to 512 sequences, 512 copied blocks and 4096
- * pages (two where the copies come first, see seq_append_batch); no workspace.  A batch whose ntoks are all 0 does nothing.  After
- * KVP_ERR_CUDA from a launch the bookkeeping stands.
+ * pages (two where the copies come first, see seq_append_batch); no workspace.
+ * A batch whose ntoks are all 0 does nothing.  After KVP_ERR_CUDA from a launch
+ * the bookkeeping stands.
  */
 int seq_append_rope(kvp_pool *pool, int32_t nseq, const int32_t *seqs, const int32_t *ntoks, const void *k,
                     const void *v, const kvp_rope_desc *rope, const int32_t *positions, const void *q, void *q_out,

@@ -308,8 +308,8 @@ cudaError_t launch_step_write_pb(const KvWrite &w, const void *q_src, void *q_ds
 }
 
 bool step_write_fits(const KvWrite &w, size_t plan_bytes) {
-    return !w.copies_first && w.ntok <= kSmallSlots && w.ncow <= kSmallCow && plan_bytes <= kStepPlanMax && plan_bytes % 16 == 0 &&
-           w.d % 8 == 0;
+    return !w.copies_first && w.ntok <= kSmallSlots && w.ncow <= kSmallCow && plan_bytes <= kStepPlanMax &&
+           plan_bytes % 16 == 0 && w.d % 8 == 0;
 }
 
 cudaError_t launch_step_write(const KvWrite &w, const void *q_src, void *q_dst, size_t q_bytes, const void *plan,

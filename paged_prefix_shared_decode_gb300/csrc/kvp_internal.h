@@ -208,8 +208,8 @@ cudaError_t launch_kv_write(const KvWrite &w, cudaStream_t stream);
 // q_src to q_dst when q_src is given, and plan_bytes of a host plan image,
 // carried in the kernel parameters, to plan_dst), letting the kernel launched
 // behind it with programmatic serialisation start at once.  For appends of at
-// most 64 tokens and 16 copy-on-write blocks and plans of at most
-// kStepPlanMax bytes (step_write_fits); cudaErrorInvalidValue otherwise.
+// most 64 tokens and 16 copy-on-write blocks, without copies_first, and plans of
+// at most kStepPlanMax bytes (step_write_fits); cudaErrorInvalidValue otherwise.
 constexpr size_t kStepPlanMax = 24576;
 bool step_write_fits(const KvWrite &w, size_t plan_bytes);
 cudaError_t launch_step_write(const KvWrite &w, const void *q_src, void *q_dst, size_t q_bytes, const void *plan,
